@@ -59,10 +59,19 @@ extern "C" {
 #define BEP_DERR_INFEASIBLE  4   /* a rank did not end with exactly S*K slots     */
 #define BEP_DERR_BOUNDS      8   /* a dest / cu_seqlens / slot entry out of range */
 #define BEP_DERR_TIMEOUT    16   /* a bounded device wait gave up                 */
+#define BEP_DERR_NONFINITE  32   /* a router logit is NaN or +inf, or a key NaN   */
 
 /* modes ([P4] "The memory contract": how to set B) */
 #define BEP_TRAIN 0   /* B == E/R: every expert the GEMM touches is local        */
 #define BEP_INFER 1   /* B <  E/R: remote experts beyond B read from home rows   */
+
+/* element types of router logits */
+#define BEP_F32  0
+#define BEP_BF16 1
+
+/* router scores */
+#define BEP_SCORE_SOFTMAX 0   /* softmax over the token's E logits               */
+#define BEP_SCORE_SIGMOID 1   /* sigmoid of each logit                           */
 
 /* Size limits checked by bep_create: 1 <= R <= 64, 1 <= E <= 2048, E % R == 0,
  * 1 <= K <= 32, K <= E, S >= 0, R*S*K < 2^31, H % 64 == 0, H' % 64 == 0,
@@ -274,6 +283,121 @@ int bep_grouped_gemm_dw_overwrite(bep_ctx* ctx, const int32_t* cu_seqlens, const
  *   red [R, B, H, H'] fp32 (in/out: consumed slots become zero). */
 int bep_reduce_grad(bep_ctx* ctx, const int32_t* slot_expert, float* g_home, float* red,
                     void* stream);
+
+/* Routing: the choice of experts and the gates that bep_plan and bep_combine take.
+ * With s_e = softmax(l)_e or sigmoid(l_e) in fp32 and key_e = s_e + bias[e]:
+ *   - with groups > 1, experts [g*E/groups, (g+1)*E/groups) form group g; a group
+ *     scores the sum of its group_top (1 or 2) largest keys, and the top_groups
+ *     best groups are kept (ties: the lowest group);
+ *   - topk[r,t,:] = the K kept experts of the largest keys, largest first (ties:
+ *     the lowest expert), always K different ones;
+ *   - gates[r,t,k] = scale * s_k / sum_j s_j (renorm != 0; 0 where the sum is 0)
+ *     or scale * s_k: the bias moves the choice only;
+ *   - load[e] += the number of tokens that chose e, when load is given (the caller
+ *     zeroes it; what a balance bias is updated from).
+ * Without a bias and with groups scored by one key the order is the logits' own.
+ * A logit at its type's lowest finite value or below (-inf) masks the expert: it
+ * ranks after all others and its gate is 0. A NaN or +inf logit counts as masked
+ * and latches BEP_DERR_NONFINITE, as a NaN key does.
+ *   logits [R, S, E] fp32 or bf16 (logits_type BEP_F32 / BEP_BF16), aligned to the
+ *   type; bias [E] fp32 or NULL; topk [R, S, K] int32 out; gates [R, S, K] fp32
+ *   out; load [E] int32 in/out or NULL.
+ * BEP_ERR_ARG: an unknown score or type, groups/top_groups/group_top out of range,
+ * a scale that is not finite. BEP_ERR_SIZE: groups > 32, E % groups != 0, or fewer
+ * than K experts in top_groups groups. */
+typedef struct bep_route_config {
+    int32_t score;        /* BEP_SCORE_SOFTMAX or BEP_SCORE_SIGMOID */
+    int32_t groups;       /* 1: no groups                           */
+    int32_t top_groups;   /* groups kept                            */
+    int32_t group_top;    /* keys summed into a group's score: 1, 2 */
+    int32_t renorm;       /* gates divided by their sum             */
+    float scale;          /* factor of every gate                   */
+} bep_route_config;
+int bep_route(bep_ctx* ctx, const bep_route_config* rc, const void* logits, int32_t logits_type,
+              const float* bias, int32_t* topk, float* gates, int32_t* load, void* stream);
+
+/* Gradient of the logits from the gates' (bep_combine_dgates); the choice itself
+ * and the bias have none. With dv_k = scale * dg_k, or with renorm
+ * scale * (dg_k - sum_j dg_j w_j) / sum_j s_j, w = s / sum s over the chosen:
+ *   sigmoid: dl_k = dv_k s_k (1 - s_k) for the chosen, 0 for the others;
+ *   softmax: dl_e = s_e (dv_e - sum_k dv_k s_k), dv_e = 0 for the others.
+ * A masked expert's gradient is 0.
+ *   logits [R, S, E] as given to bep_route; topk [R, S, K] from it (K different
+ *   experts a token); dgates [R, S, K] fp32; dlogits [R, S, E] out, of logits_type,
+ *   every element written; not the logits' own buffer (BEP_ERR_ARG).
+ * A topk entry outside [0, E) is skipped and latches BEP_DERR_EXPERT_ID. */
+int bep_route_bwd(bep_ctx* ctx, const bep_route_config* rc, const void* logits, int32_t logits_type,
+                  const int32_t* topk, const float* dgates, void* dlogits, void* stream);
+
+/* Gated activation of an expert's first projection, over the R*S*K receive rows:
+ *   a[row, c] = g * sigmoid(g) * u,  g = h[row, c], u = h[row, F + c]
+ * (fp32, one rounding to bf16), and, when codes and scales are given, the 8-bit
+ * checkpoint of h that bep_swiglu_bwd reads in place of h: blocks of 32 elements
+ * share a power of two 2^e, the smallest (e >= -127) with max |h| <= 127 * 2^e;
+ *   codes[row, i] = round-half-even(h[row, i] / 2^e),  scales[row, i/32] = e + 127.
+ * The values are codes * 2^e: within 2^(e-1) of h. A block with an infinity or a
+ * NaN gets the scale 0xFF and all its values are NaN.
+ *   h [R*S*K, 2F] bf16; a [R*S*K, F] bf16 out; codes [R*S*K, 2F] int8 out;
+ *   scales [R*S*K, 2F/32] uint8 out; codes and scales are both given or both NULL.
+ *   F % 32 == 0, F >= 32 (BEP_ERR_ARG). */
+int bep_swiglu(bep_ctx* ctx, const uint16_t* h, int32_t F, uint16_t* a, int8_t* codes,
+               uint8_t* scales, void* stream);
+
+/* Backward of bep_swiglu from its checkpoint (g, u the checkpoint's values,
+ * s = sigmoid(g)):
+ *   dh[row, c] = da * u * s * (1 + g * (1 - s)),  dh[row, F + c] = da * g * s,
+ * and a[row, c] = g * s * u again, when a is given (the operand of the second
+ * projection's weight gradient, which then need not be kept from the forward).
+ *   da [R*S*K, F] bf16; dh [R*S*K, 2F] bf16 out; a [R*S*K, F] bf16 out or NULL. */
+int bep_swiglu_bwd(bep_ctx* ctx, const uint16_t* da, int32_t F, const int8_t* codes,
+                   const uint8_t* scales, uint16_t* dh, uint16_t* a, void* stream);
+
+/* 4-bit experts. Elements are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
+ * code = sign * 8 + index), two a byte, the even element in the low 4 bits. Blocks of
+ * 32 elements along the reduction share a power of two 2^e, the smallest (e >= -127)
+ * with max |v| <= 6 * 2^e, held as the byte e + 127; elements round to the nearest
+ * value, ties to the even code. A block with an infinity or a NaN gets the byte 0xFF:
+ * all its values are NaN.
+ *
+ * Quantises the home rows [0, E) of a weight tensor, once, before serving:
+ *   w      [E, H, H'] bf16 (blocks run along H)
+ *   codes  [E, H', H/2] out
+ *   scales [E, ceil(H'/128), ceil(H/128), 512] out: in each 512-byte block, output
+ *          column n (of 128) and block k (of 4) at byte (n%32)*16 + (n/32)*4 + k.
+ *          Bytes of columns >= H' and blocks >= H/32 are not written and not used. */
+int bep_mx_quantize_weight(bep_ctx* ctx, const uint16_t* w, uint8_t* codes, uint8_t* scales,
+                           void* stream);
+
+/* bep_dispatch in 4 bits: every token is quantised once and its codes and scales are
+ * written to its K receive rows.
+ *   x [R, S, H] bf16; dest [R, S, K]; codes [R*S*K, H/2] out;
+ *   scales [R*S*K, 16*ceil(H/512)] out: block k of a row at byte k; bytes from H/32 on
+ *   are not written and not used. */
+int bep_dispatch_mx(bep_ctx* ctx, const uint16_t* x, const int32_t* dest, uint8_t* codes,
+                    uint8_t* scales, void* stream);
+
+/* The gated activation of bep_swiglu, quantised to 4 bits for the second projection
+ * (the fp32 activation is rounded once, to e2m1):
+ *   h [R*S*K, 2F] bf16; codes [R*S*K, F/2] out; scales [R*S*K, 16*ceil(F/512)] out.
+ *   F % 64 == 0, F >= 64 (BEP_ERR_ARG). */
+int bep_swiglu_mx(bep_ctx* ctx, const uint16_t* h, int32_t F, uint8_t* codes, uint8_t* scales,
+                  void* stream);
+
+/* The grouped product on 4-bit rows and weights: for rank u and every non-empty segment,
+ *   y[u*S*K + seg, :] = rows[u*S*K + seg, :] @ W(expert), expert = rho for rho < E and
+ *   slot_expert[u][rho - E] for a prefetch slot: the slots' replicas are read from the
+ *   home rows, which all R ranks of this GPU share, so nothing is prefetched.
+ * Products of the 4-bit values, fp32 accumulation, bf16 (round to nearest even) output.
+ * Rows outside every segment are not written; a bad cu_seqlens is refused as in
+ * bep_grouped_gemm. A non-empty slot segment without an expert in [0, E) is skipped and
+ * latches BEP_DERR_BOUNDS.
+ *   cu_seqlens [R, E+B+1]; slot_expert [R, B]; codes, scales as bep_dispatch_mx or
+ *   bep_swiglu_mx (F = H) wrote them; w_codes, w_scales from bep_mx_quantize_weight;
+ *   y [R*S*K, H'] bf16 out.
+ * BEP_ERR_SIZE: 2^31 or more work units of 128 rows x 128 outputs. */
+int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert,
+                        const uint8_t* codes, const uint8_t* scales, const uint8_t* w_codes,
+                        const uint8_t* w_scales, uint16_t* y, void* stream);
 
 /* SM budget of the token-moving kernels (dispatch, combine, combine_bwd,
  * combine_dgates, dispatch_bwd): their grids are sized for `sms` SMs, so

@@ -31,8 +31,13 @@ BEP_DERR_DUP_ID = 2
 BEP_DERR_INFEASIBLE = 4
 BEP_DERR_BOUNDS = 8
 BEP_DERR_TIMEOUT = 16
+BEP_DERR_NONFINITE = 32
 BEP_TRAIN = 0
 BEP_INFER = 1
+BEP_F32 = 0
+BEP_BF16 = 1
+BEP_SCORE_SOFTMAX = 0
+BEP_SCORE_SIGMOID = 1
 
 # every entry point declared in include/bep.h
 SYMBOLS = ("bep_create", "bep_destroy", "bep_plan", "bep_plan_noalloc", "bep_prefetch_weight",
@@ -40,7 +45,9 @@ SYMBOLS = ("bep_create", "bep_destroy", "bep_plan", "bep_plan_noalloc", "bep_pre
            "bep_combine_dgates", "bep_dispatch_bwd", "bep_grouped_gemm_dx", "bep_grouped_gemm_dw",
            "bep_grouped_gemm_dw_overwrite",
            "bep_grouped_gemm_vm", "bep_weights_create", "bep_weights_get",
-           "bep_weights_destroy", "bep_reduce_grad", "bep_set_comm_sms", "bep_wait_selftest",
+           "bep_weights_destroy", "bep_reduce_grad", "bep_route", "bep_route_bwd", "bep_swiglu",
+           "bep_swiglu_bwd", "bep_mx_quantize_weight", "bep_dispatch_mx", "bep_swiglu_mx",
+           "bep_grouped_gemm_mx", "bep_set_comm_sms", "bep_wait_selftest",
            "bep_status", "bep_clear_status", "bep_strerror")
 
 _lib = None
@@ -55,6 +62,11 @@ class BepError(RuntimeError):
 
 class _Config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("R", "E", "B", "K", "S", "H", "Hp", "mode")]
+
+
+class _RouteConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "top_groups", "group_top",
+                                              "renorm")] + [("scale", ctypes.c_float)]
 
 
 def load(path: str = LIB_PATH):
@@ -91,6 +103,14 @@ def load(path: str = LIB_PATH):
             "bep_grouped_gemm_dw": (ctypes.c_int, [vp, p, p, p, p, p, vp]),
             "bep_grouped_gemm_dw_overwrite": (ctypes.c_int, [vp, p, p, p, p, p, vp]),
             "bep_reduce_grad": (ctypes.c_int, [vp, p, p, p, vp]),
+            "bep_route": (ctypes.c_int, [vp, ctypes.POINTER(_RouteConfig), p, i32, p, p, p, p, vp]),
+            "bep_route_bwd": (ctypes.c_int, [vp, ctypes.POINTER(_RouteConfig), p, i32, p, p, p, vp]),
+            "bep_swiglu": (ctypes.c_int, [vp, p, i32, p, p, p, vp]),
+            "bep_swiglu_bwd": (ctypes.c_int, [vp, p, i32, p, p, p, p, vp]),
+            "bep_mx_quantize_weight": (ctypes.c_int, [vp, p, p, p, vp]),
+            "bep_dispatch_mx": (ctypes.c_int, [vp, p, p, p, p, vp]),
+            "bep_swiglu_mx": (ctypes.c_int, [vp, p, i32, p, p, vp]),
+            "bep_grouped_gemm_mx": (ctypes.c_int, [vp, p, p, p, p, p, p, p, vp]),
             "bep_status": (ctypes.c_int, [vp, ctypes.POINTER(i32), vp]),
             "bep_clear_status": (ctypes.c_int, [vp, vp]),
             "bep_strerror": (ctypes.c_char_p, [i32]),
@@ -454,6 +474,191 @@ def bep_reduce_grad(ctx: Context, slot_expert, g_home, red, stream=None):
     _check(load().bep_reduce_grad(ctx.handle, _ptr(slot_expert, _i32(), "slot_expert"),
                                   _ptr(g_home, _f32(), "g_home"), _ptr(red, _f32(), "red"),
                                   _stream(stream)), "bep_reduce_grad")
+
+
+@dataclass(frozen=True)
+class RouteConfig:
+    """How tokens choose experts (bep_route_config)."""
+    score: int = BEP_SCORE_SOFTMAX
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1
+    renorm: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _RouteConfig(self.score, self.groups, self.top_groups,
+                                                    self.group_top, int(self.renorm), self.scale))
+
+
+def _logits_type(t):
+    import torch
+    return BEP_F32 if t.dtype == torch.float32 else BEP_BF16
+
+
+def _logits_dtypes():
+    import torch
+    return (torch.float32, torch.bfloat16)
+
+
+def bep_route(ctx: Context, rc: RouteConfig, logits, topk, gates, bias=None, load=None, stream=None):
+    """logits [R,S,E] fp32 or bf16 -> topk int32, gates fp32 [R,S,K]; bias fp32 [E] moves the
+    choice only; load int32 [E] gets the tokens per expert added."""
+    c = ctx.cfg
+    _numel(logits, c.R * c.S * c.E, "logits")
+    _numel(topk, c.R * c.S * c.K, "topk")
+    _numel(gates, c.R * c.S * c.K, "gates")
+    _numel(bias, c.E, "bias")
+    _numel(load, c.E, "load")
+    # (the module's load() has an argument's name here; the context has loaded the library)
+    _check(_lib.bep_route(ctx.handle, ctypes.byref(rc._c), _ptr(logits, _logits_dtypes(), "logits"),
+                          _logits_type(logits), _ptr(bias, _f32(), "bias", optional=True),
+                          _ptr(topk, _i32(), "topk"), _ptr(gates, _f32(), "gates"),
+                          _ptr(load, _i32(), "load", optional=True), _stream(stream)), "bep_route")
+
+
+def bep_route_bwd(ctx: Context, rc: RouteConfig, logits, topk, dgates, dlogits, stream=None):
+    """dlogits [R,S,E] (of the logits' type) from the gates' gradients [R,S,K]."""
+    c = ctx.cfg
+    _numel(logits, c.R * c.S * c.E, "logits")
+    _numel(topk, c.R * c.S * c.K, "topk")
+    _numel(dgates, c.R * c.S * c.K, "dgates")
+    _numel(dlogits, c.R * c.S * c.E, "dlogits")
+    _check(load().bep_route_bwd(ctx.handle, ctypes.byref(rc._c),
+                                _ptr(logits, _logits_dtypes(), "logits"), _logits_type(logits),
+                                _ptr(topk, _i32(), "topk"), _ptr(dgates, _f32(), "dgates"),
+                                _ptr(dlogits, (logits.dtype,), "dlogits"), _stream(stream)),
+           "bep_route_bwd")
+
+
+def _i8():
+    import torch
+    return (torch.int8,)
+
+
+def _u8():
+    import torch
+    return (torch.uint8,)
+
+
+class ActCheckpoint:
+    """The 8-bit checkpoint of `rows` rows of 2F activations (bep_swiglu, bep_swiglu_bwd)."""
+
+    def __init__(self, rows: int, F: int, device="cuda"):
+        import torch
+        self.codes = torch.empty((rows, 2 * F), dtype=torch.int8, device=device)
+        self.scales = torch.empty((rows, 2 * F // 32), dtype=torch.uint8, device=device)
+
+
+def bep_swiglu(ctx: Context, h, a, codes=None, scales=None, stream=None):
+    """a = g * sigmoid(g) * u for h = [g | u]; codes and scales receive h's 8-bit checkpoint."""
+    c = ctx.cfg
+    F = int(a.shape[-1])
+    _numel(h, c.R * c.C * 2 * F, "h")
+    _numel(a, c.R * c.C * F, "a")
+    _numel(codes, c.R * c.C * 2 * F, "codes")
+    _numel(scales, c.R * c.C * 2 * F // 32, "scales")
+    _check(load().bep_swiglu(ctx.handle, _ptr(h, _bf16(), "h"), F, _ptr(a, _bf16(), "a"),
+                             _ptr(codes, _i8(), "codes", optional=True),
+                             _ptr(scales, _u8(), "scales", optional=True), _stream(stream)),
+           "bep_swiglu")
+
+
+def bep_swiglu_bwd(ctx: Context, da, codes, scales, dh, a=None, stream=None):
+    """dh [rows, 2F] from da [rows, F] and the checkpoint; a receives the activation again."""
+    c = ctx.cfg
+    F = int(da.shape[-1])
+    _numel(da, c.R * c.C * F, "da")
+    _numel(codes, c.R * c.C * 2 * F, "codes")
+    _numel(scales, c.R * c.C * 2 * F // 32, "scales")
+    _numel(dh, c.R * c.C * 2 * F, "dh")
+    _numel(a, c.R * c.C * F, "a")
+    _check(load().bep_swiglu_bwd(ctx.handle, _ptr(da, _bf16(), "da"), F, _ptr(codes, _i8(), "codes"),
+                                 _ptr(scales, _u8(), "scales"), _ptr(dh, _bf16(), "dh"),
+                                 _ptr(a, _bf16(), "a", optional=True), _stream(stream)),
+           "bep_swiglu_bwd")
+
+
+def mx_scale_pitch(H: int) -> int:
+    """Bytes of one quantised row's scales."""
+    return 16 * ((H + 511) // 512)
+
+
+class MxRows:
+    """`rows` quantised rows of H elements: codes [rows, H/2], scales [rows, mx_scale_pitch(H)]."""
+
+    def __init__(self, rows: int, H: int, device="cuda"):
+        import torch
+        self.codes = torch.empty((rows, H // 2), dtype=torch.uint8, device=device)
+        self.scales = torch.empty((rows, mx_scale_pitch(H)), dtype=torch.uint8, device=device)
+
+
+class MxWeight:
+    """Buffers of the E experts' 4-bit weights of a context's projection: codes [E, H', H/2],
+    scales [E, ceil(H'/128), ceil(H/128), 512]."""
+
+    def __init__(self, ctx: Context, device="cuda"):
+        import torch
+        c = ctx.cfg
+        self.codes = torch.empty((c.E, c.Hp, c.H // 2), dtype=torch.uint8, device=device)
+        self.scales = torch.zeros((c.E, (c.Hp + 127) // 128, (c.H + 127) // 128, 512),
+                                  dtype=torch.uint8, device=device)
+
+
+def _weight_numels(c, codes, scales, prefix):
+    _numel(codes, c.E * c.Hp * c.H // 2, prefix + "codes")
+    _numel(scales, c.E * ((c.Hp + 127) // 128) * ((c.H + 127) // 128) * 512, prefix + "scales")
+
+
+def bep_mx_quantize_weight(ctx: Context, w, codes, scales, stream=None):
+    """w bf16 [E, H, H'] -> 4-bit codes and scales (the buffers of an MxWeight)."""
+    c = ctx.cfg
+    _numel(w, c.E * c.H * c.Hp, "w")
+    _weight_numels(c, codes, scales, "")
+    _check(load().bep_mx_quantize_weight(ctx.handle, _ptr(w, _bf16(), "w"), _ptr(codes, _u8(), "codes"),
+                                         _ptr(scales, _u8(), "scales"), _stream(stream)),
+           "bep_mx_quantize_weight")
+
+
+def bep_dispatch_mx(ctx: Context, x, dest, codes, scales, stream=None):
+    """Quantises every token to 4 bits and writes it to its K receive rows (an MxRows)."""
+    c = ctx.cfg
+    _numel(x, c.R * c.S * c.H, "x")
+    _numel(dest, c.R * c.S * c.K, "dest")
+    _numel(codes, c.R * c.C * c.H // 2, "codes")
+    _numel(scales, c.R * c.C * mx_scale_pitch(c.H), "scales")
+    _check(load().bep_dispatch_mx(ctx.handle, _ptr(x, _bf16(), "x"), _ptr(dest, _i32(), "dest"),
+                                  _ptr(codes, _u8(), "codes"), _ptr(scales, _u8(), "scales"),
+                                  _stream(stream)), "bep_dispatch_mx")
+
+
+def bep_swiglu_mx(ctx: Context, h, codes, scales, stream=None):
+    """The gated activation of h [rows, 2F] in 4 bits (an MxRows of F elements)."""
+    c = ctx.cfg
+    F = int(h.shape[-1]) // 2
+    _numel(h, c.R * c.C * 2 * F, "h")
+    _numel(codes, c.R * c.C * F // 2, "codes")
+    _numel(scales, c.R * c.C * mx_scale_pitch(F), "scales")
+    _check(load().bep_swiglu_mx(ctx.handle, _ptr(h, _bf16(), "h"), F, _ptr(codes, _u8(), "codes"),
+                                _ptr(scales, _u8(), "scales"), _stream(stream)), "bep_swiglu_mx")
+
+
+def bep_grouped_gemm_mx(ctx: Context, cu_seqlens, slot_expert, codes, scales, w_codes, w_scales, y,
+                        stream=None):
+    """y[seg] = rows[seg] @ W(expert of seg), both in 4 bits; slots are read from the home rows."""
+    c = ctx.cfg
+    _numel(cu_seqlens, c.R * (c.E + c.B + 1), "cu_seqlens")
+    _numel(slot_expert, c.R * c.B, "slot_expert")
+    _numel(codes, c.R * c.C * c.H // 2, "codes")
+    _numel(scales, c.R * c.C * mx_scale_pitch(c.H), "scales")
+    _weight_numels(c, w_codes, w_scales, "w_")
+    _numel(y, c.R * c.C * c.Hp, "y")
+    _check(load().bep_grouped_gemm_mx(ctx.handle, _ptr(cu_seqlens, _i32(), "cu_seqlens"),
+                                      _ptr(slot_expert, _i32(), "slot_expert"),
+                                      _ptr(codes, _u8(), "codes"), _ptr(scales, _u8(), "scales"),
+                                      _ptr(w_codes, _u8(), "w_codes"),
+                                      _ptr(w_scales, _u8(), "w_scales"), _ptr(y, _bf16(), "y"),
+                                      _stream(stream)), "bep_grouped_gemm_mx")
 
 
 def bep_status(ctx: Context, stream=None) -> int:

@@ -1,0 +1,178 @@
+// Gated activation between an expert's two projections (sm_103a), and its backward from an
+// 8-bit checkpoint.
+//
+//   h = [g | u], bf16 [rows, 2F];  a = g * sigmoid(g) * u                    (bf16 out)
+//   checkpoint: h in int8 with a power-of-two scale per 32 elements (mxfmt.cuh)
+//   backward, with g^, u^ the checkpoint's values and s = sigmoid(g^):
+//     dg = da * u^ * s * (1 + g^ (1 - s)),  du = da * g^ * s,  a^ = g^ * s * u^
+// All arithmetic is fp32 with one rounding at the end of each output.
+//
+// Element-wise over rows, so bound by HBM: forward 4F + 2F + 2F (1 + 1/32) bytes a row,
+// backward 2F (1 + 1/32) + 2F + 4F + 2F. A thread owns 8 columns of both halves (16-byte
+// loads and stores of bf16, 8-byte of int8); the 4 threads of a block of 32 find its largest
+// magnitude with two shuffles.
+
+#include "mxfmt.cuh"
+
+namespace bep {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+// Quantises this thread's 8 of a block's 32 values; the scale byte is the block's.
+__device__ __forceinline__ uint2 quantise8(const float* f, uint32_t* byte) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(f[i]) & 0x7fffffffu);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    *byte = mx8_scale_byte(amax);
+    if (*byte == kMxNan) return make_uint2(0, 0);
+    const float inv = mx_inverse(*byte);
+    return make_uint2(pack_int8x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                      pack_int8x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+}
+
+// n: vectors of 8 columns in all rows (rows * F / 8, a multiple of 4, below 2^31).
+template <bool kSave>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const uint4* __restrict__ h,
+                                                          uint4* __restrict__ a,
+                                                          uint2* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales, uint32_t n,
+                                                          FastDiv cols) {
+    const uint32_t step = gridDim.x * kThreads;
+    const uint32_t rounds = (n + step - 1) / step;   // whole warps stay together for the shuffles
+    uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    for (uint32_t r = 0; r < rounds; ++r, i += step) {
+        const bool in = i < n;
+        uint4 vg = make_uint4(0, 0, 0, 0), vu = vg;
+        const uint32_t row = in ? fast_div(i, cols) : 0;
+        const uint32_t c = in ? i - row * cols.d : 0;
+        const uint64_t at = (uint64_t)row * (2 * cols.d) + c;   // gate vector; the up vector is cols.d on
+        if (in) {
+            vg = __ldcs(h + at);
+            vu = __ldcs(h + at + cols.d);
+        }
+        float g[8], u[8];
+        unpack8(vg, g);
+        unpack8(vu, u);
+        if (kSave) {
+            uint32_t bg, bu;
+            const uint2 qg = quantise8(g, &bg), qu = quantise8(u, &bu);
+            if (in) {
+                __stcs(codes + at, qg);
+                __stcs(codes + at + cols.d, qu);
+                if ((c & 3u) == 0) {
+                    scales[at >> 2] = (uint8_t)bg;
+                    scales[(at + cols.d) >> 2] = (uint8_t)bu;
+                }
+            }
+        }
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = g[j] * fast_sigmoid(g[j]) * u[j];
+        if (in) __stcs(a + i, pack8(o));
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const uint4* __restrict__ da,
+                                                              const uint2* __restrict__ codes,
+                                                              const uint8_t* __restrict__ scales,
+                                                              uint4* __restrict__ dh,
+                                                              uint4* __restrict__ a, uint32_t n,
+                                                              FastDiv cols) {
+    const uint32_t step = gridDim.x * kThreads;
+    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < n;) {
+        const uint32_t row = fast_div(i, cols);
+        const uint32_t c = i - row * cols.d;
+        const uint64_t at = (uint64_t)row * (2 * cols.d) + c;
+        const uint2 qg = __ldcs(codes + at), qu = __ldcs(codes + at + cols.d);
+        const float sg = mx_scale(scales[at >> 2]), su = mx_scale(scales[(at + cols.d) >> 2]);
+        float d[8], og[8], ou[8], oa[8];
+        unpack8(__ldcs(da + i), d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float g = int8_at(j < 4 ? qg.x : qg.y, j & 3) * sg;
+            const float u = int8_at(j < 4 ? qu.x : qu.y, j & 3) * su;
+            const float s = fast_sigmoid(g);
+            const float gs = g * s;
+            og[j] = d[j] * u * (s + gs * (1.0f - s));
+            ou[j] = d[j] * gs;
+            oa[j] = gs * u;
+        }
+        __stcs(dh + at, pack8(og));
+        __stcs(dh + at + cols.d, pack8(ou));
+        if (a) __stcs(a + i, pack8(oa));
+        if (n - i <= step) break;
+        i += step;
+    }
+}
+
+// Rows are taken in slabs of fewer than 2^31 vectors, so that positions fit 32 bits.
+template <typename F>
+cudaError_t by_slabs(int64_t rows, int F8, F&& launch) {
+    const int64_t most = ((int64_t)1 << 30) / F8 > 0 ? ((int64_t)1 << 30) / F8 : 1;
+    for (int64_t r0 = 0; r0 < rows; r0 += most) {
+        const int64_t nr = rows - r0 < most ? rows - r0 : most;
+        const cudaError_t err = launch(r0, (uint32_t)(nr * F8));
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+int grid_for(uint32_t n, int num_sms) {
+    const int64_t g = ((int64_t)n + kThreads - 1) / kThreads, cap = (int64_t)num_sms * 8;
+    return (int)(g < cap ? g : cap);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(int64_t rows, int F, const uint16_t* h, uint16_t* a, int8_t* codes,
+                          uint8_t* scales, int num_sms, cudaStream_t st) {
+    const int F8 = F / 8;
+    const FastDiv cols = make_fast_div((uint32_t)F8);
+    return by_slabs(rows, F8, [&](int64_t r0, uint32_t n) {
+        const uint4* hp = reinterpret_cast<const uint4*>(h) + r0 * 2 * F8;
+        uint4* ap = reinterpret_cast<uint4*>(a) + r0 * F8;
+        const int grid = grid_for(n, num_sms);
+        if (codes)
+            swiglu_kernel<true><<<grid, kThreads, 0, st>>>(
+                hp, ap, reinterpret_cast<uint2*>(codes) + r0 * 2 * F8, scales + r0 * (F8 / 2), n, cols);
+        else
+            swiglu_kernel<false><<<grid, kThreads, 0, st>>>(hp, ap, nullptr, nullptr, n, cols);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_swiglu_bwd(int64_t rows, int F, const uint16_t* da, const int8_t* codes,
+                              const uint8_t* scales, uint16_t* dh, uint16_t* a, int num_sms,
+                              cudaStream_t st) {
+    const int F8 = F / 8;
+    const FastDiv cols = make_fast_div((uint32_t)F8);
+    return by_slabs(rows, F8, [&](int64_t r0, uint32_t n) {
+        swiglu_bwd_kernel<<<grid_for(n, num_sms), kThreads, 0, st>>>(
+            reinterpret_cast<const uint4*>(da) + r0 * F8,
+            reinterpret_cast<const uint2*>(codes) + r0 * 2 * F8, scales + r0 * (F8 / 2),
+            reinterpret_cast<uint4*>(dh) + r0 * 2 * F8,
+            a ? reinterpret_cast<uint4*>(a) + r0 * F8 : nullptr, n, cols);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace bep

@@ -97,7 +97,8 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return BEP_ERR_CUDA;
-    if (bep::plan_setup(dev) != cudaSuccess || bep::gemm_setup(dev) != cudaSuccess)
+    if (bep::plan_setup(dev) != cudaSuccess || bep::gemm_setup(dev) != cudaSuccess ||
+        bep::mx_setup() != cudaSuccess)
         return BEP_ERR_CUDA;
 
     const size_t E = d.E, R = d.R, NC = d.NC, NROW = d.NROW, NP = d.E + d.R;
@@ -332,6 +333,118 @@ int bep_combine_dgates(bep_ctx* ctx, const uint16_t* dout, const uint16_t* y, co
                                               comm_sms(ctx), as_stream(stream)));
 }
 
+static int check_route(const bep_ctx* ctx, const bep_route_config* rc, int32_t logits_type) {
+    if (!ctx || !rc) return BEP_ERR_ARG;
+    if (rc->score != BEP_SCORE_SOFTMAX && rc->score != BEP_SCORE_SIGMOID) return BEP_ERR_ARG;
+    if (logits_type != BEP_F32 && logits_type != BEP_BF16) return BEP_ERR_ARG;
+    if (rc->groups < 1 || rc->top_groups < 1 || rc->top_groups > rc->groups) return BEP_ERR_ARG;
+    if (rc->group_top < 1 || rc->group_top > 2) return BEP_ERR_ARG;
+    if (!(rc->scale - rc->scale == 0.0f)) return BEP_ERR_ARG;   // infinite or NaN
+    if (rc->groups > 32 || ctx->d.E % rc->groups != 0) return BEP_ERR_SIZE;
+    // the kept groups hold at least K experts
+    if (ctx->d.E / rc->groups * rc->top_groups < ctx->d.K) return BEP_ERR_SIZE;
+    return BEP_OK;
+}
+
+int bep_route(bep_ctx* ctx, const bep_route_config* rc, const void* logits, int32_t logits_type,
+              const float* bias, int32_t* topk, float* gates, int32_t* load, void* stream) {
+    BEP_RANGE("bep_route");
+    const int bad = check_route(ctx, rc, logits_type);
+    if (bad) return bad;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!logits || !topk || !gates) return BEP_ERR_ARG;
+    if (!aligned(logits, logits_type == BEP_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk, 4) ||
+        !aligned(gates, 4) || !aligned(load, 4))
+        return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_route(ctx->d, ctx->ws, *rc, logits, logits_type, bias, topk, gates,
+                                     load, ctx->num_sms, as_stream(stream)));
+}
+
+int bep_route_bwd(bep_ctx* ctx, const bep_route_config* rc, const void* logits, int32_t logits_type,
+                  const int32_t* topk, const float* dgates, void* dlogits, void* stream) {
+    BEP_RANGE("bep_route_bwd");
+    const int bad = check_route(ctx, rc, logits_type);
+    if (bad) return bad;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!logits || !topk || !dgates || !dlogits || logits == dlogits) return BEP_ERR_ARG;
+    const uintptr_t a = logits_type == BEP_F32 ? 4 : 2;
+    if (!aligned(logits, a) || !aligned(dlogits, a) || !aligned(topk, 4) || !aligned(dgates, 4))
+        return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_route_bwd(ctx->d, ctx->ws, *rc, logits, logits_type, topk, dgates,
+                                         dlogits, ctx->num_sms, as_stream(stream)));
+}
+
+int bep_swiglu(bep_ctx* ctx, const uint16_t* h, int32_t F, uint16_t* a, int8_t* codes,
+               uint8_t* scales, void* stream) {
+    BEP_RANGE("bep_swiglu");
+    if (!ctx || F < 32 || F % 32 != 0 || !codes != !scales) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!h || !a) return BEP_ERR_ARG;
+    if (!aligned(h, 16) || !aligned(a, 16) || !aligned(codes, 16)) return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_swiglu((int64_t)ctx->d.R * ctx->d.C, F, h, a, codes, scales,
+                                      ctx->num_sms, as_stream(stream)));
+}
+
+int bep_swiglu_bwd(bep_ctx* ctx, const uint16_t* da, int32_t F, const int8_t* codes,
+                   const uint8_t* scales, uint16_t* dh, uint16_t* a, void* stream) {
+    BEP_RANGE("bep_swiglu_bwd");
+    if (!ctx || F < 32 || F % 32 != 0) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!da || !codes || !scales || !dh) return BEP_ERR_ARG;
+    if (!aligned(da, 16) || !aligned(codes, 16) || !aligned(dh, 16) || !aligned(a, 16))
+        return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_swiglu_bwd((int64_t)ctx->d.R * ctx->d.C, F, da, codes, scales, dh, a,
+                                          ctx->num_sms, as_stream(stream)));
+}
+
+int bep_mx_quantize_weight(bep_ctx* ctx, const uint16_t* w, uint8_t* codes, uint8_t* scales,
+                           void* stream) {
+    BEP_RANGE("bep_mx_quantize_weight");
+    if (!ctx || !w || !codes || !scales) return BEP_ERR_ARG;
+    if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_mx_weight(ctx->d, w, codes, scales, as_stream(stream)));
+}
+
+int bep_dispatch_mx(bep_ctx* ctx, const uint16_t* x, const int32_t* dest, uint8_t* codes,
+                    uint8_t* scales, void* stream) {
+    BEP_RANGE("bep_dispatch_mx");
+    if (!ctx) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!x || !dest || !codes || !scales) return BEP_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(dest, 4) || !aligned(codes, 16) || !aligned(scales, 16))
+        return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_dispatch_mx(ctx->d, ctx->ws, x, dest, codes, scales, comm_sms(ctx),
+                                           as_stream(stream)));
+}
+
+int bep_swiglu_mx(bep_ctx* ctx, const uint16_t* h, int32_t F, uint8_t* codes, uint8_t* scales,
+                  void* stream) {
+    BEP_RANGE("bep_swiglu_mx");
+    if (!ctx || F < 64 || F % 64 != 0) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!h || !codes || !scales) return BEP_ERR_ARG;
+    if (!aligned(h, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_swiglu_mx((int64_t)ctx->d.R * ctx->d.C, F, h, codes, scales,
+                                         ctx->num_sms, as_stream(stream)));
+}
+
+int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert,
+                        const uint8_t* codes, const uint8_t* scales, const uint8_t* w_codes,
+                        const uint8_t* w_scales, uint16_t* y, void* stream) {
+    BEP_RANGE("bep_grouped_gemm_mx");
+    if (!ctx) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!cu_seqlens || !slot_expert || !codes || !scales || !w_codes || !w_scales || !y)
+        return BEP_ERR_ARG;
+    if (!aligned(cu_seqlens, 4) || !aligned(slot_expert, 4) || !aligned(codes, 16) ||
+        !aligned(scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(y, 16))
+        return BEP_ERR_ALIGN;
+    // work units (row tiles x 128-column output tiles) are counted in 32 bits
+    if ((int64_t)ctx->d.max_tiles * ((ctx->d.Hp + 127) / 128) >= ((int64_t)1 << 31)) return BEP_ERR_SIZE;
+    return cuda_rc(bep::launch_grouped_gemm_mx(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales,
+                                               w_codes, w_scales, y, ctx->num_sms, as_stream(stream)));
+}
+
 int bep_wait_selftest(bep_ctx* ctx, int32_t timeout_us, void* stream) {
     if (!ctx || timeout_us < 1 || timeout_us > 10000000) return BEP_ERR_ARG;
     return cuda_rc(bep::launch_wait_selftest(ctx->ws, (uint64_t)timeout_us * 1000ull,
@@ -374,6 +487,7 @@ const char* bep_strerror(int32_t code) {
         case BEP_DERR_INFEASIBLE: return "device: plan does not give every rank S*K slots";
         case BEP_DERR_BOUNDS: return "device: index out of range";
         case BEP_DERR_TIMEOUT: return "device: bounded wait timed out";
+        case BEP_DERR_NONFINITE: return "device: a router logit or key is NaN or +infinity";
         default: return code > 0 ? "device: several error bits" : "unknown error";
     }
 }

@@ -99,6 +99,39 @@ cudaError_t launch_grouped_gemm_dw(const Dims& d, const Workspace& ws, const int
                                    const uint16_t* recv, const uint16_t* dy, float* g_home,
                                    float* red, int accumulate, int num_sms, cudaStream_t st);
 
+// cuTensorMapEncodeTiled of the driver (nullptr: not found) and the work list of 128-row tiles
+// in (rank, row) order, long and short segments merged (gemm.cu)
+void* tensor_map_encoder();
+cudaError_t launch_gemm_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st);
+// routing (route.cu)
+cudaError_t launch_route(const Dims& d, const Workspace& ws, const bep_route_config& rc,
+                         const void* logits, int logits_type, const float* bias, int32_t* topk,
+                         float* gates, int32_t* load, int num_sms, cudaStream_t st);
+cudaError_t launch_route_bwd(const Dims& d, const Workspace& ws, const bep_route_config& rc,
+                             const void* logits, int logits_type, const int32_t* topk,
+                             const float* dgates, void* dlogits, int num_sms, cudaStream_t st);
+// gated activation (act.cu)
+cudaError_t launch_swiglu(int64_t rows, int F, const uint16_t* h, uint16_t* a, int8_t* codes,
+                          uint8_t* scales, int num_sms, cudaStream_t st);
+cudaError_t launch_swiglu_bwd(int64_t rows, int F, const uint16_t* da, const int8_t* codes,
+                              const uint8_t* scales, uint16_t* dh, uint16_t* a, int num_sms,
+                              cudaStream_t st);
+// 4-bit experts (mx.cu)
+inline int mx_scale_pitch(int H) { return 16 * ((H + 511) / 512); }   // bytes of a row's scales
+cudaError_t mx_setup();
+cudaError_t launch_mx_weight(const Dims& d, const uint16_t* w, uint8_t* codes, uint8_t* scales,
+                             cudaStream_t st);
+cudaError_t launch_dispatch_mx(const Dims& d, const Workspace& ws, const uint16_t* x,
+                               const int32_t* dest, uint8_t* codes, uint8_t* scales, int num_sms,
+                               cudaStream_t st);
+cudaError_t launch_swiglu_mx(int64_t rows, int F, const uint16_t* h, uint8_t* codes,
+                             uint8_t* scales, int num_sms, cudaStream_t st);
+cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int32_t* cu,
+                                   const int32_t* slot_expert, const uint8_t* codes,
+                                   const uint8_t* scales, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, uint16_t* y, int num_sms,
+                                   cudaStream_t st);
+
 __device__ __forceinline__ int64_t i64max(int64_t a, int64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ int64_t i64min(int64_t a, int64_t b) { return a < b ? a : b; }
 

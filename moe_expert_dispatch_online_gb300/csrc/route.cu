@@ -1,0 +1,432 @@
+// Routing of tokens to experts (sm_103a): scores, groups, top-K, gates, loads, and the
+// gradient of the logits.
+//
+//   s_e  = sigmoid(l_e), or softmax(l)_e over the token's E logits        (fp32)
+//   key  = s_e + bias_e; the K largest keys are chosen, ties to the lowest index,
+//          from the top_groups groups whose group_top largest keys sum highest
+//   g_k  = scale * s_k / sum_j s_j (renorm; 0 where the sum is 0), or scale * s_k
+// Backward, with dv_k = dL/ds_k:
+//   dv_k = scale * dg_k, or with renorm scale * (dg_k - sum_j dg_j w_j) / Z, w = s / Z
+//   sigmoid: dl_k = dv_k s_k (1 - s_k), other experts 0
+//   softmax: dl_e = s_e (dv_e - sum_k dv_k s_k). With renorm that sum is 0 and
+//            dl_k = scale * w_k (dg_k - sum_j dg_j w_j), other experts 0, where w is the
+//            softmax of the K chosen logits alone: no other logit is read.
+//
+// One warp owns one token; lane l holds experts l, l + 32, ... in registers, so each load
+// instruction covers 32 consecutive logits whatever E and its alignment are.
+
+#include <cuda_bf16.h>
+#include <float.h>
+
+#include "bep_internal.cuh"
+
+namespace bep {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kAll = 0xffffffffu;
+
+// Ranks below every key of an expert that can be chosen.
+constexpr uint32_t kGone = 0u;     // chosen already, outside the kept groups, or no expert
+constexpr uint32_t kMasked = 1u;   // logit at the type's lowest value or below
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p);
+template <>
+__device__ __forceinline__ float load_logit<float>(const float* p) {
+    return __ldg(p);
+}
+template <>
+__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) {
+    return __uint_as_float((uint32_t)__ldg(p) << 16);
+}
+// lowest finite value of the logits' type: at or below it an expert is masked
+template <typename T>
+__device__ __forceinline__ float lowest() {
+    return sizeof(T) == 4 ? -FLT_MAX : __uint_as_float(0xff7f0000u);
+}
+template <typename T>
+__device__ __forceinline__ void store_grad(T* p, float v);
+template <>
+__device__ __forceinline__ void store_grad<float>(float* p, float v) {
+    *p = v;
+}
+template <>
+__device__ __forceinline__ void store_grad<uint16_t>(uint16_t* p, float v) {
+    *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Unsigned order of the result = order of the floats; -0 counts as +0. Results are >= 0x7fffff.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t b = __float_as_uint(f + 0.0f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+struct RouteParams {
+    int64_t ntok;
+    int E, K;
+    int groups, top_groups, group_top, group_size;
+    int softmax, renorm;
+    float scale;
+};
+
+// Larger two of (a1 >= a2) and (b1 >= b2).
+__device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+    const uint32_t lo = min(a1, b1);
+    a1 = max(a1, b1);
+    a2 = max(lo, max(a2, b2));
+}
+
+// ------------------------------------------------------------------------------ forward
+// V: experts a lane holds (E <= 32 V). Scores of all E experts are needed only where keys
+// are more than the logits' order (a bias, sums of two keys) or where the softmax is not
+// renormalised over the chosen ones.
+template <int V, typename T>
+__global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ logits,
+                                                         const float* __restrict__ bias,
+                                                         int32_t* __restrict__ topk,
+                                                         float* __restrict__ gates,
+                                                         int32_t* __restrict__ load,
+                                                         const RouteParams p, int32_t* status) {
+    extern __shared__ uint32_t smem[];   // loads [E], then each warp's group scores and keys [E]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int* s_load = reinterpret_cast<int*>(smem);
+    uint32_t* s_key = smem + p.E + warp * p.E;
+    if (load) {
+        for (int e = threadIdx.x; e < p.E; e += kThreads) s_load[e] = 0;
+        __syncthreads();
+    }
+    const float low = lowest<T>();
+    const bool by_score = bias != nullptr || (p.groups > 1 && p.group_top > 1);
+    const bool row_sum = p.softmax && (by_score || !p.renorm);
+    int bad = 0;
+    for (int64_t tok = (int64_t)blockIdx.x * kWarps + warp; tok < p.ntok;
+         tok += (int64_t)gridDim.x * kWarps) {
+        const T* row = logits + tok * p.E;
+        float x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            x[i] = e < p.E ? load_logit(row + e) : -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!(x[i] <= FLT_MAX)) {   // NaN or +inf: reported, and never chosen before a number
+                bad = 1;
+                x[i] = -INFINITY;
+            }
+            if (x[i] <= low) x[i] = -INFINITY;
+            top = fmaxf(top, x[i]);
+        }
+        float inv = 0.0f;   // 1 / sum of exp(l - top)
+        if (p.softmax) {
+            top = warp_max(top);
+            if (row_sum) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum += x[i] == -INFINITY ? 0.0f : expf(x[i] - top);
+                sum = warp_sum(sum);
+                inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            }
+        }
+        uint32_t key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane + 32 * i;
+            float k = x[i];
+            if (by_score && x[i] != -INFINITY) {
+                k = p.softmax ? expf(x[i] - top) * inv : sigmoid(x[i]);
+                if (bias && e < p.E) k += __ldg(bias + e);
+                if (k != k) bad = 1;
+            }
+            key[i] = e >= p.E ? kGone : (x[i] == -INFINITY || k != k) ? kMasked : ordered(k);
+        }
+        if (p.groups > 1) {
+            // `per` lanes (a power of two) scan each group's keys for its two largest
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane + 32 * i < p.E) s_key[lane + 32 * i] = key[i];
+            __syncwarp();
+            int per = 32;
+            while (per * p.groups > 32) per >>= 1;
+            const int g = lane / per, part = lane & (per - 1);
+            uint32_t k1 = kGone, k2 = kGone;
+            if (g < p.groups)
+                for (int j = part; j < p.group_size; j += per)
+                    merge2(k1, k2, s_key[g * p.group_size + j], kGone);
+            for (int o = 1; o < per; o <<= 1) {
+                const uint32_t b1 = __shfl_xor_sync(kAll, k1, o), b2 = __shfl_xor_sync(kAll, k2, o);
+                merge2(k1, k2, b1, b2);
+            }
+            // the group's score: its leading keys that are numbers; a group without any is last
+            uint32_t score = kGone;
+            if (g < p.groups) {
+                if (k1 <= kMasked) score = kMasked;
+                else if (p.group_top == 1 || k2 <= kMasked) score = k1;
+                else score = ordered(unordered(k1) + unordered(k2));
+            }
+            int rank = 0;
+            for (int o = 0; o < p.groups; ++o) {
+                const uint32_t other = __shfl_sync(kAll, score, o * per);
+                if (other > score || (other == score && o < g)) ++rank;
+            }
+            const unsigned keep = __ballot_sync(kAll, g < p.groups && rank < p.top_groups);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 32 * i;
+                if (e < p.E && !((keep >> (e / p.group_size * per)) & 1u)) key[i] = kGone;
+            }
+            __syncwarp();
+        }
+        // K rounds: the warp's largest key, the lowest expert that has it
+        uint32_t best = kGone;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = lane + 32 * i;
+            }
+        int mine = 0;
+        for (int k = 0; k < p.K; ++k) {
+            const uint32_t m = __reduce_max_sync(kAll, best);
+            const int e = (int)__reduce_min_sync(kAll, best == m ? (unsigned)at : 0x7fffffffu);
+            if (lane == k) mine = e;
+            if ((e & 31) == lane) {
+                best = kGone;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (lane + 32 * i == e) key[i] = kGone;
+                    if (key[i] > best) {
+                        best = key[i];
+                        at = lane + 32 * i;
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        // gates of the chosen experts, lane k for the k-th
+        float xs = -INFINITY;
+        if (lane < p.K) {
+            xs = load_logit(row + mine);
+            if (!(xs <= FLT_MAX) || xs <= low) xs = -INFINITY;
+        }
+        float ref = top;
+        if (p.softmax && !row_sum) ref = warp_max(xs);
+        float sc = 0.0f;
+        if (xs != -INFINITY)
+            sc = p.softmax ? expf(xs - ref) * (row_sum ? inv : 1.0f) : sigmoid(xs);
+        if (p.renorm) {
+            const float z = warp_sum(sc);
+            sc = z > 0.0f ? sc / z : 0.0f;
+        }
+        if (lane < p.K) {
+            topk[tok * p.K + lane] = mine;
+            gates[tok * p.K + lane] = p.scale * sc;
+            if (load) atomicAdd(&s_load[mine], 1);
+        }
+    }
+    if (__any_sync(kAll, bad) && lane == 0) set_status(status, BEP_DERR_NONFINITE);
+    if (load) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += kThreads)
+            if (s_load[e]) atomicAdd(&load[e], s_load[e]);
+    }
+}
+
+// ------------------------------------------------------------------------------ backward
+// kDense: softmax without renorm, every logit has a gradient. Otherwise only the K chosen
+// logits are read: the row is written as zeros and the K values over it.
+template <int V, typename T, bool kDense>
+__global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict__ logits,
+                                                             const int32_t* __restrict__ topk,
+                                                             const float* __restrict__ dgates,
+                                                             T* __restrict__ dlogits,
+                                                             const RouteParams p, int32_t* status) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float low = lowest<T>();
+    int bad = 0;
+    for (int64_t tok = (int64_t)blockIdx.x * kWarps + warp; tok < p.ntok;
+         tok += (int64_t)gridDim.x * kWarps) {
+        const T* row = logits + tok * p.E;
+        T* out = dlogits + tok * p.E;
+        int e = -1;
+        float dg = 0.0f, xs = -INFINITY;
+        if (lane < p.K) {
+            e = topk[tok * p.K + lane];
+            if (e < 0 || e >= p.E) {
+                bad |= BEP_DERR_EXPERT_ID;
+                e = -1;
+            } else {
+                dg = dgates[tok * p.K + lane];
+                xs = load_logit(row + e);
+                if (!(xs <= FLT_MAX) || xs <= low) xs = -INFINITY;
+            }
+        }
+        float v;   // dL/dl of this lane's chosen expert
+        if (kDense) {
+            float x[V], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int j = lane + 32 * i;
+                x[i] = j < p.E ? load_logit(row + j) : -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!(x[i] <= FLT_MAX) || x[i] <= low) x[i] = -INFINITY;
+                top = fmaxf(top, x[i]);
+            }
+            top = warp_max(top);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[i] = x[i] == -INFINITY ? 0.0f : expf(x[i] - top);
+                sum += x[i];
+            }
+            sum = warp_sum(sum);
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const float s = xs == -INFINITY ? 0.0f : expf(xs - top) * inv;
+            const float dot = warp_sum(s * dg);
+            v = p.scale * s * (dg - dot);
+            const float c = -p.scale * dot * inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane + 32 * i < p.E) store_grad(out + lane + 32 * i, c * x[i]);
+        } else {
+            float s, w = 0.0f, z = 0.0f;
+            if (p.softmax) {
+                const float top = warp_max(xs);
+                s = xs == -INFINITY ? 0.0f : expf(xs - top);
+            } else {
+                s = xs == -INFINITY ? 0.0f : sigmoid(xs);
+            }
+            float d = dg;
+            if (p.renorm) {
+                z = warp_sum(s);
+                w = z > 0.0f ? s / z : 0.0f;
+                d = dg - warp_sum(dg * w);
+            }
+            if (p.softmax) v = p.scale * w * d;                                       // renorm
+            else v = p.scale * (p.renorm ? w : s) * d * (xs == -INFINITY ? 0.0f : sigmoid(-xs));
+            for (int j = lane; j < p.E; j += 32) store_grad(out + j, 0.0f);
+        }
+        __syncwarp();   // the row's fill is ordered before the chosen experts' values
+        if (e >= 0) store_grad(out + e, v);
+    }
+    const unsigned any = __reduce_or_sync(kAll, (unsigned)bad);
+    if (any && lane == 0) set_status(status, (int)any);
+}
+
+RouteParams params_of(const Dims& d, const bep_route_config& rc) {
+    RouteParams p;
+    p.ntok = (int64_t)d.R * d.S;
+    p.E = d.E;
+    p.K = d.K;
+    p.groups = rc.groups;
+    p.top_groups = rc.top_groups;
+    p.group_top = rc.group_top;
+    p.group_size = d.E / rc.groups;
+    p.softmax = rc.score == BEP_SCORE_SOFTMAX;
+    p.renorm = rc.renorm != 0;
+    p.scale = rc.scale;
+    return p;
+}
+
+int grid_for(int64_t ntok, int num_sms, int per_sm) {
+    const int64_t g = (ntok + kWarps - 1) / kWarps, cap = (int64_t)num_sms * per_sm;
+    return (int)(g < cap ? g : cap);
+}
+
+// Calls fn with the smallest per-lane count that holds E experts.
+template <typename F>
+cudaError_t with_width(int E, F&& fn) {
+    if (E <= 32) return fn(std::integral_constant<int, 1>());
+    if (E <= 64) return fn(std::integral_constant<int, 2>());
+    if (E <= 128) return fn(std::integral_constant<int, 4>());
+    if (E <= 256) return fn(std::integral_constant<int, 8>());
+    if (E <= 384) return fn(std::integral_constant<int, 12>());
+    if (E <= 512) return fn(std::integral_constant<int, 16>());
+    if (E <= 1024) return fn(std::integral_constant<int, 32>());
+    return fn(std::integral_constant<int, 64>());
+}
+
+template <typename T>
+cudaError_t route_typed(const Dims& d, const Workspace& ws, const RouteParams& p, const T* logits,
+                        const float* bias, int32_t* topk, float* gates, int32_t* load, int num_sms,
+                        cudaStream_t st) {
+    // shared memory: the loads, and the keys of each warp where groups are cut
+    const size_t smem = ((size_t)d.E + (p.groups > 1 ? (size_t)kWarps * d.E : 0)) * 4;
+    return with_width(d.E, [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        if (smem > 48 * 1024) {
+            const cudaError_t err = cudaFuncSetAttribute(
+                route_kernel<V, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (err != cudaSuccess) return err;
+        }
+        route_kernel<V, T><<<grid_for(p.ntok, num_sms, 8), kThreads, smem, st>>>(
+            logits, bias, topk, gates, load, p, ws.status);
+        return cudaGetLastError();
+    });
+}
+
+template <typename T>
+cudaError_t route_bwd_typed(const Dims& d, const Workspace& ws, const RouteParams& p,
+                            const T* logits, const int32_t* topk, const float* dgates, T* dlogits,
+                            int num_sms, cudaStream_t st) {
+    const int grid = grid_for(p.ntok, num_sms, 8);
+    if (!p.softmax || p.renorm) {
+        route_bwd_kernel<1, T, false>
+            <<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
+        return cudaGetLastError();
+    }
+    return with_width(d.E, [&](auto v) {
+        route_bwd_kernel<decltype(v)::value, T, true>
+            <<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace
+
+cudaError_t launch_route(const Dims& d, const Workspace& ws, const bep_route_config& rc,
+                         const void* logits, int logits_type, const float* bias, int32_t* topk,
+                         float* gates, int32_t* load, int num_sms, cudaStream_t st) {
+    const RouteParams p = params_of(d, rc);
+    if (p.ntok == 0) return cudaSuccess;
+    if (logits_type == BEP_F32)
+        return route_typed(d, ws, p, static_cast<const float*>(logits), bias, topk, gates, load,
+                           num_sms, st);
+    return route_typed(d, ws, p, static_cast<const uint16_t*>(logits), bias, topk, gates, load,
+                       num_sms, st);
+}
+
+cudaError_t launch_route_bwd(const Dims& d, const Workspace& ws, const bep_route_config& rc,
+                             const void* logits, int logits_type, const int32_t* topk,
+                             const float* dgates, void* dlogits, int num_sms, cudaStream_t st) {
+    const RouteParams p = params_of(d, rc);
+    if (p.ntok == 0) return cudaSuccess;
+    if (logits_type == BEP_F32)
+        return route_bwd_typed(d, ws, p, static_cast<const float*>(logits), topk, dgates,
+                               static_cast<float*>(dlogits), num_sms, st);
+    return route_bwd_typed(d, ws, p, static_cast<const uint16_t*>(logits), topk, dgates,
+                           static_cast<uint16_t*>(dlogits), num_sms, st);
+}
+
+}  // namespace bep
