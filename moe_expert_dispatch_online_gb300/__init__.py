@@ -13,6 +13,7 @@ PyTorch provides device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -136,10 +137,24 @@ def _check(rc: int, where: str):
 
 
 def _stream(stream):
+    """Raw handle of `stream`, or of the current device's current stream."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(int(stream.cuda_stream))
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream)
+
+
+def _arg(t, dtypes, n, name, optional=False):
+    """Device pointer of a dense CUDA tensor of n elements, checked in one pass: small calls are
+    bound by the host, and each look at a tensor costs it 0.1 us or more."""
+    try:
+        if t.is_cuda and t.dtype in dtypes and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _ptr(t, dtypes, name, optional)   # says what is wrong
+    _numel(t, n, name)
+    return p
 
 
 def _ptr(t, dtypes, name, optional=False):
@@ -164,16 +179,19 @@ def _numel(t, n, name):
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
 
 
+@functools.cache
 def _bf16():
     import torch
     return (torch.bfloat16, torch.int16, torch.uint16)
 
 
+@functools.cache
 def _i32():
     import torch
     return (torch.int32,)
 
 
+@functools.cache
 def _f32():
     import torch
     return (torch.float32,)
@@ -487,8 +505,9 @@ class RouteConfig:
     scale: float = 1.0
 
     def __post_init__(self):
-        object.__setattr__(self, "_c", _RouteConfig(self.score, self.groups, self.top_groups,
-                                                    self.group_top, int(self.renorm), self.scale))
+        c = _RouteConfig(self.score, self.groups, self.top_groups, self.group_top, int(self.renorm),
+                         self.scale)
+        object.__setattr__(self, "_ref", ctypes.byref(c))   # keeps c alive
 
 
 def _logits_type(t):
@@ -496,6 +515,7 @@ def _logits_type(t):
     return BEP_F32 if t.dtype == torch.float32 else BEP_BF16
 
 
+@functools.cache
 def _logits_dtypes():
     import torch
     return (torch.float32, torch.bfloat16)
@@ -505,37 +525,34 @@ def bep_route(ctx: Context, rc: RouteConfig, logits, topk, gates, bias=None, loa
     """logits [R,S,E] fp32 or bf16 -> topk int32, gates fp32 [R,S,K]; bias fp32 [E] moves the
     choice only; load int32 [E] gets the tokens per expert added."""
     c = ctx.cfg
-    _numel(logits, c.R * c.S * c.E, "logits")
-    _numel(topk, c.R * c.S * c.K, "topk")
-    _numel(gates, c.R * c.S * c.K, "gates")
-    _numel(bias, c.E, "bias")
-    _numel(load, c.E, "load")
+    T = c.R * c.S
     # (the module's load() has an argument's name here; the context has loaded the library)
-    _check(_lib.bep_route(ctx.handle, ctypes.byref(rc._c), _ptr(logits, _logits_dtypes(), "logits"),
-                          _logits_type(logits), _ptr(bias, _f32(), "bias", optional=True),
-                          _ptr(topk, _i32(), "topk"), _ptr(gates, _f32(), "gates"),
-                          _ptr(load, _i32(), "load", optional=True), _stream(stream)), "bep_route")
+    _check(_lib.bep_route(ctx.handle, rc._ref, _arg(logits, _logits_dtypes(), T * c.E, "logits"),
+                          _logits_type(logits),
+                          None if bias is None else _arg(bias, _f32(), c.E, "bias"),
+                          _arg(topk, _i32(), T * c.K, "topk"), _arg(gates, _f32(), T * c.K, "gates"),
+                          None if load is None else _arg(load, _i32(), c.E, "load"),
+                          _stream(stream)), "bep_route")
 
 
 def bep_route_bwd(ctx: Context, rc: RouteConfig, logits, topk, dgates, dlogits, stream=None):
     """dlogits [R,S,E] (of the logits' type) from the gates' gradients [R,S,K]."""
     c = ctx.cfg
-    _numel(logits, c.R * c.S * c.E, "logits")
-    _numel(topk, c.R * c.S * c.K, "topk")
-    _numel(dgates, c.R * c.S * c.K, "dgates")
-    _numel(dlogits, c.R * c.S * c.E, "dlogits")
-    _check(load().bep_route_bwd(ctx.handle, ctypes.byref(rc._c),
-                                _ptr(logits, _logits_dtypes(), "logits"), _logits_type(logits),
-                                _ptr(topk, _i32(), "topk"), _ptr(dgates, _f32(), "dgates"),
-                                _ptr(dlogits, (logits.dtype,), "dlogits"), _stream(stream)),
+    T = c.R * c.S
+    _check(load().bep_route_bwd(ctx.handle, rc._ref, _arg(logits, _logits_dtypes(), T * c.E, "logits"),
+                                _logits_type(logits), _arg(topk, _i32(), T * c.K, "topk"),
+                                _arg(dgates, _f32(), T * c.K, "dgates"),
+                                _arg(dlogits, (logits.dtype,), T * c.E, "dlogits"), _stream(stream)),
            "bep_route_bwd")
 
 
+@functools.cache
 def _i8():
     import torch
     return (torch.int8,)
 
 
+@functools.cache
 def _u8():
     import torch
     return (torch.uint8,)
@@ -552,30 +569,22 @@ class ActCheckpoint:
 
 def bep_swiglu(ctx: Context, h, a, codes=None, scales=None, stream=None):
     """a = g * sigmoid(g) * u for h = [g | u]; codes and scales receive h's 8-bit checkpoint."""
-    c = ctx.cfg
     F = int(a.shape[-1])
-    _numel(h, c.R * c.C * 2 * F, "h")
-    _numel(a, c.R * c.C * F, "a")
-    _numel(codes, c.R * c.C * 2 * F, "codes")
-    _numel(scales, c.R * c.C * 2 * F // 32, "scales")
-    _check(load().bep_swiglu(ctx.handle, _ptr(h, _bf16(), "h"), F, _ptr(a, _bf16(), "a"),
-                             _ptr(codes, _i8(), "codes", optional=True),
-                             _ptr(scales, _u8(), "scales", optional=True), _stream(stream)),
-           "bep_swiglu")
+    n = ctx.cfg.R * ctx.cfg.C * F
+    _check(load().bep_swiglu(ctx.handle, _arg(h, _bf16(), 2 * n, "h"), F, _arg(a, _bf16(), n, "a"),
+                             None if codes is None else _arg(codes, _i8(), 2 * n, "codes"),
+                             None if scales is None else _arg(scales, _u8(), n // 16, "scales"),
+                             _stream(stream)), "bep_swiglu")
 
 
 def bep_swiglu_bwd(ctx: Context, da, codes, scales, dh, a=None, stream=None):
     """dh [rows, 2F] from da [rows, F] and the checkpoint; a receives the activation again."""
-    c = ctx.cfg
     F = int(da.shape[-1])
-    _numel(da, c.R * c.C * F, "da")
-    _numel(codes, c.R * c.C * 2 * F, "codes")
-    _numel(scales, c.R * c.C * 2 * F // 32, "scales")
-    _numel(dh, c.R * c.C * 2 * F, "dh")
-    _numel(a, c.R * c.C * F, "a")
-    _check(load().bep_swiglu_bwd(ctx.handle, _ptr(da, _bf16(), "da"), F, _ptr(codes, _i8(), "codes"),
-                                 _ptr(scales, _u8(), "scales"), _ptr(dh, _bf16(), "dh"),
-                                 _ptr(a, _bf16(), "a", optional=True), _stream(stream)),
+    n = ctx.cfg.R * ctx.cfg.C * F
+    _check(load().bep_swiglu_bwd(ctx.handle, _arg(da, _bf16(), n, "da"), F,
+                                 _arg(codes, _i8(), 2 * n, "codes"),
+                                 _arg(scales, _u8(), n // 16, "scales"), _arg(dh, _bf16(), 2 * n, "dh"),
+                                 None if a is None else _arg(a, _bf16(), n, "a"), _stream(stream)),
            "bep_swiglu_bwd")
 
 
@@ -605,60 +614,53 @@ class MxWeight:
                                   dtype=torch.uint8, device=device)
 
 
-def _weight_numels(c, codes, scales, prefix):
-    _numel(codes, c.E * c.Hp * c.H // 2, prefix + "codes")
-    _numel(scales, c.E * ((c.Hp + 127) // 128) * ((c.H + 127) // 128) * 512, prefix + "scales")
+def _mx_weight(c, codes, scales, prefix=""):
+    return (_arg(codes, _u8(), c.E * c.Hp * c.H // 2, prefix + "codes"),
+            _arg(scales, _u8(), c.E * ((c.Hp + 127) // 128) * ((c.H + 127) // 128) * 512,
+                 prefix + "scales"))
+
+
+def _mx_rows(c, F, codes, scales):
+    return (_arg(codes, _u8(), c.R * c.C * F // 2, "codes"),
+            _arg(scales, _u8(), c.R * c.C * mx_scale_pitch(F), "scales"))
 
 
 def bep_mx_quantize_weight(ctx: Context, w, codes, scales, stream=None):
     """w bf16 [E, H, H'] -> 4-bit codes and scales (the buffers of an MxWeight)."""
     c = ctx.cfg
-    _numel(w, c.E * c.H * c.Hp, "w")
-    _weight_numels(c, codes, scales, "")
-    _check(load().bep_mx_quantize_weight(ctx.handle, _ptr(w, _bf16(), "w"), _ptr(codes, _u8(), "codes"),
-                                         _ptr(scales, _u8(), "scales"), _stream(stream)),
+    _check(load().bep_mx_quantize_weight(ctx.handle, _arg(w, _bf16(), c.E * c.H * c.Hp, "w"),
+                                         *_mx_weight(c, codes, scales), _stream(stream)),
            "bep_mx_quantize_weight")
 
 
 def bep_dispatch_mx(ctx: Context, x, dest, codes, scales, stream=None):
     """Quantises every token to 4 bits and writes it to its K receive rows (an MxRows)."""
     c = ctx.cfg
-    _numel(x, c.R * c.S * c.H, "x")
-    _numel(dest, c.R * c.S * c.K, "dest")
-    _numel(codes, c.R * c.C * c.H // 2, "codes")
-    _numel(scales, c.R * c.C * mx_scale_pitch(c.H), "scales")
-    _check(load().bep_dispatch_mx(ctx.handle, _ptr(x, _bf16(), "x"), _ptr(dest, _i32(), "dest"),
-                                  _ptr(codes, _u8(), "codes"), _ptr(scales, _u8(), "scales"),
-                                  _stream(stream)), "bep_dispatch_mx")
+    _check(load().bep_dispatch_mx(ctx.handle, _arg(x, _bf16(), c.R * c.S * c.H, "x"),
+                                  _arg(dest, _i32(), c.R * c.C, "dest"),
+                                  *_mx_rows(c, c.H, codes, scales), _stream(stream)),
+           "bep_dispatch_mx")
 
 
 def bep_swiglu_mx(ctx: Context, h, codes, scales, stream=None):
     """The gated activation of h [rows, 2F] in 4 bits (an MxRows of F elements)."""
     c = ctx.cfg
     F = int(h.shape[-1]) // 2
-    _numel(h, c.R * c.C * 2 * F, "h")
-    _numel(codes, c.R * c.C * F // 2, "codes")
-    _numel(scales, c.R * c.C * mx_scale_pitch(F), "scales")
-    _check(load().bep_swiglu_mx(ctx.handle, _ptr(h, _bf16(), "h"), F, _ptr(codes, _u8(), "codes"),
-                                _ptr(scales, _u8(), "scales"), _stream(stream)), "bep_swiglu_mx")
+    _check(load().bep_swiglu_mx(ctx.handle, _arg(h, _bf16(), c.R * c.C * 2 * F, "h"), F,
+                                *_mx_rows(c, F, codes, scales), _stream(stream)), "bep_swiglu_mx")
 
 
 def bep_grouped_gemm_mx(ctx: Context, cu_seqlens, slot_expert, codes, scales, w_codes, w_scales, y,
                         stream=None):
     """y[seg] = rows[seg] @ W(expert of seg), both in 4 bits; slots are read from the home rows."""
     c = ctx.cfg
-    _numel(cu_seqlens, c.R * (c.E + c.B + 1), "cu_seqlens")
-    _numel(slot_expert, c.R * c.B, "slot_expert")
-    _numel(codes, c.R * c.C * c.H // 2, "codes")
-    _numel(scales, c.R * c.C * mx_scale_pitch(c.H), "scales")
-    _weight_numels(c, w_codes, w_scales, "w_")
-    _numel(y, c.R * c.C * c.Hp, "y")
-    _check(load().bep_grouped_gemm_mx(ctx.handle, _ptr(cu_seqlens, _i32(), "cu_seqlens"),
-                                      _ptr(slot_expert, _i32(), "slot_expert"),
-                                      _ptr(codes, _u8(), "codes"), _ptr(scales, _u8(), "scales"),
-                                      _ptr(w_codes, _u8(), "w_codes"),
-                                      _ptr(w_scales, _u8(), "w_scales"), _ptr(y, _bf16(), "y"),
-                                      _stream(stream)), "bep_grouped_gemm_mx")
+    _check(load().bep_grouped_gemm_mx(ctx.handle,
+                                      _arg(cu_seqlens, _i32(), c.R * (c.E + c.B + 1), "cu_seqlens"),
+                                      _arg(slot_expert, _i32(), c.R * c.B, "slot_expert"),
+                                      *_mx_rows(c, c.H, codes, scales),
+                                      *_mx_weight(c, w_codes, w_scales, "w_"),
+                                      _arg(y, _bf16(), c.R * c.C * c.Hp, "y"), _stream(stream)),
+           "bep_grouped_gemm_mx")
 
 
 def bep_status(ctx: Context, stream=None) -> int:
