@@ -95,21 +95,5 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
     return __fdividef(1.0f, 1.0f + __expf(-x));
 }
 
-// Division of n < 2^31 by an invariant d < 2^31 (a multiply and a shift).
-struct FastDiv {
-    uint32_t d, m, s;
-};
-__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
-    return (__umulhi(n, f.m) + n) >> f.s;
-}
-inline FastDiv make_fast_div(uint32_t d) {
-    FastDiv f;
-    f.d = d;
-    f.s = 0;
-    while ((1ull << f.s) < d) ++f.s;
-    f.m = (uint32_t)((((1ull << 32) * ((1ull << f.s) - d)) / d) + 1);
-    return f;
-}
-
 }  // namespace
 }  // namespace bep

@@ -79,10 +79,69 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// The scores of all E experts (keys, and the softmax's sum) use the hardware's 2^x and
+// reciprocal, 2 units in the last place of fp32 or fewer, in 2 and 4 instructions; the K gates
+// themselves use expf and a rounded division. 0 for an argument below about -87.
+__device__ __forceinline__ float fast_exp(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fast_exp(-x)));
+    return r;
+}
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A token's logits, lane l's at l + 32 i (the last expert again past E). One maximum and one
+// minimum an element tell the ordinary row, all finite and unmasked, from one that has to be
+// looked at element by element. *top: this lane's largest logit that is a number (-inf: none).
+// The result: whether the row is ordinary; otherwise its masked logits are -inf, and *bad is set
+// for a NaN or +inf among them. Past E: -inf in either case.
+template <int V, bool kFull, typename T>
+__device__ __forceinline__ bool load_row(const T* __restrict__ row, int E, int lane, float (&x)[V],
+                                         float* top, int* bad) {
+    float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = load_logit(row + (kFull ? lane + 32 * i : min(lane + 32 * i, E - 1)));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        hi = max_nan(hi, x[i]);
+        lo = fminf(lo, x[i]);
+    }
+    const bool ordinary = __all_sync(kAll, hi <= FLT_MAX && lo > lowest<T>());
+    if (!ordinary) {
+        hi = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!(x[i] <= FLT_MAX)) {
+                *bad = 1;
+                x[i] = -INFINITY;
+            }
+            if (x[i] <= lowest<T>()) x[i] = -INFINITY;
+            hi = fmaxf(hi, x[i]);
+        }
+    }
+    if (!kFull) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i >= E) x[i] = -INFINITY;
+    }
+    *top = hi;
+    return ordinary;
+}
+
 struct RouteParams {
     int64_t ntok;
     int E, K;
     int groups, top_groups, group_top, group_size;
+    FastDiv group_of;   // expert -> its group
     int softmax, renorm;
     float scale;
 };
@@ -95,24 +154,101 @@ __device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, 
 }
 
 // ------------------------------------------------------------------------------ forward
+// Selection. A key's leading bits and the expert's index (complemented) make one 32-bit word,
+// so that a round is one warp-wide maximum that names the winner and breaks ties. Each lane keeps
+// its three largest words. Where that does not decide -- a lane's three have all won (about 5
+// tokens in 100 at 8 of 384), or two of the K + 1 leading words agree in all their key bits (as
+// many) -- the choice is made again on whole keys, with a second reduction for the index.
+// 65,536 tokens, 8 of 384 by softmax and bias: 130 us with whole keys in every round and
+// element-by-element checks, 86 us with two words a lane, rescanned when both have won.
+template <int V>
+struct Packed {
+    static constexpr int kBits = V <= 1 ? 6 : V <= 2 ? 7 : V <= 4 ? 8 : V <= 12 ? 9 : V <= 16 ? 10 : V <= 32 ? 11 : 12;
+    static_assert(32 * V < (1 << kBits), "an index and its complement differ from 0");
+    static constexpr uint32_t kIndex = (1u << kBits) - 1;
+};
+
+// The K experts of the largest keys, lane k for the k-th. kAny: every key is an expert's.
+// exact: the words hold whole keys.
+template <int V, bool kAny>
+__device__ __forceinline__ int choose_packed(const uint32_t (&key)[V], int K, int lane, bool exact,
+                                             bool* decided) {
+    constexpr uint32_t kIndex = Packed<V>::kIndex;
+    uint32_t t1 = 0, t2 = 0, t3 = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        uint32_t w = (key[i] & ~kIndex) | (kIndex - 32 * i - lane);
+        if (!kAny && key[i] == kGone) w = 0;
+        if (V > 2) t3 = max(t3, min(t2, w));
+        t2 = max(t2, min(t1, w));
+        t1 = max(t1, w);
+    }
+    uint32_t mine = 0, before = ~0u, near = ~0u;
+    bool spent = false;
+    for (int k = 0; k < K; ++k) {
+        const uint32_t m = __reduce_max_sync(kAll, t1);
+        near = min(near, m ^ before);
+        before = m;
+        if (lane == k) mine = m;
+        if (t1 == m) {
+            t1 = t2;
+            t2 = t3;
+            t3 = 0;
+            spent = t1 == 0;
+        }
+    }
+    near = min(near, __reduce_max_sync(kAll, t1) ^ before);   // the first that is not chosen
+    *decided = (exact || near > kIndex) && !(V > 3 && __any_sync(kAll, spent));
+    return (int)(kIndex - (mine & kIndex));
+}
+
+// The same on whole keys: the warp's largest key, then the lowest expert that has it.
+template <int V>
+__device__ __forceinline__ int choose_whole(uint32_t (&key)[V], int K, int lane) {
+    int mine = 0;
+    for (int k = 0; k < K; ++k) {
+        uint32_t best = kGone;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = lane + 32 * i;
+            }
+        const uint32_t m = __reduce_max_sync(kAll, best);
+        const int e = (int)__reduce_min_sync(kAll, best == m ? (unsigned)at : 0x7fffffffu);
+        if (lane == k) mine = e;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane + 32 * i == e) key[i] = kGone;
+    }
+    return mine;
+}
+
 // V: experts a lane holds (E <= 32 V). Scores of all E experts are needed only where keys
 // are more than the logits' order (a bias, sums of two keys) or where the softmax is not
 // renormalised over the chosen ones.
-template <int V, typename T>
+// kPlain: E = 32 V and no groups.
+template <int V, typename T, bool kPlain>
 __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ logits,
                                                          const float* __restrict__ bias,
                                                          int32_t* __restrict__ topk,
                                                          float* __restrict__ gates,
                                                          int32_t* __restrict__ load,
                                                          const RouteParams p, int32_t* status) {
-    extern __shared__ uint32_t smem[];   // loads [E], then each warp's group scores and keys [E]
+    extern __shared__ uint32_t smem[];   // loads [E], the bias [E], then each warp's keys [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* s_load = reinterpret_cast<int*>(smem);
-    uint32_t* s_key = smem + p.E + warp * p.E;
-    if (load) {
-        for (int e = threadIdx.x; e < p.E; e += kThreads) s_load[e] = 0;
-        __syncthreads();
+    float* s_bias = reinterpret_cast<float*>(smem + p.E);
+    uint32_t* s_key = smem + (2 + warp) * p.E;
+    int bias_nan = 0;
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        s_load[e] = 0;
+        const float b = bias ? __ldg(bias + e) : 0.0f;
+        s_bias[e] = b;
+        bias_nan |= b != b;
     }
+    bias_nan = __syncthreads_or(bias_nan);
     const float low = lowest<T>();
     const bool by_score = bias != nullptr || (p.groups > 1 && p.group_top > 1);
     const bool row_sum = p.softmax && (by_score || !p.renorm);
@@ -120,46 +256,50 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
     for (int64_t tok = (int64_t)blockIdx.x * kWarps + warp; tok < p.ntok;
          tok += (int64_t)gridDim.x * kWarps) {
         const T* row = logits + tok * p.E;
-        float x[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            x[i] = e < p.E ? load_logit(row + e) : -INFINITY;
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            if (!(x[i] <= FLT_MAX)) {   // NaN or +inf: reported, and never chosen before a number
-                bad = 1;
-                x[i] = -INFINITY;
-            }
-            if (x[i] <= low) x[i] = -INFINITY;
-            top = fmaxf(top, x[i]);
-        }
+        float x[V], top;
+        const bool ordinary = load_row<V, kPlain>(row, p.E, lane, x, &top, &bad) && !bias_nan;
         float inv = 0.0f;   // 1 / sum of exp(l - top)
-        if (p.softmax) {
-            top = warp_max(top);
-            if (row_sum) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum += x[i] == -INFINITY ? 0.0f : expf(x[i] - top);
-                sum = warp_sum(sum);
-                inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            }
-        }
         uint32_t key[V];
+        if (row_sum) {
+            top = warp_max(top);
+            if (top == -INFINITY) top = 0.0f;   // nothing to choose from: all scores 0
+            float ex[V], sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            float k = x[i];
-            if (by_score && x[i] != -INFINITY) {
-                k = p.softmax ? expf(x[i] - top) * inv : sigmoid(x[i]);
-                if (bias && e < p.E) k += __ldg(bias + e);
-                if (k != k) bad = 1;
+            for (int i = 0; i < V; ++i) {
+                ex[i] = fast_exp(x[i] - top);
+                sum += ex[i];
             }
-            key[i] = e >= p.E ? kGone : (x[i] == -INFINITY || k != k) ? kMasked : ordered(k);
+            sum = warp_sum(sum);
+            inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                key[i] = ordered(by_score ? __fadd_rn(__fmul_rn(ex[i], inv), s_bias[kPlain ? lane + 32 * i : min(lane + 32 * i, p.E - 1)])
+                                          : x[i]);
+        } else if (by_score) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                key[i] = ordered(__fadd_rn(fast_sigmoid(x[i]), s_bias[kPlain ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = ordered(x[i]);
         }
-        if (p.groups > 1) {
+        if (!ordinary) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 32 * i;
+                if (by_score && e < p.E && s_bias[e] != s_bias[e]) {
+                    bad = 1;
+                    key[i] = kMasked;
+                }
+                if (x[i] == -INFINITY) key[i] = kMasked;
+            }
+        }
+        if (!kPlain) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane + 32 * i >= p.E) key[i] = kGone;
+        }
+        if (!kPlain && p.groups > 1) {
             // `per` lanes (a power of two) scan each group's keys for its two largest
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -192,37 +332,13 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int e = lane + 32 * i;
-                if (e < p.E && !((keep >> (e / p.group_size * per)) & 1u)) key[i] = kGone;
+                if (e < p.E && !((keep >> (fast_div(e, p.group_of) * per)) & 1u)) key[i] = kGone;
             }
             __syncwarp();
         }
-        // K rounds: the warp's largest key, the lowest expert that has it
-        uint32_t best = kGone;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = lane + 32 * i;
-            }
-        int mine = 0;
-        for (int k = 0; k < p.K; ++k) {
-            const uint32_t m = __reduce_max_sync(kAll, best);
-            const int e = (int)__reduce_min_sync(kAll, best == m ? (unsigned)at : 0x7fffffffu);
-            if (lane == k) mine = e;
-            if ((e & 31) == lane) {
-                best = kGone;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (lane + 32 * i == e) key[i] = kGone;
-                    if (key[i] > best) {
-                        best = key[i];
-                        at = lane + 32 * i;
-                    }
-                }
-            }
-            __syncwarp();
-        }
+        bool decided;
+        int mine = choose_packed<V, kPlain>(key, p.K, lane, sizeof(T) == 2 && !by_score, &decided);
+        if (!decided) mine = choose_whole(key, p.K, lane);
         // gates of the chosen experts, lane k for the k-th
         float xs = -INFINITY;
         if (lane < p.K) {
@@ -254,8 +370,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
 
 // ------------------------------------------------------------------------------ backward
 // kDense: softmax without renorm, every logit has a gradient. Otherwise only the K chosen
-// logits are read: the row is written as zeros and the K values over it.
-template <int V, typename T, bool kDense>
+// logits are read: the row is written as zeros and the K values over it. kFull: E = 32 V.
+template <int V, typename T, bool kDense, bool kFull>
 __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict__ logits,
                                                              const int32_t* __restrict__ topk,
                                                              const float* __restrict__ dgates,
@@ -283,21 +399,14 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict
         }
         float v;   // dL/dl of this lane's chosen expert
         if (kDense) {
-            float x[V], top = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int j = lane + 32 * i;
-                x[i] = j < p.E ? load_logit(row + j) : -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (!(x[i] <= FLT_MAX) || x[i] <= low) x[i] = -INFINITY;
-                top = fmaxf(top, x[i]);
-            }
+            float x[V], top, sum = 0.0f;
+            int masked = 0;   // reported by the forward
+            load_row<V, kFull>(row, p.E, lane, x, &top, &masked);
             top = warp_max(top);
+            if (top == -INFINITY) top = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                x[i] = x[i] == -INFINITY ? 0.0f : expf(x[i] - top);
+                x[i] = fast_exp(x[i] - top);
                 sum += x[i];
             }
             sum = warp_sum(sum);
@@ -308,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict
             const float c = -p.scale * dot * inv;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (lane + 32 * i < p.E) store_grad(out + lane + 32 * i, c * x[i]);
+                if (kFull || lane + 32 * i < p.E) store_grad(out + lane + 32 * i, c * x[i]);
         } else {
             float s, w = 0.0f, z = 0.0f;
             if (p.softmax) {
@@ -343,6 +452,7 @@ RouteParams params_of(const Dims& d, const bep_route_config& rc) {
     p.top_groups = rc.top_groups;
     p.group_top = rc.group_top;
     p.group_size = d.E / rc.groups;
+    p.group_of = make_fast_div((uint32_t)p.group_size);
     p.softmax = rc.score == BEP_SCORE_SOFTMAX;
     p.renorm = rc.renorm != 0;
     p.scale = rc.scale;
@@ -371,17 +481,18 @@ template <typename T>
 cudaError_t route_typed(const Dims& d, const Workspace& ws, const RouteParams& p, const T* logits,
                         const float* bias, int32_t* topk, float* gates, int32_t* load, int num_sms,
                         cudaStream_t st) {
-    // shared memory: the loads, and the keys of each warp where groups are cut
-    const size_t smem = ((size_t)d.E + (p.groups > 1 ? (size_t)kWarps * d.E : 0)) * 4;
+    // shared memory: the loads and the bias, and the keys of each warp where groups are cut
+    const size_t smem = (2 * (size_t)d.E + (p.groups > 1 ? (size_t)kWarps * d.E : 0)) * 4;
     return with_width(d.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
+        const auto kernel = (p.groups == 1 && d.E == 32 * V) ? route_kernel<V, T, true> : route_kernel<V, T, false>;
         if (smem > 48 * 1024) {
-            const cudaError_t err = cudaFuncSetAttribute(
-                route_kernel<V, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            const cudaError_t err =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (err != cudaSuccess) return err;
         }
-        route_kernel<V, T><<<grid_for(p.ntok, num_sms, 8), kThreads, smem, st>>>(
-            logits, bias, topk, gates, load, p, ws.status);
+        kernel<<<grid_for(p.ntok, num_sms, 8), kThreads, smem, st>>>(logits, bias, topk, gates, load, p,
+                                                                     ws.status);
         return cudaGetLastError();
     });
 }
@@ -392,13 +503,14 @@ cudaError_t route_bwd_typed(const Dims& d, const Workspace& ws, const RouteParam
                             int num_sms, cudaStream_t st) {
     const int grid = grid_for(p.ntok, num_sms, 8);
     if (!p.softmax || p.renorm) {
-        route_bwd_kernel<1, T, false>
+        route_bwd_kernel<1, T, false, false>
             <<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
         return cudaGetLastError();
     }
     return with_width(d.E, [&](auto v) {
-        route_bwd_kernel<decltype(v)::value, T, true>
-            <<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
+        constexpr int V = decltype(v)::value;
+        const auto kernel = d.E == 32 * V ? route_bwd_kernel<V, T, true, true> : route_bwd_kernel<V, T, true, false>;
+        kernel<<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
         return cudaGetLastError();
     });
 }
