@@ -98,7 +98,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return BEP_ERR_CUDA;
     if (bep::plan_setup(dev) != cudaSuccess || bep::gemm_setup(dev) != cudaSuccess ||
-        bep::mx_setup() != cudaSuccess)
+        bep::mx_setup(dev) != cudaSuccess)
         return BEP_ERR_CUDA;
 
     const size_t E = d.E, R = d.R, NC = d.NC, NROW = d.NROW, NP = d.E + d.R;
@@ -439,8 +439,9 @@ int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* 
     if (!aligned(cu_seqlens, 4) || !aligned(slot_expert, 4) || !aligned(codes, 16) ||
         !aligned(scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(y, 16))
         return BEP_ERR_ALIGN;
-    // work units (row tiles x 128-column output tiles) are counted in 32 bits
-    if ((int64_t)ctx->d.max_tiles * ((ctx->d.Hp + 127) / 128) >= ((int64_t)1 << 31)) return BEP_ERR_SIZE;
+    // work units (row tiles x 128-column output tiles) and scale blocks are counted in 32 bits
+    const int64_t mt = (ctx->d.Hp + 127) / 128, kb = (ctx->d.H + 127) / 128;
+    if (ctx->d.max_tiles * mt >= ((int64_t)1 << 31) || ctx->d.E * mt * kb >= ((int64_t)1 << 30)) return BEP_ERR_SIZE;
     return cuda_rc(bep::launch_grouped_gemm_mx(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales,
                                                w_codes, w_scales, y, ctx->num_sms, as_stream(stream)));
 }

@@ -99,10 +99,11 @@ cudaError_t launch_grouped_gemm_dw(const Dims& d, const Workspace& ws, const int
                                    const uint16_t* recv, const uint16_t* dy, float* g_home,
                                    float* red, int accumulate, int num_sms, cudaStream_t st);
 
-// cuTensorMapEncodeTiled of the driver (nullptr: not found) and the work list of 128-row tiles
-// in (rank, row) order, long and short segments merged (gemm.cu)
+// cuTensorMapEncodeTiled of the driver (nullptr: not found), and the work list of the 4-bit
+// product: tiles of at most kMxRows rows (gemm.cu)
+constexpr int kMxRows = 192;
 void* tensor_map_encoder();
-cudaError_t launch_gemm_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st);
+cudaError_t launch_mx_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st);
 // routing (route.cu)
 cudaError_t launch_route(const Dims& d, const Workspace& ws, const bep_route_config& rc,
                          const void* logits, int logits_type, const float* bias, int32_t* topk,
@@ -118,7 +119,7 @@ cudaError_t launch_swiglu_bwd(int64_t rows, int F, const uint16_t* da, const int
                               cudaStream_t st);
 // 4-bit experts (mx.cu)
 inline int mx_scale_pitch(int H) { return 16 * ((H + 511) / 512); }   // bytes of a row's scales
-cudaError_t mx_setup();
+cudaError_t mx_setup(int device);
 cudaError_t launch_mx_weight(const Dims& d, const uint16_t* w, uint8_t* codes, uint8_t* scales,
                              cudaStream_t st);
 cudaError_t launch_dispatch_mx(const Dims& d, const Workspace& ws, const uint16_t* x,

@@ -104,80 +104,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
-// ---- SM pairs (a cluster of two CTAs running one cta_group::2 MMA stream)
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_id() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_count() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-
-// Address of the same shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-
-// Arrive on the mbarrier at the same shared-memory offset in CTA `rank` of the cluster.
-__device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank))
-                 : "memory");
-}
-
-// TMA tile load into this CTA's shared memory whose completion is counted on an
-// mbarrier of either CTA of the pair (bar_cl: a shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cl, void* dst, int c0,
-                                                 int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cl), "r"(c0), "r"(c1)
-        : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait (as mbar_wait) for a barrier that the other CTA of the pair arrives on,
-// with cluster-scope acquire: what that CTA wrote before its release is visible after.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                                  int32_t* status) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > kTimeoutNs) {
-            *abort_flag = 1;
-            set_status(status, BEP_DERR_TIMEOUT);
-            return false;
-        }
-    }
-}
-
 // Zero the rows [tail, 16 * ceil(tail / 16)) of a stage's two 64-column A chunks and
 // two B chunks in this CTA's shared memory (whole 128-byte rows, so the swizzle does
 // not matter), then make the stores visible to the tensor core's async proxy. Warp-wide.
@@ -205,25 +131,6 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Arrive once on the mbarrier at this offset in both CTAs of the pair when every MMA
-// issued so far by this thread has completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
-// The same commit, arriving on CTA 0's barrier only (drain after an abort).
-__device__ __forceinline__ void mma_commit_pair_lead(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)1)
         : "memory");
 }
 
@@ -266,6 +173,7 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* s_warp, int* tot
 //   the order is plain (rank, row, m).
 // seg_mode == 3: as 0 with tiles of <= 256 rows (two m-tiles: the kFwd2 units), for the
 //   segments of kDualMinRows rows or more only; seg_mode == 4: as 0 for the other segments.
+// seg_mode == 5: as 0 with tiles of <= 192 rows (the 4-bit product's N tiles).
 // seg_mode == 1: one entry per non-empty segment, rows = its length (DW).
 // seg_mode == 2: as 1, plus an entry with rows = 0 for every expert whose home segment
 //   (rank e / (E/R), row e) is empty, so that an overwriting DW writes its zeros; a
@@ -283,7 +191,7 @@ __global__ void __launch_bounds__(1024) gemm_tiles_kernel(const int32_t* __restr
                                                           Workspace ws, int seg_mode) {
     const bool dw = seg_mode == 1 || seg_mode == 2;
     // FWD/DX: rows per tile (kFwd2: two m-tiles)
-    const int tile = seg_mode == 3 ? 2 * kBM : kBM;
+    const int tile = seg_mode == 3 ? 2 * kBM : seg_mode == 5 ? kMxRows : kBM;
     auto tile_of = [&](int) { return tile; };
     __shared__ int s_warp[33];
     const int n_items = d.R * d.NROW;
@@ -1357,8 +1265,8 @@ void* tensor_map_encoder() {
     return get_encoder() == cudaSuccess ? reinterpret_cast<void*>(g_encode) : nullptr;
 }
 
-cudaError_t launch_gemm_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st) {
-    gemm_tiles_kernel<<<1, 1024, 0, st>>>(cu, d, ws, 0);
+cudaError_t launch_mx_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st) {
+    gemm_tiles_kernel<<<1, 1024, 0, st>>>(cu, d, ws, 5);
     return cudaGetLastError();
 }
 

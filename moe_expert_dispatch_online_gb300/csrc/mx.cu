@@ -148,27 +148,42 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 }
 
 // ------------------------------------------------------------------------ product
-// The weights are the M operand (128 outputs n a tile) and the rows the N operand (16..128 of
-// one segment), so that a segment of a few rows costs a narrow MMA and not a 128-row one.
-//   warp 0  TMA: weight codes, weight scales and row codes of 256 reduction steps a stage
-//   warp 1  copies the stage's scales to TMEM and issues tcgen05.mma.kind::mxf4 (K = 64)
-//   warps 2, 3  put the rows' scales (any row offset, so no TMA) in tensor-core order
+// The weights are the M operand and the rows of one segment the N operand (32..192), so that a
+// segment of a few rows costs a narrow MMA and not a 128-row one. A cluster of two CTAs shares a
+// tile of 256 outputs x N rows (cta_group::2): CTA r holds outputs 128 r.. and half of the rows,
+// so that a stage brings 31 KB to each SM for what takes one CTA 43 KB: an SM takes in about 61
+// bytes a cycle from L2, and at 4 bits that, not the tensor core, bounds a tile (one CTA alone
+// with N <= 128: 4.97 ms for 524,288 rows by 7168 x 2048, 3.5 ms of it without any MMA).
+//   warp 0     TMA: codes of 128 outputs and of N/2 rows; 256 reduction steps a stage
+//   warp 1     (CTA 0) copies each stage's scales to both TMEMs, issues tcgen05.mma.kind::mxf4
+//   warps 2, 3 put all N rows' scales (any row offset, so no TMA) in tensor-core order, make them
+//              visible to the async proxy, and only then start the stage's TMA load of the weight
+//              scales: its bytes on CTA 0's barrier stand for both (a remote arrive per stage in
+//              their place, with its release at cluster scope, cost 1,000 cycles a stage)
 //   warps 4-7  epilogue: TMEM to bf16 y, while the next unit runs in the other accumulator
+//   barrier    owner   arrivals
+//   full[s]    CTA 0   CTA 0's producer (expect_tx) + both CTAs' TMA bytes
+//   empty[s]   both    the MMA thread's multicast commit
+//   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
+//   tempty[a]  CTA 0   the 4 epilogue warps of each CTA
 constexpr int kMxStages = 6;
-constexpr int kMxK = 256;                 // reduction elements a stage: 128 bytes of codes
-constexpr int kMxTile = 128 * 128;        // bytes: 128 rows x 128 bytes
-constexpr int kMxSf = 1024;               // bytes: scales of 128 rows x 8 blocks
-constexpr int kMxStageBytes = 2 * kMxTile + 2 * kMxSf;
+constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
+constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
+constexpr int kMxB = kMxRows / 2 * 128;        // bytes: half of the rows
+constexpr int kMxSfa = 1024;                   // bytes: 2 blocks of 512
+constexpr int kMxSfb = 2048;                   // bytes: (2 reduction blocks) x (rows 0..127, 128..255)
+constexpr int kMxStageBytes = kMxA + kMxB + kMxSfa + kMxSfb;
 constexpr int kMxTmemCols = 512;
-constexpr int kMxSfCols = 16;             // TMEM columns of one stage's scales (A 8, B 8)
-constexpr int kMxSfBase = 256;            // two accumulators of 128 columns lie before
+constexpr int kMxSfBase = 2 * kMxRows;         // two accumulators lie before
+constexpr int kMxSfCols = 24;                  // TMEM columns of a stage's scales: A 2 x 4, B 2 x 8
+constexpr int kMxSlots = (kMxTmemCols - kMxSfBase) / kMxSfCols;   // 5
+static_assert(kMxSlots >= 2 && kMxSlots <= kMxStages, "a slot is free once its stage is");
 
 struct MxParams {
     const MTile* tiles;
     const int32_t* ntiles;
     const int32_t* slot_expert;
     const uint8_t* row_scales;
-    const uint8_t* w_scales;
     uint16_t* y;
     int64_t nrows;
     int E, H, Hp, MT, KB, pitch;
@@ -176,35 +191,28 @@ struct MxParams {
 };
 
 struct MxUnit {
-    int row0, rows, expert, mt;
+    int row0, rows, expert, mp;
 };
 
 // The unit's tile and expert; expert < 0 for a slot whose expert is unknown (reported, skipped).
-__device__ __forceinline__ MxUnit mx_unit(const MxParams& p, int unit) {
-    const int t = unit / p.MT;
+__device__ __forceinline__ MxUnit mx_unit(const MxParams& p, int unit, int MP) {
+    const int t = unit / MP;
     const MTile tile = p.tiles[t];
     MxUnit u;
     u.row0 = tile.row0;
     u.rows = tile.rows;
-    u.mt = unit - t * p.MT;
+    u.mp = unit - t * MP;
     u.expert = tile.wsel >= 0 ? tile.wsel : p.slot_expert[-1 - tile.wsel];
     if (u.expert >= p.E) u.expert = -1;
     return u;
 }
 
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
-                                            int c0, int c1, int c2) {
+__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cl, void* dst, int c0,
+                                                 int c1, int c2) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-            "r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cl), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
 
@@ -213,17 +221,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
-// 32 rows x 16 bytes of scales to 4 TMEM columns, in each of the four 32-lane quarters.
+// In each CTA of the pair: 32 rows x 16 bytes of scales from its shared memory to 4 columns of
+// its TMEM, in each of the four 32-lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
                  : "memory");
 }
 
-// Instruction descriptor, kind::mxf4: e2m1 operands (1 at bits 7 and 10), N >> 3 at bit 17,
-// e8m0 scales (bit 23), M >> 7 at bit 27; the first of the K step's two scale bytes (0 or 2 of
-// the TMEM word's four) at bits 4 (B) and 29 (A).
+// Instruction descriptor, kind::mxf4, M = 256: e2m1 operands (1 at bits 7 and 10), N >> 3 at bit
+// 17, e8m0 scales (bit 23), M >> 7 at bit 27; the first of the K step's two scale bytes (0 or 2
+// of the TMEM word's four) at bits 4 (B) and 29 (A).
 __device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf) {
-    return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) |
+    return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (2u << 27) |
            (sf << 29);
 }
 
@@ -233,26 +242,28 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
             "r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ int round16(int v) { return (v + 15) & ~15; }
+// Rows of a unit's MMA: N in steps of 32, half of it in each CTA.
+__device__ __forceinline__ int mma_rows(int rows) { return (rows + 31) & ~31; }
 
 __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
-    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX16,
-    const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX64,
-    const __grid_constant__ CUtensorMap tmX128, const MxParams p) {
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
+    const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ CUtensorMap tmX32,
+    const __grid_constant__ CUtensorMap tmX64, const __grid_constant__ CUtensorMap tmX96,
+    const MxParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* smA = smem;
-    uint8_t* smB = smA + kMxStages * kMxTile;
-    uint8_t* smSA = smB + kMxStages * kMxTile;
-    uint8_t* smSB = smSA + kMxStages * kMxSf;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smSB + kMxStages * kMxSf);
+    uint8_t* smB = smA + kMxStages * kMxA;
+    uint8_t* smSA = smB + kMxStages * kMxB;
+    uint8_t* smSB = smSA + kMxStages * kMxSfa;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smSB + kMxStages * kMxSfb);
     uint64_t* empty = full + kMxStages;
     uint64_t* tfull = empty + kMxStages;
     uint64_t* tempty = tfull + 2;
@@ -260,63 +271,66 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     int32_t* status = p.status;
+    const uint32_t rank = cluster_rank();
+    const bool lead = rank == 0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMxStages; ++s) {
-            mbar_init(&full[s], 2);   // the TMA thread (with its bytes) and the scale warp
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], 4);
+            mbar_init(&tempty[a], 8);
         }
         mbar_init(drain, 1);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+        // one warp of each CTA performs the pair's allocation together (all of both TMEMs)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(s_tmem)),
                      "r"(kMxTmemCols)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before any remote arrive or multicast commit
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
 
-    const int total = *p.ntiles * p.MT;
+    const int MP = (p.MT + 1) / 2;             // pairs of 128-output tiles
+    const int total = *p.ntiles * MP;
     const int nst = (p.H + kMxK - 1) / kMxK;   // stages a unit
+    const int cl0 = (int)cluster_id(), ncl = (int)cluster_count();
     uint32_t pr_s = 0, pr_ph = 0, pr_armed = 0;
 
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
-            for (int unit = blockIdx.x; unit < total && live; unit += gridDim.x) {
-                const MxUnit u = mx_unit(p, unit);
+            for (int unit = cl0; unit < total && live; unit += ncl) {
+                const MxUnit u = mx_unit(p, unit, MP);
                 if (u.expert < 0) {
-                    set_status(status, BEP_DERR_BOUNDS);
+                    if (lead) set_status(status, BEP_DERR_BOUNDS);
                     continue;
                 }
-                const CUtensorMap* tmX = u.rows <= 16   ? &tmX16
-                                         : u.rows <= 32 ? &tmX32
-                                         : u.rows <= 64 ? &tmX64
-                                                        : &tmX128;
-                const int box = u.rows <= 16 ? 16 : u.rows <= 32 ? 32 : u.rows <= 64 ? 64 : 128;
-                const uint8_t* sf = p.w_scales + ((int64_t)u.expert * p.MT + u.mt) * p.KB * 512;
+                const int half = mma_rows(u.rows) / 2;
+                const CUtensorMap* tmX = half <= 16 ? &tmX16 : half <= 32 ? &tmX32 : half <= 64 ? &tmX64 : &tmX96;
+                const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 96;
+                const int mt = 2 * u.mp + (int)rank;   // past H' for the last odd tile: zeros
                 for (int k = 0; k < nst; ++k) {
                     if (!mbar_wait(&empty[pr_s], pr_ph ^ 1u, s_abort, status)) {
                         live = false;
                         break;
                     }
-                    const uint32_t sf_bytes = 2 * k + 1 < p.KB ? 1024 : 512;
-                    mbar_arrive_expect_tx(&full[pr_s], kMxTile + box * 128 + sf_bytes);
+                    if (lead) mbar_arrive_expect_tx(&full[pr_s], 2 * (kMxA + kMxSfa + box * 128));
                     ++pr_armed;
-                    tma_load_3d(&tmW, &full[pr_s], smA + pr_s * kMxTile, k * 128, u.mt * 128, u.expert);
-                    tma_load_2d(tmX, &full[pr_s], smB + pr_s * kMxTile, k * 128, u.row0);
-                    bulk_load(smSA + pr_s * kMxSf, sf + (int64_t)k * 1024, sf_bytes, &full[pr_s]);
+                    const uint32_t bar = cluster_addr(&full[pr_s], 0);
+                    tma_load_3d_pair(&tmW, bar, smA + pr_s * kMxA, k * 128, mt * 128, u.expert);
+                    tma_load_2d_pair(tmX, bar, smB + pr_s * kMxB, k * 128, u.row0 + (int)rank * half);
                     if (++pr_s == kMxStages) {
                         pr_s = 0;
                         pr_ph ^= 1u;
@@ -325,75 +339,96 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lead) {
+            // the whole warp runs the loops, so that descriptors stay in uniform registers
             const uint64_t da = sdesc_sw128(smem_u32(smA), 16, 1024), db = sdesc_sw128(smem_u32(smB), 16, 1024);
             const uint64_t dsa = sdesc_scales(smem_u32(smSA)), dsb = sdesc_scales(smem_u32(smSB));
-            uint32_t s = 0, ph = 0;
+            uint32_t s = 0, ph = 0;                    // ring stage
+            uint32_t slot = 0;                         // TMEM scale columns
+            uint32_t old = 0, old_ph = 0, done = 0;    // the stage that used the slot before
             int it = 0;
             bool live = true;
-            for (int unit = blockIdx.x; unit < total && live; unit += gridDim.x) {
-                const MxUnit u = mx_unit(p, unit);
+            for (int unit = cl0; unit < total && live; unit += ncl) {
+                const MxUnit u = mx_unit(p, unit, MP);
                 if (u.expert < 0) continue;
-                const int N = round16(u.rows);
+                const int N = mma_rows(u.rows);
                 const int acc = it & 1;
-                if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)))
+                    break;
                 ++it;
-                const uint32_t dt = tmem_base + acc * 128;
+                const uint32_t dt = tmem_base + acc * kMxRows;
                 const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
                 for (int k = 0; k < nst; ++k) {
-                    if (!mbar_wait(&full[s], ph, s_abort, status)) {
+                    // a slot's scales are overwritten once the MMAs that read them have completed
+                    if (done >= (uint32_t)kMxSlots) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(&empty[old], old_ph, s_abort, status))) {
+                            live = false;
+                            break;
+                        }
+                        if (++old == kMxStages) {
+                            old = 0;
+                            old_ph ^= 1u;
+                        }
+                    } else {
+                        ++done;
+                    }
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, s_abort, status))) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
-                    // descriptors count 16-byte units: a tile is 1024 of them, a K step 2, a scale block 32
-                    const uint64_t a = da + s * (kMxTile / 16), b = db + s * (kMxTile / 16);
-                    const uint64_t sa = dsa + s * (kMxSf / 16), sb = dsb + s * (kMxSf / 16);
-                    // the scales' TMEM columns belong to the ring stage: they are overwritten only
-                    // after the stage's last use has been committed
-                    const uint32_t ta = tmem_base + kMxSfBase + s * kMxSfCols, tb = ta + 8;
+                    // descriptors count 16-byte units: a K step is 2 of them, a scale block 32
+                    const uint64_t a = da + s * (kMxA / 16), b = db + s * (kMxB / 16);
+                    const uint64_t sa = dsa + s * (kMxSfa / 16), sb = dsb + s * (kMxSfb / 16);
+                    const uint32_t ta = tmem_base + kMxSfBase + slot * kMxSfCols, tb = ta + 8;
                     const int steps = min(4, (p.H - k * kMxK) / 64);
-                    copy_scales(ta, sa);
-                    copy_scales(tb, sb);
-                    mma_mxf4(dt, a, b, id0, ta, tb, k != 0);
-                    if (steps > 1) mma_mxf4(dt, a + 2, b + 2, id2, ta, tb, 1);
-                    if (steps > 2) {
-                        copy_scales(ta + 4, sa + 32);
-                        copy_scales(tb + 4, sb + 32);
-                        mma_mxf4(dt, a + 4, b + 4, id0, ta + 4, tb + 4, 1);
-                        if (steps > 3) mma_mxf4(dt, a + 6, b + 6, id2, ta + 4, tb + 4, 1);
+                    if (elect_one()) {
+                        copy_scales(ta, sa);
+                        copy_scales(tb, sb);
+                        if (N > 128) copy_scales(tb + 4, sb + 32);
+                        mma_mxf4(dt, a, b, id0, ta, tb, k != 0);
+                        if (steps > 1) mma_mxf4(dt, a + 2, b + 2, id2, ta, tb, 1);
+                        if (steps > 2) {
+                            copy_scales(ta + 4, sa + 32);
+                            copy_scales(tb + 8, sb + 64);
+                            if (N > 128) copy_scales(tb + 12, sb + 96);
+                            mma_mxf4(dt, a + 4, b + 4, id0, ta + 4, tb + 8, 1);
+                            if (steps > 3) mma_mxf4(dt, a + 6, b + 6, id2, ta + 4, tb + 8, 1);
+                        }
+                        mma_commit_pair(&empty[s]);
+                        if (k == nst - 1) mma_commit_pair(&tfull[acc]);
                     }
-                    mma_commit(&empty[s]);
+                    __syncwarp();
                     if (++s == kMxStages) {
                         s = 0;
                         ph ^= 1u;
                     }
+                    if (++slot == kMxSlots) slot = 0;
                 }
-                if (live) mma_commit(&tfull[acc]);
             }
         }
     } else if (warp < 4) {
         // A 16-byte piece of a row's scales serves two stages; the two warps take the pieces in
-        // turn and hold two of their own in flight, so a load has four pieces (eight stages) to
-        // arrive: with one warp one piece ahead these loads, not the operands', set the pace
-        // (decode of 64 rows by 384 experts' 7168 x 2048: 120 us instead of 95).
+        // turn and hold two of their own in flight, so a load has four pieces to arrive.
+        constexpr int kC = kMxRows / 32;
         const int mine = warp - 2;
         uint32_t s = 0, ph = 0;
         bool live = true;
         const int pieces = (nst + 1) / 2;
-        for (int unit = blockIdx.x; unit < total && live; unit += gridDim.x) {
-            const MxUnit u = mx_unit(p, unit);
+        for (int unit = cl0; unit < total && live; unit += ncl) {
+            const MxUnit u = mx_unit(p, unit, MP);
             if (u.expert < 0) continue;
-            const int N = round16(u.rows);
-            const uint4* src[4];
+            const int N = mma_rows(u.rows);
+            const int srow = (u.expert * p.MT + 2 * u.mp + (int)rank) * p.KB;
+            const uint4* src[kC];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < kC; ++c) {
                 const int64_t row = min((int64_t)u.row0 + 32 * c + lane, p.nrows - 1);
                 src[c] = reinterpret_cast<const uint4*>(p.row_scales + row * p.pitch);
             }
-            uint4 v0[4] = {}, v1[4] = {};
+            uint4 v0[kC] = {}, v1[kC] = {};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < kC; ++c)
                 if (32 * c < N) {
                     if (mine < pieces) v0[c] = __ldg(src[c] + mine);
                     if (mine + 2 < pieces) v1[c] = __ldg(src[c] + mine + 2);
@@ -408,9 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                     }
                     continue;
                 }
-                uint4 v[4];
+                uint4 v[kC];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < kC; ++c) {
                     v[c] = v0[c];
                     v0[c] = v1[c];
                     if (32 * c < N && g + 4 < pieces) v1[c] = __ldg(src[c] + g + 4);
@@ -420,16 +455,17 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                         live = false;
                         break;
                     }
-                    uint32_t* d = reinterpret_cast<uint32_t*>(smSB + s * kMxSf) + lane * 4;
+                    uint32_t* d = reinterpret_cast<uint32_t*>(smSB + s * kMxSfb) + lane * 4;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < kC; ++c)
                         if (32 * c < N) {
-                            d[c] = half ? v[c].z : v[c].x;
-                            d[128 + c] = half ? v[c].w : v[c].y;
+                            d[(c >> 2) * 128 + (c & 3)] = half ? v[c].z : v[c].x;
+                            d[256 + (c >> 2) * 128 + (c & 3)] = half ? v[c].w : v[c].y;
                         }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[s]);
+                    if (lane == 0)
+                        tma_load_2d_pair(&tmS, cluster_addr(&full[s], 0), smSA + s * kMxSfa, 0, srow + 2 * (2 * g + half));
                     if (++s == kMxStages) {
                         s = 0;
                         ph ^= 1u;
@@ -437,22 +473,22 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else {
         const int quarter = warp - 4;
         int it = 0;
-        for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
-            const MxUnit u = mx_unit(p, unit);
+        for (int unit = cl0; unit < total; unit += ncl) {
+            const MxUnit u = mx_unit(p, unit, MP);
             if (u.expert < 0) continue;
             const int acc = it & 1;
             if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, status))) break;
             ++it;
             tc_fence_after();
             // lane l of quarter q holds output n = 128 mt + 32 q + l, its columns the rows
-            const int n0 = u.mt * 128 + quarter * 32;
+            const int n0 = (2 * u.mp + (int)rank) * 128 + quarter * 32;
             const bool odd = lane & 1;
             for (int c0 = 0; c0 < u.rows; c0 += 32) {
                 uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 128 + c0, r);
+                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * kMxRows + c0, r);
                 // lanes 2i and 2i + 1 trade a row each, so that a lane stores two outputs of one row
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -467,14 +503,19 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[acc]);
+            if (lane == 0) {
+                if (lead) mbar_arrive(&tempty[acc]);
+                else mbar_arrive_rank(&tempty[acc], 0);
+            }
         }
     }
 
     __syncthreads();
     if (*s_abort) {
-        // A wait gave up: what was started lands before shared memory and TMEM are released.
-        if (warp == 0 && lane == 0) {
+        // A wait gave up: what was started lands before shared memory and TMEM are released, each
+        // wait bounded. CTA 0's full phases count CTA 1's bytes too; CTA 1's loads of a stage that
+        // CTA 0 never armed cannot be observed, and the short sleep bounds those.
+        if (warp == 0 && lane == 0 && lead) {
             for (uint32_t i = 0; i < pr_armed && i < (uint32_t)kMxStages; ++i) {
                 if (pr_s == 0) {
                     pr_s = kMxStages;
@@ -483,15 +524,18 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                 --pr_s;
                 mbar_drain(&full[pr_s], pr_ph);
             }
-        } else if (warp == 1 && lane == 0) {
-            mma_commit(drain);
+        } else if (warp == 1 && lane == 0 && lead) {
+            mma_commit_pair_lead(drain);
             mbar_drain(drain, 0);
         }
+        if (threadIdx.x == 0)
+            for (int i = 0; i < 20; ++i) __nanosleep(10000);
         __syncthreads();
     }
+    cluster_sync();   // neither CTA leaves while the other may still signal it or read its tiles
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(kMxTmemCols)
                      : "memory");
     }
@@ -499,7 +543,19 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
 
 constexpr size_t kMxSmem = 1024 + (size_t)kMxStages * kMxStageBytes + (2 * kMxStages + 5) * 8 + 16;
 
-// u8 tensor of `dims` (innermost first, dense but for `pitch` bytes a row), 128-byte boxes of
+// Scale blocks as rows of 128 words, 2 rows a box.
+bool encode_scales(CUtensorMap* m, const void* base, uint64_t blocks) {
+    void* fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t d[2] = {128, blocks}, strides[1] = {512};
+    const cuuint32_t box[2] = {128, 2}, estr[2] = {1, 1};
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+               m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), d, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// u8 tensor of `dims` (innermost first, dense), 128-byte boxes of
 // `box_rows` rows, 128-byte swizzle.
 bool encode_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, uint32_t box_rows) {
     void* fn = tensor_map_encoder();
@@ -515,6 +571,26 @@ bool encode_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of two that can be resident at once, per device: the grid, so that the units are
+// spread evenly over CTAs that run from the start.
+constexpr int kMaxDevices = 64;
+int g_mx_clusters[kMaxDevices] = {};
+
+cudaLaunchConfig_t mx_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kMxSmem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 int grid_for(int64_t warps, int num_sms) {
     const int64_t g = (warps + kThreads / 32 - 1) / (kThreads / 32), cap = (int64_t)num_sms * 8;
     return (int)(g < cap ? (g > 0 ? g : 1) : cap);
@@ -522,9 +598,17 @@ int grid_for(int64_t warps, int num_sms) {
 
 }  // namespace
 
-cudaError_t mx_setup() {
-    return cudaFuncSetAttribute(grouped_gemm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)kMxSmem);
+cudaError_t mx_setup(int device) {
+    cudaError_t err = cudaFuncSetAttribute(grouped_gemm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)kMxSmem);
+    if (err != cudaSuccess) return err;
+    if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
+    int nsm = 0;
+    err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, device);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = mx_config(nsm / 2, nullptr, attr);
+    return cudaOccupancyMaxActiveClusters(&g_mx_clusters[device], grouped_gemm_mx_kernel, &cfg);
 }
 
 cudaError_t launch_mx_weight(const Dims& d, const uint16_t* w, uint8_t* codes, uint8_t* scales,
@@ -562,16 +646,12 @@ cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int
                                    cudaStream_t st) {
     const uint64_t wd[3] = {(uint64_t)d.H / 2, (uint64_t)d.Hp, (uint64_t)d.E};
     const uint64_t xd[2] = {(uint64_t)d.H / 2, (uint64_t)d.R * d.C};
-    CUtensorMap tmW, tmX[4];
-    if (!encode_u8(&tmW, w_codes, 3, wd, 128)) return cudaErrorInvalidValue;
-    for (int i = 0; i < 4; ++i)
-        if (!encode_u8(&tmX[i], codes, 2, xd, 16u << i)) return cudaErrorInvalidValue;
+    const uint32_t boxes[4] = {16, 32, 64, kMxRows / 2};
     MxParams p;
     p.tiles = ws.tiles;
     p.ntiles = ws.ntiles;
     p.slot_expert = slot_expert;
     p.row_scales = scales;
-    p.w_scales = w_scales;
     p.y = y;
     p.nrows = (int64_t)d.R * d.C;
     p.E = d.E;
@@ -581,10 +661,20 @@ cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int
     p.KB = (d.H + 127) / 128;
     p.pitch = mx_scale_pitch(d.H);
     p.status = ws.status;
-    const cudaError_t err = launch_gemm_tiles(d, ws, cu, st);
+    CUtensorMap tmW, tmS, tmX[4];
+    if (!encode_u8(&tmW, w_codes, 3, wd, 128)) return cudaErrorInvalidValue;
+    if (!encode_scales(&tmS, w_scales, (uint64_t)d.E * p.MT * p.KB)) return cudaErrorInvalidValue;
+    for (int i = 0; i < 4; ++i)
+        if (!encode_u8(&tmX[i], codes, 2, xd, boxes[i])) return cudaErrorInvalidValue;
+    const cudaError_t err = launch_mx_tiles(d, ws, cu, st);
     if (err != cudaSuccess) return err;
-    grouped_gemm_mx_kernel<<<num_sms, kThreads, kMxSmem, st>>>(tmW, tmX[0], tmX[1], tmX[2], tmX[3], p);
-    return cudaGetLastError();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || g_mx_clusters[dev] < 1)
+        return cudaErrorInvalidDevice;
+    cudaLaunchAttribute attr[1];
+    const int pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+    cudaLaunchConfig_t cfg = mx_config(g_mx_clusters[dev] < pairs ? g_mx_clusters[dev] : pairs, st, attr);
+    return cudaLaunchKernelEx(&cfg, grouped_gemm_mx_kernel, tmW, tmS, tmX[0], tmX[1], tmX[2], tmX[3], p);
 }
 
 }  // namespace bep

@@ -23,8 +23,9 @@
 namespace bep {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: large CTAs, since each adds its loads to memory once; half as many where a
+// lane's experts need more than 128 registers.
+constexpr int threads_for(int V) { return V > 16 ? 256 : 512; }
 constexpr unsigned kAll = 0xffffffffu;
 
 // Ranks below every key of an expert that can be chosen.
@@ -60,7 +61,7 @@ __device__ __forceinline__ void store_grad<uint16_t>(uint16_t* p, float v) {
 // Unsigned order of the result = order of the floats; -0 counts as +0. Results are >= 0x7fffff.
 __device__ __forceinline__ uint32_t ordered(float f) {
     const uint32_t b = __float_as_uint(f + 0.0f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
@@ -82,14 +83,15 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 // The scores of all E experts (keys, and the softmax's sum) use the hardware's 2^x and
 // reciprocal, 2 units in the last place of fp32 or fewer, in 2 and 4 instructions; the K gates
 // themselves use expf and a rounded division. 0 for an argument below about -87.
-__device__ __forceinline__ float fast_exp(float x) {
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float fast_exp2(float x) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float fast_sigmoid(float x) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fast_exp(-x)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fast_exp2(x * -kLog2e)));
     return r;
 }
 // Maximum that keeps a NaN.
@@ -105,11 +107,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // The result: whether the row is ordinary; otherwise its masked logits are -inf, and *bad is set
 // for a NaN or +inf among them. Past E: -inf in either case.
 template <int V, bool kFull, typename T>
-__device__ __forceinline__ bool load_row(const T* __restrict__ row, int E, int lane, float (&x)[V],
-                                         float* top, int* bad) {
-    float hi = -INFINITY, lo = INFINITY;
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, float (&x)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = load_logit(row + (kFull ? lane + 32 * i : min(lane + 32 * i, E - 1)));
+}
+template <int V, bool kFull, typename T>
+__device__ __forceinline__ bool look_over(int E, int lane, float (&x)[V], float* top, int* bad) {
+    float hi = -INFINITY, lo = INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         hi = max_nan(hi, x[i]);
@@ -141,7 +145,6 @@ struct RouteParams {
     int64_t ntok;
     int E, K;
     int groups, top_groups, group_top, group_size;
-    FastDiv group_of;   // expert -> its group
     int softmax, renorm;
     float scale;
 };
@@ -160,7 +163,8 @@ __device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, 
 // tokens in 100 at 8 of 384), or two of the K + 1 leading words agree in all their key bits (as
 // many) -- the choice is made again on whole keys, with a second reduction for the index.
 // 65,536 tokens, 8 of 384 by softmax and bias: 130 us with whole keys in every round and
-// element-by-element checks, 86 us with two words a lane, rescanned when both have won.
+// element-by-element checks, 86 us with two words a lane, rescanned when both have won, 43 us
+// now; bound by the integer pipe (about 480 instructions a token, two thirds of them there).
 template <int V>
 struct Packed {
     static constexpr int kBits = V <= 1 ? 6 : V <= 2 ? 7 : V <= 4 ? 8 : V <= 12 ? 9 : V <= 16 ? 10 : V <= 32 ? 11 : 12;
@@ -183,22 +187,23 @@ __device__ __forceinline__ int choose_packed(const uint32_t (&key)[V], int K, in
         t2 = max(t2, min(t1, w));
         t1 = max(t1, w);
     }
-    uint32_t mine = 0, before = ~0u, near = ~0u;
-    bool spent = false;
+    const bool any = t1 != 0;
+    uint32_t mine = 0;
     for (int k = 0; k < K; ++k) {
         const uint32_t m = __reduce_max_sync(kAll, t1);
-        near = min(near, m ^ before);
-        before = m;
         if (lane == k) mine = m;
         if (t1 == m) {
             t1 = t2;
             t2 = t3;
             t3 = 0;
-            spent = t1 == 0;
         }
     }
-    near = min(near, __reduce_max_sync(kAll, t1) ^ before);   // the first that is not chosen
-    *decided = (exact || near > kIndex) && !(V > 3 && __any_sync(kAll, spent));
+    const bool spent = V > 3 && any && t1 == 0;   // this lane may have had a fourth
+    const uint32_t next = __reduce_max_sync(kAll, t1);   // the first that is not chosen
+    uint32_t after = __shfl_down_sync(kAll, mine, 1);   // every lane takes part
+    if (lane == K - 1) after = next;
+    const bool near = !exact && lane < K && (mine ^ after) <= kIndex;
+    *decided = !__any_sync(kAll, spent || near);
     return (int)(kIndex - (mine & kIndex));
 }
 
@@ -228,14 +233,15 @@ __device__ __forceinline__ int choose_whole(uint32_t (&key)[V], int K, int lane)
 // V: experts a lane holds (E <= 32 V). Scores of all E experts are needed only where keys
 // are more than the logits' order (a bias, sums of two keys) or where the softmax is not
 // renormalised over the chosen ones.
-// kPlain: E = 32 V and no groups.
-template <int V, typename T, bool kPlain>
-__global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ logits,
+// kFull: E = 32 V. kGroups: some groups are cut.
+template <int V, typename T, bool kFull, bool kGroups>
+__global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restrict__ logits,
                                                          const float* __restrict__ bias,
                                                          int32_t* __restrict__ topk,
                                                          float* __restrict__ gates,
                                                          int32_t* __restrict__ load,
                                                          const RouteParams p, int32_t* status) {
+    constexpr int kThreads = threads_for(V), kWarps = kThreads / 32;
     extern __shared__ uint32_t smem[];   // loads [E], the bias [E], then each warp's keys [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* s_load = reinterpret_cast<int*>(smem);
@@ -250,14 +256,20 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
     }
     bias_nan = __syncthreads_or(bias_nan);
     const float low = lowest<T>();
-    const bool by_score = bias != nullptr || (p.groups > 1 && p.group_top > 1);
+    const bool by_score = bias != nullptr || (kGroups && p.group_top > 1);
     const bool row_sum = p.softmax && (by_score || !p.renorm);
+    int per = 32;   // lanes that scan a group
+    while (kGroups && per * p.groups > 32) per >>= 1;
+    const int g = lane / per, part = lane & (per - 1);
     int bad = 0;
-    for (int64_t tok = (int64_t)blockIdx.x * kWarps + warp; tok < p.ntok;
-         tok += (int64_t)gridDim.x * kWarps) {
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    float x[V];
+    int64_t tok = (int64_t)blockIdx.x * kWarps + warp;
+    if (tok < p.ntok) load_row<V, kFull>(logits + tok * p.E, p.E, lane, x);
+    for (; tok < p.ntok; tok += step) {
         const T* row = logits + tok * p.E;
-        float x[V], top;
-        const bool ordinary = load_row<V, kPlain>(row, p.E, lane, x, &top, &bad) && !bias_nan;
+        float top;
+        const bool ordinary = look_over<V, kFull, T>(p.E, lane, x, &top, &bad) && !bias_nan;
         float inv = 0.0f;   // 1 / sum of exp(l - top)
         uint32_t key[V];
         if (row_sum) {
@@ -266,19 +278,19 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
             float ex[V], sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                ex[i] = fast_exp(x[i] - top);
+                ex[i] = fast_exp2((x[i] - top) * kLog2e);
                 sum += ex[i];
             }
             sum = warp_sum(sum);
             inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = ordered(by_score ? __fadd_rn(__fmul_rn(ex[i], inv), s_bias[kPlain ? lane + 32 * i : min(lane + 32 * i, p.E - 1)])
+                key[i] = ordered(by_score ? fmaf(ex[i], inv, s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)])
                                           : x[i]);
         } else if (by_score) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = ordered(__fadd_rn(fast_sigmoid(x[i]), s_bias[kPlain ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
+                key[i] = ordered(__fadd_rn(fast_sigmoid(x[i]), s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) key[i] = ordered(x[i]);
@@ -294,24 +306,26 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
                 if (x[i] == -INFINITY) key[i] = kMasked;
             }
         }
-        if (!kPlain) {
+        if (!kFull) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (lane + 32 * i >= p.E) key[i] = kGone;
         }
-        if (!kPlain && p.groups > 1) {
+        // the keys hold all the choice needs: the next token's logits arrive while it is made
+        if (tok + step < p.ntok) load_row<V, kFull>(row + step * p.E, p.E, lane, x);
+        if (kGroups) {
             // `per` lanes (a power of two) scan each group's keys for its two largest
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (lane + 32 * i < p.E) s_key[lane + 32 * i] = key[i];
+                if (kFull || lane + 32 * i < p.E) s_key[lane + 32 * i] = key[i];
             __syncwarp();
-            int per = 32;
-            while (per * p.groups > 32) per >>= 1;
-            const int g = lane / per, part = lane & (per - 1);
             uint32_t k1 = kGone, k2 = kGone;
             if (g < p.groups)
-                for (int j = part; j < p.group_size; j += per)
-                    merge2(k1, k2, s_key[g * p.group_size + j], kGone);
+                for (int j = part; j < p.group_size; j += per) {
+                    const uint32_t k = s_key[g * p.group_size + j];
+                    k2 = max(k2, min(k1, k));
+                    k1 = max(k1, k);
+                }
             for (int o = 1; o < per; o <<= 1) {
                 const uint32_t b1 = __shfl_xor_sync(kAll, k1, o), b2 = __shfl_xor_sync(kAll, k2, o);
                 merge2(k1, k2, b1, b2);
@@ -326,18 +340,17 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
             int rank = 0;
             for (int o = 0; o < p.groups; ++o) {
                 const uint32_t other = __shfl_sync(kAll, score, o * per);
-                if (other > score || (other == score && o < g)) ++rank;
+                rank += other > score || (other == score && o < g);
             }
-            const unsigned keep = __ballot_sync(kAll, g < p.groups && rank < p.top_groups);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                if (e < p.E && !((keep >> (fast_div(e, p.group_of) * per)) & 1u)) key[i] = kGone;
-            }
+            if (g < p.groups && rank >= p.top_groups)
+                for (int j = part; j < p.group_size; j += per) s_key[g * p.group_size + j] = kGone;
             __syncwarp();
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (kFull || lane + 32 * i < p.E) key[i] = s_key[lane + 32 * i];
         }
         bool decided;
-        int mine = choose_packed<V, kPlain>(key, p.K, lane, sizeof(T) == 2 && !by_score, &decided);
+        int mine = choose_packed<V, kFull && !kGroups>(key, p.K, lane, sizeof(T) == 2 && !by_score, &decided);
         if (!decided) mine = choose_whole(key, p.K, lane);
         // gates of the chosen experts, lane k for the k-th
         float xs = -INFINITY;
@@ -372,45 +385,59 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const T* __restrict__ l
 // kDense: softmax without renorm, every logit has a gradient. Otherwise only the K chosen
 // logits are read: the row is written as zeros and the K values over it. kFull: E = 32 V.
 template <int V, typename T, bool kDense, bool kFull>
-__global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict__ logits,
+__global__ void __launch_bounds__(threads_for(V)) route_bwd_kernel(const T* __restrict__ logits,
                                                              const int32_t* __restrict__ topk,
                                                              const float* __restrict__ dgates,
                                                              T* __restrict__ dlogits,
                                                              const RouteParams p, int32_t* status) {
+    constexpr int kWarps = threads_for(V) / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float low = lowest<T>();
     int bad = 0;
-    for (int64_t tok = (int64_t)blockIdx.x * kWarps + warp; tok < p.ntok;
-         tok += (int64_t)gridDim.x * kWarps) {
+    const int64_t step = (int64_t)gridDim.x * kWarps;
+    float next[V];
+    int64_t tok = (int64_t)blockIdx.x * kWarps + warp;
+    if (kDense && tok < p.ntok) load_row<V, kFull>(logits + tok * p.E, p.E, lane, next);
+    for (; tok < p.ntok; tok += step) {
         const T* row = logits + tok * p.E;
         T* out = dlogits + tok * p.E;
+        float x[V];
+        if (kDense) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = next[i];
+            if (tok + step < p.ntok) load_row<V, kFull>(row + step * p.E, p.E, lane, next);
+        }
         int e = -1;
         float dg = 0.0f, xs = -INFINITY;
         if (lane < p.K) {
             e = topk[tok * p.K + lane];
+            dg = dgates[tok * p.K + lane];
             if (e < 0 || e >= p.E) {
                 bad |= BEP_DERR_EXPERT_ID;
                 e = -1;
-            } else {
-                dg = dgates[tok * p.K + lane];
-                xs = load_logit(row + e);
-                if (!(xs <= FLT_MAX) || xs <= low) xs = -INFINITY;
+                dg = 0.0f;
             }
         }
+        auto chosen_logit = [&]() {
+            if (e < 0) return -INFINITY;
+            const float v = load_logit(row + e);
+            return !(v <= FLT_MAX) || v <= low ? -INFINITY : v;
+        };
         float v;   // dL/dl of this lane's chosen expert
         if (kDense) {
-            float x[V], top, sum = 0.0f;
+            float top, sum = 0.0f;
             int masked = 0;   // reported by the forward
-            load_row<V, kFull>(row, p.E, lane, x, &top, &masked);
+            look_over<V, kFull, T>(p.E, lane, x, &top, &masked);
             top = warp_max(top);
             if (top == -INFINITY) top = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                x[i] = fast_exp(x[i] - top);
+                x[i] = fast_exp2((x[i] - top) * kLog2e);
                 sum += x[i];
             }
             sum = warp_sum(sum);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            xs = chosen_logit();
             const float s = xs == -INFINITY ? 0.0f : expf(xs - top) * inv;
             const float dot = warp_sum(s * dg);
             v = p.scale * s * (dg - dot);
@@ -420,6 +447,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict
                 if (kFull || lane + 32 * i < p.E) store_grad(out + lane + 32 * i, c * x[i]);
         } else {
             float s, w = 0.0f, z = 0.0f;
+            xs = chosen_logit();
             if (p.softmax) {
                 const float top = warp_max(xs);
                 s = xs == -INFINITY ? 0.0f : expf(xs - top);
@@ -434,7 +462,13 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const T* __restrict
             }
             if (p.softmax) v = p.scale * w * d;                                       // renorm
             else v = p.scale * (p.renorm ? w : s) * d * (xs == -INFINITY ? 0.0f : sigmoid(-xs));
-            for (int j = lane; j < p.E; j += 32) store_grad(out + j, 0.0f);
+            const uint32_t bytes = (uint32_t)p.E * sizeof(T);
+            if (((reinterpret_cast<uintptr_t>(out) | bytes) & 15) == 0) {
+                for (uint32_t j = lane; j < bytes / 16; j += 32)
+                    reinterpret_cast<uint4*>(out)[j] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int j = lane; j < p.E; j += 32) store_grad(out + j, 0.0f);
+            }
         }
         __syncwarp();   // the row's fill is ordered before the chosen experts' values
         if (e >= 0) store_grad(out + e, v);
@@ -452,15 +486,16 @@ RouteParams params_of(const Dims& d, const bep_route_config& rc) {
     p.top_groups = rc.top_groups;
     p.group_top = rc.group_top;
     p.group_size = d.E / rc.groups;
-    p.group_of = make_fast_div((uint32_t)p.group_size);
     p.softmax = rc.score == BEP_SCORE_SOFTMAX;
     p.renorm = rc.renorm != 0;
     p.scale = rc.scale;
     return p;
 }
 
-int grid_for(int64_t ntok, int num_sms, int per_sm) {
-    const int64_t g = (ntok + kWarps - 1) / kWarps, cap = (int64_t)num_sms * per_sm;
+// Two CTAs an SM at most: what the registers let in.
+int grid_for(int64_t ntok, int num_sms, int threads) {
+    const int warps = threads / 32;
+    const int64_t g = (ntok + warps - 1) / warps, cap = (int64_t)num_sms * 2;
     return (int)(g < cap ? g : cap);
 }
 
@@ -481,17 +516,20 @@ template <typename T>
 cudaError_t route_typed(const Dims& d, const Workspace& ws, const RouteParams& p, const T* logits,
                         const float* bias, int32_t* topk, float* gates, int32_t* load, int num_sms,
                         cudaStream_t st) {
-    // shared memory: the loads and the bias, and the keys of each warp where groups are cut
-    const size_t smem = (2 * (size_t)d.E + (p.groups > 1 ? (size_t)kWarps * d.E : 0)) * 4;
+    const bool cut = p.top_groups < p.groups;
     return with_width(d.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        const auto kernel = (p.groups == 1 && d.E == 32 * V) ? route_kernel<V, T, true> : route_kernel<V, T, false>;
+        // shared memory: the loads and the bias, and the keys of each warp where groups are cut
+        const size_t smem = (2 * (size_t)d.E + (cut ? (size_t)(threads_for(V) / 32) * d.E : 0)) * 4;
+        const bool all = d.E == 32 * V;
+        const auto kernel = all ? (cut ? route_kernel<V, T, true, true> : route_kernel<V, T, true, false>)
+                                : (cut ? route_kernel<V, T, false, true> : route_kernel<V, T, false, false>);
         if (smem > 48 * 1024) {
             const cudaError_t err =
                 cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (err != cudaSuccess) return err;
         }
-        kernel<<<grid_for(p.ntok, num_sms, 8), kThreads, smem, st>>>(logits, bias, topk, gates, load, p,
+        kernel<<<grid_for(p.ntok, num_sms, threads_for(V)), threads_for(V), smem, st>>>(logits, bias, topk, gates, load, p,
                                                                      ws.status);
         return cudaGetLastError();
     });
@@ -501,16 +539,17 @@ template <typename T>
 cudaError_t route_bwd_typed(const Dims& d, const Workspace& ws, const RouteParams& p,
                             const T* logits, const int32_t* topk, const float* dgates, T* dlogits,
                             int num_sms, cudaStream_t st) {
-    const int grid = grid_for(p.ntok, num_sms, 8);
     if (!p.softmax || p.renorm) {
         route_bwd_kernel<1, T, false, false>
-            <<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
+            <<<grid_for(p.ntok, num_sms, threads_for(1)), threads_for(1), 0, st>>>(logits, topk, dgates,
+                                                                                dlogits, p, ws.status);
         return cudaGetLastError();
     }
     return with_width(d.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
         const auto kernel = d.E == 32 * V ? route_bwd_kernel<V, T, true, true> : route_bwd_kernel<V, T, true, false>;
-        kernel<<<grid, kThreads, 0, st>>>(logits, topk, dgates, dlogits, p, ws.status);
+        kernel<<<grid_for(p.ntok, num_sms, threads_for(V)), threads_for(V), 0, st>>>(
+            logits, topk, dgates, dlogits, p, ws.status);
         return cudaGetLastError();
     });
 }
