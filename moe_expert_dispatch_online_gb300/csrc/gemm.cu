@@ -189,6 +189,7 @@ constexpr int kDualMinRows = 768;
 
 __global__ void __launch_bounds__(1024) gemm_tiles_kernel(const int32_t* __restrict__ cu, Dims d,
                                                           Workspace ws, int seg_mode) {
+    grid_launch_dependents();   // the 4-bit product may set itself up
     const bool dw = seg_mode == 1 || seg_mode == 2;
     // FWD/DX: rows per tile (kFwd2: two m-tiles)
     const int tile = seg_mode == 3 ? 2 * kBM : seg_mode == 5 ? kMxRows : kBM;
@@ -284,6 +285,9 @@ __global__ void __launch_bounds__(1024) gemm_tiles_kernel(const int32_t* __restr
         if (!ok) set_status(ws.status, BEP_DERR_BOUNDS);
         *ws.ntiles = ok ? total : 0;
     }
+    // launched early (launch_mx_tiles): this kernel ends after its predecessor, so that whoever
+    // waits for it has both
+    grid_wait();
 }
 
 struct GemmParams {
@@ -1266,8 +1270,16 @@ void* tensor_map_encoder() {
 }
 
 cudaError_t launch_mx_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st) {
-    gemm_tiles_kernel<<<1, 1024, 0, st>>>(cu, d, ws, 5);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(1024, 1, 1);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gemm_tiles_kernel, cu, d, ws, 5);
 }
 
 cudaError_t launch_wait_selftest(const Workspace& ws, uint64_t timeout_ns, cudaStream_t st) {

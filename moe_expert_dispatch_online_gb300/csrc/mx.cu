@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_mx_kernel(const uint4* __re
                                                                int64_t ntok, int K, int nblk,
                                                                int runs, int pitch, int64_t nrows,
                                                                int32_t* status) {
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
     const int64_t nitem = ntok * runs;
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
                                                              uint4* __restrict__ codes,
                                                              uint8_t* __restrict__ scales,
                                                              int64_t nblocks, int nblk, int pitch) {
+    grid_launch_dependents();
     const int64_t step = (int64_t)gridDim.x * kThreads;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < nblocks; i += step) {
         const int64_t row = i / nblk;
@@ -161,6 +163,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //              scales: its bytes on CTA 0's barrier stand for both (a remote arrive per stage in
 //              their place, with its release at cluster scope, cost 1,000 cycles a stage)
 //   warps 4-7  epilogue: TMEM to bf16 y, while the next unit runs in the other accumulator
+// Launches overlap: the kernel that writes the rows lets the work list's kernel start at once (it
+// reads neither rows nor scales, and nothing that kernel writes), and that one lets this kernel
+// set up its barriers and TMEM; both wait for their predecessor's end before what depends on it.
 //   barrier    owner   arrivals
 //   full[s]    CTA 0   CTA 0's producer (expect_tx) + both CTAs' TMA bytes
 //   empty[s]   both    the MMA thread's multicast commit
@@ -205,6 +210,12 @@ __device__ __forceinline__ MxUnit mx_unit(const MxParams& p, int unit, int MP) {
     u.expert = tile.wsel >= 0 ? tile.wsel : p.slot_expert[-1 - tile.wsel];
     if (u.expert >= p.E) u.expert = -1;
     return u;
+}
+
+// The unit at `unit`, or an unused one past the last: read one unit ahead, since a unit may last
+// only a few stages.
+__device__ __forceinline__ MxUnit mx_first(const MxParams& p, int unit, int total, int MP) {
+    return unit < total ? mx_unit(p, unit, MP) : MxUnit{0, 0, -1, 0};
 }
 
 __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cl, void* dst, int c0,
@@ -301,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     cluster_sync();   // both CTAs' barriers exist before any remote arrive or multicast commit
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
+    grid_wait();      // launched early: the work list and the rows are complete from here on
 
     const int MP = (p.MT + 1) / 2;             // pairs of 128-output tiles
     const int total = *p.ntiles * MP;
@@ -311,8 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
+            MxUnit next = mx_first(p, cl0, total, MP);
             for (int unit = cl0; unit < total && live; unit += ncl) {
-                const MxUnit u = mx_unit(p, unit, MP);
+                const MxUnit u = next;
+                next = mx_first(p, unit + ncl, total, MP);
                 if (u.expert < 0) {
                     if (lead) set_status(status, BEP_DERR_BOUNDS);
                     continue;
@@ -348,8 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             uint32_t old = 0, old_ph = 0, done = 0;    // the stage that used the slot before
             int it = 0;
             bool live = true;
+            MxUnit next = mx_first(p, cl0, total, MP);
             for (int unit = cl0; unit < total && live; unit += ncl) {
-                const MxUnit u = mx_unit(p, unit, MP);
+                const MxUnit u = next;
+                next = mx_first(p, unit + ncl, total, MP);
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
                 const int acc = it & 1;
@@ -408,31 +424,45 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             }
         }
     } else if (warp < 4) {
-        // A 16-byte piece of a row's scales serves two stages; the two warps take the pieces in
-        // turn and hold two of their own in flight, so a load has four pieces to arrive.
+        // A 16-byte piece of a row's scales serves two stages; the two warps take a unit's pieces in
+        // turn. Loads run two of a warp's own pieces ahead of the stores, across units, so that
+        // their latency is hidden at four stages a unit as well.
         constexpr int kC = kMxRows / 32;
         const int mine = warp - 2;
-        uint32_t s = 0, ph = 0;
-        bool live = true;
         const int pieces = (nst + 1) / 2;
-        for (int unit = cl0; unit < total && live; unit += ncl) {
-            const MxUnit u = mx_unit(p, unit, MP);
-            if (u.expert < 0) continue;
-            const int N = mma_rows(u.rows);
-            const int srow = (u.expert * p.MT + 2 * u.mp + (int)rank) * p.KB;
-            const uint4* src[kC];
+        const uint4* src[kC] = {};
+        int l_unit = cl0 - ncl, l_piece = pieces, l_rows = 0;   // the load cursor
+        auto load = [&](uint4* v) {
+            while (l_piece >= pieces) {   // the next unit that has a piece for this warp
+                l_unit += ncl;
+                if (l_unit >= total) return;
+                const MxUnit u = mx_unit(p, l_unit, MP);
+                if (u.expert < 0) continue;
+                l_piece = mine;
+                l_rows = mma_rows(u.rows);
 #pragma unroll
-            for (int c = 0; c < kC; ++c) {
-                const int64_t row = min((int64_t)u.row0 + 32 * c + lane, p.nrows - 1);
-                src[c] = reinterpret_cast<const uint4*>(p.row_scales + row * p.pitch);
+                for (int c = 0; c < kC; ++c) {
+                    const int64_t row = min((int64_t)u.row0 + 32 * c + lane, p.nrows - 1);
+                    src[c] = reinterpret_cast<const uint4*>(p.row_scales + row * p.pitch);
+                }
             }
-            uint4 v0[kC] = {}, v1[kC] = {};
 #pragma unroll
             for (int c = 0; c < kC; ++c)
-                if (32 * c < N) {
-                    if (mine < pieces) v0[c] = __ldg(src[c] + mine);
-                    if (mine + 2 < pieces) v1[c] = __ldg(src[c] + mine + 2);
-                }
+                if (32 * c < l_rows) v[c] = __ldg(src[c] + l_piece);
+            l_piece += 2;
+        };
+        uint4 v0[kC] = {}, v1[kC] = {};
+        load(v0);
+        load(v1);
+        uint32_t s = 0, ph = 0;
+        bool live = true;
+        MxUnit u = mx_first(p, cl0, total, MP);
+        for (int unit = cl0; unit < total && live; unit += ncl) {
+            const MxUnit cur = u;
+            u = mx_first(p, unit + ncl, total, MP);
+            if (cur.expert < 0) continue;
+            const int N = mma_rows(cur.rows);
+            const int srow = (cur.expert * p.MT + 2 * cur.mp + (int)rank) * p.KB;
             for (int g = 0; g < pieces && live; ++g) {
                 const int here = min(2, nst - 2 * g);   // stages of this piece
                 if ((g & 1) != mine) {
@@ -448,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                 for (int c = 0; c < kC; ++c) {
                     v[c] = v0[c];
                     v0[c] = v1[c];
-                    if (32 * c < N && g + 4 < pieces) v1[c] = __ldg(src[c] + g + 4);
                 }
+                load(v1);
                 for (int half = 0; half < here; ++half) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, s_abort, status))) {
                         live = false;
@@ -476,8 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     } else {
         const int quarter = warp - 4;
         int it = 0;
+        MxUnit next = mx_first(p, cl0, total, MP);
         for (int unit = cl0; unit < total; unit += ncl) {
-            const MxUnit u = mx_unit(p, unit, MP);
+            const MxUnit u = next;
+            next = mx_first(p, unit + ncl, total, MP);
             if (u.expert < 0) continue;
             const int acc = it & 1;
             if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, status))) break;
@@ -586,8 +618,10 @@ cudaLaunchConfig_t mx_config(int clusters, cudaStream_t st, cudaLaunchAttribute*
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cfg;
 }
 
@@ -606,7 +640,7 @@ cudaError_t mx_setup(int device) {
     int nsm = 0;
     err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, device);
     if (err != cudaSuccess) return err;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = mx_config(nsm / 2, nullptr, attr);
     return cudaOccupancyMaxActiveClusters(&g_mx_clusters[device], grouped_gemm_mx_kernel, &cfg);
 }
@@ -671,7 +705,7 @@ cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || g_mx_clusters[dev] < 1)
         return cudaErrorInvalidDevice;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const int pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
     cudaLaunchConfig_t cfg = mx_config(g_mx_clusters[dev] < pairs ? g_mx_clusters[dev] : pairs, st, attr);
     return cudaLaunchKernelEx(&cfg, grouped_gemm_mx_kernel, tmW, tmS, tmX[0], tmX[1], tmX[2], tmX[3], p);
