@@ -521,6 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             for (int c0 = 0; c0 < u.rows; c0 += 32) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * kMxRows + c0, r);
+                if (c0 + 32 >= u.rows) {   // the accumulator is read out: free it before the stores
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_rank_relaxed(&tempty[acc], 0);
+                }
                 // lanes 2i and 2i + 1 trade a row each, so that a lane stores two outputs of one row
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -532,12 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                         *reinterpret_cast<uint32_t*>(p.y + ((int64_t)u.row0 + c) * p.Hp + n0 + (lane & ~1)) =
                             odd ? pack_bf16x2(got, keep) : pack_bf16x2(keep, got);
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (lead) mbar_arrive(&tempty[acc]);
-                else mbar_arrive_rank(&tempty[acc], 0);
             }
         }
     }

@@ -198,6 +198,13 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
                  : "memory");
 }
 
+// The same without release semantics, for an arrive that publishes nothing in memory (a TMEM
+// accumulator read out): a release at cluster scope waits for the thread's global stores.
+__device__ __forceinline__ void mbar_arrive_rank_relaxed(uint64_t* bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank))
+                 : "memory");
+}
+
 // TMA tile load into this CTA's shared memory whose completion is counted on an
 // mbarrier of either CTA of the pair (bar_cl: a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar_cl, void* dst, int c0,
