@@ -399,7 +399,7 @@ int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* 
                         const uint8_t* codes, const uint8_t* scales, const uint8_t* w_codes,
                         const uint8_t* w_scales, uint16_t* y, void* stream);
 
-/* SM budget of the token-moving kernels (dispatch, combine, combine_bwd,
+/* SM budget of the token-moving kernels (dispatch, dispatch_mx, combine, combine_bwd,
  * combine_dgates, dispatch_bwd): their grids are sized for `sms` SMs, so
  * the rest of the GPU stays free for concurrent work, as a communication
  * library with a fixed SM budget runs ([P4] "Benchmarks against DeepEP v2":

@@ -382,7 +382,7 @@ int bep_swiglu(bep_ctx* ctx, const uint16_t* h, int32_t F, uint16_t* a, int8_t* 
     if (!h || !a) return BEP_ERR_ARG;
     if (!aligned(h, 16) || !aligned(a, 16) || !aligned(codes, 16)) return BEP_ERR_ALIGN;
     return cuda_rc(bep::launch_swiglu((int64_t)ctx->d.R * ctx->d.C, F, h, a, codes, scales,
-                                      ctx->num_sms, as_stream(stream)));
+                                      as_stream(stream)));
 }
 
 int bep_swiglu_bwd(bep_ctx* ctx, const uint16_t* da, int32_t F, const int8_t* codes,
@@ -394,7 +394,7 @@ int bep_swiglu_bwd(bep_ctx* ctx, const uint16_t* da, int32_t F, const int8_t* co
     if (!aligned(da, 16) || !aligned(codes, 16) || !aligned(dh, 16) || !aligned(a, 16))
         return BEP_ERR_ALIGN;
     return cuda_rc(bep::launch_swiglu_bwd((int64_t)ctx->d.R * ctx->d.C, F, da, codes, scales, dh, a,
-                                          ctx->num_sms, as_stream(stream)));
+                                          as_stream(stream)));
 }
 
 int bep_mx_quantize_weight(bep_ctx* ctx, const uint16_t* w, uint8_t* codes, uint8_t* scales,
@@ -414,7 +414,7 @@ int bep_dispatch_mx(bep_ctx* ctx, const uint16_t* x, const int32_t* dest, uint8_
     if (!aligned(x, 16) || !aligned(dest, 4) || !aligned(codes, 16) || !aligned(scales, 16))
         return BEP_ERR_ALIGN;
     return cuda_rc(bep::launch_dispatch_mx(ctx->d, ctx->ws, x, dest, codes, scales, comm_sms(ctx),
-                                           as_stream(stream)));
+                                           ctx->num_sms, as_stream(stream)));
 }
 
 int bep_swiglu_mx(bep_ctx* ctx, const uint16_t* h, int32_t F, uint8_t* codes, uint8_t* scales,
@@ -425,7 +425,7 @@ int bep_swiglu_mx(bep_ctx* ctx, const uint16_t* h, int32_t F, uint8_t* codes, ui
     if (!h || !codes || !scales) return BEP_ERR_ARG;
     if (!aligned(h, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return BEP_ERR_ALIGN;
     return cuda_rc(bep::launch_swiglu_mx((int64_t)ctx->d.R * ctx->d.C, F, h, codes, scales,
-                                         ctx->num_sms, as_stream(stream)));
+                                         as_stream(stream)));
 }
 
 int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert,

@@ -113,20 +113,19 @@ cudaError_t launch_route_bwd(const Dims& d, const Workspace& ws, const bep_route
                              const float* dgates, void* dlogits, int num_sms, cudaStream_t st);
 // gated activation (act.cu)
 cudaError_t launch_swiglu(int64_t rows, int F, const uint16_t* h, uint16_t* a, int8_t* codes,
-                          uint8_t* scales, int num_sms, cudaStream_t st);
+                          uint8_t* scales, cudaStream_t st);
 cudaError_t launch_swiglu_bwd(int64_t rows, int F, const uint16_t* da, const int8_t* codes,
-                              const uint8_t* scales, uint16_t* dh, uint16_t* a, int num_sms,
-                              cudaStream_t st);
+                              const uint8_t* scales, uint16_t* dh, uint16_t* a, cudaStream_t st);
 // 4-bit experts (mx.cu)
 inline int mx_scale_pitch(int H) { return 16 * ((H + 511) / 512); }   // bytes of a row's scales
 cudaError_t mx_setup(int device);
 cudaError_t launch_mx_weight(const Dims& d, const uint16_t* w, uint8_t* codes, uint8_t* scales,
                              cudaStream_t st);
 cudaError_t launch_dispatch_mx(const Dims& d, const Workspace& ws, const uint16_t* x,
-                               const int32_t* dest, uint8_t* codes, uint8_t* scales, int num_sms,
+                               const int32_t* dest, uint8_t* codes, uint8_t* scales, int sms, int num_sms,
                                cudaStream_t st);
 cudaError_t launch_swiglu_mx(int64_t rows, int F, const uint16_t* h, uint8_t* codes,
-                             uint8_t* scales, int num_sms, cudaStream_t st);
+                             uint8_t* scales, cudaStream_t st);
 cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int32_t* cu,
                                    const int32_t* slot_expert, const uint8_t* codes,
                                    const uint8_t* scales, const uint8_t* w_codes,
