@@ -99,11 +99,8 @@ cudaError_t launch_grouped_gemm_dw(const Dims& d, const Workspace& ws, const int
                                    const uint16_t* recv, const uint16_t* dy, float* g_home,
                                    float* red, int accumulate, int num_sms, cudaStream_t st);
 
-// cuTensorMapEncodeTiled of the driver (nullptr: not found), and the work list of the 4-bit
-// product: tiles of at most kMxRows rows (gemm.cu)
-constexpr int kMxRows = 192;
+// cuTensorMapEncodeTiled of the driver, nullptr if it is not found (gemm.cu)
 void* tensor_map_encoder();
-cudaError_t launch_mx_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st);
 // routing (route.cu)
 cudaError_t launch_route(const Dims& d, const Workspace& ws, const bep_route_config& rc,
                          const void* logits, int logits_type, const float* bias, int32_t* topk,

@@ -173,7 +173,6 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* s_warp, int* tot
 //   the order is plain (rank, row, m).
 // seg_mode == 3: as 0 with tiles of <= 256 rows (two m-tiles: the kFwd2 units), for the
 //   segments of kDualMinRows rows or more only; seg_mode == 4: as 0 for the other segments.
-// seg_mode == 5: as 0 with tiles of <= 192 rows (the 4-bit product's N tiles).
 // seg_mode == 1: one entry per non-empty segment, rows = its length (DW).
 // seg_mode == 2: as 1, plus an entry with rows = 0 for every expert whose home segment
 //   (rank e / (E/R), row e) is empty, so that an overwriting DW writes its zeros; a
@@ -189,10 +188,9 @@ constexpr int kDualMinRows = 768;
 
 __global__ void __launch_bounds__(1024) gemm_tiles_kernel(const int32_t* __restrict__ cu, Dims d,
                                                           Workspace ws, int seg_mode) {
-    grid_launch_dependents();   // the 4-bit product may set itself up
     const bool dw = seg_mode == 1 || seg_mode == 2;
     // FWD/DX: rows per tile (kFwd2: two m-tiles)
-    const int tile = seg_mode == 3 ? 2 * kBM : seg_mode == 5 ? kMxRows : kBM;
+    const int tile = seg_mode == 3 ? 2 * kBM : kBM;
     auto tile_of = [&](int) { return tile; };
     __shared__ int s_warp[33];
     const int n_items = d.R * d.NROW;
@@ -285,9 +283,6 @@ __global__ void __launch_bounds__(1024) gemm_tiles_kernel(const int32_t* __restr
         if (!ok) set_status(ws.status, BEP_DERR_BOUNDS);
         *ws.ntiles = ok ? total : 0;
     }
-    // launched early (launch_mx_tiles): this kernel ends after its predecessor, so that whoever
-    // waits for it has both
-    grid_wait();
 }
 
 struct GemmParams {
@@ -1267,19 +1262,6 @@ cudaError_t launch_mode(const CUtensorMap& a, const CUtensorMap& b0, const CUten
 
 void* tensor_map_encoder() {
     return get_encoder() == cudaSuccess ? reinterpret_cast<void*>(g_encode) : nullptr;
-}
-
-cudaError_t launch_mx_tiles(const Dims& d, const Workspace& ws, const int32_t* cu, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(1, 1, 1);
-    cfg.blockDim = dim3(1024, 1, 1);
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_tiles_kernel, cu, d, ws, 5);
 }
 
 cudaError_t launch_wait_selftest(const Workspace& ws, uint64_t timeout_ns, cudaStream_t st) {

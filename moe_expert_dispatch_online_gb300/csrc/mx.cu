@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //   empty[s]   both    the MMA thread's multicast commit
 //   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
 //   tempty[a]  CTA 0   the 4 epilogue warps of each CTA
+constexpr int kMxRows = 192;                   // rows of a tile at most
 constexpr int kMxStages = 6;
 constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
 constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
@@ -262,6 +263,97 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64
 // Rows of a unit's MMA: N in steps of 32, half of it in each CTA.
 __device__ __forceinline__ int mma_rows(int rows) { return (rows + 31) & ~31; }
 
+// The work list: tiles of at most kMxRows rows of one segment, in (rank, row) order. One CTA; a
+// thread holds four segments at a time, all loaded at once (8 ranks x 433 segments: 3 us; a
+// thread with four consecutive segments loaded twice took 7). A table with any inconsistent
+// segment is refused as a whole.
+__global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* __restrict__ cu, Dims d, FastDiv nrow,
+                                                        Workspace ws) {
+    constexpr int kS = 4, kChunk = kS * 1024;
+    __shared__ int s_sum[kS * 32];
+    grid_launch_dependents();   // the product may set itself up
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int items = d.R * d.NROW;
+    int a[kS], len[kS];
+    auto segments = [&](int base) {
+        int bad = 0;
+#pragma unroll
+        for (int r = 0; r < kS; ++r) {
+            const int i = base + r * 1024 + threadIdx.x;
+            a[r] = len[r] = 0;
+            if (i < items) {
+                const int u = (int)fast_div((uint32_t)i, nrow);
+                a[r] = __ldg(cu + i + u);   // rank u's table has one more entry than segments
+                len[r] = __ldg(cu + i + u + 1);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kS; ++r) {
+            bad |= a[r] < 0 || len[r] < a[r] || (int64_t)len[r] > d.C;
+            len[r] -= a[r];
+        }
+        return bad;
+    };
+    int bad = 0;
+    for (int base = 0; base < items; base += kChunk) bad |= segments(base);
+    const bool ok = !__syncthreads_or(bad);
+    int total = 0;
+    for (int base = 0; base < items && ok; base += kChunk) {
+        if (items > kChunk) segments(base);
+        int before[kS];   // tiles of this warp's run of 32 segments before this lane's
+#pragma unroll
+        for (int r = 0; r < kS; ++r) {
+            const int n = (len[r] + kMxRows - 1) / kMxRows;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            before[r] = incl - n;
+            if (lane == 31) s_sum[r * 32 + warp] = incl;
+        }
+        __syncthreads();
+        // every warp: exclusive prefix of the 128 runs; lane l of round r holds run (r, l)
+        int run_base[kS], sum = total;
+#pragma unroll
+        for (int r = 0; r < kS; ++r) {
+            const int n = s_sum[r * 32 + lane];
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            run_base[r] = sum + __shfl_sync(0xffffffffu, incl - n, warp);
+            sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        total = sum;
+#pragma unroll
+        for (int r = 0; r < kS; ++r) {
+            if (len[r] <= 0) continue;
+            const int i = base + r * 1024 + threadIdx.x;
+            const int u = (int)fast_div((uint32_t)i, nrow), rho = i - u * d.NROW;
+            MTile t;
+            t.wsel = rho < d.E ? rho : -(1 + u * d.B + (rho - d.E));
+            t.pad = 0;
+            MTile* out = ws.tiles + run_base[r] + before[r];
+            for (int m = 0; m < len[r]; m += kMxRows) {
+                t.row0 = (int32_t)(u * d.C + a[r] + m);
+                t.rows = min(kMxRows, len[r] - m);
+                *out++ = t;
+            }
+        }
+        __syncthreads();   // s_sum is written again by the next chunk
+    }
+    if (threadIdx.x == 0) {
+        if (!ok) set_status(ws.status, BEP_DERR_BOUNDS);
+        *ws.ntiles = ok ? total : 0;
+    }
+    // launched early: this kernel ends after its predecessor, so that whoever waits for it has both
+    grid_wait();
+}
+
 __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
     const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ CUtensorMap tmX32,
@@ -286,6 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     const bool lead = rank == 0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 32) {
+        const CUtensorMap* maps[] = {&tmW, &tmS, &tmX16, &tmX32, &tmX64, &tmX96};
+        for (const CUtensorMap* m : maps)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMxStages; ++s) {
             mbar_init(&full[s], 1);
@@ -702,7 +799,17 @@ cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int
     if (!encode_scales(&tmS, w_scales, (uint64_t)d.E * p.MT * p.KB)) return cudaErrorInvalidValue;
     for (int i = 0; i < 4; ++i)
         if (!encode_u8(&tmX[i], codes, 2, xd, boxes[i])) return cudaErrorInvalidValue;
-    const cudaError_t err = launch_mx_tiles(d, ws, cu, st);
+    cudaLaunchConfig_t tc = {};
+    cudaLaunchAttribute early;
+    tc.gridDim = dim3(1, 1, 1);
+    tc.blockDim = dim3(1024, 1, 1);
+    tc.stream = st;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    tc.attrs = &early;
+    tc.numAttrs = 1;
+    const cudaError_t err =
+        cudaLaunchKernelEx(&tc, mx_tiles_kernel, cu, d, make_fast_div((uint32_t)d.NROW), ws);
     if (err != cudaSuccess) return err;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || g_mx_clusters[dev] < 1)
