@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 // The weights are the M operand and the rows of one segment the N operand (32..192), so that a
 // segment of a few rows costs a narrow MMA and not a 128-row one. A cluster of two CTAs shares a
 // tile of 256 outputs x N rows (cta_group::2): CTA r holds outputs 128 r.. and half of the rows,
-// so that a stage brings 31 KB to each SM for what takes one CTA 43 KB: an SM takes in about 61
-// bytes a cycle from L2, and at 4 bits that, not the tensor core, bounds a tile (one CTA alone
-// with N <= 128: 4.97 ms for 524,288 rows by 7168 x 2048, 3.5 ms of it without any MMA).
+// so that a stage brings 33 KB to each SM for what takes one CTA 47 KB. At 4 bits an SM's shared
+// memory bounds a tile, not the tensor core: per stage of 224 rows 33 KB arrive and the MMAs read
+// 44 KB, 600 cycles at 128 bytes a cycle for 390 of MMAs. 524,288 rows by 7168 x 2048: 4.97 ms with
+// one CTA and N <= 128, 2.92 with pairs and N <= 192, 2.71 with N <= 224 (5.7 PFLOP/s).
 //   warp 0     TMA: codes of 128 outputs and of N/2 rows; 256 reduction steps a stage
 //   warp 1     (CTA 0) copies each stage's scales to both TMEMs, issues tcgen05.mma.kind::mxf4
 //   warps 2, 3 put all N rows' scales (any row offset, so no TMA) in tensor-core order, make them
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //   empty[s]   both    the MMA thread's multicast commit
 //   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
 //   tempty[a]  CTA 0   the 4 epilogue warps of each CTA
-constexpr int kMxRows = 192;                   // rows of a tile at most
+constexpr int kMxRows = 224;                   // rows of a tile at most
 constexpr int kMxStages = 6;
 constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
 constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* __restric
 __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
     const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ CUtensorMap tmX32,
-    const __grid_constant__ CUtensorMap tmX64, const __grid_constant__ CUtensorMap tmX96,
+    const __grid_constant__ CUtensorMap tmX64, const __grid_constant__ CUtensorMap tmXtop,
     const MxParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 32) {
-        const CUtensorMap* maps[] = {&tmW, &tmS, &tmX16, &tmX32, &tmX64, &tmX96};
+        const CUtensorMap* maps[] = {&tmW, &tmS, &tmX16, &tmX32, &tmX64, &tmXtop};
         for (const CUtensorMap* m : maps)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
@@ -429,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
                     continue;
                 }
                 const int half = mma_rows(u.rows) / 2;
-                const CUtensorMap* tmX = half <= 16 ? &tmX16 : half <= 32 ? &tmX32 : half <= 64 ? &tmX64 : &tmX96;
-                const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 96;
+                const CUtensorMap* tmX = half <= 16 ? &tmX16 : half <= 32 ? &tmX32 : half <= 64 ? &tmX64 : &tmXtop;
+                const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : kMxRows / 2;
                 const int mt = 2 * u.mp + (int)rank;   // past H' for the last odd tile: zeros
                 for (int k = 0; k < nst; ++k) {
                     if (!mbar_wait(&empty[pr_s], pr_ph ^ 1u, s_abort, status)) {

@@ -101,25 +101,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// A token's logits, lane l's at l + 32 i (the last expert again past E). One maximum and one
-// minimum an element tell the ordinary row, all finite and unmasked, from one that has to be
-// looked at element by element. *top: this lane's largest logit that is a number (-inf: none).
-// The result: whether the row is ordinary; otherwise its masked logits are -inf, and *bad is set
-// for a NaN or +inf among them. Past E: -inf in either case.
+// A token's logits, lane l's at l + 32 i (the last expert again past E).
 template <int V, bool kFull, typename T>
 __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, float (&x)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = load_logit(row + (kFull ? lane + 32 * i : min(lane + 32 * i, E - 1)));
 }
+// One maximum an element tells the ordinary row, whose magnitudes are all kOrdinary at most, from
+// one that is looked at element by element. In an ordinary row nothing is masked and e^l needs no
+// reference to stay inside fp32 (e^40 = 2e17, 2048 terms), nor to be as exact as e^(l - max): the
+// argument's rounding is relative to the logits in either case. Otherwise masked logits become
+// -inf and *bad is set for a NaN or +inf among them. *top: the softmax's reference, 0 or the
+// row's largest logit. Past E: -inf in either case.
+constexpr float kOrdinary = 40.0f;
 template <int V, bool kFull, typename T>
 __device__ __forceinline__ bool look_over(int E, int lane, float (&x)[V], float* top, int* bad) {
-    float hi = -INFINITY, lo = INFINITY;
+    float hi = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        hi = max_nan(hi, x[i]);
-        lo = fminf(lo, x[i]);
-    }
-    const bool ordinary = __all_sync(kAll, hi <= FLT_MAX && lo > lowest<T>());
+    for (int i = 0; i < V; ++i) hi = max_nan(hi, fabsf(x[i]));
+    const bool ordinary = __all_sync(kAll, hi <= kOrdinary);
+    *top = 0.0f;
     if (!ordinary) {
         hi = -INFINITY;
 #pragma unroll
@@ -131,15 +132,19 @@ __device__ __forceinline__ bool look_over(int E, int lane, float (&x)[V], float*
             if (x[i] <= lowest<T>()) x[i] = -INFINITY;
             hi = fmaxf(hi, x[i]);
         }
+        hi = warp_max(hi);
+        if (hi > -INFINITY) *top = hi;   // else nothing to choose from: all scores 0
     }
     if (!kFull) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (lane + 32 * i >= E) x[i] = -INFINITY;
     }
-    *top = hi;
     return ordinary;
 }
+
+// e^(x - top); the difference first, so that a large top costs no precision
+__device__ __forceinline__ float exp_of(float x, float top) { return fast_exp2((x - top) * kLog2e); }
 
 struct RouteParams {
     int64_t ntok;
@@ -273,12 +278,10 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
         float inv = 0.0f;   // 1 / sum of exp(l - top)
         uint32_t key[V];
         if (row_sum) {
-            top = warp_max(top);
-            if (top == -INFINITY) top = 0.0f;   // nothing to choose from: all scores 0
             float ex[V], sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                ex[i] = fast_exp2((x[i] - top) * kLog2e);
+                ex[i] = exp_of(x[i], top);
                 sum += ex[i];
             }
             sum = warp_sum(sum);
@@ -428,11 +431,9 @@ __global__ void __launch_bounds__(threads_for(V)) route_bwd_kernel(const T* __re
             float top, sum = 0.0f;
             int masked = 0;   // reported by the forward
             look_over<V, kFull, T>(p.E, lane, x, &top, &masked);
-            top = warp_max(top);
-            if (top == -INFINITY) top = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                x[i] = fast_exp2((x[i] - top) * kLog2e);
+                x[i] = exp_of(x[i], top);
                 sum += x[i];
             }
             sum = warp_sum(sum);
