@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //              visible to the async proxy, and only then start the stage's TMA load of the weight
 //              scales: its bytes on CTA 0's barrier stand for both (a remote arrive per stage in
 //              their place, with its release at cluster scope, cost 1,000 cycles a stage)
-//   warps 4-7  epilogue: TMEM to bf16 y, while the next unit runs in the other accumulator
+//   warps 4-11 epilogue: TMEM to bf16 y, while the next unit runs in the other accumulator
 // Launches overlap: the kernel that writes the rows lets the work list's kernel start at once (it
 // reads neither rows nor scales, and nothing that kernel writes), and that one lets this kernel
 // set up its barriers and TMEM; both wait for their predecessor's end before what depends on it.
@@ -171,14 +171,17 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //   full[s]    CTA 0   CTA 0's producer (expect_tx) + both CTAs' TMA bytes
 //   empty[s]   both    the MMA thread's multicast commit
 //   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
-//   tempty[a]  CTA 0   the 4 epilogue warps of each CTA
+//   tempty[a]  CTA 0   the 8 epilogue warps of each CTA
 constexpr int kMxRows = 224;                   // rows of a tile at most
+constexpr int kMxEpiWarps = 8;                 // two for each quarter of TMEM's lanes
+constexpr int kMxThreads = 32 * (4 + kMxEpiWarps);
 constexpr int kMxStages = 6;
 constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
 constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
 constexpr int kMxB = kMxRows / 2 * 128;        // bytes: half of the rows
 constexpr int kMxSfa = 1024;                   // bytes: 2 blocks of 512
 constexpr int kMxSfb = 2048;                   // bytes: (2 reduction blocks) x (rows 0..127, 128..255)
+constexpr int kMxOut = 32 * 64;                // bytes: an epilogue warp's 32 rows x 32 outputs
 constexpr int kMxStageBytes = kMxA + kMxB + kMxSfa + kMxSfb;
 constexpr int kMxTmemCols = 512;
 constexpr int kMxSfBase = 2 * kMxRows;         // two accumulators lie before
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* __restric
     grid_wait();
 }
 
-__global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
+__global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
     const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ CUtensorMap tmX32,
     const __grid_constant__ CUtensorMap tmX64, const __grid_constant__ CUtensorMap tmXtop,
@@ -367,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     uint8_t* smB = smA + kMxStages * kMxA;
     uint8_t* smSA = smB + kMxStages * kMxB;
     uint8_t* smSB = smSA + kMxStages * kMxSfa;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smSB + kMxStages * kMxSfb);
+    uint8_t* smO = smSB + kMxStages * kMxSfb;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smO + kMxEpiWarps * kMxOut);
     uint64_t* empty = full + kMxStages;
     uint64_t* tfull = empty + kMxStages;
     uint64_t* tempty = tfull + 2;
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], 8);
+            mbar_init(&tempty[a], 2 * kMxEpiWarps);
         }
         mbar_init(drain, 1);
         *s_abort = 0;
@@ -602,7 +606,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             }
         }
     } else {
-        const int quarter = warp - 4;
+        // A warp owns a quarter's 32 outputs of every second run of 32 rows. Its lanes hold one output
+        // each and a row's outputs lie together in y, so each run is turned in shared memory (2-byte
+        // stores with fixed offsets, conflict-free) and leaves as 16-byte pieces, 64 bytes a row.
+        // One warp a scheduler issues slowly: with 4 warps that traded outputs by shuffles and stored
+        // 4 bytes a lane, 131,000 rows of 256 by 5760 took 991 us.
+        const int quarter = warp & 3, second = (warp - 4) >> 2;
+        uint8_t* stg = smO + (warp - 4) * kMxOut;
         int it = 0;
         MxUnit next = mx_first(p, cl0, total, MP);
         for (int unit = cl0; unit < total; unit += ncl) {
@@ -615,26 +625,38 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
             tc_fence_after();
             // lane l of quarter q holds output n = 128 mt + 32 q + l, its columns the rows
             const int n0 = (2 * u.mp + (int)rank) * 128 + quarter * 32;
-            const bool odd = lane & 1;
-            for (int c0 = 0; c0 < u.rows; c0 += 32) {
+            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * kMxRows;
+            bool held = true;
+            for (int c0 = 32 * second; c0 < u.rows; c0 += 64) {
                 uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * kMxRows + c0, r);
-                if (c0 + 32 >= u.rows) {   // the accumulator is read out: free it before the stores
+                tmem_ld_32x32b_x32(tacc + c0, r);
+                if (c0 + 64 >= u.rows) {   // this warp has read all its runs: free them before the stores
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_rank_relaxed(&tempty[acc], 0);
+                    held = false;
                 }
-                // lanes 2i and 2i + 1 trade a row each, so that a lane stores two outputs of one row
+                if (n0 >= p.Hp) continue;
+                uint16_t* col = reinterpret_cast<uint16_t*>(stg) + lane;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float keep = __uint_as_float(odd ? r[2 * j + 1] : r[2 * j]);
-                    const float give = __uint_as_float(odd ? r[2 * j] : r[2 * j + 1]);
-                    const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-                    const int c = c0 + 2 * j + (odd ? 1 : 0);
-                    if (c < u.rows && n0 < p.Hp)
-                        *reinterpret_cast<uint32_t*>(p.y + ((int64_t)u.row0 + c) * p.Hp + n0 + (lane & ~1)) =
-                            odd ? pack_bf16x2(got, keep) : pack_bf16x2(keep, got);
+                    const uint32_t two = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    col[(2 * j) * 32] = (uint16_t)two;
+                    col[(2 * j + 1) * 32] = (uint16_t)(two >> 16);
                 }
+                __syncwarp();
+                const uint4* piece = reinterpret_cast<const uint4*>(stg) + lane;
+                uint16_t* out = p.y + ((int64_t)u.row0 + c0 + (lane >> 2)) * p.Hp + n0 + (lane & 3) * 8;
+                const int left = u.rows - c0 - (lane >> 2);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (8 * j < left) *reinterpret_cast<uint4*>(out + (int64_t)(8 * j) * p.Hp) = piece[32 * j];
+                __syncwarp();   // the next run is staged in the same place
+            }
+            if (held) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_rank_relaxed(&tempty[acc], 0);
             }
         }
     }
@@ -670,7 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_mx_kernel(
     }
 }
 
-constexpr size_t kMxSmem = 1024 + (size_t)kMxStages * kMxStageBytes + (2 * kMxStages + 5) * 8 + 16;
+constexpr size_t kMxSmem =
+    1024 + (size_t)kMxStages * kMxStageBytes + kMxEpiWarps * kMxOut + (2 * kMxStages + 5) * 8 + 16;
 
 // Scale blocks as rows of 128 words, 2 rows a box.
 bool encode_scales(CUtensorMap* m, const void* base, uint64_t blocks) {
@@ -708,7 +731,7 @@ int g_mx_clusters[kMaxDevices] = {};
 cudaLaunchConfig_t mx_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(kMxThreads, 1, 1);
     cfg.dynamicSmemBytes = kMxSmem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
