@@ -181,7 +181,7 @@ constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
 constexpr int kMxB = kMxRows / 2 * 128;        // bytes: half of the rows
 constexpr int kMxSfa = 1024;                   // bytes: 2 blocks of 512
 constexpr int kMxSfb = 2048;                   // bytes: (2 reduction blocks) x (rows 0..127, 128..255)
-constexpr int kMxOut = 32 * 64;                // bytes: an epilogue warp's 32 rows x 32 outputs
+constexpr int kMxOut = 32 * 256;               // bytes: four epilogue warps' 32 rows x 128 outputs
 constexpr int kMxStageBytes = kMxA + kMxB + kMxSfa + kMxSfb;
 constexpr int kMxTmemCols = 512;
 constexpr int kMxSfBase = 2 * kMxRows;         // two accumulators lie before
@@ -262,6 +262,23 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64
             "r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
+}
+
+// Named barriers of four epilogue warps.
+__device__ __forceinline__ void quad_sync(int id) {
+    asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool quad_all(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.and.pred p, %1, 128, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
 }
 
 // Rows of a unit's MMA: N in steps of 32, half of it in each CTA.
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     uint8_t* smSA = smB + kMxStages * kMxB;
     uint8_t* smSB = smSA + kMxStages * kMxSfa;
     uint8_t* smO = smSB + kMxStages * kMxSfb;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smO + kMxEpiWarps * kMxOut);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smO + kMxEpiWarps / 4 * kMxOut);
     uint64_t* empty = full + kMxStages;
     uint64_t* tfull = empty + kMxStages;
     uint64_t* tempty = tfull + 2;
@@ -526,21 +543,22 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             }
         }
     } else if (warp < 4) {
-        // A 16-byte piece of a row's scales serves two stages; the two warps take a unit's pieces in
-        // turn. Loads run two of a warp's own pieces ahead of the stores, across units, so that
+        // A 16-byte piece of a row's scales serves two stages; the two warps take the pieces in turn,
+        // across units. Loads run two of a warp's own pieces ahead of the stores, across units, so that
         // their latency is hidden at four stages a unit as well.
         constexpr int kC = kMxRows / 32;
         const int mine = warp - 2;
         const int pieces = (nst + 1) / 2;
         const uint4* src[kC] = {};
-        int l_unit = cl0 - ncl, l_piece = pieces, l_rows = 0;   // the load cursor
+        int l_unit = cl0 - ncl, l_piece = pieces + mine, l_rows = 0;   // the load cursor
         auto load = [&](uint4* v) {
             while (l_piece >= pieces) {   // the next unit that has a piece for this warp
                 l_unit += ncl;
                 if (l_unit >= total) return;
                 const MxUnit u = mx_unit(p, l_unit, MP);
                 if (u.expert < 0) continue;
-                l_piece = mine;
+                l_piece -= pieces;
+                if (l_piece >= pieces) continue;   // all of this unit's are the other warp's
                 l_rows = mma_rows(u.rows);
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
@@ -558,6 +576,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         load(v1);
         uint32_t s = 0, ph = 0;
         bool live = true;
+        int own = mine;   // this warp's next piece of the unit
         MxUnit u = mx_first(p, cl0, total, MP);
         for (int unit = cl0; unit < total && live; unit += ncl) {
             const MxUnit cur = u;
@@ -567,7 +586,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             const int srow = (cur.expert * p.MT + 2 * cur.mp + (int)rank) * p.KB;
             for (int g = 0; g < pieces && live; ++g) {
                 const int here = min(2, nst - 2 * g);   // stages of this piece
-                if ((g & 1) != mine) {
+                if (g != own) {
                     s += here;
                     if (s >= kMxStages) {
                         s -= kMxStages;
@@ -575,6 +594,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     }
                     continue;
                 }
+                own += 2;
                 uint4 v[kC];
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
@@ -604,15 +624,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     }
                 }
             }
+            own -= pieces;
         }
     } else {
-        // A warp owns a quarter's 32 outputs of every second run of 32 rows. Its lanes hold one output
-        // each and a row's outputs lie together in y, so each run is turned in shared memory (2-byte
-        // stores with fixed offsets, conflict-free) and leaves as 16-byte pieces, 64 bytes a row.
-        // One warp a scheduler issues slowly: with 4 warps that traded outputs by shuffles and stored
-        // 4 bytes a lane, 131,000 rows of 256 by 5760 took 991 us.
+        // Four warps, one for each quarter of TMEM's lanes, own every second run of 32 rows. A lane
+        // holds one output of 32 rows, and a row's outputs lie together in y, so the run is turned in
+        // shared memory (2-byte stores with fixed offsets, conflict-free) and leaves as whole rows of
+        // 256 bytes, 16 a lane. One warp a scheduler issues slowly and 64-byte pieces of rows write
+        // slowly: 131,000 rows of 256 by 5760 took 991 us with 4 warps that traded outputs by shuffles
+        // and stored 4 bytes a lane, 415 us with 8 that each turned and stored their own 64 bytes.
         const int quarter = warp & 3, second = (warp - 4) >> 2;
-        uint8_t* stg = smO + (warp - 4) * kMxOut;
+        uint8_t* stg = smO + second * kMxOut;
         int it = 0;
         MxUnit next = mx_first(p, cl0, total, MP);
         for (int unit = cl0; unit < total; unit += ncl) {
@@ -620,11 +642,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             next = mx_first(p, unit + ncl, total, MP);
             if (u.expert < 0) continue;
             const int acc = it & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, status))) break;
+            // the four give up together, so that none waits for another at their barrier
+            if (!quad_all(1 + second, mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, status))) break;
             ++it;
             tc_fence_after();
             // lane l of quarter q holds output n = 128 mt + 32 q + l, its columns the rows
-            const int n0 = (2 * u.mp + (int)rank) * 128 + quarter * 32;
+            const int n0 = (2 * u.mp + (int)rank) * 128;
             const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * kMxRows;
             bool held = true;
             for (int c0 = 32 * second; c0 < u.rows; c0 += 64) {
@@ -636,22 +659,22 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     if (lane == 0) mbar_arrive_rank_relaxed(&tempty[acc], 0);
                     held = false;
                 }
-                if (n0 >= p.Hp) continue;
-                uint16_t* col = reinterpret_cast<uint16_t*>(stg) + lane;
+                quad_sync(1 + second);   // the run before has been read
+                uint16_t* col = reinterpret_cast<uint16_t*>(stg) + quarter * 32 + lane;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const uint32_t two = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                    col[(2 * j) * 32] = (uint16_t)two;
-                    col[(2 * j + 1) * 32] = (uint16_t)(two >> 16);
+                    col[(2 * j) * 128] = (uint16_t)two;
+                    col[(2 * j + 1) * 128] = (uint16_t)(two >> 16);
                 }
-                __syncwarp();
-                const uint4* piece = reinterpret_cast<const uint4*>(stg) + lane;
-                uint16_t* out = p.y + ((int64_t)u.row0 + c0 + (lane >> 2)) * p.Hp + n0 + (lane & 3) * 8;
-                const int left = u.rows - c0 - (lane >> 2);
+                quad_sync(1 + second);   // the run is staged
+                const int row = quarter * 8 + (lane >> 4), n = n0 + (lane & 15) * 8;
+                const uint4* piece = reinterpret_cast<const uint4*>(stg) + quarter * 128 + lane;
+                uint16_t* out = p.y + ((int64_t)u.row0 + c0 + row) * p.Hp + n;
+                const int left = n < p.Hp ? u.rows - c0 - row : 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (8 * j < left) *reinterpret_cast<uint4*>(out + (int64_t)(8 * j) * p.Hp) = piece[32 * j];
-                __syncwarp();   // the next run is staged in the same place
+                    if (2 * j < left) *reinterpret_cast<uint4*>(out + (int64_t)(2 * j) * p.Hp) = piece[32 * j];
             }
             if (held) {
                 tc_fence_before();
@@ -693,7 +716,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
 }
 
 constexpr size_t kMxSmem =
-    1024 + (size_t)kMxStages * kMxStageBytes + kMxEpiWarps * kMxOut + (2 * kMxStages + 5) * 8 + 16;
+    1024 + (size_t)kMxStages * kMxStageBytes + kMxEpiWarps / 4 * kMxOut + (2 * kMxStages + 5) * 8 + 16;
 
 // Scale blocks as rows of 128 words, 2 rows a box.
 bool encode_scales(CUtensorMap* m, const void* base, uint64_t blocks) {
