@@ -73,6 +73,8 @@ class _RouteConfig(ctypes.Structure):
 def load(path: str = LIB_PATH):
     """Loads libbep.so (raises if it is absent: build it with ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -138,10 +140,16 @@ def _check(rc: int, where: str):
 
 def _stream(stream):
     """Raw handle of `stream`, or of the current device's current stream."""
-    import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        device, current = _current_stream()
+        return current(device())
     return int(stream.cuda_stream)
+
+
+@functools.cache
+def _current_stream():
+    import torch
+    return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _arg(t, dtypes, n, name, optional=False):
@@ -227,6 +235,7 @@ class Context:
         _check(lib.bep_create(ctypes.byref(c), ctypes.byref(h)), "bep_create")
         self.cfg = cfg
         self.handle = h
+        self._tokens, self._rows = cfg.R * cfg.S, cfg.R * cfg.C   # tokens, receive rows
 
     def close(self):
         if self.handle:
@@ -511,8 +520,7 @@ class RouteConfig:
 
 
 def _logits_type(t):
-    import torch
-    return BEP_F32 if t.dtype == torch.float32 else BEP_BF16
+    return BEP_F32 if t.dtype == _logits_dtypes()[0] else BEP_BF16
 
 
 @functools.cache
@@ -524,25 +532,23 @@ def _logits_dtypes():
 def bep_route(ctx: Context, rc: RouteConfig, logits, topk, gates, bias=None, load=None, stream=None):
     """logits [R,S,E] fp32 or bf16 -> topk int32, gates fp32 [R,S,K]; bias fp32 [E] moves the
     choice only; load int32 [E] gets the tokens per expert added."""
-    c = ctx.cfg
-    T = c.R * c.S
+    E = ctx.cfg.E
     # (the module's load() has an argument's name here; the context has loaded the library)
-    _check(_lib.bep_route(ctx.handle, rc._ref, _arg(logits, _logits_dtypes(), T * c.E, "logits"),
-                          _logits_type(logits),
-                          None if bias is None else _arg(bias, _f32(), c.E, "bias"),
-                          _arg(topk, _i32(), T * c.K, "topk"), _arg(gates, _f32(), T * c.K, "gates"),
-                          None if load is None else _arg(load, _i32(), c.E, "load"),
-                          _stream(stream)), "bep_route")
+    _check(_lib.bep_route(ctx.handle, rc._ref,
+                          _arg(logits, _logits_dtypes(), ctx._tokens * E, "logits"),
+                          _logits_type(logits), None if bias is None else _arg(bias, _f32(), E, "bias"),
+                          _arg(topk, _i32(), ctx._rows, "topk"), _arg(gates, _f32(), ctx._rows, "gates"),
+                          None if load is None else _arg(load, _i32(), E, "load"), _stream(stream)),
+           "bep_route")
 
 
 def bep_route_bwd(ctx: Context, rc: RouteConfig, logits, topk, dgates, dlogits, stream=None):
     """dlogits [R,S,E] (of the logits' type) from the gates' gradients [R,S,K]."""
-    c = ctx.cfg
-    T = c.R * c.S
-    _check(load().bep_route_bwd(ctx.handle, rc._ref, _arg(logits, _logits_dtypes(), T * c.E, "logits"),
-                                _logits_type(logits), _arg(topk, _i32(), T * c.K, "topk"),
-                                _arg(dgates, _f32(), T * c.K, "dgates"),
-                                _arg(dlogits, (logits.dtype,), T * c.E, "dlogits"), _stream(stream)),
+    n = ctx._tokens * ctx.cfg.E
+    _check(load().bep_route_bwd(ctx.handle, rc._ref, _arg(logits, _logits_dtypes(), n, "logits"),
+                                _logits_type(logits), _arg(topk, _i32(), ctx._rows, "topk"),
+                                _arg(dgates, _f32(), ctx._rows, "dgates"),
+                                _arg(dlogits, (logits.dtype,), n, "dlogits"), _stream(stream)),
            "bep_route_bwd")
 
 
@@ -570,7 +576,7 @@ class ActCheckpoint:
 def bep_swiglu(ctx: Context, h, a, codes=None, scales=None, stream=None):
     """a = g * sigmoid(g) * u for h = [g | u]; codes and scales receive h's 8-bit checkpoint."""
     F = int(a.shape[-1])
-    n = ctx.cfg.R * ctx.cfg.C * F
+    n = ctx._rows * F
     _check(load().bep_swiglu(ctx.handle, _arg(h, _bf16(), 2 * n, "h"), F, _arg(a, _bf16(), n, "a"),
                              None if codes is None else _arg(codes, _i8(), 2 * n, "codes"),
                              None if scales is None else _arg(scales, _u8(), n // 16, "scales"),
@@ -580,7 +586,7 @@ def bep_swiglu(ctx: Context, h, a, codes=None, scales=None, stream=None):
 def bep_swiglu_bwd(ctx: Context, da, codes, scales, dh, a=None, stream=None):
     """dh [rows, 2F] from da [rows, F] and the checkpoint; a receives the activation again."""
     F = int(da.shape[-1])
-    n = ctx.cfg.R * ctx.cfg.C * F
+    n = ctx._rows * F
     _check(load().bep_swiglu_bwd(ctx.handle, _arg(da, _bf16(), n, "da"), F,
                                  _arg(codes, _i8(), 2 * n, "codes"),
                                  _arg(scales, _u8(), n // 16, "scales"), _arg(dh, _bf16(), 2 * n, "dh"),
@@ -620,9 +626,9 @@ def _mx_weight(c, codes, scales, prefix=""):
                  prefix + "scales"))
 
 
-def _mx_rows(c, F, codes, scales):
-    return (_arg(codes, _u8(), c.R * c.C * F // 2, "codes"),
-            _arg(scales, _u8(), c.R * c.C * mx_scale_pitch(F), "scales"))
+def _mx_rows(rows, F, codes, scales):
+    return (_arg(codes, _u8(), rows * F // 2, "codes"),
+            _arg(scales, _u8(), rows * mx_scale_pitch(F), "scales"))
 
 
 def bep_mx_quantize_weight(ctx: Context, w, codes, scales, stream=None):
@@ -636,18 +642,18 @@ def bep_mx_quantize_weight(ctx: Context, w, codes, scales, stream=None):
 def bep_dispatch_mx(ctx: Context, x, dest, codes, scales, stream=None):
     """Quantises every token to 4 bits and writes it to its K receive rows (an MxRows)."""
     c = ctx.cfg
-    _check(load().bep_dispatch_mx(ctx.handle, _arg(x, _bf16(), c.R * c.S * c.H, "x"),
-                                  _arg(dest, _i32(), c.R * c.C, "dest"),
-                                  *_mx_rows(c, c.H, codes, scales), _stream(stream)),
+    _check(load().bep_dispatch_mx(ctx.handle, _arg(x, _bf16(), ctx._tokens * c.H, "x"),
+                                  _arg(dest, _i32(), ctx._rows, "dest"),
+                                  *_mx_rows(ctx._rows, c.H, codes, scales), _stream(stream)),
            "bep_dispatch_mx")
 
 
 def bep_swiglu_mx(ctx: Context, h, codes, scales, stream=None):
     """The gated activation of h [rows, 2F] in 4 bits (an MxRows of F elements)."""
-    c = ctx.cfg
     F = int(h.shape[-1]) // 2
-    _check(load().bep_swiglu_mx(ctx.handle, _arg(h, _bf16(), c.R * c.C * 2 * F, "h"), F,
-                                *_mx_rows(c, F, codes, scales), _stream(stream)), "bep_swiglu_mx")
+    _check(load().bep_swiglu_mx(ctx.handle, _arg(h, _bf16(), ctx._rows * 2 * F, "h"), F,
+                                *_mx_rows(ctx._rows, F, codes, scales), _stream(stream)),
+           "bep_swiglu_mx")
 
 
 def bep_grouped_gemm_mx(ctx: Context, cu_seqlens, slot_expert, codes, scales, w_codes, w_scales, y,
@@ -657,9 +663,9 @@ def bep_grouped_gemm_mx(ctx: Context, cu_seqlens, slot_expert, codes, scales, w_
     _check(load().bep_grouped_gemm_mx(ctx.handle,
                                       _arg(cu_seqlens, _i32(), c.R * (c.E + c.B + 1), "cu_seqlens"),
                                       _arg(slot_expert, _i32(), c.R * c.B, "slot_expert"),
-                                      *_mx_rows(c, c.H, codes, scales),
+                                      *_mx_rows(ctx._rows, c.H, codes, scales),
                                       *_mx_weight(c, w_codes, w_scales, "w_"),
-                                      _arg(y, _bf16(), c.R * c.C * c.Hp, "y"), _stream(stream)),
+                                      _arg(y, _bf16(), ctx._rows * c.Hp, "y"), _stream(stream)),
            "bep_grouped_gemm_mx")
 
 
