@@ -167,6 +167,10 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 // Launches overlap: the kernel that writes the rows lets the work list's kernel start at once (it
 // reads neither rows nor scales, and nothing that kernel writes), and that one lets this kernel
 // set up its barriers and TMEM; both wait for their predecessor's end before what depends on it.
+// A polling warp takes issue slots from the warps that issue MMAs and scales, and a held one wakes
+// late: the producer and the epilogue, which have time, are held in their waits, the MMA and scale
+// warps poll (all polling 2.67 ms at 524,288 rows of 7168 by 2048 and 220 us at 96 of 1024 by 7168,
+// all held 2.81 ms and 213 us, so divided 2.56-2.65 ms and 198 us).
 //   barrier    owner   arrivals
 //   full[s]    CTA 0   CTA 0's producer (expect_tx) + both CTAs' TMA bytes
 //   empty[s]   both    the MMA thread's multicast commit
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //   tempty[a]  CTA 0   the 8 epilogue warps of each CTA
 constexpr int kMxRows = 224;                   // rows of a tile at most
 constexpr int kMxEpiWarps = 8;                 // two for each quarter of TMEM's lanes
-constexpr int kMxThreads = 32 * (4 + kMxEpiWarps);
+constexpr int kMxThreads = 32 * (4 + kMxEpiWarps);   // producer, MMA, two scale warps, epilogue
 constexpr int kMxStages = 6;
 constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
 constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
@@ -188,6 +192,11 @@ constexpr int kMxSfBase = 2 * kMxRows;         // two accumulators lie before
 constexpr int kMxSfCols = 24;                  // TMEM columns of a stage's scales: A 2 x 4, B 2 x 8
 constexpr int kMxSlots = (kMxTmemCols - kMxSfBase) / kMxSfCols;   // 5
 static_assert(kMxSlots >= 2 && kMxSlots <= kMxStages, "a slot is free once its stage is");
+// A parity wait tells two neighbouring phases apart, no more. A scale warp fills two stages of every
+// 2 kMxScaleWarps, and to fill them it had to see the ring's previous round; with at most a ring
+// between its turns, the phase it waits for next is at most one ahead of the barrier's.
+constexpr int kMxScaleWarps = 2;
+static_assert(2 * kMxScaleWarps <= kMxStages, "a scale warp's turns lie at most one ring apart");
 
 struct MxParams {
     const MTile* tiles;
@@ -232,16 +241,23 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_
         : "memory");
 }
 
-// Shared-memory descriptor of a 512-byte scale block: 32 rows of 16 bytes, no swizzle, groups
-// of 8 rows 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
+// Descriptors reach the instructions as a low word (address in 16-byte units; operands: leading
+// offset 1) beside a constant high word. Operands: 8-row groups 1024 bytes apart, version 1, 128-byte
+// swizzle. Scales: 32 rows of 16 bytes, groups of 8 rows 128 bytes apart, version 1, no swizzle.
+#define BEP_MX_OPERAND_HI "0x40004040"
+#define BEP_MX_SCALES_HI "0x00004008"
+__device__ __forceinline__ uint32_t operand_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t scales_lo(uint32_t saddr) { return (saddr >> 4) & 0x3FFFu; }
+
 // In each CTA of the pair: 32 rows x 16 bytes of scales from its shared memory to 4 columns of
 // its TMEM, in each of the four 32-lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t lo) {
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\t"
+        "mov.b64 d, {%1, " BEP_MX_SCALES_HI "};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+        "r"(lo)
+        : "memory");
 }
 
 // Instruction descriptor, kind::mxf4, M = 256: e2m1 operands (1 at bits 7 and 10), N >> 3 at bit
@@ -252,16 +268,30 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf) {
            (sf << 29);
 }
 
-__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-            "r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+// kAdd: adds to the accumulator; otherwise when `add` is not 0.
+template <bool kAdd>
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t add = 1) {
+    if (kAdd)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, " BEP_MX_OPERAND_HI "};\n\t"
+            "mov.b64 db, {%2, " BEP_MX_OPERAND_HI "};\n\t"
+            "setp.eq.u32 p, 0, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem),
+            "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, " BEP_MX_OPERAND_HI "};\n\t"
+            "mov.b64 db, {%2, " BEP_MX_OPERAND_HI "};\n\t"
+            "setp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::
+                "r"(d_tmem),
+            "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(add)
+            : "memory");
 }
 
 // Named barriers of four epilogue warps.
@@ -455,7 +485,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                 const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : kMxRows / 2;
                 const int mt = 2 * u.mp + (int)rank;   // past H' for the last odd tile: zeros
                 for (int k = 0; k < nst; ++k) {
-                    if (!mbar_wait(&empty[pr_s], pr_ph ^ 1u, s_abort, status)) {
+                    if (!mbar_wait_held(&empty[pr_s], pr_ph ^ 1u, s_abort, status)) {
                         live = false;
                         break;
                     }
@@ -474,8 +504,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     } else if (warp == 1) {
         if (lead) {
             // the whole warp runs the loops, so that descriptors stay in uniform registers
-            const uint64_t da = sdesc_sw128(smem_u32(smA), 16, 1024), db = sdesc_sw128(smem_u32(smB), 16, 1024);
-            const uint64_t dsa = sdesc_scales(smem_u32(smSA)), dsb = sdesc_scales(smem_u32(smSB));
+            const uint32_t da = operand_lo(smem_u32(smA)), db = operand_lo(smem_u32(smB));
+            const uint32_t dsa = scales_lo(smem_u32(smSA)), dsb = scales_lo(smem_u32(smSB));
             uint32_t s = 0, ph = 0;                    // ring stage
             uint32_t slot = 0;                         // TMEM scale columns
             uint32_t old = 0, old_ph = 0, done = 0;    // the stage that used the slot before
@@ -488,7 +518,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
                 const int acc = it & 1;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)))
+                if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)))
                     break;
                 ++it;
                 const uint32_t dt = tmem_base + acc * kMxRows;
@@ -507,28 +537,28 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     } else {
                         ++done;
                     }
-                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, s_abort, status))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, s_abort, status))) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
                     // descriptors count 16-byte units: a K step is 2 of them, a scale block 32
-                    const uint64_t a = da + s * (kMxA / 16), b = db + s * (kMxB / 16);
-                    const uint64_t sa = dsa + s * (kMxSfa / 16), sb = dsb + s * (kMxSfb / 16);
+                    const uint32_t a = da + s * (kMxA / 16), b = db + s * (kMxB / 16);
+                    const uint32_t sa = dsa + s * (kMxSfa / 16), sb = dsb + s * (kMxSfb / 16);
                     const uint32_t ta = tmem_base + kMxSfBase + slot * kMxSfCols, tb = ta + 8;
                     const int steps = min(4, (p.H - k * kMxK) / 64);
                     if (elect_one()) {
                         copy_scales(ta, sa);
                         copy_scales(tb, sb);
                         if (N > 128) copy_scales(tb + 4, sb + 32);
-                        mma_mxf4(dt, a, b, id0, ta, tb, k != 0);
-                        if (steps > 1) mma_mxf4(dt, a + 2, b + 2, id2, ta, tb, 1);
+                        mma_mxf4<false>(dt, a, b, id0, ta, tb, k != 0);
+                        if (steps > 1) mma_mxf4<true>(dt, a + 2, b + 2, id2, ta, tb);
                         if (steps > 2) {
                             copy_scales(ta + 4, sa + 32);
                             copy_scales(tb + 8, sb + 64);
                             if (N > 128) copy_scales(tb + 12, sb + 96);
-                            mma_mxf4(dt, a + 4, b + 4, id0, ta + 4, tb + 8, 1);
-                            if (steps > 3) mma_mxf4(dt, a + 6, b + 6, id2, ta + 4, tb + 8, 1);
+                            mma_mxf4<true>(dt, a + 4, b + 4, id0, ta + 4, tb + 8);
+                            if (steps > 3) mma_mxf4<true>(dt, a + 6, b + 6, id2, ta + 4, tb + 8);
                         }
                         mma_commit_pair(&empty[s]);
                         if (k == nst - 1) mma_commit_pair(&tfull[acc]);
@@ -542,11 +572,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                 }
             }
         }
-    } else if (warp < 4) {
+    } else if (warp < 2 + kMxScaleWarps) {
         // A 16-byte piece of a row's scales serves two stages; the two warps take the pieces in turn,
         // across units. Loads run two of a warp's own pieces ahead of the stores, across units, so that
         // their latency is hidden at four stages a unit as well.
         constexpr int kC = kMxRows / 32;
+        static_assert(kC == 7, "four words of the first 128 rows and three of the rest");
         const int mine = warp - 2;
         const int pieces = (nst + 1) / 2;
         const uint4* src[kC] = {};
@@ -569,7 +600,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
 #pragma unroll
             for (int c = 0; c < kC; ++c)
                 if (32 * c < l_rows) v[c] = __ldg(src[c] + l_piece);
-            l_piece += 2;
+            l_piece += kMxScaleWarps;
         };
         uint4 v0[kC] = {}, v1[kC] = {};
         load(v0);
@@ -594,7 +625,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     }
                     continue;
                 }
-                own += 2;
+                own += kMxScaleWarps;
                 uint4 v[kC];
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
@@ -607,13 +638,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                         live = false;
                         break;
                     }
-                    uint32_t* d = reinterpret_cast<uint32_t*>(smSB + s * kMxSfb) + lane * 4;
-#pragma unroll
-                    for (int c = 0; c < kC; ++c)
-                        if (32 * c < N) {
-                            d[(c >> 2) * 128 + (c & 3)] = half ? v[c].z : v[c].x;
-                            d[256 + (c >> 2) * 128 + (c & 3)] = half ? v[c].w : v[c].y;
-                        }
+                    // row 32 c + lane of an atom's 128: word c of the lane's 16 bytes
+                    uint4* d = reinterpret_cast<uint4*>(smSB + s * kMxSfb) + lane;
+                    d[0] = half ? make_uint4(v[0].z, v[1].z, v[2].z, v[3].z) : make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+                    d[64] = half ? make_uint4(v[0].w, v[1].w, v[2].w, v[3].w) : make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+                    if (N > 128) {
+                        d[32] = half ? make_uint4(v[4].z, v[5].z, v[6].z, 0) : make_uint4(v[4].x, v[5].x, v[6].x, 0);
+                        d[96] = half ? make_uint4(v[4].w, v[5].w, v[6].w, 0) : make_uint4(v[4].y, v[5].y, v[6].y, 0);
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0)
@@ -642,8 +674,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             next = mx_first(p, unit + ncl, total, MP);
             if (u.expert < 0) continue;
             const int acc = it & 1;
-            // the four give up together, so that none waits for another at their barrier
-            if (!quad_all(1 + second, mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, status))) break;
+            // one warp waits for the accumulator and the others for it at their barrier, which costs the
+            // busy warps no issue slots; the four give up together, so that none waits for another there
+            const bool ready = quarter != 0 || mbar_wait_held(&tfull[acc], (it >> 1) & 1, s_abort, status);
+            if (!quad_all(1 + second, ready)) break;
             ++it;
             tc_fence_after();
             // lane l of quarter q holds output n = 128 mt + 32 q + l, its columns the rows

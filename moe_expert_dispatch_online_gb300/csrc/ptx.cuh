@@ -87,6 +87,36 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// The same bounded wait for kernels whose roles share schedulers with busy warps: the hardware may
+// hold the thread for up to kHoldNs at a time instead of letting it poll, so a waiting warp takes
+// no issue slots. The abort flag and the limit are looked at between holds.
+constexpr uint32_t kHoldNs = 50000;
+__device__ __forceinline__ bool mbar_wait_held(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               int32_t* status) {
+    auto held = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
+            : "memory");
+        return ok != 0;
+    };
+    if (held()) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (held()) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > kTimeoutNs) {
+            *abort_flag = 1;
+            set_status(status, BEP_DERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // After a bounded wait gave up: wait, again with a limit, for a phase this
 // thread knows it started (TMA bytes it armed, MMAs it committed), ignoring
 // the abort flag. Used only on the abort path, so that the kernel frees TMEM
