@@ -167,10 +167,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 // Launches overlap: the kernel that writes the rows lets the work list's kernel start at once (it
 // reads neither rows nor scales, and nothing that kernel writes), and that one lets this kernel
 // set up its barriers and TMEM; both wait for their predecessor's end before what depends on it.
-// A polling warp takes issue slots from the warps that issue MMAs and scales, and a held one wakes
-// late: the producer and the epilogue, which have time, are held in their waits, the MMA and scale
-// warps poll (all polling 2.67 ms at 524,288 rows of 7168 by 2048 and 220 us at 96 of 1024 by 7168,
-// all held 2.81 ms and 213 us, so divided 2.56-2.65 ms and 198 us).
+// A polling warp takes issue slots from the warps that issue MMAs and scales, so every role but the
+// scale warps is held in its waits by the hardware, and one of four epilogue warps waits for all four
+// (96 rows by 384 experts' 1024 x 7168: 195 us, 220 us with every warp polling).
 //   barrier    owner   arrivals
 //   full[s]    CTA 0   CTA 0's producer (expect_tx) + both CTAs' TMA bytes
 //   empty[s]   both    the MMA thread's multicast commit
@@ -179,7 +178,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 constexpr int kMxRows = 224;                   // rows of a tile at most
 constexpr int kMxEpiWarps = 8;                 // two for each quarter of TMEM's lanes
 constexpr int kMxThreads = 32 * (4 + kMxEpiWarps);   // producer, MMA, two scale warps, epilogue
-constexpr int kMxStages = 6;
+// Five stages: 2.42 ms at 524,288 rows by 7168 x 2048 and 76.5 us at 64, 2.54 ms and 75.1 us with six,
+// 2.64 ms and 81 us with four.
+constexpr int kMxStages = 5;
 constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
 constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes
 constexpr int kMxB = kMxRows / 2 * 128;        // bytes: half of the rows
@@ -502,8 +503,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             }
         }
     } else if (warp == 1) {
-        if (lead) {
-            // the whole warp runs the loops, so that descriptors stay in uniform registers
+        if (lead && elect_one()) {
+            // one thread, known to the compiler as one (524,288 rows by 7168 x 2048: 2.50 ms; with the
+            // whole warp in the waits and one lane at the instructions 2.56-2.68 ms)
             const uint32_t da = operand_lo(smem_u32(smA)), db = operand_lo(smem_u32(smB));
             const uint32_t dsa = scales_lo(smem_u32(smSA)), dsb = scales_lo(smem_u32(smSB));
             uint32_t s = 0, ph = 0;                    // ring stage
@@ -518,15 +520,14 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
                 const int acc = it & 1;
-                if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)))
-                    break;
+                if (!mbar_wait_held(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)) break;
                 ++it;
                 const uint32_t dt = tmem_base + acc * kMxRows;
                 const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
                 for (int k = 0; k < nst; ++k) {
                     // a slot's scales are overwritten once the MMAs that read them have completed
                     if (done >= (uint32_t)kMxSlots) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(&empty[old], old_ph, s_abort, status))) {
+                        if (!mbar_wait_held(&empty[old], old_ph, s_abort, status)) {
                             live = false;
                             break;
                         }
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     } else {
                         ++done;
                     }
-                    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, s_abort, status))) {
+                    if (!mbar_wait_held(&full[s], ph, s_abort, status)) {
                         live = false;
                         break;
                     }
@@ -547,23 +548,20 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     const uint32_t sa = dsa + s * (kMxSfa / 16), sb = dsb + s * (kMxSfb / 16);
                     const uint32_t ta = tmem_base + kMxSfBase + slot * kMxSfCols, tb = ta + 8;
                     const int steps = min(4, (p.H - k * kMxK) / 64);
-                    if (elect_one()) {
-                        copy_scales(ta, sa);
-                        copy_scales(tb, sb);
-                        if (N > 128) copy_scales(tb + 4, sb + 32);
-                        mma_mxf4<false>(dt, a, b, id0, ta, tb, k != 0);
-                        if (steps > 1) mma_mxf4<true>(dt, a + 2, b + 2, id2, ta, tb);
-                        if (steps > 2) {
-                            copy_scales(ta + 4, sa + 32);
-                            copy_scales(tb + 8, sb + 64);
-                            if (N > 128) copy_scales(tb + 12, sb + 96);
-                            mma_mxf4<true>(dt, a + 4, b + 4, id0, ta + 4, tb + 8);
-                            if (steps > 3) mma_mxf4<true>(dt, a + 6, b + 6, id2, ta + 4, tb + 8);
-                        }
-                        mma_commit_pair(&empty[s]);
-                        if (k == nst - 1) mma_commit_pair(&tfull[acc]);
+                    copy_scales(ta, sa);
+                    copy_scales(tb, sb);
+                    if (N > 128) copy_scales(tb + 4, sb + 32);
+                    mma_mxf4<false>(dt, a, b, id0, ta, tb, k != 0);
+                    if (steps > 1) mma_mxf4<true>(dt, a + 2, b + 2, id2, ta, tb);
+                    if (steps > 2) {
+                        copy_scales(ta + 4, sa + 32);
+                        copy_scales(tb + 8, sb + 64);
+                        if (N > 128) copy_scales(tb + 12, sb + 96);
+                        mma_mxf4<true>(dt, a + 4, b + 4, id0, ta + 4, tb + 8);
+                        if (steps > 3) mma_mxf4<true>(dt, a + 6, b + 6, id2, ta + 4, tb + 8);
                     }
-                    __syncwarp();
+                    mma_commit_pair(&empty[s]);
+                    if (k == nst - 1) mma_commit_pair(&tfull[acc]);
                     if (++s == kMxStages) {
                         s = 0;
                         ph ^= 1u;
@@ -693,7 +691,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     if (lane == 0) mbar_arrive_rank_relaxed(&tempty[acc], 0);
                     held = false;
                 }
-                quad_sync(1 + second);   // the run before has been read
+                quad_sync(1 + second);   // the run before has been read (two buffers measured 3% slower)
                 uint16_t* col = reinterpret_cast<uint16_t*>(stg) + quarter * 32 + lane;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
