@@ -150,13 +150,16 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 }
 
 // ------------------------------------------------------------------------ product
-// The weights are the M operand and the rows of one segment the N operand (32..192), so that a
+// The weights are the M operand and the rows of one segment the N operand (32..224), so that a
 // segment of a few rows costs a narrow MMA and not a 128-row one. A cluster of two CTAs shares a
 // tile of 256 outputs x N rows (cta_group::2): CTA r holds outputs 128 r.. and half of the rows,
-// so that a stage brings 33 KB to each SM for what takes one CTA 47 KB. At 4 bits an SM's shared
-// memory bounds a tile, not the tensor core: per stage of 224 rows 33 KB arrive and the MMAs read
-// 44 KB, 600 cycles at 128 bytes a cycle for 390 of MMAs. 524,288 rows by 7168 x 2048: 4.97 ms with
-// one CTA and N <= 128, 2.92 with pairs and N <= 192, 2.71 with N <= 224 (5.7 PFLOP/s).
+// so that a stage brings 33 KB to each SM for what takes one CTA 47 KB. Few rows: the weights'
+// HBM stream bounds it (96 rows by 384 experts' 1024 x 7168, 1.30 GB: 195 us, 99% of the copy rate).
+// Many rows: a stage of 224 rows takes the tensor pipe 390 cycles for its MMAs and about 120 for the
+// six scale copies, which share the pipe, and the stage's bytes about as long to arrive in shared
+// memory that the MMAs are reading; the two overlap to about 600 cycles. 524,288 rows by 7168 x 2048:
+// 4.97 ms with one CTA and N <= 128, 2.92 with pairs and N <= 192, 2.67 with N <= 224, 2.42-2.57 now
+// (6.0-6.4 PFLOP/s).
 //   warp 0     TMA: codes of 128 outputs and of N/2 rows; 256 reduction steps a stage
 //   warp 1     (CTA 0) copies each stage's scales to both TMEMs, issues tcgen05.mma.kind::mxf4
 //   warps 2, 3 put all N rows' scales (any row offset, so no TMA) in tensor-core order, make them
@@ -191,7 +194,7 @@ constexpr int kMxStageBytes = kMxA + kMxB + kMxSfa + kMxSfb;
 constexpr int kMxTmemCols = 512;
 constexpr int kMxSfBase = 2 * kMxRows;         // two accumulators lie before
 constexpr int kMxSfCols = 24;                  // TMEM columns of a stage's scales: A 2 x 4, B 2 x 8
-constexpr int kMxSlots = (kMxTmemCols - kMxSfBase) / kMxSfCols;   // 5
+constexpr int kMxSlots = (kMxTmemCols - kMxSfBase) / kMxSfCols;   // 2
 static_assert(kMxSlots >= 2 && kMxSlots <= kMxStages, "a slot is free once its stage is");
 // A parity wait tells two neighbouring phases apart, no more. A scale warp fills two stages of every
 // 2 kMxScaleWarps, and to fill them it had to see the ring's previous round; with at most a ring

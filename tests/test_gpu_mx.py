@@ -328,3 +328,53 @@ def test_another_stream_no_rows_and_refusals(lib):
     bep.bep_grouped_gemm_mx(ctx, cu, t["se"], e, e, w.codes, w.scales, y[0][:0])
     assert bep.bep_status(ctx) == 0
     ctx.close()
+
+
+@pytest.mark.parametrize("R,S,E,K,H,Hp", [(8, 61, 24, 4, 7168, 256), (2, 900, 4, 2, 256, 1344), (1, 2000, 3, 1, 512, 192)])
+def test_calls_in_a_row_give_the_same_bits(lib, R, S, E, K, H, Hp):
+    """Dispatch and product queued many times without a wait between them: launches overlap, rings and
+    accumulators wrap, and rows are rewritten while the call before has just ended."""
+    bep = lib
+    ctx, t = planned(bep, R, S, E, K, H, Hp, None, seed=5, skew=1.0)
+    _, w = weights(bep, ctx)
+    x = [torch.randn(R, S, H, device=DEV).bfloat16() for _ in range(2)]
+    rows = bep.MxRows(R * S * K, H)
+    y = [torch.empty(R * S * K, Hp, dtype=torch.bfloat16, device=DEV) for _ in range(12)]
+    for i, out in enumerate(y):
+        bep.bep_dispatch_mx(ctx, x[i % 2], t["dest"], rows.codes, rows.scales)
+        bep.bep_grouped_gemm_mx(ctx, t["cu"], t["se"], rows.codes, rows.scales, w.codes, w.scales, out)
+    assert bep.bep_status(ctx) == 0
+    for i in range(2, 12):
+        assert torch.equal(y[i].view(torch.int16), y[i % 2].view(torch.int16))
+    assert not torch.equal(y[0], y[1])
+    ctx.close()
+
+
+def test_a_graph_and_an_sm_budget_give_the_same_bits(lib):
+    bep = lib
+    ctx, t = planned(bep, 4, 300, 16, 3, 576, 320, None, skew=1.0)
+    _, w = weights(bep, ctx)
+    x = torch.randn(4, 300, 576, device=DEV).bfloat16()
+    rows, y = bep.MxRows(3600, 576), torch.empty(3600, 320, dtype=torch.bfloat16, device=DEV)
+
+    def step():
+        bep.bep_dispatch_mx(ctx, x, t["dest"], rows.codes, rows.scales)
+        bep.bep_grouped_gemm_mx(ctx, t["cu"], t["se"], rows.codes, rows.scales, w.codes, w.scales, y)
+
+    step()
+    torch.cuda.synchronize()
+    want = y.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+        step()
+    y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    bep.bep_set_comm_sms(ctx, 3)
+    y.zero_()
+    step()
+    assert bep.bep_status(ctx) == 0
+    assert torch.equal(y, want)
+    ctx.close()
