@@ -178,15 +178,18 @@ struct Packed {
 };
 
 // The K experts of the largest keys, lane k for the k-th. kAny: every key is an expert's.
-// exact: the words hold whole keys.
+// exact: the words hold whole keys. raw: the keys are the floats' own bits, in order only from +0
+// on, which is decided as long as K + 1 keys are not negative (two integer instructions an expert
+// fewer than keys in order throughout).
 template <int V, bool kAny>
-__device__ __forceinline__ int choose_packed(const uint32_t (&key)[V], int K, int lane, bool exact,
+__device__ __forceinline__ int choose_packed(const uint32_t (&key)[V], int K, int lane, bool exact, bool raw,
                                              bool* decided) {
     constexpr uint32_t kIndex = Packed<V>::kIndex;
+    const uint32_t c = (kIndex - lane) + (raw ? 0x80000000u : 0u);
     uint32_t t1 = 0, t2 = 0, t3 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        uint32_t w = (key[i] & ~kIndex) | (kIndex - 32 * i - lane);
+        uint32_t w = (key[i] & ~kIndex) ^ (c - 32 * i);
         if (!kAny && key[i] == kGone) w = 0;
         if (V > 2) t3 = max(t3, min(t2, w));
         t2 = max(t2, min(t1, w));
@@ -208,7 +211,7 @@ __device__ __forceinline__ int choose_packed(const uint32_t (&key)[V], int K, in
     uint32_t after = __shfl_down_sync(kAll, mine, 1);   // every lane takes part
     if (lane == K - 1) after = next;
     const bool near = !exact && lane < K && (mine ^ after) <= kIndex;
-    *decided = !__any_sync(kAll, spent || near);
+    *decided = !__any_sync(kAll, spent || near) && (!raw || next >= 0x80000000u);
     return (int)(kIndex - (mine & kIndex));
 }
 
@@ -288,15 +291,21 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
             inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = ordered(by_score ? fmaf(ex[i], inv, s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)])
-                                          : x[i]);
+                key[i] = by_score ? __float_as_uint(fmaf(ex[i], inv, s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]))
+                                  : __float_as_uint(x[i]);
         } else if (by_score) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = ordered(__fadd_rn(fast_sigmoid(x[i]), s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
+                key[i] = __float_as_uint(
+                    __fadd_rn(fast_sigmoid(x[i]), s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = ordered(x[i]);
+            for (int i = 0; i < V; ++i) key[i] = __float_as_uint(x[i]);
+        }
+        const bool raw = kFull && !kGroups && by_score && ordinary;   // a score with a bias: never -0
+        if (!raw) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = ordered(__uint_as_float(key[i]));
         }
         if (!ordinary) {
 #pragma unroll
@@ -353,8 +362,14 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
                 if (kFull || lane + 32 * i < p.E) key[i] = s_key[lane + 32 * i];
         }
         bool decided;
-        int mine = choose_packed<V, kFull && !kGroups>(key, p.K, lane, sizeof(T) == 2 && !by_score, &decided);
-        if (!decided) mine = choose_whole(key, p.K, lane);
+        int mine = choose_packed<V, kFull && !kGroups>(key, p.K, lane, sizeof(T) == 2 && !by_score, raw, &decided);
+        if (!decided) {
+            if (raw) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) key[i] = ordered(__uint_as_float(key[i]));
+            }
+            mine = choose_whole(key, p.K, lane);
+        }
         // gates of the chosen experts, lane k for the k-th
         float xs = -INFINITY;
         if (lane < p.K) {

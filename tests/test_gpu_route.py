@@ -248,3 +248,36 @@ def test_refusals(lib):
         bep.bep_route_bwd(ctx, rc, lg, topk, g, lg)
     assert bep.bep_status(ctx) == 0
     ctx.close()
+
+
+@pytest.mark.parametrize("E,K", [(64, 4), (384, 8), (90, 3)])
+def test_negative_and_mixed_keys(lib, E, K):
+    """Biases that leave no key, a few, or K keys positive."""
+    bep = lib
+    S = 40
+    for softmax in (True, False):
+        for shift in (-2.0, -0.5, -0.02, 0.0):
+            for seed in range(20):
+                rng = np.random.default_rng([E, seed, int(-100 * shift)])
+                x = draw_logits(rng, S, E, False)
+                bias = np.float32(rng.normal(size=E) * 0.05 + shift).astype(np.float64)
+                want, gap = ref.choose(x, K, softmax, bias, 1, 1, 1, ref.LOWEST["f32"])
+                if gap > 4e-6:
+                    break
+            else:
+                pytest.fail("no inputs without a near tie")
+            ctx = context(bep, 1, S, E, K)
+            rc = bep.RouteConfig(bep.BEP_SCORE_SOFTMAX if softmax else bep.BEP_SCORE_SIGMOID)
+            _, topk, g = routed(bep, ctx, rc, x, False, bias)
+            assert bep.bep_status(ctx) == 0
+            assert np.array_equal(topk.cpu().numpy()[0], want)
+            assert np.all(np.abs(g.cpu().numpy()[0] - ref.gates(x, want, softmax, True, 1.0, ref.LOWEST["f32"]))
+                          <= score_tol(E, K))
+            ctx.close()
+    # equal keys, positive and negative, across lanes and registers: the lowest experts
+    for shift in (-3.0, 3.0):
+        ctx = context(bep, 1, 1, E, K)
+        _, topk, _ = routed(bep, ctx, bep.RouteConfig(bep.BEP_SCORE_SIGMOID), np.zeros((1, E)), False,
+                            np.full(E, shift))
+        assert topk.cpu().tolist()[0][0] == list(range(K))
+        ctx.close()
