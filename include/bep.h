@@ -295,7 +295,7 @@ int bep_reduce_grad(bep_ctx* ctx, const int32_t* slot_expert, float* g_home, flo
  *     or scale * s_k: the bias moves the choice only;
  *   - load[e] += the number of tokens that chose e, when load is given (the caller
  *     zeroes it; what a balance bias is updated from).
- * Without a bias and with groups scored by one key the order is the logits' own.
+ * Without a bias the order of the kept experts is the logits' own.
  * A logit at its type's lowest finite value or below (-inf) masks the expert: it
  * ranks after all others and its gate is 0. A NaN or +inf logit counts as masked
  * and latches BEP_DERR_NONFINITE, as a NaN key does.

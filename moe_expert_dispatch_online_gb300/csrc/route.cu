@@ -172,7 +172,7 @@ __device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, 
 // now; bound by the integer pipe (about 480 instructions a token, two thirds of them there).
 template <int V>
 struct Packed {
-    static constexpr int kBits = V <= 1 ? 6 : V <= 2 ? 7 : V <= 4 ? 8 : V <= 12 ? 9 : V <= 16 ? 10 : V <= 32 ? 11 : 12;
+    static constexpr int kBits = V <= 1 ? 6 : V <= 3 ? 7 : V <= 7 ? 8 : V <= 15 ? 9 : V <= 16 ? 10 : V <= 32 ? 11 : 12;
     static_assert(32 * V < (1 << kBits), "an index and its complement differ from 0");
     static constexpr uint32_t kIndex = (1u << kBits) - 1;
 };
@@ -323,8 +323,6 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
             for (int i = 0; i < V; ++i)
                 if (lane + 32 * i >= p.E) key[i] = kGone;
         }
-        // the keys hold all the choice needs: the next token's logits arrive while it is made
-        if (tok + step < p.ntok) load_row<V, kFull>(row + step * p.E, p.E, lane, x);
         if (kGroups) {
             // `per` lanes (a power of two) scan each group's keys for its two largest
 #pragma unroll
@@ -360,9 +358,18 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (kFull || lane + 32 * i < p.E) key[i] = s_key[lane + 32 * i];
+            if (by_score && !bias) {
+                // scores were for the groups' sums: without a bias their order is the logits', which
+                // for bf16 logits, often equal, the words below hold whole
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (key[i] > kMasked) key[i] = ordered(x[i]);
+            }
         }
+        // the keys hold all the choice needs: the next token's logits arrive while it is made
+        if (tok + step < p.ntok) load_row<V, kFull>(row + step * p.E, p.E, lane, x);
         bool decided;
-        int mine = choose_packed<V, kFull && !kGroups>(key, p.K, lane, sizeof(T) == 2 && !by_score, raw, &decided);
+        int mine = choose_packed<V, kFull && !kGroups>(key, p.K, lane, sizeof(T) == 2 && !bias, raw, &decided);
         if (!decided) {
             if (raw) {
 #pragma unroll
@@ -520,7 +527,10 @@ template <typename F>
 cudaError_t with_width(int E, F&& fn) {
     if (E <= 32) return fn(std::integral_constant<int, 1>());
     if (E <= 64) return fn(std::integral_constant<int, 2>());
+    if (E <= 96) return fn(std::integral_constant<int, 3>());
     if (E <= 128) return fn(std::integral_constant<int, 4>());
+    if (E <= 160) return fn(std::integral_constant<int, 5>());
+    if (E <= 192) return fn(std::integral_constant<int, 6>());
     if (E <= 256) return fn(std::integral_constant<int, 8>());
     if (E <= 384) return fn(std::integral_constant<int, 12>());
     if (E <= 512) return fn(std::integral_constant<int, 16>());
