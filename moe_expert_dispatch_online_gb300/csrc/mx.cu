@@ -217,24 +217,34 @@ struct MxUnit {
     int row0, rows, expert, mp;
 };
 
-// The unit's tile and expert; expert < 0 for a slot whose expert is unknown (reported, skipped).
-__device__ __forceinline__ MxUnit mx_unit(const MxParams& p, int unit, int MP) {
-    const int t = unit / MP;
-    const MTile tile = p.tiles[t];
-    MxUnit u;
-    u.row0 = tile.row0;
-    u.rows = tile.rows;
-    u.mp = unit - t * MP;
-    u.expert = tile.wsel >= 0 ? tile.wsel : p.slot_expert[-1 - tile.wsel];
-    if (u.expert >= p.E) u.expert = -1;
-    return u;
-}
-
-// The unit at `unit`, or an unused one past the last: read one unit ahead, since a unit may last
-// only a few stages.
-__device__ __forceinline__ MxUnit mx_first(const MxParams& p, int unit, int total, int MP) {
-    return unit < total ? mx_unit(p, unit, MP) : MxUnit{0, 0, -1, 0};
-}
+// A cluster's units lie `ncl` apart in (tile, pair of output tiles) order, the pair fastest: a walk
+// over them without a division, since a unit may last only a few stages.
+struct MxWalk {
+    int unit, tile, mp;        // the next unit
+    int dtile, dmp, MP, ncl;   // its successor
+    __device__ __forceinline__ MxWalk(int first, int ncl_, int MP_)
+        : unit(first), tile(first / MP_), mp(first % MP_), dtile(ncl_ / MP_), dmp(ncl_ % MP_), MP(MP_), ncl(ncl_) {}
+    // The unit's tile and expert; expert < 0 for a slot whose expert is unknown (reported, skipped)
+    // and past the last unit.
+    __device__ __forceinline__ MxUnit take(const MxParams& p, int total) {
+        if (unit >= total) return MxUnit{0, 0, -1, 0};
+        const MTile t = p.tiles[tile];
+        MxUnit u;
+        u.row0 = t.row0;
+        u.rows = t.rows;
+        u.mp = mp;
+        u.expert = t.wsel >= 0 ? t.wsel : p.slot_expert[-1 - t.wsel];
+        if (u.expert >= p.E) u.expert = -1;
+        unit += ncl;
+        tile += dtile;
+        mp += dmp;
+        if (mp >= MP) {
+            mp -= MP;
+            ++tile;
+        }
+        return u;
+    }
+};
 
 __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cl, void* dst, int c0,
                                                  int c1, int c2) {
@@ -476,10 +486,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
-            MxUnit next = mx_first(p, cl0, total, MP);
+            MxWalk walk(cl0, ncl, MP);
+            MxUnit next = walk.take(p, total);   // read a unit ahead
             for (int unit = cl0; unit < total && live; unit += ncl) {
                 const MxUnit u = next;
-                next = mx_first(p, unit + ncl, total, MP);
+                next = walk.take(p, total);
                 if (u.expert < 0) {
                     if (lead) set_status(status, BEP_DERR_BOUNDS);
                     continue;
@@ -516,10 +527,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             uint32_t old = 0, old_ph = 0, done = 0;    // the stage that used the slot before
             int it = 0;
             bool live = true;
-            MxUnit next = mx_first(p, cl0, total, MP);
+            MxWalk walk(cl0, ncl, MP);
+            MxUnit next = walk.take(p, total);   // read a unit ahead
             for (int unit = cl0; unit < total && live; unit += ncl) {
                 const MxUnit u = next;
-                next = mx_first(p, unit + ncl, total, MP);
+                next = walk.take(p, total);
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
                 const int acc = it & 1;
@@ -582,12 +594,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         const int mine = warp - 2;
         const int pieces = (nst + 1) / 2;
         const uint4* src[kC] = {};
-        int l_unit = cl0 - ncl, l_piece = pieces + mine, l_rows = 0;   // the load cursor
+        MxWalk l_walk(cl0, ncl, MP);   // the load cursor: unit, piece and rows
+        int l_piece = pieces + mine, l_rows = 0;
         auto load = [&](uint4* v) {
             while (l_piece >= pieces) {   // the next unit that has a piece for this warp
-                l_unit += ncl;
-                if (l_unit >= total) return;
-                const MxUnit u = mx_unit(p, l_unit, MP);
+                if (l_walk.unit >= total) return;
+                const MxUnit u = l_walk.take(p, total);
                 if (u.expert < 0) continue;
                 l_piece -= pieces;
                 if (l_piece >= pieces) continue;   // all of this unit's are the other warp's
@@ -609,10 +621,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         uint32_t s = 0, ph = 0;
         bool live = true;
         int own = mine;   // this warp's next piece of the unit
-        MxUnit u = mx_first(p, cl0, total, MP);
+        MxWalk walk(cl0, ncl, MP);
+        MxUnit u = walk.take(p, total);
         for (int unit = cl0; unit < total && live; unit += ncl) {
             const MxUnit cur = u;
-            u = mx_first(p, unit + ncl, total, MP);
+            u = walk.take(p, total);
             if (cur.expert < 0) continue;
             const int N = mma_rows(cur.rows);
             const int srow = (cur.expert * p.MT + 2 * cur.mp + (int)rank) * p.KB;
@@ -669,10 +682,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         const int quarter = warp & 3, second = (warp - 4) >> 2;
         uint8_t* stg = smO + second * kMxOut;
         int it = 0;
-        MxUnit next = mx_first(p, cl0, total, MP);
+        MxWalk walk(cl0, ncl, MP);
+        MxUnit next = walk.take(p, total);
         for (int unit = cl0; unit < total; unit += ncl) {
             const MxUnit u = next;
-            next = mx_first(p, unit + ncl, total, MP);
+            next = walk.take(p, total);
             if (u.expert < 0) continue;
             const int acc = it & 1;
             // one warp waits for the accumulator and the others for it at their barrier, which costs the
