@@ -163,9 +163,9 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //   warp 0     TMA: codes of 128 outputs and of N/2 rows; 256 reduction steps a stage
 //   warp 1     (CTA 0) copies each stage's scales to both TMEMs, issues tcgen05.mma.kind::mxf4
 //   warps 2, 3 put all N rows' scales (any row offset, so no TMA) in tensor-core order, make them
-//              visible to the async proxy, and only then start the stage's TMA load of the weight
-//              scales: its bytes on CTA 0's barrier stand for both (a remote arrive per stage in
-//              their place, with its release at cluster scope, cost 1,000 cycles a stage)
+//              visible to the async proxy and arrive on CTA 0's barrier behind a release of shared memory
+//              alone (a release of everything at cluster scope takes about 1,800 cycles a stage: 7.1 ms
+//              at 524,288 rows by 7168 x 2048)
 //   warps 4-11 epilogue: TMEM to bf16 y, while the next unit runs in the other accumulator
 // Launches overlap: the kernel that writes the rows lets the work list's kernel start at once (it
 // reads neither rows nor scales, and nothing that kernel writes), and that one lets this kernel
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 // scale warps is held in its waits by the hardware, and one of four epilogue warps waits for all four
 // (96 rows by 384 experts' 1024 x 7168: 195 us, 220 us with every warp polling).
 //   barrier    owner   arrivals
-//   full[s]    CTA 0   CTA 0's producer (expect_tx) + both CTAs' TMA bytes
+//   full[s]    CTA 0   CTA 0's producer (expect_tx), a scale warp of each CTA + both CTAs' TMA bytes
 //   empty[s]   both    the MMA thread's multicast commit
 //   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
 //   tempty[a]  CTA 0   the 8 epilogue warps of each CTA
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMxStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 3);
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                 const CUtensorMap* tmX = half <= 16 ? &tmX16 : half <= 32 ? &tmX32 : half <= 64 ? &tmX64 : &tmXtop;
                 const int box = half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : kMxRows / 2;
                 const int mt = 2 * u.mp + (int)rank;   // past H' for the last odd tile: zeros
+                const int srow = (u.expert * p.MT + mt) * p.KB;
                 for (int k = 0; k < nst; ++k) {
                     if (!mbar_wait_held(&empty[pr_s], pr_ph ^ 1u, s_abort, status)) {
                         live = false;
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     const uint32_t bar = cluster_addr(&full[pr_s], 0);
                     tma_load_3d_pair(&tmW, bar, smA + pr_s * kMxA, k * 128, mt * 128, u.expert);
                     tma_load_2d_pair(tmX, bar, smB + pr_s * kMxB, k * 128, u.row0 + (int)rank * half);
+                    tma_load_2d_pair(&tmS, bar, smSA + pr_s * kMxSfa, 0, srow + 2 * k);
                     if (++pr_s == kMxStages) {
                         pr_s = 0;
                         pr_ph ^= 1u;
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
                 const int acc = it & 1;
-                if (!mbar_wait_held(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)) break;
+                if (!mbar_wait_held<true>(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, status)) break;
                 ++it;
                 const uint32_t dt = tmem_base + acc * kMxRows;
                 const uint32_t id0 = idesc_mxf4(N, 0), id2 = idesc_mxf4(N, 2);
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     } else {
                         ++done;
                     }
-                    if (!mbar_wait_held(&full[s], ph, s_abort, status)) {
+                    if (!mbar_wait_held<true>(&full[s], ph, s_abort, status)) {
                         live = false;
                         break;
                     }
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             }
 #pragma unroll
             for (int c = 0; c < kC; ++c)
-                if (32 * c < l_rows) v[c] = __ldg(src[c] + l_piece);
+                if (32 * c < l_rows) v[c] = src[c][l_piece];   // written while this kernel was starting: no __ldg
             l_piece += kMxScaleWarps;
         };
         uint4 v0[kC] = {}, v1[kC] = {};
@@ -628,7 +630,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             u = walk.take(p, total);
             if (cur.expert < 0) continue;
             const int N = mma_rows(cur.rows);
-            const int srow = (cur.expert * p.MT + 2 * cur.mp + (int)rank) * p.KB;
             for (int g = 0; g < pieces && live; ++g) {
                 const int here = min(2, nst - 2 * g);   // stages of this piece
                 if (g != own) {
@@ -662,8 +663,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0)
-                        tma_load_2d_pair(&tmS, cluster_addr(&full[s], 0), smSA + s * kMxSfa, 0, srow + 2 * (2 * g + half));
+                    if (lane == 0) mbar_arrive_rank_shared(&full[s], 0);
                     if (++s == kMxStages) {
                         s = 0;
                         ph ^= 1u;

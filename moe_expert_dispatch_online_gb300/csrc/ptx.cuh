@@ -90,18 +90,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // The same bounded wait for kernels whose roles share schedulers with busy warps: the hardware may
 // hold the thread for up to kHoldNs at a time instead of letting it poll, so a waiting warp takes
 // no issue slots. The abort flag and the limit are looked at between holds.
+// kPair: for a barrier that the other CTA of the pair arrives on (mbar_arrive_rank_shared or _relaxed): the
+// wait is at cluster scope, and what either CTA released in its shared memory is visible after it.
 constexpr uint32_t kHoldNs = 50000;
+template <bool kPair = false>
 __device__ __forceinline__ bool mbar_wait_held(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                int32_t* status) {
     auto held = [&]() {
         uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
-            : "memory");
+        if (kPair)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t"
+                "@p fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
+                : "memory");
         return ok != 0;
     };
     if (held()) return true;
@@ -233,6 +246,15 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_rank_relaxed(uint64_t* bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank))
                  : "memory");
+}
+
+// The same with a release of this CTA's shared memory alone: what this thread wrote there, or saw written
+// there by the threads of its CTA, is visible to whoever waits with mbar_wait_held<true>.
+__device__ __forceinline__ void mbar_arrive_rank_shared(uint64_t* bar, uint32_t rank) {
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank))
+        : "memory");
 }
 
 // TMA tile load into this CTA's shared memory whose completion is counted on an
