@@ -167,9 +167,10 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 //              alone (a release of everything at cluster scope takes about 1,800 cycles a stage: 7.1 ms
 //              at 524,288 rows by 7168 x 2048)
 //   warps 4-11 epilogue: TMEM to bf16 y, while the next unit runs in the other accumulator
-// Launches overlap: the kernel that writes the rows lets the work list's kernel start at once (it
-// reads neither rows nor scales, and nothing that kernel writes), and that one lets this kernel
-// set up its barriers and TMEM; both wait for their predecessor's end before what depends on it.
+// Launches overlap: the kernel that writes the rows lets the work list's kernel be launched at once, and
+// that one lets this kernel set up its barriers and TMEM. Both wait for the end of what precedes them
+// before they read anything: the kernel before them need not be one of this library, and whatever it is
+// may be what writes cu_seqlens.
 // A polling warp takes issue slots from the warps that issue MMAs and scales, so every role but the
 // scale warps is held in its waits by the hardware, and one of four epilogue warps waits for all four
 // (96 rows by 384 experts' 1024 x 7168: 195 us, 220 us with every warp polling).
@@ -332,11 +333,13 @@ __device__ __forceinline__ int mma_rows(int rows) { return (rows + 31) & ~31; }
 // thread holds four segments at a time, all loaded at once (8 ranks x 433 segments: 3 us; a
 // thread with four consecutive segments loaded twice took 7). A table with any inconsistent
 // segment is refused as a whole.
-__global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* __restrict__ cu, Dims d, FastDiv nrow,
-                                                        Workspace ws) {
+__global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* cu, Dims d, FastDiv nrow, Workspace ws) {
     constexpr int kS = 4, kChunk = kS * 1024;
     __shared__ int s_sum[kS * 32];
     grid_launch_dependents();   // the product may set itself up
+    // cu may still be being written up to here: no load of it may come earlier, nor take the
+    // non-coherent path, which the compiler may move and which wants memory constant from the start
+    grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int items = d.R * d.NROW;
     int a[kS], len[kS];
@@ -348,8 +351,8 @@ __global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* __restric
             a[r] = len[r] = 0;
             if (i < items) {
                 const int u = (int)fast_div((uint32_t)i, nrow);
-                a[r] = __ldg(cu + i + u);   // rank u's table has one more entry than segments
-                len[r] = __ldg(cu + i + u + 1);
+                a[r] = cu[i + u];   // rank u's table has one more entry than segments
+                len[r] = cu[i + u + 1];
             }
         }
 #pragma unroll
@@ -415,8 +418,6 @@ __global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* __restric
         if (!ok) set_status(ws.status, BEP_DERR_BOUNDS);
         *ws.ntiles = ok ? total : 0;
     }
-    // launched early: this kernel ends after its predecessor, so that whoever waits for it has both
-    grid_wait();
 }
 
 __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
