@@ -383,11 +383,12 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
             xs = load_logit(row + mine);
             if (!(xs <= FLT_MAX) || xs <= low) xs = -INFINITY;
         }
-        float ref = top;
-        if (p.softmax && !row_sum) ref = warp_max(xs);
+        // renormalised, the row's sum cancels: the largest chosen logit is the reference, as in the
+        // backward, so that experts far below the row's largest (kept from it by a bias) keep their ratios
+        const float ref = p.softmax && p.renorm ? warp_max(xs) : top;
         float sc = 0.0f;
         if (xs != -INFINITY)
-            sc = p.softmax ? expf(xs - ref) * (row_sum ? inv : 1.0f) : sigmoid(xs);
+            sc = p.softmax ? expf(xs - ref) * (p.renorm ? 1.0f : inv) : sigmoid(xs);
         if (p.renorm) {
             const float z = warp_sum(sc);
             sc = z > 0.0f ? sc / z : 0.0f;

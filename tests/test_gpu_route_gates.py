@@ -1,0 +1,54 @@
+"""Gates and logit gradients of the router where scores lie far apart, against the 64-bit reference, with
+a bound for every entry from its own terms."""
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as ref
+from test_gpu_route import DEV, context, routed, score_tol
+
+pytestmark = pytest.mark.gpu
+LOW = ref.LOWEST["f32"]
+
+
+def gradient(bep, ctx, rc, lg, topk, dg):
+    dl = torch.full_like(lg, float("nan"))
+    bep.bep_route_bwd(ctx, rc, lg, topk, torch.from_numpy(np.float32(dg)).to(DEV).view(topk.shape), dl)
+    return dl.float().cpu().numpy().reshape(-1, ctx.cfg.E).astype(np.float64)
+
+
+def gate_bound(rel, w, dg, scale):
+    """|error| of scale * w_k (dg_k - sum_j dg_j w_j): each factor has a relative error below rel."""
+    return rel * scale * w * (np.abs(dg) + (np.abs(dg) * w).sum(1, keepdims=True))
+
+
+@pytest.mark.parametrize("E,K", [(8, 3), (64, 4), (90, 5), (384, 8)])
+@pytest.mark.parametrize("off", (-np.inf, -1e9))
+def test_renormalised_gates_without_the_dominant_expert(lib, E, K, off):
+    """A bias disables the expert whose logit leads by d: the others' gates do not depend on d."""
+    bep = lib
+    lead = np.array([0.0, 20.0, 60.0, 85.0, 88.0, 95.0, 100.0, 104.0, 150.0, 600.0])
+    T = len(lead)
+    x = np.tile(-0.375 * np.minimum(np.arange(E), 24.0), (T, 1))   # falls with e, as the bias does
+    x[:, 2] = lead + 5
+    bias = np.float32(0.01 * (E - np.arange(E))).astype(np.float64)
+    bias[2] = off
+    want = np.tile(np.r_[0, 1, 3:K + 1], (T, 1))
+    ctx = context(bep, 1, T, E, K)
+    rc = bep.RouteConfig(bep.BEP_SCORE_SOFTMAX, renorm=True, scale=2.5)
+    lg, topk, g = routed(bep, ctx, rc, x, False, bias)
+    assert bep.bep_status(ctx) == 0
+    assert np.array_equal(topk.cpu().numpy()[0], want)
+    w = np.exp(np.take_along_axis(x, want, 1))
+    w /= w.sum(1, keepdims=True)
+    got = g.cpu().numpy()[0].astype(np.float64)
+    assert np.all(np.abs(got - 2.5 * w) <= score_tol(K, K) * 2.5 * w)
+    dg = np.float32(np.random.default_rng([E, K]).normal(size=(T, K))).astype(np.float64)
+    dl = gradient(bep, ctx, rc, lg, topk, dg)
+    wd = ref.route_bwd(x, want, dg, True, True, 2.5, LOW)
+    tol = np.zeros_like(wd)
+    np.put_along_axis(tol, want, gate_bound(2 * score_tol(K, K), w, dg, 2.5), 1)
+    # the reference's own row sum cancels to 1e-16 of the largest term, which the dominant score scales
+    s, _ = ref.scores(x, True, LOW)
+    assert np.all(np.abs(dl - wd) <= tol + 1e-14 * s)
+    ctx.close()
