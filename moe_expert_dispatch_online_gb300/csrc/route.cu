@@ -68,9 +68,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 }
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+    return unordered(__reduce_max_sync(kAll, ordered(v)));
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -107,21 +105,33 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = load_logit(row + (kFull ? lane + 32 * i : min(lane + 32 * i, E - 1)));
 }
-// One maximum an element tells the ordinary row, whose magnitudes are all kOrdinary at most, from
-// one that is looked at element by element. In an ordinary row nothing is masked and e^l needs no
-// reference to stay inside fp32 (e^40 = 2e17, 2048 terms), nor to be as exact as e^(l - max): the
-// argument's rounding is relative to the logits in either case. Otherwise masked logits become
-// -inf and *bad is set for a NaN or +inf among them. *top: the softmax's reference, 0 or the
-// row's largest logit. Past E: -inf in either case.
+// An ordinary row's magnitudes are all kOrdinary at most: nothing is masked in it, and no score or
+// exponential underflows. Other rows are looked at element by element: masked logits become -inf and
+// *bad is set for a NaN or +inf among them. *top: the softmax's reference, the row's largest logit (0 if
+// there is none, and for sigmoids). Without a reference the argument's rounding would grow with the
+// logits and not with their distance from the largest: 8 logits near 36 then have scores 2.4e-6 off, and
+// 2.6e-7 with it. Past E: -inf in either case.
 constexpr float kOrdinary = 40.0f;
 template <int V, bool kFull, typename T>
-__device__ __forceinline__ bool look_over(int E, int lane, float (&x)[V], float* top, int* bad) {
-    float hi = 0.0f;
+__device__ __forceinline__ bool look_over(int E, int lane, bool softmax, float (&x)[V], float* top, int* bad) {
+    float hi = -INFINITY, far = 0.0f;
+    if (softmax) {
+        float lo = INFINITY;
 #pragma unroll
-    for (int i = 0; i < V; ++i) hi = max_nan(hi, fabsf(x[i]));
-    const bool ordinary = __all_sync(kAll, hi <= kOrdinary);
+        for (int i = 0; i < V; ++i) {
+            hi = max_nan(hi, x[i]);
+            lo = fminf(lo, x[i]);
+        }
+        far = max_nan(hi, -lo);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) far = max_nan(far, fabsf(x[i]));
+    }
+    const bool ordinary = __all_sync(kAll, far <= kOrdinary);
     *top = 0.0f;
-    if (!ordinary) {
+    if (ordinary) {
+        if (softmax) *top = warp_max(hi);
+    } else {
         hi = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -133,7 +143,7 @@ __device__ __forceinline__ bool look_over(int E, int lane, float (&x)[V], float*
             hi = fmaxf(hi, x[i]);
         }
         hi = warp_max(hi);
-        if (hi > -INFINITY) *top = hi;   // else nothing to choose from: all scores 0
+        if (softmax && hi > -INFINITY) *top = hi;   // else nothing to choose from: all scores 0
     }
     if (!kFull) {
 #pragma unroll
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
     for (; tok < p.ntok; tok += step) {
         const T* row = logits + tok * p.E;
         float top;
-        const bool ordinary = look_over<V, kFull, T>(p.E, lane, x, &top, &bad) && !bias_nan;
+        const bool ordinary = look_over<V, kFull, T>(p.E, lane, row_sum, x, &top, &bad) && !bias_nan;
         float inv = 0.0f;   // 1 / sum of exp(l - top)
         uint32_t key[V];
         if (row_sum) {
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(threads_for(V)) route_bwd_kernel(const T* __re
         if (kDense) {
             float top, sum = 0.0f;
             int masked = 0;   // reported by the forward
-            look_over<V, kFull, T>(p.E, lane, x, &top, &masked);
+            look_over<V, kFull, T>(p.E, lane, true, x, &top, &masked);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 x[i] = exp_of(x[i], top);

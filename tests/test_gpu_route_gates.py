@@ -52,3 +52,55 @@ def test_renormalised_gates_without_the_dominant_expert(lib, E, K, off):
     s, _ = ref.scores(x, True, LOW)
     assert np.all(np.abs(dl - wd) <= tol + 1e-14 * s)
     ctx.close()
+
+
+# Relative error of a softmax gate, in units of 2^-24: expf 4 and the row's exponentials 4 (2 units in the
+# last place each) and up to 6 from their arguments (x - top) log2(e), rounded at magnitudes of 8 here; the
+# sum of E terms, lane by lane and over 5 butterfly steps; the reciprocal, two products and the scale, 4.
+def soft_tol(E):
+    return (4 + 4 + 6 + E / 32 + 5 + 4) * 2.0 ** -24
+
+
+def fast_rel(x, E):
+    """The same for the score of any expert: its own argument is rounded relative to its distance from the
+    row's largest logit (1.5 roundings of it, the constant's one among them)."""
+    return soft_tol(E) + (x.max(1, keepdims=True) - x) * 2.0 ** -23
+
+
+def dense_bound(x, topk, dg, scale, E):
+    """|error| of scale * s_e (dg_e - sum_k dg_k s_k), dg_e = 0 for the others, from its own terms."""
+    s, _ = ref.scores(x, True, LOW)
+    rel = fast_rel(x, E)
+    at = np.zeros_like(s)
+    np.put_along_axis(at, topk, np.abs(dg), 1)
+    return 2 * scale * rel * s * (at + (at * s).sum(1, keepdims=True))
+
+
+@pytest.mark.parametrize("E,K", [(8, 2), (33, 7), (128, 8), (192, 6), (384, 8), (512, 16), (2048, 32)])
+@pytest.mark.parametrize("off", (0.0, 30.0, -30.0, 37.0, -37.0, 500.0))
+@pytest.mark.parametrize("use_bias", (False, True))
+def test_softmax_gates_and_every_gradient(lib, E, K, off, use_bias):
+    """Gates that are not renormalised, and the gradient of every logit, around a common offset."""
+    bep = lib
+    T = 24
+    for seed in range(40):
+        rng = np.random.default_rng([E, K, seed])
+        x = np.clip(np.round(rng.normal(size=(T, E)) * 1.0 * 4096) / 4096, -2.75, 2.75) + off
+        bias = np.float32(rng.normal(size=E) * 0.3 / E).astype(np.float64) if use_bias else None
+        want, gap = ref.choose(x, K, True, bias, 1, 1, 1, LOW)
+        if gap > 4e-6 / E:
+            break
+    else:
+        pytest.fail("no inputs without a near tie")
+    ctx = context(bep, 1, T, E, K)
+    rc = bep.RouteConfig(bep.BEP_SCORE_SOFTMAX, renorm=False, scale=1.5)
+    lg, topk, g = routed(bep, ctx, rc, x, False, bias)
+    assert bep.bep_status(ctx) == 0
+    assert np.array_equal(topk.cpu().numpy()[0], want)
+    wg = ref.gates(x, want, True, False, 1.5, LOW)
+    assert np.all(np.abs(g.cpu().numpy()[0] - wg) <= soft_tol(E) * wg)
+    dg = np.float32(rng.normal(size=(T, K))).astype(np.float64)
+    dl = gradient(bep, ctx, rc, lg, topk, dg)
+    wd = ref.route_bwd(x, want, dg, True, False, 1.5, LOW)
+    assert np.all(np.abs(dl - wd) <= dense_bound(x, want, dg, 1.5, E))
+    ctx.close()
