@@ -291,11 +291,14 @@ int bep_reduce_grad(bep_ctx* ctx, const int32_t* slot_expert, float* g_home, flo
  *     best groups are kept (ties: the lowest group);
  *   - topk[r,t,:] = the K kept experts of the largest keys, largest first (ties:
  *     the lowest expert), always K different ones;
- *   - gates[r,t,k] = scale * s_k / sum_j s_j (renorm != 0; 0 where the sum is 0)
- *     or scale * s_k: the bias moves the choice only;
+ *   - gates[r,t,k] = scale * s_k / sum_j s_j (renorm != 0; formed from the chosen
+ *     logits, so scores too small for fp32 keep their ratios; 0 where all the
+ *     chosen are masked) or scale * s_k: the bias moves the choice only;
  *   - load[e] += the number of tokens that chose e, when load is given (the caller
  *     zeroes it; what a balance bias is updated from).
- * Without a bias the order of the kept experts is the logits' own.
+ * Without a bias the order of the kept experts is the logits' own. With one, keys
+ * that fp32 does not tell apart are equal: scores below 2^-150 (a sigmoid from a
+ * logit of -104 down) count as 0.
  * A logit at its type's lowest finite value or below (-inf) masks the expert: it
  * ranks after all others and its gate is 0. A NaN or +inf logit counts as masked
  * and latches BEP_DERR_NONFINITE, as a NaN key does.

@@ -4,7 +4,7 @@
 //   s_e  = sigmoid(l_e), or softmax(l)_e over the token's E logits        (fp32)
 //   key  = s_e + bias_e; the K largest keys are chosen, ties to the lowest index,
 //          from the top_groups groups whose group_top largest keys sum highest
-//   g_k  = scale * s_k / sum_j s_j (renorm; 0 where the sum is 0), or scale * s_k
+//   g_k  = scale * s_k / sum_j s_j (renorm; 0 where every chosen expert is masked), or scale * s_k
 // Backward, with dv_k = dL/ds_k:
 //   dv_k = scale * dg_k, or with renorm scale * (dg_k - sum_j dg_j w_j) / Z, w = s / Z
 //   sigmoid: dl_k = dv_k s_k (1 - s_k), other experts 0
@@ -76,11 +76,16 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// down to the smallest subnormal (x = -103), where 1 / (1 + e^-x) would be 0 from -89 on
+__device__ __forceinline__ float sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    return (x < 0.0f ? e : 1.0f) / (1.0f + e);
+}
 
-// The scores of all E experts (keys, and the softmax's sum) use the hardware's 2^x and
-// reciprocal, 2 units in the last place of fp32 or fewer, in 2 and 4 instructions; the K gates
-// themselves use expf and a rounded division. 0 for an argument below about -87.
+// The scores of all E experts of an ordinary row (keys, and the softmax's sum) use the hardware's 2^x and
+// reciprocal, 2 units in the last place of fp32 each beside the rounding of x log2(e), in 2 and 4
+// instructions; the K gates, and the keys of other rows, use expf and a rounded division. Results below
+// 2^-126 are 0, which an ordinary row's never are.
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float fast_exp2(float x) {
     float r;
@@ -292,11 +297,15 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
         uint32_t key[V];
         if (row_sum) {
             float ex[V], sum = 0.0f;
+            if (ordinary) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                ex[i] = exp_of(x[i], top);
-                sum += ex[i];
+                for (int i = 0; i < V; ++i) ex[i] = exp_of(x[i], top);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) ex[i] = expf(x[i] - top);
             }
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += ex[i];
             sum = warp_sum(sum);
             inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -304,10 +313,18 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
                 key[i] = by_score ? __float_as_uint(fmaf(ex[i], inv, s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]))
                                   : __float_as_uint(x[i]);
         } else if (by_score) {
+            float sg[V];
+            if (ordinary) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) sg[i] = fast_sigmoid(x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) sg[i] = sigmoid(x[i]);
+            }
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 key[i] = __float_as_uint(
-                    __fadd_rn(fast_sigmoid(x[i]), s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
+                    __fadd_rn(sg[i], s_bias[kFull ? lane + 32 * i : min(lane + 32 * i, p.E - 1)]));
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) key[i] = __float_as_uint(x[i]);
@@ -395,10 +412,12 @@ __global__ void __launch_bounds__(threads_for(V)) route_kernel(const T* __restri
         }
         // renormalised, the row's sum cancels: the largest chosen logit is the reference, as in the
         // backward, so that experts far below the row's largest (kept from it by a bias) keep their ratios
-        const float ref = p.softmax && p.renorm ? warp_max(xs) : top;
+        const float ref = p.renorm ? warp_max(xs) : top;
         float sc = 0.0f;
-        if (xs != -INFINITY)
-            sc = p.softmax ? expf(xs - ref) * (p.renorm ? 1.0f : inv) : sigmoid(xs);
+        if (xs != -INFINITY) {
+            if (p.softmax) sc = expf(xs - ref) * (p.renorm ? 1.0f : inv);
+            else sc = p.renorm && ref < -kOrdinary ? expf(xs - ref) : sigmoid(xs);   // e^x itself there
+        }
         if (p.renorm) {
             const float z = warp_sum(sc);
             sc = z > 0.0f ? sc / z : 0.0f;
@@ -482,8 +501,8 @@ __global__ void __launch_bounds__(threads_for(V)) route_bwd_kernel(const T* __re
         } else {
             float s, w = 0.0f, z = 0.0f;
             xs = chosen_logit();
-            if (p.softmax) {
-                const float top = warp_max(xs);
+            const float top = warp_max(xs);
+            if (p.softmax || (p.renorm && top < -kOrdinary)) {
                 s = xs == -INFINITY ? 0.0f : expf(xs - top);
             } else {
                 s = xs == -INFINITY ? 0.0f : sigmoid(xs);

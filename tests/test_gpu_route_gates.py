@@ -104,3 +104,42 @@ def test_softmax_gates_and_every_gradient(lib, E, K, off, use_bias):
     wd = ref.route_bwd(x, want, dg, True, False, 1.5, LOW)
     assert np.all(np.abs(dl - wd) <= dense_bound(x, want, dg, 1.5, E))
     ctx.close()
+
+
+@pytest.mark.parametrize("E,K", [(8, 3), (64, 4), (90, 5), (384, 8), (2048, 32)])
+@pytest.mark.parametrize("softmax", (False, True))
+@pytest.mark.parametrize("groups", (1, 2))
+@pytest.mark.parametrize("renorm", (True, False))
+def test_scores_below_the_smallest_normal(lib, E, K, softmax, groups, renorm):
+    """Scores that fp32 holds as subnormals only: still in order, and renormalised gates keep their ratios."""
+    bep = lib
+    x = np.full((3, E), -102.0)
+    # the best have the highest indices, a quarter apart: their scores differ by 20 units of 2^-149 or more
+    x[:, E - K:] = -(88.0 + 12.0 / (K + 1) * np.arange(1, K + 1))[::-1] + np.zeros((3, 1))
+    if softmax:
+        x[:, 0] = 0.0                             # the row's largest, and the first choice
+        x[1, 0] = 10.0
+        x[1, 1:] += 10.0
+    if groups == 2 and softmax:
+        x[:, E // 2] = x[:, 0]                    # in the group of the others
+        x[:, 0] = -102.0
+    x = np.float32(x).astype(np.float64)
+    bias = np.zeros(E) if groups == 1 else None   # groups of two keys: by score without a bias
+    want, _ = ref.choose(x, K, softmax, bias, groups, 1, 2 if groups > 1 else 1, LOW)
+    ctx = context(bep, 1, 3, E, K)
+    rc = bep.RouteConfig(bep.BEP_SCORE_SOFTMAX if softmax else bep.BEP_SCORE_SIGMOID, groups=groups, top_groups=1,
+                         group_top=2 if groups > 1 else 1, renorm=renorm, scale=2.0)
+    lg, topk, g = routed(bep, ctx, rc, x, False, bias)
+    assert bep.bep_status(ctx) == 0
+    assert np.array_equal(topk.cpu().numpy()[0], want)
+    wg = ref.gates(x, want, softmax, renorm, 2.0, LOW)
+    # half a unit of a subnormal score or gate, and the scale; normal ones within a few roundings
+    assert np.all(np.abs(g.cpu().numpy()[0] - wg) <= soft_tol(E) * wg + 4 * 2.0 ** -149)
+    if renorm and not softmax:
+        dg = np.float32(np.random.default_rng(E).normal(size=(3, K))).astype(np.float64)
+        dl = gradient(bep, ctx, rc, lg, topk, dg)
+        wd = ref.route_bwd(x, want, dg, False, True, 2.0, LOW)
+        tol = np.zeros_like(wd)
+        np.put_along_axis(tol, want, gate_bound(2 * score_tol(K, K), wg / 2, dg, 2.0), 1)
+        assert np.all(np.abs(dl - wd) <= tol)
+    ctx.close()
