@@ -334,7 +334,8 @@ int bep_route_bwd(bep_ctx* ctx, const bep_route_config* rc, const void* logits, 
 
 /* Gated activation of an expert's first projection, over the R*S*K receive rows:
  *   a[row, c] = g * sigmoid(g) * u,  g = h[row, c], u = h[row, F + c]
- * (fp32, one rounding to bf16), and, when codes and scales are given, the 8-bit
+ * (fp32, one rounding to bf16; 0 for a gate below -174, where the sigmoid is under
+ * 2^-251), and, when codes and scales are given, the 8-bit
  * checkpoint of h that bep_swiglu_bwd reads in place of h: blocks of 32 elements
  * share a power of two 2^e, the smallest (e >= -127) with max |h| <= 127 * 2^e;
  *   codes[row, i] = round-half-even(h[row, i] / 2^e),  scales[row, i/32] = e + 127.

@@ -22,14 +22,7 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ void block_to_f32(const uint4* v, float* f) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
-            f[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
+    for (int j = 0; j < 4; ++j) bf16x8_to_f32(v[j], f + 8 * j);
 }
 
 // ------------------------------------------------------------------------ weights
@@ -131,19 +124,22 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
         const int64_t row = i / nblk;
         const int b = (int)(i - row * nblk);
         const uint4* src = h + (row * 2 * nblk + b) * 4;
-        float g[kMxBlock], u[kMxBlock];
+        float a[kMxBlock];
         uint4 v[4], t[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[j] = __ldg(src + j);
             t[j] = __ldg(src + (int64_t)nblk * 4 + j);
         }
-        block_to_f32(v, g);
-        block_to_f32(t, u);
 #pragma unroll
-        for (int j = 0; j < kMxBlock; ++j) g[j] = g[j] * fast_sigmoid(g[j]) * u[j];
+        for (int j = 0; j < 4; ++j) {
+            float g[8], u[8];
+            bf16x8_to_f32(v[j], g);
+            bf16x8_to_f32(t[j], u);
+            gated8(g, u, a + 8 * j);
+        }
         uint4 q;
-        const uint32_t byte = mx4_block(g, &q);
+        const uint32_t byte = mx4_block(a, &q);
         codes[i] = q;
         scales[row * pitch + b] = (uint8_t)byte;
     }
