@@ -518,6 +518,9 @@ class RouteConfig:
                          self.scale)
         object.__setattr__(self, "_ref", ctypes.byref(c))   # keeps c alive
 
+    def __reduce__(self):   # copies and pickles are made from the fields: _ref is each object's own
+        return type(self), (self.score, self.groups, self.top_groups, self.group_top, self.renorm, self.scale)
+
 
 def _logits_type(t):
     return BEP_F32 if t.dtype == _logits_dtypes()[0] else BEP_BF16
