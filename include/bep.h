@@ -398,7 +398,9 @@ int bep_swiglu_mx(bep_ctx* ctx, const uint16_t* h, int32_t F, uint8_t* codes, ui
  *   cu_seqlens [R, E+B+1]; slot_expert [R, B]; codes, scales as bep_dispatch_mx or
  *   bep_swiglu_mx (F = H) wrote them; w_codes, w_scales from bep_mx_quantize_weight;
  *   y [R*S*K, H'] bf16 out.
- * BEP_ERR_SIZE: 2^31 or more work units of 128 rows x 128 outputs, or scale blocks. */
+ * BEP_ERR_SIZE: 2^31 or more work units of 128 rows x 128 outputs, or scale blocks.
+ * BEP_ERR_CUDA also where the device cannot hold the kernel's pairs of CTAs (the
+ * other calls of the context work all the same). */
 int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert,
                         const uint8_t* codes, const uint8_t* scales, const uint8_t* w_codes,
                         const uint8_t* w_scales, uint16_t* y, void* stream);

@@ -26,6 +26,7 @@ struct bep_ctx {
     void* blob;
     int device;
     int num_sms;
+    int mx_clusters;   // pairs of CTAs of the 4-bit product that fit the device, 0: it cannot run
     int comm_sms;   // SM budget of the token-moving kernels (0: every SM)
 };
 
@@ -97,9 +98,14 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return BEP_ERR_CUDA;
-    if (bep::plan_setup(dev) != cudaSuccess || bep::gemm_setup(dev) != cudaSuccess ||
-        bep::mx_setup(dev) != cudaSuccess)
+    if (bep::plan_setup(dev) != cudaSuccess || bep::gemm_setup(dev) != cudaSuccess)
         return BEP_ERR_CUDA;
+    // one entry point alone needs this: a context that never calls it works without
+    int mx_clusters = 0;
+    if (bep::mx_setup(dev, &mx_clusters) != cudaSuccess) {
+        mx_clusters = 0;
+        cudaGetLastError();
+    }
 
     const size_t E = d.E, R = d.R, NC = d.NC, NROW = d.NROW, NP = d.E + d.R;
     const size_t nslots = (size_t)d.R * d.B;
@@ -154,6 +160,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ctx->blob = blob;
     ctx->device = dev;
     ctx->num_sms = sms;
+    ctx->mx_clusters = mx_clusters;
     ctx->comm_sms = 0;
     *out = ctx;
     return BEP_OK;
@@ -442,8 +449,9 @@ int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* 
     // work units (row tiles x 128-column output tiles) and scale blocks are counted in 32 bits
     const int64_t mt = (ctx->d.Hp + 127) / 128, kb = (ctx->d.H + 127) / 128;
     if (ctx->d.max_tiles * mt >= ((int64_t)1 << 31) || ctx->d.E * mt * kb >= ((int64_t)1 << 30)) return BEP_ERR_SIZE;
+    if (ctx->mx_clusters < 1) return BEP_ERR_CUDA;
     return cuda_rc(bep::launch_grouped_gemm_mx(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales,
-                                               w_codes, w_scales, y, ctx->num_sms, as_stream(stream)));
+                                               w_codes, w_scales, y, ctx->mx_clusters, as_stream(stream)));
 }
 
 int bep_wait_selftest(bep_ctx* ctx, int32_t timeout_us, void* stream) {

@@ -115,7 +115,7 @@ cudaError_t launch_swiglu_bwd(int64_t rows, int F, const uint16_t* da, const int
                               const uint8_t* scales, uint16_t* dh, uint16_t* a, cudaStream_t st);
 // 4-bit experts (mx.cu)
 inline int mx_scale_pitch(int H) { return 16 * ((H + 511) / 512); }   // bytes of a row's scales
-cudaError_t mx_setup(int device);
+cudaError_t mx_setup(int device, int* clusters);
 cudaError_t launch_mx_weight(const Dims& d, const uint16_t* w, uint8_t* codes, uint8_t* scales,
                              cudaStream_t st);
 cudaError_t launch_dispatch_mx(const Dims& d, const Workspace& ws, const uint16_t* x,
@@ -126,7 +126,7 @@ cudaError_t launch_swiglu_mx(int64_t rows, int F, const uint16_t* h, uint8_t* co
 cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int32_t* cu,
                                    const int32_t* slot_expert, const uint8_t* codes,
                                    const uint8_t* scales, const uint8_t* w_codes,
-                                   const uint8_t* w_scales, uint16_t* y, int num_sms,
+                                   const uint8_t* w_scales, uint16_t* y, int clusters,
                                    cudaStream_t st);
 
 __device__ __forceinline__ int64_t i64max(int64_t a, int64_t b) { return a > b ? a : b; }

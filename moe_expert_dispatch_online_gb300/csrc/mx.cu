@@ -792,11 +792,6 @@ bool encode_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of two that can be resident at once, per device: the grid, so that the units are
-// spread evenly over CTAs that run from the start.
-constexpr int kMaxDevices = 64;
-int g_mx_clusters[kMaxDevices] = {};
-
 cudaLaunchConfig_t mx_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
@@ -824,17 +819,18 @@ int grid_for(int64_t warps, int sms, int num_sms) {
 
 }  // namespace
 
-cudaError_t mx_setup(int device) {
+// *clusters: clusters of two that can be resident at once: the grid, so that the units are spread evenly over
+// CTAs that run from the start.
+cudaError_t mx_setup(int device, int* clusters) {
     cudaError_t err = cudaFuncSetAttribute(grouped_gemm_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)kMxSmem);
     if (err != cudaSuccess) return err;
-    if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
     int nsm = 0;
     err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, device);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = mx_config(nsm / 2, nullptr, attr);
-    return cudaOccupancyMaxActiveClusters(&g_mx_clusters[device], grouped_gemm_mx_kernel, &cfg);
+    return cudaOccupancyMaxActiveClusters(clusters, grouped_gemm_mx_kernel, &cfg);
 }
 
 cudaError_t launch_mx_weight(const Dims& d, const uint16_t* w, uint8_t* codes, uint8_t* scales,
@@ -868,7 +864,7 @@ cudaError_t launch_swiglu_mx(int64_t rows, int F, const uint16_t* h, uint8_t* co
 cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int32_t* cu,
                                    const int32_t* slot_expert, const uint8_t* codes,
                                    const uint8_t* scales, const uint8_t* w_codes,
-                                   const uint8_t* w_scales, uint16_t* y, int num_sms,
+                                   const uint8_t* w_scales, uint16_t* y, int clusters,
                                    cudaStream_t st) {
     const uint64_t wd[3] = {(uint64_t)d.H / 2, (uint64_t)d.Hp, (uint64_t)d.E};
     const uint64_t xd[2] = {(uint64_t)d.H / 2, (uint64_t)d.R * d.C};
@@ -904,12 +900,8 @@ cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int
     const cudaError_t err =
         cudaLaunchKernelEx(&tc, mx_tiles_kernel, cu, d, make_fast_div((uint32_t)d.NROW), ws);
     if (err != cudaSuccess) return err;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || g_mx_clusters[dev] < 1)
-        return cudaErrorInvalidDevice;
     cudaLaunchAttribute attr[2];
-    const int pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
-    cudaLaunchConfig_t cfg = mx_config(g_mx_clusters[dev] < pairs ? g_mx_clusters[dev] : pairs, st, attr);
+    cudaLaunchConfig_t cfg = mx_config(clusters, st, attr);
     return cudaLaunchKernelEx(&cfg, grouped_gemm_mx_kernel, tmW, tmS, tmX[0], tmX[1], tmX[2], tmX[3], p);
 }
 
