@@ -152,7 +152,7 @@ def _current_stream():
     return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _arg(t, dtypes, n, name, optional=False):
+def _arg(t, dtypes, n, name):
     """Device pointer of a dense CUDA tensor of n elements, checked in one pass: small calls are
     bound by the host, and each look at a tensor costs it 0.1 us or more."""
     try:
@@ -160,7 +160,7 @@ def _arg(t, dtypes, n, name, optional=False):
             return t.data_ptr()
     except AttributeError:
         pass
-    p = _ptr(t, dtypes, name, optional)   # says what is wrong
+    p = _ptr(t, dtypes, name)   # says what is wrong
     _numel(t, n, name)
     return p
 

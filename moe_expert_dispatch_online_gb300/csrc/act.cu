@@ -43,8 +43,8 @@ __device__ __forceinline__ uint2 quantise8(const float* f, uint32_t* byte) {
 
 // One pass, no loop: a CTA takes kU runs of 256 consecutive vectors, all of whose loads are in
 // flight at once, and the CTAs follow one another through memory. A grid that strides over the
-// rows instead reaches 87-93% of the copy rate; this reaches 102-105%.
-// 524,288 rows of 1024 + 1024 (4.33 GB, 5.40 GB): forward 777 -> 622 us, backward 868 -> 764 us.
+// rows instead reaches 87-93% of the copy rate; this reaches 101-104%.
+// 524,288 rows of 1024 + 1024 (4.33 GB, 5.40 GB): forward 625 us, 746 with the striding grid; backward 803 us.
 // n: vectors of 8 columns in all rows (rows * F / 8, a multiple of 4, below 2^31).
 template <bool kSave, int kU>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const uint4* __restrict__ h,
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const uint4* __restric
     }
 }
 
-// One vector a thread: two or more in flight measured no faster here (764 us each).
+// One vector a thread: two or more in flight measured no faster here.
 __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const uint4* __restrict__ da,
                                                               const uint2* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales,
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const uint4* __res
     asm volatile("" ::"r"(qg.x), "r"(qu.x), "f"(d[0]));   // all loads before the branch
     // Codes are 127 at most: with a scale of 1/2 or less no gate of the block lies beyond 63.5. A tiny one is
     // left to a loop that reads its elements again, so that the rare case costs the other one no registers
-    // (807 us at 524,288 rows of 1024 + 1024; 836 us with both forms unrolled, 798 us with the common one alone).
+    // (524,288 rows of 1024 + 1024, side by side: 807 us; both forms unrolled 836 us; the common one alone 798 us).
     if (sg > 0.5f) {
         float low = 0.0f;
 #pragma unroll
@@ -163,7 +163,7 @@ cudaError_t by_slabs(int64_t rows, int F8, F&& launch) {
 }
 
 // Three vectors a thread from 2^22 of them on (67 million: 691 -> 622 us); below, one, which spreads
-// a small call over more CTAs (2,048 vectors: 1.9 us, 2.4 us with three; 670,000: 8.0 us either way).
+// a small call over more CTAs (2,048 vectors: 1.9 us, 2.4 us with three; 670,000: the same either way).
 constexpr uint32_t kManyVectors = 1u << 22;
 
 template <bool kSave, int kU>

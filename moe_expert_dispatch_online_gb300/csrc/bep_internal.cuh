@@ -17,10 +17,11 @@ constexpr int kMaxK = 32;
 constexpr int kBM = 128;
 constexpr int kBK = 64;
 
-// One GEMM m-tile: 128 (or fewer, at a segment's end) receive rows that share a weight row.
+// One GEMM m-tile: receive rows that share a weight row, at most 128, 256 (two m-tiles a unit) or 224 (4-bit
+// product) of them by the kernel that the list is for, fewer at a segment's end; for dW a whole segment.
 struct MTile {
     int32_t row0;    // first global receive row
-    int32_t rows;    // valid rows, 1..128
+    int32_t rows;    // valid rows, 1 or more
     int32_t wsel;    // >= 0: home row index into w_home; < 0: -(1 + u*B + j), slot of w_slots
     int32_t pad;
 };
@@ -136,7 +137,7 @@ __device__ __forceinline__ void set_status(int32_t* status, int bits) {
     atomicOr(status, bits);
 }
 
-// Division of n < 2^31 by an invariant d < 2^31 (a multiply and a shift).
+// Division of n < 2^31 by an invariant d < 2^31: a multiply and a shift, by the method of Granlund and Montgomery.
 struct FastDiv {
     uint32_t d, m, s;
 };

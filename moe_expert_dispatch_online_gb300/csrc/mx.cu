@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 // Many rows: a stage of 224 rows takes the tensor pipe 390 cycles for its MMAs and about 120 for the
 // six scale copies, which share the pipe, and the stage's bytes about as long to arrive in shared
 // memory that the MMAs are reading; the two overlap to about 600 cycles. 524,288 rows by 7168 x 2048:
-// 4.97 ms with one CTA and N <= 128, 2.92 with pairs and N <= 192, 2.67 with N <= 224, 2.42-2.57 now
-// (6.0-6.4 PFLOP/s).
+// 4.97 ms with one CTA and N <= 128, 2.92 with pairs and N <= 192, 2.67 with N <= 224, 2.46-2.6 now
+// (5.9-6.3 PFLOP/s; the ordered hand-over of the row scales, below, is 3% of it).
 //   warp 0     TMA: codes of 128 outputs and of N/2 rows; 256 reduction steps a stage
 //   warp 1     (CTA 0) copies each stage's scales to both TMEMs, issues tcgen05.mma.kind::mxf4
 //   warps 2, 3 put all N rows' scales (any row offset, so no TMA) in tensor-core order, make them
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_mx_kernel(const uint4* __rest
 constexpr int kMxRows = 224;                   // rows of a tile at most
 constexpr int kMxEpiWarps = 8;                 // two for each quarter of TMEM's lanes
 constexpr int kMxThreads = 32 * (4 + kMxEpiWarps);   // producer, MMA, two scale warps, epilogue
-// Five stages: 2.42 ms at 524,288 rows by 7168 x 2048 and 76.5 us at 64, 2.54 ms and 75.1 us with six,
-// 2.64 ms and 81 us with four.
+// Stages, compared before the row scales' hand-over cost its 3%: five 2.42 ms at 524,288 rows by 7168 x 2048 and
+// 76.5 us at 64, six 2.54 ms and 75.1 us, four 2.64 ms and 81 us.
 constexpr int kMxStages = 5;
 constexpr int kMxK = 256;                      // reduction elements a stage: 128 bytes of codes
 constexpr int kMxA = 128 * 128;                // bytes: 128 outputs x 128 bytes

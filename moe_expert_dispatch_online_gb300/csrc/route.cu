@@ -183,8 +183,8 @@ __device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, 
 // tokens in 100 at 8 of 384), or two of the K + 1 leading words agree in all their key bits (as
 // many) -- the choice is made again on whole keys, with a second reduction for the index.
 // 65,536 tokens, 8 of 384 by softmax and bias: 130 us with whole keys in every round and
-// element-by-element checks, 86 us with two words a lane, rescanned when both have won, 40 us
-// now; bound by the integer pipe and the chain of reductions (470 instructions a token).
+// element-by-element checks, 86 us with two words a lane, rescanned when both have won, 42 us
+// now; bound by the integer pipe and the chain of reductions (490 instructions a token).
 template <int V>
 struct Packed {
     static constexpr int kBits = V <= 1 ? 6 : V <= 3 ? 7 : V <= 7 ? 8 : V <= 15 ? 9 : V <= 16 ? 10 : V <= 32 ? 11 : 12;
