@@ -69,9 +69,9 @@ def fake(tmp_path_factory):
     for name, text in (("shim.h", SHIM), ("runtime.cpp", RUNTIME), ("parts.cpp", PARTS)):
         (d / name).write_text(text)
     so = d / "fake.so"
-    # what no test calls stays unresolved
+    # what no test calls stays unresolved; the stand-ins come before a runtime that the process has loaded
     subprocess.run([_build.nvcc(), "-x", "c++", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-cudart", "none",
-                    "-Xlinker", "-z", "-Xlinker", "lazy", "-include", str(d / "shim.h"), "-I", _build.CSRC,
+                    *("-Xlinker", "-z", "-Xlinker", "lazy", "-Xlinker", "-Bsymbolic"), "-include", str(d / "shim.h"), "-I", _build.CSRC,
                     "-o", str(so), os.path.join(_build.CSRC, "bep.cu"), str(d / "runtime.cpp"),
                     str(d / "parts.cpp")], check=True)
     lib = ctypes.CDLL(str(so), mode=os.RTLD_LAZY)
