@@ -206,9 +206,9 @@ def prepare(case, seed):
         s["y"] = torch.empty(rows, Hp, dtype=torch.bfloat16, device=DEV)
         if c["op"] == "i8":
             w = s.pop("w")
-            s["w"] = bep.I8Weight(s["ctx"])
-            bep.bep_i8_quantize_weight(s["ctx"], w, s["w"].codes, s["w"].scales)
-            s["rows"] = bep.I8Rows(rows, H)
+            s["w"] = bep.IntWeight(s["ctx"])
+            bep.bep_int_quantize_weight(s["ctx"], w, s["w"].codes, s["w"].scales)
+            s["rows"] = bep.IntRows(rows, H)
         elif c["train"]:
             s["dx"] = torch.empty(rows, H, dtype=torch.bfloat16, device=DEV)
             s["dw"] = torch.empty(E, H, Hp, dtype=torch.float32, device=DEV)
@@ -232,10 +232,10 @@ def run(state):
 def _own_i8(s):
     bep, ctx, rows, w = s["bep"], s["ctx"], s["rows"], s["w"]
     if s["case"]["stage"] == "first":
-        bep.bep_dispatch_i8(ctx, s["x"], s["dest"], rows.codes, rows.scales)
+        bep.bep_dispatch_int(ctx, s["x"], s["dest"], rows.codes, rows.scales)
     else:
-        bep.bep_swiglu_i8(ctx, s["h"], rows.codes, rows.scales)
-    bep.bep_grouped_gemm_i8(ctx, s["cu"], s["slot_expert"], rows.codes, rows.scales, w.codes, w.scales, s["y"])
+        bep.bep_swiglu_int(ctx, s["h"], rows.codes, rows.scales)
+    bep.bep_grouped_gemm_int(ctx, s["cu"], s["slot_expert"], rows.codes, rows.scales, w.codes, w.scales, s["y"])
     return s["y"]
 
 
