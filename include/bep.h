@@ -405,7 +405,45 @@ int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* 
                         const uint8_t* codes, const uint8_t* scales, const uint8_t* w_codes,
                         const uint8_t* w_scales, uint16_t* y, void* stream);
 
-/* SM budget of the token-moving kernels (dispatch, dispatch_mx, combine, combine_bwd,
+/* 8-bit experts. Elements are integers of -127..127 with one fp32 scale for each row (a token's row,
+ * an activation's row, an expert's output channel): with m the row's largest magnitude,
+ *   code = round-half-even(127 v / m),  scale = m / 127  (codes 0 where m is 0)
+ * and the values are code * scale. A row with an infinity or a NaN gets the scale NaN and codes 0: all
+ * its values are NaN. (Below m = 2^-119 the scale is one of fp32's subnormal numbers, with fewer bits.)
+ *
+ * Quantises the home rows [0, E) of a weight tensor, once, before serving:
+ *   w [E, H, H'] bf16 (a channel runs along H); codes [E, H', H] int8 out; scales [E, H'] fp32 out. */
+int bep_int_quantize_weight(bep_ctx* ctx, const uint16_t* w, int8_t* codes, float* scales, void* stream);
+
+/* bep_dispatch in 8 bits: every token is quantised once and its codes and scale are written to its K
+ * receive rows.
+ *   x [R, S, H] bf16; dest [R, S, K]; codes [R*S*K, H] int8 out; scales [R*S*K] fp32 out. */
+int bep_dispatch_int(bep_ctx* ctx, const uint16_t* x, const int32_t* dest, int8_t* codes, float* scales,
+                    void* stream);
+
+/* The gated activation of bep_swiglu, quantised to 8 bits for the second projection (the fp32 activation is
+ * rounded once, to its integer):
+ *   h [R*S*K, 2F] bf16; codes [R*S*K, F] int8 out; scales [R*S*K] fp32 out. F % 64 == 0, F >= 64
+ *   (BEP_ERR_ARG). */
+int bep_swiglu_int(bep_ctx* ctx, const uint16_t* h, int32_t F, int8_t* codes, float* scales, void* stream);
+
+/* The grouped product on 8-bit rows and weights: for rank u and every non-empty segment,
+ *   y[u*S*K + seg, n] = (sum_h code[row, h] * w_code[expert, n, h]) * w_scale[expert, n] * scale[row],
+ * expert = rho for rho < E and slot_expert[u][rho - E] for a prefetch slot: the slots' replicas are read from
+ * the home rows, which all R ranks of this GPU share, so nothing is prefetched.
+ * The sum is exact as long as its parts stay below 2^24 (with H <= 1040 always), rounded to fp32 as it grows
+ * beyond; y is bf16 (round to nearest even). Rows outside every segment are not written; a bad cu_seqlens is
+ * refused as in bep_grouped_gemm. A non-empty slot segment without an expert in [0, E) is skipped and latches
+ * BEP_DERR_BOUNDS.
+ *   cu_seqlens [R, E+B+1]; slot_expert [R, B]; codes, scales as bep_dispatch_int or bep_swiglu_int (F = H) wrote
+ *   them; w_codes, w_scales from bep_int_quantize_weight; y [R*S*K, H'] bf16 out.
+ * BEP_ERR_SIZE: 2^31 or more work units of 128 rows x 128 outputs. BEP_ERR_CUDA also where the device cannot
+ * hold the kernel's pairs of CTAs. */
+int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const int8_t* codes,
+                        const float* scales, const int8_t* w_codes, const float* w_scales, uint16_t* y,
+                        void* stream);
+
+/* SM budget of the token-moving kernels (dispatch, dispatch_mx, dispatch_int, combine, combine_bwd,
  * combine_dgates, dispatch_bwd): their grids are sized for `sms` SMs, so
  * the rest of the GPU stays free for concurrent work, as a communication
  * library with a fixed SM budget runs ([P4] "Benchmarks against DeepEP v2":

@@ -48,7 +48,8 @@ SYMBOLS = ("bep_create", "bep_destroy", "bep_plan", "bep_plan_noalloc", "bep_pre
            "bep_grouped_gemm_vm", "bep_weights_create", "bep_weights_get",
            "bep_weights_destroy", "bep_reduce_grad", "bep_route", "bep_route_bwd", "bep_swiglu",
            "bep_swiglu_bwd", "bep_mx_quantize_weight", "bep_dispatch_mx", "bep_swiglu_mx",
-           "bep_grouped_gemm_mx", "bep_set_comm_sms", "bep_wait_selftest",
+           "bep_grouped_gemm_mx", "bep_int_quantize_weight", "bep_dispatch_int", "bep_swiglu_int",
+           "bep_grouped_gemm_int", "bep_set_comm_sms", "bep_wait_selftest",
            "bep_status", "bep_clear_status", "bep_strerror")
 
 _lib = None
@@ -114,6 +115,10 @@ def load(path: str = LIB_PATH):
             "bep_dispatch_mx": (ctypes.c_int, [vp, p, p, p, p, vp]),
             "bep_swiglu_mx": (ctypes.c_int, [vp, p, i32, p, p, vp]),
             "bep_grouped_gemm_mx": (ctypes.c_int, [vp, p, p, p, p, p, p, p, vp]),
+            "bep_int_quantize_weight": (ctypes.c_int, [vp, p, p, p, vp]),
+            "bep_dispatch_int": (ctypes.c_int, [vp, p, p, p, p, vp]),
+            "bep_swiglu_int": (ctypes.c_int, [vp, p, i32, p, p, vp]),
+            "bep_grouped_gemm_int": (ctypes.c_int, [vp, p, p, p, p, p, p, p, vp]),
             "bep_status": (ctypes.c_int, [vp, ctypes.POINTER(i32), vp]),
             "bep_clear_status": (ctypes.c_int, [vp, vp]),
             "bep_strerror": (ctypes.c_char_p, [i32]),
@@ -670,6 +675,73 @@ def bep_grouped_gemm_mx(ctx: Context, cu_seqlens, slot_expert, codes, scales, w_
                                       *_mx_weight(c, w_codes, w_scales, "w_"),
                                       _arg(y, _bf16(), ctx._rows * c.Hp, "y"), _stream(stream)),
            "bep_grouped_gemm_mx")
+
+
+class IntRows:
+    """`rows` rows of H elements in 8 bits: codes int8 [rows, H], scales fp32 [rows]."""
+
+    def __init__(self, rows: int, H: int, device="cuda"):
+        import torch
+        self.codes = torch.empty((rows, H), dtype=torch.int8, device=device)
+        self.scales = torch.empty(rows, dtype=torch.float32, device=device)
+
+
+class IntWeight:
+    """Buffers of the E experts' 8-bit weights of a context's projection: codes int8 [E, H', H],
+    scales fp32 [E, H']."""
+
+    def __init__(self, ctx: Context, device="cuda"):
+        import torch
+        c = ctx.cfg
+        self.codes = torch.empty((c.E, c.Hp, c.H), dtype=torch.int8, device=device)
+        self.scales = torch.empty((c.E, c.Hp), dtype=torch.float32, device=device)
+
+
+def _i8_weight(c, codes, scales, prefix=""):
+    return (_arg(codes, _i8(), c.E * c.Hp * c.H, prefix + "codes"),
+            _arg(scales, _f32(), c.E * c.Hp, prefix + "scales"))
+
+
+def _i8_rows(rows, F, codes, scales):
+    return _arg(codes, _i8(), rows * F, "codes"), _arg(scales, _f32(), rows, "scales")
+
+
+def bep_int_quantize_weight(ctx: Context, w, codes, scales, stream=None):
+    """w bf16 [E, H, H'] -> 8-bit codes and the channels' scales (the buffers of an IntWeight)."""
+    c = ctx.cfg
+    _check(load().bep_int_quantize_weight(ctx.handle, _arg(w, _bf16(), c.E * c.H * c.Hp, "w"),
+                                         *_i8_weight(c, codes, scales), _stream(stream)),
+           "bep_int_quantize_weight")
+
+
+def bep_dispatch_int(ctx: Context, x, dest, codes, scales, stream=None):
+    """Quantises every token to 8 bits and writes it to its K receive rows (an IntRows)."""
+    H = ctx.cfg.H
+    _check(load().bep_dispatch_int(ctx.handle, _arg(x, _bf16(), ctx._tokens * H, "x"),
+                                  _arg(dest, _i32(), ctx._rows, "dest"),
+                                  *_i8_rows(ctx._rows, H, codes, scales), _stream(stream)),
+           "bep_dispatch_int")
+
+
+def bep_swiglu_int(ctx: Context, h, codes, scales, stream=None):
+    """The gated activation of h [rows, 2F] in 8 bits (an IntRows of F elements)."""
+    F = int(h.shape[-1]) // 2
+    _check(load().bep_swiglu_int(ctx.handle, _arg(h, _bf16(), ctx._rows * 2 * F, "h"), F,
+                                *_i8_rows(ctx._rows, F, codes, scales), _stream(stream)),
+           "bep_swiglu_int")
+
+
+def bep_grouped_gemm_int(ctx: Context, cu_seqlens, slot_expert, codes, scales, w_codes, w_scales, y,
+                        stream=None):
+    """y[seg] = rows[seg] @ W(expert of seg), both in 8 bits; slots are read from the home rows."""
+    c = ctx.cfg
+    _check(load().bep_grouped_gemm_int(ctx.handle,
+                                      _arg(cu_seqlens, _i32(), c.R * (c.E + c.B + 1), "cu_seqlens"),
+                                      _arg(slot_expert, _i32(), c.R * c.B, "slot_expert"),
+                                      *_i8_rows(ctx._rows, c.H, codes, scales),
+                                      *_i8_weight(c, w_codes, w_scales, "w_"),
+                                      _arg(y, _bf16(), ctx._rows * c.Hp, "y"), _stream(stream)),
+           "bep_grouped_gemm_int")
 
 
 def bep_status(ctx: Context, stream=None) -> int:

@@ -27,6 +27,7 @@ struct bep_ctx {
     int device;
     int num_sms;
     int mx_clusters;   // pairs of CTAs of the 4-bit product that fit the device, 0: it cannot run
+    int i8_clusters;   // the same of the 8-bit product, -1 until its first call
     int comm_sms;   // SM budget of the token-moving kernels (0: every SM)
 };
 
@@ -161,6 +162,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ctx->device = dev;
     ctx->num_sms = sms;
     ctx->mx_clusters = mx_clusters;
+    ctx->i8_clusters = -1;
     ctx->comm_sms = 0;
     *out = ctx;
     return BEP_OK;
@@ -452,6 +454,58 @@ int bep_grouped_gemm_mx(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* 
     if (ctx->mx_clusters < 1) return BEP_ERR_CUDA;
     return cuda_rc(bep::launch_grouped_gemm_mx(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales,
                                                w_codes, w_scales, y, ctx->mx_clusters, as_stream(stream)));
+}
+
+int bep_int_quantize_weight(bep_ctx* ctx, const uint16_t* w, int8_t* codes, float* scales, void* stream) {
+    BEP_RANGE("bep_int_quantize_weight");
+    if (!ctx || !w || !codes || !scales) return BEP_ERR_ARG;
+    if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_i8_weight(ctx->d, w, codes, scales, as_stream(stream)));
+}
+
+int bep_dispatch_int(bep_ctx* ctx, const uint16_t* x, const int32_t* dest, int8_t* codes, float* scales,
+                    void* stream) {
+    BEP_RANGE("bep_dispatch_int");
+    if (!ctx) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!x || !dest || !codes || !scales) return BEP_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(dest, 4) || !aligned(codes, 16) || !aligned(scales, 4)) return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_dispatch_i8(ctx->d, ctx->ws, x, dest, codes, scales, comm_sms(ctx), ctx->num_sms,
+                                           as_stream(stream)));
+}
+
+int bep_swiglu_int(bep_ctx* ctx, const uint16_t* h, int32_t F, int8_t* codes, float* scales, void* stream) {
+    BEP_RANGE("bep_swiglu_int");
+    if (!ctx || F < 64 || F % 64 != 0) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!h || !codes || !scales) return BEP_ERR_ARG;
+    if (!aligned(h, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return BEP_ERR_ALIGN;
+    return cuda_rc(bep::launch_swiglu_i8((int64_t)ctx->d.R * ctx->d.C, F, h, codes, scales, as_stream(stream)));
+}
+
+int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const int8_t* codes,
+                        const float* scales, const int8_t* w_codes, const float* w_scales, uint16_t* y,
+                        void* stream) {
+    BEP_RANGE("bep_grouped_gemm_int");
+    if (!ctx) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!cu_seqlens || !slot_expert || !codes || !scales || !w_codes || !w_scales || !y) return BEP_ERR_ARG;
+    if (!aligned(cu_seqlens, 4) || !aligned(slot_expert, 4) || !aligned(codes, 16) || !aligned(scales, 4) ||
+        !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 16))
+        return BEP_ERR_ALIGN;
+    // work units (row tiles x 128-column output tiles) are counted in 32 bits
+    if (ctx->d.max_tiles * (int64_t)((ctx->d.Hp + 127) / 128) >= ((int64_t)1 << 31)) return BEP_ERR_SIZE;
+    if (ctx->i8_clusters < 0) {   // nothing here touches the stream, so the first call may be a captured one
+        int clusters = 0;
+        if (bep::i8_setup(ctx->device, &clusters) != cudaSuccess) {
+            cudaGetLastError();
+            return BEP_ERR_CUDA;
+        }
+        ctx->i8_clusters = clusters;
+    }
+    if (ctx->i8_clusters < 1) return BEP_ERR_CUDA;
+    return cuda_rc(bep::launch_grouped_gemm_i8(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales, w_codes,
+                                               w_scales, y, ctx->i8_clusters, as_stream(stream)));
 }
 
 int bep_wait_selftest(bep_ctx* ctx, int32_t timeout_us, void* stream) {

@@ -1,0 +1,798 @@
+// Experts in 8-bit integers (sm_103a): quantisation of weights, tokens and activations with one
+// scale a row (channel), and the grouped product of the integers.
+//
+//   v = [v_h]: m = max |v|, q_h = round-half-even(127 v_h / m), s = m / 127
+//   y[row, n] = (sum_h q[row, h] qw[expert(row), n, h]) * sw[expert, n] * s[row]      (bf16 out)
+//
+// Layouts. Both operands lie along the reduction, so the weights are transposed when they are
+// quantised: row codes [rows, H], row scales [rows] fp32, weight codes [E, H', H], scales [E, H'].
+
+#include <cuda_fp16.h>
+
+#include "mxfmt.cuh"
+#include "tiles.cuh"
+
+namespace bep {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------------ format
+// A row's grid: values are multiplied by the power of two `up`, which brings the largest to [1, 4) (and
+// far smaller ones to 0, which their integer is anyway), so that 127 v and the quotient stay inside fp32.
+// 127 v is exact for a bf16 v, and a quotient of two such numbers is a tie or at least 2^-16 of itself
+// away from one, so that one rounding of the division never decides an integer.
+struct Grid {
+    float up, m, scale;
+};
+__device__ __forceinline__ Grid grid_of(uint32_t amax_bits) {
+    Grid g;
+    if (amax_bits >= 0x7f800000u) {   // an infinity or a NaN: every value of the row is NaN
+        g.up = 0.0f;
+        g.m = 1.0f;
+        g.scale = __uint_as_float(0x7fc00000u);
+        return g;
+    }
+    const float m = __uint_as_float(amax_bits);
+    const int b = (int)(amax_bits >> 23);
+    g.up = __uint_as_float((uint32_t)max(254 - b, 1) << 23);
+    g.m = amax_bits ? m * g.up : 1.0f;
+    g.scale = __fdiv_rn(m, 127.0f);
+    return g;
+}
+// 0 for a row with an infinity or a NaN (up is 0: v * up is 0 or NaN, which converts to 0)
+__device__ __forceinline__ int code_of(float v, const Grid& g) {
+    return __float2int_rn(__fdiv_rn(127.0f * (v * g.up), g.m));
+}
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+    return __byte_perm(__byte_perm((uint32_t)a, (uint32_t)b, 0x0040), __byte_perm((uint32_t)c, (uint32_t)d, 0x0040),
+                       0x5410);
+}
+__device__ __forceinline__ uint2 codes8(const float* f, const Grid& g) {
+    return make_uint2(pack4(code_of(f[0], g), code_of(f[1], g), code_of(f[2], g), code_of(f[3], g)),
+                      pack4(code_of(f[4], g), code_of(f[5], g), code_of(f[6], g), code_of(f[7], g)));
+}
+// Largest magnitude of eight bf16, as two bf16 bit patterns in a word (NaN above infinity above all).
+__device__ __forceinline__ uint32_t top2(const uint4& v) {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+}
+__device__ __forceinline__ uint32_t top_f32(uint32_t two) { return max(two & 0xffffu, two >> 16) << 16; }
+
+// ------------------------------------------------------------------------ weights
+// One CTA: 32 columns n of one expert over the whole reduction, twice: the columns' largest magnitudes, then
+// (from L2) their integers, which meet in shared memory, 256 rows h at a time, and leave as runs along h.
+constexpr int kWCols = 32, kWRows = 256;
+__global__ void __launch_bounds__(kThreads) i8_weight_kernel(const uint4* __restrict__ w, int8_t* __restrict__ codes,
+                                                             float* __restrict__ scales, int H, int Hp) {
+    __shared__ uint32_t s_top[kThreads / 4][kWCols];
+    __shared__ Grid s_grid[kWCols];
+    __shared__ uint32_t s_codes[kWCols][kWRows / 4 + 1];   // a word more a column: stores of a warp conflict-free
+    const int e = blockIdx.y, n0 = blockIdx.x * kWCols;
+    const int v = threadIdx.x & 3, r = threadIdx.x >> 2;
+    const int pitch = Hp / 8;
+    const uint4* src = w + (int64_t)e * H * pitch + n0 / 8 + v;
+    uint32_t t[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int h = r; h < H; h += kThreads / 4) {
+        const uint4 x = __ldg(src + (int64_t)h * pitch);
+        t[0] = __vmaxu2(t[0], x.x & 0x7fff7fffu);
+        t[1] = __vmaxu2(t[1], x.y & 0x7fff7fffu);
+        t[2] = __vmaxu2(t[2], x.z & 0x7fff7fffu);
+        t[3] = __vmaxu2(t[3], x.w & 0x7fff7fffu);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        s_top[r][8 * v + 2 * j] = t[j] << 16;
+        s_top[r][8 * v + 2 * j + 1] = t[j] & 0xffff0000u;
+    }
+    __syncthreads();
+    if (threadIdx.x < kWCols) {
+        uint32_t top = 0;
+        for (int i = 0; i < kThreads / 4; ++i) top = max(top, s_top[i][threadIdx.x]);
+        const Grid g = grid_of(top);
+        s_grid[threadIdx.x] = g;
+        scales[(int64_t)e * Hp + n0 + threadIdx.x] = g.scale;
+    }
+    __syncthreads();
+    for (int h0 = 0; h0 < H; h0 += kWRows) {
+        const int h = h0 + 4 * r;
+        if (h < H) {
+            float f[4][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bf16x8_to_f32(__ldg(src + (int64_t)(h + i) * pitch), f[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const Grid g = s_grid[8 * v + j];
+                s_codes[8 * v + j][r] = pack4(code_of(f[0][j], g), code_of(f[1][j], g), code_of(f[2][j], g), code_of(f[3][j], g));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = threadIdx.x; i < kWCols * kWRows / 16; i += kThreads) {
+            const int n = i / (kWRows / 16), p = i % (kWRows / 16);
+            if (h0 + 16 * p < H) {
+                const uint32_t* c = &s_codes[n][4 * p];
+                *reinterpret_cast<uint4*>(codes + ((int64_t)e * Hp + n0 + n) * H + h0 + 16 * p) =
+                    make_uint4(c[0], c[1], c[2], c[3]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------------ dispatch
+// Largest of a value over the CTA (every thread calls it).
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s_warp) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (blockDim.x == 32) return v;
+    __syncthreads();   // the last row's maxima have been read
+    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, n = blockDim.x >> 5;
+    return __reduce_max_sync(0xffffffffu, lane < n ? s_warp[lane] : 0u);
+}
+
+// codes[dest[tok, k]], scales[dest[tok, k]] = i8(x[tok]). A CTA per token: a thread holds kHold pieces of 16
+// elements between the two passes over them, and what lies beyond (rows of more than 8192 * kHold) it reads again.
+constexpr int kDispatchThreads = 512, kHold = 2;
+__global__ void __launch_bounds__(kDispatchThreads) dispatch_i8_kernel(const uint4* __restrict__ x,
+                                                                       const int32_t* __restrict__ dest,
+                                                                       uint4* __restrict__ codes,
+                                                                       float* __restrict__ scales, int64_t ntok, int K,
+                                                                       int pieces, int64_t nrows, int32_t* status) {
+    __shared__ uint32_t s_warp[kDispatchThreads / 32];
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    for (int64_t tok = blockIdx.x; tok < ntok; tok += gridDim.x) {
+        int dl = 0;
+        bool ok = true;
+        if (lane < K) {
+            dl = dest[tok * K + lane];
+            ok = dl >= 0 && (int64_t)dl < nrows;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, ok);
+        if (m != 0xffffffffu && threadIdx.x == 0) set_status(status, BEP_DERR_BOUNDS);
+        const uint4* src = x + tok * pieces * 2;
+        uint4 a[kHold], b[kHold];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+            const int p = threadIdx.x + j * blockDim.x;
+            a[j] = b[j] = make_uint4(0, 0, 0, 0);
+            if (p < pieces) {
+                a[j] = __ldg(src + 2 * p);
+                b[j] = __ldg(src + 2 * p + 1);
+            }
+            top = __vmaxu2(top, __vmaxu2(top2(a[j]), top2(b[j])));
+        }
+        for (int p = threadIdx.x + kHold * blockDim.x; p < pieces; p += blockDim.x)
+            top = __vmaxu2(top, __vmaxu2(top2(__ldg(src + 2 * p)), top2(__ldg(src + 2 * p + 1))));
+        const Grid g = grid_of(block_max(top_f32(top), s_warp));
+        auto put = [&](const uint4& lo, const uint4& hi, int p) {
+            float f[16];
+            bf16x8_to_f32(lo, f);
+            bf16x8_to_f32(hi, f + 8);
+            const uint2 c0 = codes8(f, g), c1 = codes8(f + 8, g);
+            return make_uint4(c0.x, c0.y, c1.x, c1.y);
+        };
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+            const int p = threadIdx.x + j * blockDim.x;
+            a[j] = put(a[j], b[j], p);
+        }
+        for (int k = 0; k < K; ++k) {
+            const int64_t row = __shfl_sync(0xffffffffu, dl, k);
+            if (!((m >> k) & 1u)) continue;
+#pragma unroll
+            for (int j = 0; j < kHold; ++j) {
+                const int p = threadIdx.x + j * blockDim.x;
+                if (p < pieces) codes[row * pieces + p] = a[j];
+            }
+            if (threadIdx.x == 0) scales[row] = g.scale;
+        }
+        for (int p = threadIdx.x + kHold * blockDim.x; p < pieces; p += blockDim.x) {
+            const uint4 c = put(__ldg(src + 2 * p), __ldg(src + 2 * p + 1), p);
+            for (int k = 0; k < K; ++k)
+                if ((m >> k) & 1u) codes[(int64_t)dest[tok * K + k] * pieces + p] = c;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------ activation
+// codes, scales = i8(g * sigmoid(g) * u) for h = [g | u]: kWarps warps a row. The activation stays in fp32
+// until its integers; a thread holds 8 * kActHold of its values between the two passes and makes the others
+// (rows longer than 8192) again.
+constexpr int kActHold = 4;
+template <int kWarps>
+__global__ void __launch_bounds__(kThreads) swiglu_i8_kernel(const uint4* __restrict__ h, uint2* __restrict__ codes,
+                                                             float* __restrict__ scales, int64_t rows, int F8) {
+    __shared__ uint32_t s_warp[kThreads / 32];
+    constexpr int kRowThreads = 32 * kWarps, kRows = kThreads / kRowThreads;
+    grid_launch_dependents();
+    const int sub = threadIdx.x / kRowThreads, t = threadIdx.x % kRowThreads;
+    const int64_t row = (int64_t)blockIdx.x * kRows + sub;
+    const bool in = row < rows;
+    const uint4* src = h + (in ? row : 0) * 2 * F8;
+    const int n = in ? F8 : 0;
+    auto act = [&](const uint4& vg, const uint4& vu, float* a) {
+        float g[8], u[8];
+        bf16x8_to_f32(vg, g);
+        bf16x8_to_f32(vu, u);
+        gated8(g, u, a);
+    };
+    uint4 vg[kActHold], vu[kActHold];
+#pragma unroll
+    for (int j = 0; j < kActHold; ++j) {
+        const int c = t + j * kRowThreads;
+        vg[j] = vu[j] = make_uint4(0, 0, 0, 0);
+        if (c < n) {
+            vg[j] = __ldcs(src + c);
+            vu[j] = __ldcs(src + F8 + c);
+        }
+    }
+    float a[kActHold][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < kActHold; ++j) {
+        act(vg[j], vu[j], a[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(a[j][i]) & 0x7fffffffu);
+    }
+    for (int c = t + kActHold * kRowThreads; c < n; c += kRowThreads) {
+        float b[8];
+        act(__ldg(src + c), __ldg(src + F8 + c), b);
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(b[i]) & 0x7fffffffu);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (kWarps > 1) {
+        if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) top = max(top, s_warp[sub * kWarps + i]);
+    }
+    const Grid g = grid_of(top);
+    if (in && t == 0) scales[row] = g.scale;
+    uint2* out = codes + row * F8;
+#pragma unroll
+    for (int j = 0; j < kActHold; ++j) {
+        const int c = t + j * kRowThreads;
+        if (c < n) out[c] = codes8(a[j], g);
+    }
+    for (int c = t + kActHold * kRowThreads; c < n; c += kRowThreads) {
+        float b[8];
+        act(__ldg(src + c), __ldg(src + F8 + c), b);
+        out[c] = codes8(b, g);
+    }
+}
+
+// ------------------------------------------------------------------------ product
+// This GPU's tensor cores multiply integers at a small fraction of their bf16 rate, so the integers become
+// fp16 on the way, which holds them exactly: 1 byte an element in HBM and L2, kind::f16 in the tensor core. Their
+// products and the sums below 2^24 are exact in the fp32 accumulator (any sum of 1,040 products; of rows
+// as they occur, all of them), larger sums are rounded to fp32 as they grow.
+// The weights are the M operand, written to TMEM by the warps that convert them, so that shared memory carries
+// them once (1 byte) and not three times; the rows of one segment are the N operand (32..256), in shared memory.
+// A cluster of two CTAs shares a tile of 256 outputs x N rows (cta_group::2): CTA r holds outputs 128 r.. and
+// converts half of the rows.
+//   warp 0       TMA: weight codes of 128 outputs, 128 reduction steps a stage
+//   warp 1       (CTA 0) tcgen05.mma, A from TMEM
+//   warps 2-9    two groups of four that take the stages in turn: a thread turns one output's 128 codes and
+//                128 bytes of row codes (read a turn ahead) into fp16
+//   warps 10-17  epilogue: TMEM, scaled, to bf16 y
+// TMEM: two accumulators of 128 rows, or one of 256, and kI8Slots stages of weights.
+//   barrier    owner   arrivals
+//   wfull[i]   each    the producer's expect_tx + TMA bytes
+//   wempty[i]  each    a group's four warps
+//   ready[s]   CTA 0   a group's four warps of each CTA
+//   free[s]    both    the MMA thread's multicast commit
+//   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
+//   tempty[a]  CTA 0   the 8 epilogue warps of each CTA
+constexpr int kI8Rows = 256;                    // rows of a tile at most
+constexpr int kI8K = 128;                       // reduction elements a stage
+constexpr int kI8Ring = 6;                      // stages of weight codes under way
+constexpr int kI8Slots = 3;                     // stages of fp16 operands
+constexpr int kI8W = 128 * kI8K;                // bytes: 128 outputs' codes
+constexpr int kI8B = kI8Rows / 2 * kI8K * 2;    // bytes: half of the rows in fp16
+constexpr int kI8Sub = kI8B / 2;                // 64 reduction steps of them
+constexpr int kI8Groups = 2;
+constexpr int kI8EpiWarps = 8;
+constexpr int kI8Threads = 32 * (2 + 4 * kI8Groups + kI8EpiWarps);
+constexpr int kI8Out = 32 * 256;                // bytes: four epilogue warps' 32 rows x 128 outputs
+constexpr int kI8Tmem = 512;
+constexpr int kI8Acc = 128;                     // TMEM columns of an accumulator
+constexpr int kI8ABase = 2 * kI8Acc, kI8ACols = kI8K / 2;
+static_assert(kI8ABase + kI8Slots * kI8ACols <= kI8Tmem, "TMEM");
+
+struct I8Params {
+    const MTile* tiles;
+    const int32_t* ntiles;
+    const int32_t* slot_expert;
+    const int8_t* codes;
+    const float* scales;
+    const float* w_scales;
+    uint16_t* y;
+    int64_t nrows;
+    int E, H, Hp, MT;
+    int32_t* status;
+};
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// 32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulator, fp16 A and B (0), both K-major, M = 256.
+__device__ __forceinline__ uint32_t idesc_f16(int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (16u << 24);
+}
+
+// D (+)= A B^T over 16 reduction steps: A in TMEM (each CTA its own 128 outputs), B in shared memory (each CTA
+// half of the rows).
+__device__ __forceinline__ void mma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// Four int8 to four fp16: the byte with its sign bit turned, behind 0x64, is 1024 + 128 + q in fp16.
+__device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t* out) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));   // 1152
+    const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+    out[0] = *reinterpret_cast<const uint32_t*>(&a);
+    out[1] = *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void i8x16_to_f16(const uint4& v, uint32_t* out) {
+    i8x4_to_f16(v.x, out);
+    i8x4_to_f16(v.y, out + 2);
+    i8x4_to_f16(v.z, out + 4);
+    i8x4_to_f16(v.w, out + 6);
+}
+
+__global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                                        const I8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint8_t* smW = smem;
+    uint8_t* smB = smW + kI8Ring * kI8W;
+    uint8_t* smO = smB + kI8Slots * kI8B;
+    uint64_t* wfull = reinterpret_cast<uint64_t*>(smO + kI8EpiWarps / 4 * kI8Out);
+    uint64_t* wempty = wfull + kI8Ring;
+    uint64_t* ready = wempty + kI8Ring;
+    uint64_t* free_ = ready + kI8Slots;
+    uint64_t* tfull = free_ + kI8Slots;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    int32_t* status = p.status;
+    const uint32_t rank = cluster_rank();
+    const bool lead = rank == 0;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kI8Ring; ++i) {
+            mbar_init(&wfull[i], 1);
+            mbar_init(&wempty[i], 4);
+        }
+        for (int s = 0; s < kI8Slots; ++s) {
+            mbar_init(&ready[s], 8);
+            mbar_init(&free_[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], 2 * kI8EpiWarps);
+        }
+        mbar_init(drain, 1);
+        *s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                     "r"(kI8Tmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before any remote arrive or multicast commit
+    tc_fence_after();
+    const uint32_t tmem_base = *s_tmem;
+    grid_wait();      // launched early: the work list and the rows are complete from here on
+
+    const int MP = (p.MT + 1) / 2;             // pairs of 128-output tiles
+    const int total = *p.ntiles * MP;
+    const int nst = (p.H + kI8K - 1) / kI8K;   // stages a unit
+    const int cl0 = (int)cluster_id(), ncl = (int)cluster_count();
+    uint32_t pr_i = 0, pr_ph = 0, pr_armed = 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool live = true;
+            UnitWalk walk(cl0, ncl, MP);
+            Unit next = walk.take(p, total);   // read a unit ahead
+            for (int unit = cl0; unit < total && live; unit += ncl) {
+                const Unit u = next;
+                next = walk.take(p, total);
+                if (u.expert < 0) {
+                    if (lead) set_status(status, BEP_DERR_BOUNDS);
+                    continue;
+                }
+                const int mt = 2 * u.mp + (int)rank;   // past H' for the last odd tile: zeros
+                for (int k = 0; k < nst; ++k) {
+                    if (!mbar_wait_held(&wempty[pr_i], pr_ph ^ 1u, s_abort, status)) {
+                        live = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&wfull[pr_i], kI8W);
+                    ++pr_armed;
+                    tma_load_3d(&tmW, &wfull[pr_i], smW + pr_i * kI8W, k * kI8K, mt * 128, u.expert);
+                    if (++pr_i == kI8Ring) {
+                        pr_i = 0;
+                        pr_ph ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lead && elect_one()) {
+            uint32_t s = 0, ph = 0;   // operand slot
+            uint32_t half = 0;        // accumulator of the next unit of up to 128 rows
+            uint32_t aph[2] = {1, 1};   // the phases that free the accumulators
+            bool live = true;
+            UnitWalk walk(cl0, ncl, MP);
+            Unit next = walk.take(p, total);
+            for (int unit = cl0; unit < total && live; unit += ncl) {
+                const Unit u = next;
+                next = walk.take(p, total);
+                if (u.expert < 0) continue;
+                const int N = mma_rows(u.rows);
+                const bool big = N > kI8Acc;
+                if (big) half = 0;
+                if (!mbar_wait_held<true>(&tempty[half], aph[half], s_abort, status)) break;
+                if (big && !mbar_wait_held<true>(&tempty[1], aph[1], s_abort, status)) break;
+                aph[half] ^= 1u;
+                if (big) aph[1] ^= 1u;
+                const uint32_t dt = tmem_base + half * kI8Acc;
+                const uint32_t idesc = idesc_f16(N);
+                for (int k = 0; k < nst; ++k) {
+                    if (!mbar_wait_held<true>(&ready[s], ph, s_abort, status)) {
+                        live = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = tmem_base + kI8ABase + s * kI8ACols;
+                    const uint32_t b = smem_u32(smB + s * kI8B);
+                    const int steps = min(kI8K, p.H - k * kI8K) / 16;   // 4 or 8
+#pragma unroll
+                    for (int kk = 0; kk < kI8K / 16; ++kk)
+                        if (kk < steps)
+                            mma_f16_pair_ts(dt, a + kk * 8, sdesc_sw128(b + (kk >> 2) * kI8Sub + (kk & 3) * 32, 16, 1024),
+                                            idesc, (k | kk) != 0);
+                    mma_commit_pair(&free_[s]);
+                    if (k == nst - 1) {
+                        mma_commit_pair(&tfull[half]);
+                        if (big) mma_commit_pair(&tfull[1]);
+                    }
+                    if (++s == kI8Slots) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!big) half ^= 1u;
+            }
+        }
+    } else if (warp < 2 + 4 * kI8Groups) {
+        const int group = (warp - 2) >> 2, quarter = warp & 3;   // four consecutive warps: each quarter of TMEM's lanes once
+        const int n = quarter * 32 + lane;                       // output of this thread, lane of TMEM
+        // rows: 8 lanes take 128 bytes of one, a warp 4 and the group 16 at a time
+        const int rsub = quarter * 4 + (lane >> 3), piece = lane & 7;
+        // a cursor over this group's stages, which are every second one across the units
+        UnitWalk walk(cl0, ncl, MP);
+        Unit u = walk.take(p, total);
+        int k = group, left = (total - cl0 + ncl - 1) / ncl;   // units from u on, u among them
+        if (total <= cl0) left = 0;
+        auto settle = [&]() {   // to the unit that holds stage k
+            while (left > 0 && (u.expert < 0 || k >= nst)) {
+                if (u.expert >= 0) k -= nst;
+                u = walk.take(p, total);
+                --left;
+            }
+        };
+        uint4 v[8];
+        auto load = [&](int half, int64_t row0, int kk) {   // written while this kernel was starting: no __ldg
+            const bool in = kk * kI8K + piece * 16 < p.H;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (16 * j < half) {
+                    const int64_t row = min(row0 + 16 * j, p.nrows - 1);
+                    v[j] = in ? *reinterpret_cast<const uint4*>(p.codes + row * p.H + kk * kI8K + piece * 16)
+                              : make_uint4(0, 0, 0, 0);
+                }
+        };
+        settle();
+        int half = 0;
+        if (left > 0) {
+            half = mma_rows(u.rows) / 2;
+            load(half, (int64_t)u.row0 + (int)rank * half + rsub, k);
+        }
+        uint32_t i = group, iph = 0, s = group, sph = 0;   // ring stage and operand slot of this turn
+        while (left > 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status))) break;
+            // rows: 16 codes a lane become two 16-byte pieces of a row of 64 fp16 (128-byte swizzle); lanes 4-7 of
+            // eight store their second piece first, so that eight lanes touch all 32 banks
+            uint8_t* sub = smB + s * kI8B + (piece >> 2) * kI8Sub;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (16 * j < half) {
+                    uint32_t f[8];
+                    i8x16_to_f16(v[j], f);
+                    const int r = 16 * j + rsub, c = 2 * (piece & 3), odd = piece >> 2;
+                    uint8_t* row = sub + r * 128;
+                    const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
+                    *reinterpret_cast<uint4*>(row + (((c + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
+                    *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
+                }
+            k += kI8Groups;
+            settle();
+            if (left > 0) {
+                half = mma_rows(u.rows) / 2;
+                load(half, (int64_t)u.row0 + (int)rank * half + rsub, k);
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait_held(&wfull[i], iph, s_abort, status))) break;
+            const uint8_t* wrow = smW + i * kI8W + n * 128;
+            const uint32_t ta = tmem_base + ((uint32_t)(quarter * 32) << 16) + kI8ABase + s * kI8ACols;
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t f[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    i8x16_to_f16(*reinterpret_cast<const uint4*>(wrow + (((4 * q + j) ^ (n & 7)) << 4)), f + 8 * j);
+                tmem_st_32x32b_x32(ta + 32 * q, f);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wempty[i]);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_rank_shared(&ready[s], 0);
+            i += kI8Groups;
+            if (i >= kI8Ring) {
+                i -= kI8Ring;
+                iph ^= 1u;
+            }
+            s += kI8Groups;
+            if (s >= kI8Slots) {
+                s -= kI8Slots;
+                sph ^= 1u;
+            }
+        }
+    } else {
+        // Four warps, one for each quarter of TMEM's lanes, own every second run of 32 rows. A lane holds one
+        // output of 32 rows, and a row's outputs lie together in y, so the run is turned in shared memory and
+        // leaves as whole rows of 256 bytes, 16 a lane.
+        const int quarter = warp & 3, second = (warp - 2 - 4 * kI8Groups) >> 2;
+        uint8_t* stg = smO + second * kI8Out;
+        uint32_t half = 0, tph[2] = {0, 0};
+        UnitWalk walk(cl0, ncl, MP);
+        Unit next = walk.take(p, total);
+        for (int unit = cl0; unit < total; unit += ncl) {
+            const Unit u = next;
+            next = walk.take(p, total);
+            if (u.expert < 0) continue;
+            const bool big = mma_rows(u.rows) > kI8Acc;
+            if (big) half = 0;
+            const int n0 = (2 * u.mp + (int)rank) * 128;
+            const int n = n0 + quarter * 32 + lane;
+            const float ws = n < p.Hp ? p.w_scales[(int64_t)u.expert * p.Hp + n] : 0.0f;
+            // one warp waits and the others for it at their barrier; the four give up together
+            bool done = quarter != 0 || mbar_wait_held(&tfull[half], tph[half], s_abort, status);
+            if (big && quarter == 0 && done) done = mbar_wait_held(&tfull[1], tph[1], s_abort, status);
+            if (!quad_all(1 + second, done)) break;
+            tph[half] ^= 1u;
+            if (big) tph[1] ^= 1u;
+            tc_fence_after();
+            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kI8Acc;
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_rank_relaxed(&tempty[half], 0);
+                    if (big) mbar_arrive_rank_relaxed(&tempty[1], 0);
+                }
+            };
+            bool held = true;
+            for (int c0 = 32 * second; c0 < u.rows; c0 += 64) {
+                // (a row behind the segment's last is never stored)
+                const float rs = p.scales[min((int64_t)u.row0 + c0 + lane, p.nrows - 1)];
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tacc + c0, r);
+                if (c0 + 64 >= u.rows) {   // this warp has read all its runs: free them before the stores
+                    release();
+                    held = false;
+                }
+                quad_sync(1 + second);   // the run before has been read
+                uint16_t* col = reinterpret_cast<uint16_t*>(stg) + quarter * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float a = __uint_as_float(r[2 * j]) * ws * __shfl_sync(0xffffffffu, rs, 2 * j);
+                    const float b = __uint_as_float(r[2 * j + 1]) * ws * __shfl_sync(0xffffffffu, rs, 2 * j + 1);
+                    const uint32_t two = pack_bf16x2(a, b);
+                    col[(2 * j) * 128] = (uint16_t)two;
+                    col[(2 * j + 1) * 128] = (uint16_t)(two >> 16);
+                }
+                quad_sync(1 + second);   // the run is staged
+                const int row = quarter * 8 + (lane >> 4), no = n0 + (lane & 15) * 8;
+                const uint4* pc = reinterpret_cast<const uint4*>(stg) + quarter * 128 + lane;
+                uint16_t* out = p.y + ((int64_t)u.row0 + c0 + row) * p.Hp + no;
+                const int rest = no < p.Hp ? u.rows - c0 - row : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (2 * j < rest) *reinterpret_cast<uint4*>(out + (int64_t)(2 * j) * p.Hp) = pc[32 * j];
+            }
+            if (held) release();
+            if (!big) half ^= 1u;
+        }
+    }
+
+    __syncthreads();
+    if (*s_abort) {
+        // A wait gave up: what was started lands before shared memory and TMEM are released, each wait bounded.
+        if (warp == 0 && lane == 0) {
+            for (uint32_t i = 0; i < pr_armed && i < (uint32_t)kI8Ring; ++i) {
+                if (pr_i == 0) {
+                    pr_i = kI8Ring;
+                    pr_ph ^= 1u;
+                }
+                --pr_i;
+                mbar_drain(&wfull[pr_i], pr_ph);
+            }
+        } else if (warp == 1 && lane == 0 && lead) {
+            mma_commit_pair_lead(drain);
+            mbar_drain(drain, 0);
+        }
+        if (threadIdx.x == 0)
+            for (int i = 0; i < 20; ++i) __nanosleep(10000);
+        __syncthreads();
+    }
+    cluster_sync();   // neither CTA leaves while the other may still signal it or read its tiles
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kI8Tmem)
+                     : "memory");
+    }
+}
+
+constexpr size_t kI8Smem = 1024 + (size_t)kI8Ring * kI8W + (size_t)kI8Slots * kI8B + kI8EpiWarps / 4 * kI8Out +
+                           (2 * kI8Ring + 2 * kI8Slots + 5) * 8 + 16;
+static_assert(kI8Smem <= 227 * 1024, "shared memory");
+
+cudaLaunchConfig_t i8_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(kI8Threads, 1, 1);
+    cfg.dynamicSmemBytes = kI8Smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+template <int kWarps>
+void run_swiglu_i8(int64_t rows, int F8, const uint4* h, uint2* codes, float* scales, cudaStream_t st) {
+    constexpr int kRows = 8 / kWarps;
+    swiglu_i8_kernel<kWarps><<<(unsigned)((rows + kRows - 1) / kRows), kThreads, 0, st>>>(h, codes, scales, rows, F8);
+}
+
+}  // namespace
+
+// *clusters: pairs of CTAs that can be resident at once: the grid of the product.
+cudaError_t i8_setup(int device, int* clusters) {
+    cudaError_t err =
+        cudaFuncSetAttribute(grouped_gemm_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kI8Smem);
+    if (err != cudaSuccess) return err;
+    int nsm = 0;
+    err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, device);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = i8_config(nsm / 2, nullptr, attr);
+    return cudaOccupancyMaxActiveClusters(clusters, grouped_gemm_i8_kernel, &cfg);
+}
+
+cudaError_t launch_i8_weight(const Dims& d, const uint16_t* w, int8_t* codes, float* scales, cudaStream_t st) {
+    const dim3 grid((unsigned)(d.Hp / kWCols), (unsigned)d.E);
+    i8_weight_kernel<<<grid, kThreads, 0, st>>>(reinterpret_cast<const uint4*>(w), codes, scales, d.H, d.Hp);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dispatch_i8(const Dims& d, const Workspace& ws, const uint16_t* x, const int32_t* dest,
+                               int8_t* codes, float* scales, int sms, int num_sms, cudaStream_t st) {
+    const int64_t ntok = (int64_t)d.R * d.S;
+    const int pieces = d.H / 16;
+    const int threads = pieces < kDispatchThreads ? (pieces + 31) / 32 * 32 : kDispatchThreads;
+    // every token its own CTA, or, under an SM budget, what that many SMs hold
+    const int64_t cap = sms < num_sms ? (int64_t)sms * (2048 / threads < 32 ? 2048 / threads : 32) : (int64_t)INT32_MAX;
+    dispatch_i8_kernel<<<(unsigned)(ntok < cap ? ntok : cap), threads, 0, st>>>(
+        reinterpret_cast<const uint4*>(x), dest, reinterpret_cast<uint4*>(codes), scales, ntok, d.K, pieces,
+        (int64_t)d.R * d.C, ws.status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_i8(int64_t rows, int F, const uint16_t* h, int8_t* codes, float* scales, cudaStream_t st) {
+    const int F8 = F / 8;
+    const uint4* hp = reinterpret_cast<const uint4*>(h);
+    uint2* cp = reinterpret_cast<uint2*>(codes);
+    // as few warps a row as hold it (kActHold * 256 elements each), so that small rows share a CTA; more where
+    // the rows alone would leave SMs idle
+    int warps = 1;
+    while (warps < 8 && (F8 > warps * 32 * kActHold || (rows * warps < 152 * 16 && F8 > warps * 32))) warps *= 2;
+    switch (warps) {
+        case 1: run_swiglu_i8<1>(rows, F8, hp, cp, scales, st); break;
+        case 2: run_swiglu_i8<2>(rows, F8, hp, cp, scales, st); break;
+        case 4: run_swiglu_i8<4>(rows, F8, hp, cp, scales, st); break;
+        default: run_swiglu_i8<8>(rows, F8, hp, cp, scales, st); break;
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
+                                   const int8_t* codes, const float* scales, const int8_t* w_codes,
+                                   const float* w_scales, uint16_t* y, int clusters, cudaStream_t st) {
+    I8Params p;
+    p.tiles = ws.tiles;
+    p.ntiles = ws.ntiles;
+    p.slot_expert = slot_expert;
+    p.codes = codes;
+    p.scales = scales;
+    p.w_scales = w_scales;
+    p.y = y;
+    p.nrows = (int64_t)d.R * d.C;
+    p.E = d.E;
+    p.H = d.H;
+    p.Hp = d.Hp;
+    p.MT = (d.Hp + 127) / 128;
+    p.status = ws.status;
+    const uint64_t wd[3] = {(uint64_t)d.H, (uint64_t)d.Hp, (uint64_t)d.E};
+    CUtensorMap tmW;
+    if (!encode_u8(&tmW, w_codes, 3, wd, 128)) return cudaErrorInvalidValue;
+    const cudaError_t err = launch_row_tiles<kI8Rows>(d, ws, cu, st);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = i8_config(clusters, st, attr);
+    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel, tmW, p);
+}
+
+}  // namespace bep

@@ -10,10 +10,8 @@
 // A 512-byte weight-scale block is the order in which the tensor core takes the scales of 128
 // rows x 4 blocks of 32: row r, block k at byte (r % 32) * 16 + (r / 32) * 4 + k.
 
-#include <cudaTypedefs.h>
-
 #include "mxfmt.cuh"
-#include "ptx.cuh"
+#include "tiles.cuh"
 
 namespace bep {
 namespace {
@@ -210,48 +208,6 @@ struct MxParams {
     int32_t* status;
 };
 
-struct MxUnit {
-    int row0, rows, expert, mp;
-};
-
-// A cluster's units lie `ncl` apart in (tile, pair of output tiles) order, the pair fastest: a walk
-// over them without a division, since a unit may last only a few stages.
-struct MxWalk {
-    int unit, tile, mp;        // the next unit
-    int dtile, dmp, MP, ncl;   // its successor
-    __device__ __forceinline__ MxWalk(int first, int ncl_, int MP_)
-        : unit(first), tile(first / MP_), mp(first % MP_), dtile(ncl_ / MP_), dmp(ncl_ % MP_), MP(MP_), ncl(ncl_) {}
-    // The unit's tile and expert; expert < 0 for a slot whose expert is unknown (reported, skipped)
-    // and past the last unit.
-    __device__ __forceinline__ MxUnit take(const MxParams& p, int total) {
-        if (unit >= total) return MxUnit{0, 0, -1, 0};
-        const MTile t = p.tiles[tile];
-        MxUnit u;
-        u.row0 = t.row0;
-        u.rows = t.rows;
-        u.mp = mp;
-        u.expert = t.wsel >= 0 ? t.wsel : p.slot_expert[-1 - t.wsel];
-        if (u.expert >= p.E) u.expert = -1;
-        unit += ncl;
-        tile += dtile;
-        mp += dmp;
-        if (mp >= MP) {
-            mp -= MP;
-            ++tile;
-        }
-        return u;
-    }
-};
-
-__device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_t bar_cl, void* dst, int c0,
-                                                 int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cl), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
 // Descriptors reach the instructions as a low word (address in 16-byte units; operands: leading
 // offset 1) beside a constant high word. Operands: 8-row groups 1024 bytes apart, version 1, 128-byte
 // swizzle. Scales: 32 rows of 16 bytes, groups of 8 rows 128 bytes apart, version 1, no swizzle.
@@ -303,117 +259,6 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint32_t a, uint32_t b
                 "r"(d_tmem),
             "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(add)
             : "memory");
-}
-
-// Named barriers of four epilogue warps.
-__device__ __forceinline__ void quad_sync(int id) {
-    asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ bool quad_all(int id, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.and.pred p, %1, 128, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
-
-// Rows of a unit's MMA: N in steps of 32, half of it in each CTA.
-__device__ __forceinline__ int mma_rows(int rows) { return (rows + 31) & ~31; }
-
-// The work list: tiles of at most kMxRows rows of one segment, in (rank, row) order. One CTA; a
-// thread holds four segments at a time, all loaded at once (8 ranks x 433 segments: 3 us; a
-// thread with four consecutive segments loaded twice took 7). A table with any inconsistent
-// segment is refused as a whole.
-__global__ void __launch_bounds__(1024) mx_tiles_kernel(const int32_t* cu, Dims d, FastDiv nrow, Workspace ws) {
-    constexpr int kS = 4, kChunk = kS * 1024;
-    __shared__ int s_sum[kS * 32];
-    grid_launch_dependents();   // the product may set itself up
-    // cu may still be being written up to here: no load of it may come earlier, nor take the
-    // non-coherent path, which the compiler may move and which wants memory constant from the start
-    grid_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int items = d.R * d.NROW;
-    int a[kS], len[kS];
-    auto segments = [&](int base) {
-        int bad = 0;
-#pragma unroll
-        for (int r = 0; r < kS; ++r) {
-            const int i = base + r * 1024 + threadIdx.x;
-            a[r] = len[r] = 0;
-            if (i < items) {
-                const int u = (int)fast_div((uint32_t)i, nrow);
-                a[r] = cu[i + u];   // rank u's table has one more entry than segments
-                len[r] = cu[i + u + 1];
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kS; ++r) {
-            bad |= a[r] < 0 || len[r] < a[r] || (int64_t)len[r] > d.C;
-            len[r] -= a[r];
-        }
-        return bad;
-    };
-    int bad = 0;
-    for (int base = 0; base < items; base += kChunk) bad |= segments(base);
-    const bool ok = !__syncthreads_or(bad);
-    int total = 0;
-    for (int base = 0; base < items && ok; base += kChunk) {
-        if (items > kChunk) segments(base);
-        int before[kS];   // tiles of this warp's run of 32 segments before this lane's
-#pragma unroll
-        for (int r = 0; r < kS; ++r) {
-            const int n = (len[r] + kMxRows - 1) / kMxRows;
-            int incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            before[r] = incl - n;
-            if (lane == 31) s_sum[r * 32 + warp] = incl;
-        }
-        __syncthreads();
-        // every warp: exclusive prefix of the 128 runs; lane l of round r holds run (r, l)
-        int run_base[kS], sum = total;
-#pragma unroll
-        for (int r = 0; r < kS; ++r) {
-            const int n = s_sum[r * 32 + lane];
-            int incl = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            run_base[r] = sum + __shfl_sync(0xffffffffu, incl - n, warp);
-            sum += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        total = sum;
-#pragma unroll
-        for (int r = 0; r < kS; ++r) {
-            if (len[r] <= 0) continue;
-            const int i = base + r * 1024 + threadIdx.x;
-            const int u = (int)fast_div((uint32_t)i, nrow), rho = i - u * d.NROW;
-            MTile t;
-            t.wsel = rho < d.E ? rho : -(1 + u * d.B + (rho - d.E));
-            t.pad = 0;
-            MTile* out = ws.tiles + run_base[r] + before[r];
-            for (int m = 0; m < len[r]; m += kMxRows) {
-                t.row0 = (int32_t)(u * d.C + a[r] + m);
-                t.rows = min(kMxRows, len[r] - m);
-                *out++ = t;
-            }
-        }
-        __syncthreads();   // s_sum is written again by the next chunk
-    }
-    if (threadIdx.x == 0) {
-        if (!ok) set_status(ws.status, BEP_DERR_BOUNDS);
-        *ws.ntiles = ok ? total : 0;
-    }
 }
 
 __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
@@ -483,10 +328,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
-            MxWalk walk(cl0, ncl, MP);
-            MxUnit next = walk.take(p, total);   // read a unit ahead
+            UnitWalk walk(cl0, ncl, MP);
+            Unit next = walk.take(p, total);   // read a unit ahead
             for (int unit = cl0; unit < total && live; unit += ncl) {
-                const MxUnit u = next;
+                const Unit u = next;
                 next = walk.take(p, total);
                 if (u.expert < 0) {
                     if (lead) set_status(status, BEP_DERR_BOUNDS);
@@ -526,10 +371,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
             uint32_t old = 0, old_ph = 0, done = 0;    // the stage that used the slot before
             int it = 0;
             bool live = true;
-            MxWalk walk(cl0, ncl, MP);
-            MxUnit next = walk.take(p, total);   // read a unit ahead
+            UnitWalk walk(cl0, ncl, MP);
+            Unit next = walk.take(p, total);   // read a unit ahead
             for (int unit = cl0; unit < total && live; unit += ncl) {
-                const MxUnit u = next;
+                const Unit u = next;
                 next = walk.take(p, total);
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
@@ -593,12 +438,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         const int mine = warp - 2;
         const int pieces = (nst + 1) / 2;
         const uint4* src[kC] = {};
-        MxWalk l_walk(cl0, ncl, MP);   // the load cursor: unit, piece and rows
+        UnitWalk l_walk(cl0, ncl, MP);   // the load cursor: unit, piece and rows
         int l_piece = pieces + mine, l_rows = 0;
         auto load = [&](uint4* v) {
             while (l_piece >= pieces) {   // the next unit that has a piece for this warp
                 if (l_walk.unit >= total) return;
-                const MxUnit u = l_walk.take(p, total);
+                const Unit u = l_walk.take(p, total);
                 if (u.expert < 0) continue;
                 l_piece -= pieces;
                 if (l_piece >= pieces) continue;   // all of this unit's are the other warp's
@@ -620,10 +465,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         uint32_t s = 0, ph = 0;
         bool live = true;
         int own = mine;   // this warp's next piece of the unit
-        MxWalk walk(cl0, ncl, MP);
-        MxUnit u = walk.take(p, total);
+        UnitWalk walk(cl0, ncl, MP);
+        Unit u = walk.take(p, total);
         for (int unit = cl0; unit < total && live; unit += ncl) {
-            const MxUnit cur = u;
+            const Unit cur = u;
             u = walk.take(p, total);
             if (cur.expert < 0) continue;
             const int N = mma_rows(cur.rows);
@@ -679,10 +524,10 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
         const int quarter = warp & 3, second = (warp - 4) >> 2;
         uint8_t* stg = smO + second * kMxOut;
         int it = 0;
-        MxWalk walk(cl0, ncl, MP);
-        MxUnit next = walk.take(p, total);
+        UnitWalk walk(cl0, ncl, MP);
+        Unit next = walk.take(p, total);
         for (int unit = cl0; unit < total; unit += ncl) {
-            const MxUnit u = next;
+            const Unit u = next;
             next = walk.take(p, total);
             if (u.expert < 0) continue;
             const int acc = it & 1;
@@ -773,22 +618,6 @@ bool encode_scales(CUtensorMap* m, const void* base, uint64_t blocks) {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
                m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), d, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// u8 tensor of `dims` (innermost first, dense), 128-byte boxes of
-// `box_rows` rows, 128-byte swizzle.
-bool encode_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, uint32_t box_rows) {
-    void* fn = tensor_map_encoder();
-    if (!fn) return false;
-    cuuint64_t d[3], strides[2];
-    cuuint32_t box[3] = {128, box_rows, 1}, estr[3] = {1, 1, 1};
-    for (int i = 0; i < rank; ++i) d[i] = dims[i];
-    strides[0] = d[0];
-    if (rank == 3) strides[1] = d[0] * d[1];
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
-               m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -888,17 +717,7 @@ cudaError_t launch_grouped_gemm_mx(const Dims& d, const Workspace& ws, const int
     if (!encode_scales(&tmS, w_scales, (uint64_t)d.E * p.MT * p.KB)) return cudaErrorInvalidValue;
     for (int i = 0; i < 4; ++i)
         if (!encode_u8(&tmX[i], codes, 2, xd, boxes[i])) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t tc = {};
-    cudaLaunchAttribute early;
-    tc.gridDim = dim3(1, 1, 1);
-    tc.blockDim = dim3(1024, 1, 1);
-    tc.stream = st;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    tc.attrs = &early;
-    tc.numAttrs = 1;
-    const cudaError_t err =
-        cudaLaunchKernelEx(&tc, mx_tiles_kernel, cu, d, make_fast_div((uint32_t)d.NROW), ws);
+    const cudaError_t err = launch_row_tiles<kMxRows>(d, ws, cu, st);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = mx_config(clusters, st, attr);
