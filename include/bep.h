@@ -437,7 +437,7 @@ int bep_swiglu_int(bep_ctx* ctx, const uint16_t* h, int32_t F, int8_t* codes, fl
  * BEP_DERR_BOUNDS.
  *   cu_seqlens [R, E+B+1]; slot_expert [R, B]; codes, scales as bep_dispatch_int or bep_swiglu_int (F = H) wrote
  *   them; w_codes, w_scales from bep_int_quantize_weight; y [R*S*K, H'] bf16 out.
- * BEP_ERR_SIZE: 2^31 or more work units of 128 rows x 128 outputs. BEP_ERR_CUDA also where the device cannot
+ * BEP_ERR_SIZE: 2^31 or more work units of 64 rows x 128 outputs. BEP_ERR_CUDA also where the device cannot
  * hold the kernel's pairs of CTAs. */
 int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const int8_t* codes,
                         const float* scales, const int8_t* w_codes, const float* w_scales, uint16_t* y,

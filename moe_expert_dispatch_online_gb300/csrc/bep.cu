@@ -62,6 +62,7 @@ int bep::make_dims(const bep_config* c, bep::Dims* d) {
     d->NC = c->R * d->NCH;
     d->NROW = c->E + c->B;
     d->max_tiles = (int)(rsk / bep::kBM + (int64_t)c->R * d->NROW + 1);
+    d->tile_cap = (int)(rsk / 64 + (int64_t)c->R * d->NROW + 1);
     return BEP_OK;
 }
 
@@ -119,7 +120,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     add(R * NROW, 4);               // lens
     add(E + 1, 4);                  // pfirst
     for (int i = 0; i < 5; ++i) add(NP, 4);
-    add((size_t)d.max_tiles, sizeof(bep::MTile));
+    add((size_t)d.tile_cap, sizeof(bep::MTile));
     add(1, 4);                      // ntiles
     add(nslots + 1, 4);             // rg_expert
     add(nslots + 1, 4);             // rg_first
@@ -144,7 +145,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ws.prank = carve<int32_t>(p, NP);
     ws.prow = carve<int32_t>(p, NP);
     ws.pbase = carve<int32_t>(p, NP);
-    ws.tiles = carve<bep::MTile>(p, (size_t)d.max_tiles);
+    ws.tiles = carve<bep::MTile>(p, (size_t)d.tile_cap);
     ws.ntiles = carve<int32_t>(p, 1);
     ws.rg_expert = carve<int32_t>(p, nslots + 1);
     ws.rg_first = carve<int32_t>(p, nslots + 1);
@@ -494,7 +495,7 @@ int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t*
         !aligned(w_codes, 16) || !aligned(w_scales, 4) || !aligned(y, 16))
         return BEP_ERR_ALIGN;
     // work units (row tiles x 128-column output tiles) are counted in 32 bits
-    if (ctx->d.max_tiles * (int64_t)((ctx->d.Hp + 127) / 128) >= ((int64_t)1 << 31)) return BEP_ERR_SIZE;
+    if (ctx->d.tile_cap * (int64_t)((ctx->d.Hp + 127) / 128) >= ((int64_t)1 << 31)) return BEP_ERR_SIZE;
     if (ctx->i8_clusters < 0) {   // nothing here touches the stream, so the first call may be a captured one
         int clusters = 0;
         if (bep::i8_setup(ctx->device, &clusters) != cudaSuccess) {

@@ -54,6 +54,7 @@ struct Dims {
     int NC;         // chunks in total
     int NROW;       // E + B
     int max_tiles;  // GEMM m-tiles upper bound
+    int tile_cap;   // entries of the work list: tiles of 64 rows, the smallest any product makes
 };
 
 // configuration checks shared by the entry points (bep.cu)

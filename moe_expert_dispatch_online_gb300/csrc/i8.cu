@@ -275,34 +275,41 @@ __global__ void __launch_bounds__(kThreads) swiglu_i8_kernel(const uint4* __rest
 // them once (1 byte) and not three times; the rows of one segment are the N operand (32..256), in shared memory.
 // A cluster of two CTAs shares a tile of 256 outputs x N rows (cta_group::2): CTA r holds outputs 128 r.. and
 // converts half of the rows.
-//   warp 0       TMA: weight codes of 128 outputs, 128 reduction steps a stage
-//   warp 1       (CTA 0) tcgen05.mma, A from TMEM
-//   warps 2-9    two groups of four that take the stages in turn: a thread turns one output's 128 codes and
-//                128 bytes of row codes (read a turn ahead) into fp16
-//   warps 10-17  epilogue: TMEM, scaled, to bf16 y
-// TMEM: two accumulators of 128 rows, or one of 256, and kI8Slots stages of weights.
+//   warp 0        TMA: weight codes of 128 outputs, 128 reduction steps a stage
+//   warp 1        (CTA 0) tcgen05.mma, A from TMEM
+//   warps 2-9     weights: two groups of four take the stages in turn; a thread turns one output's 128 codes
+//   warps 10-17   rows: two groups of four in turn; a thread turns up to 128 codes, read a turn ahead
+//   warps 18-25   epilogue: TMEM, scaled, to bf16 y
+// The four kinds of warps only meet at barriers whose signals take about 500 cycles between the CTAs, so the
+// operand stages (kSlots) have to cover filling, signalling, multiplying and freeing one.
 //   barrier    owner   arrivals
 //   wfull[i]   each    the producer's expect_tx + TMA bytes
-//   wempty[i]  each    a group's four warps
-//   ready[s]   CTA 0   a group's four warps of each CTA
+//   wempty[i]  each    a weight group's four warps
+//   ready[s]   CTA 0   a weight group's and a row group's four warps of each CTA
 //   free[s]    both    the MMA thread's multicast commit
 //   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
 //   tempty[a]  CTA 0   the 8 epilogue warps of each CTA
-constexpr int kI8Rows = 256;                    // rows of a tile at most
 constexpr int kI8K = 128;                       // reduction elements a stage
-constexpr int kI8Ring = 6;                      // stages of weight codes under way
-constexpr int kI8Slots = 3;                     // stages of fp16 operands
 constexpr int kI8W = 128 * kI8K;                // bytes: 128 outputs' codes
-constexpr int kI8B = kI8Rows / 2 * kI8K * 2;    // bytes: half of the rows in fp16
-constexpr int kI8Sub = kI8B / 2;                // 64 reduction steps of them
-constexpr int kI8Groups = 2;
 constexpr int kI8EpiWarps = 8;
-constexpr int kI8Threads = 32 * (2 + 4 * kI8Groups + kI8EpiWarps);
+constexpr int kI8Threads = 32 * (2 + 8 + 8 + kI8EpiWarps);
 constexpr int kI8Out = 32 * 256;                // bytes: four epilogue warps' 32 rows x 128 outputs
 constexpr int kI8Tmem = 512;
-constexpr int kI8Acc = 128;                     // TMEM columns of an accumulator
-constexpr int kI8ABase = 2 * kI8Acc, kI8ACols = kI8K / 2;
-static_assert(kI8ABase + kI8Slots * kI8ACols <= kI8Tmem, "TMEM");
+
+// kRows: rows of a tile at most. Fewer rows leave room for more stages under way.
+template <int kRows>
+struct I8Cfg {
+    static constexpr int kAcc = kRows < 128 ? kRows : 128;     // TMEM columns of an accumulator, of which there are two
+    static constexpr int kSlots = kRows <= 64 ? 6 : 4;         // stages of fp16 operands
+    static constexpr int kRing = kRows <= 64 ? 8 : kRows <= 128 ? 7 : 5;   // stages of weight codes under way
+    static constexpr int kB = kRows / 2 * kI8K * 2;            // bytes: half of the rows in fp16
+    static constexpr int kSub = kB / 2;                        // 64 reduction steps of them
+    static constexpr int kABase = 2 * kAcc, kACols = kI8K / 2;
+    static constexpr size_t kSmem = 1024 + (size_t)kRing * kI8W + (size_t)kSlots * kB + kI8EpiWarps / 4 * kI8Out +
+                                    (2 * kRing + 2 * kSlots + 5) * 8 + 16;
+    static_assert(kABase + kSlots * kACols <= kI8Tmem, "TMEM");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
 
 struct I8Params {
     const MTile* tiles;
@@ -372,19 +379,22 @@ __device__ __forceinline__ void i8x16_to_f16(const uint4& v, uint32_t* out) {
     i8x4_to_f16(v.w, out + 6);
 }
 
+template <int kRows>
 __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                         const I8Params p) {
+    using C = I8Cfg<kRows>;
+    constexpr int kRing = C::kRing, kSlots = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* smW = smem;
-    uint8_t* smB = smW + kI8Ring * kI8W;
-    uint8_t* smO = smB + kI8Slots * kI8B;
+    uint8_t* smB = smW + kRing * kI8W;
+    uint8_t* smO = smB + kSlots * C::kB;
     uint64_t* wfull = reinterpret_cast<uint64_t*>(smO + kI8EpiWarps / 4 * kI8Out);
-    uint64_t* wempty = wfull + kI8Ring;
-    uint64_t* ready = wempty + kI8Ring;
-    uint64_t* free_ = ready + kI8Slots;
-    uint64_t* tfull = free_ + kI8Slots;
+    uint64_t* wempty = wfull + kRing;
+    uint64_t* ready = wempty + kRing;
+    uint64_t* free_ = ready + kSlots;
+    uint64_t* tfull = free_ + kSlots;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -396,12 +406,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kI8Ring; ++i) {
+        for (int i = 0; i < kRing; ++i) {
             mbar_init(&wfull[i], 1);
             mbar_init(&wempty[i], 4);
         }
-        for (int s = 0; s < kI8Slots; ++s) {
-            mbar_init(&ready[s], 8);
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&ready[s], 16);
             mbar_init(&free_[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -452,7 +462,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                     mbar_arrive_expect_tx(&wfull[pr_i], kI8W);
                     ++pr_armed;
                     tma_load_3d(&tmW, &wfull[pr_i], smW + pr_i * kI8W, k * kI8K, mt * 128, u.expert);
-                    if (++pr_i == kI8Ring) {
+                    if (++pr_i == kRing) {
                         pr_i = 0;
                         pr_ph ^= 1u;
                     }
@@ -472,13 +482,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                 next = walk.take(p, total);
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
-                const bool big = N > kI8Acc;
+                const bool big = N > C::kAcc;
                 if (big) half = 0;
                 if (!mbar_wait_held<true>(&tempty[half], aph[half], s_abort, status)) break;
                 if (big && !mbar_wait_held<true>(&tempty[1], aph[1], s_abort, status)) break;
                 aph[half] ^= 1u;
                 if (big) aph[1] ^= 1u;
-                const uint32_t dt = tmem_base + half * kI8Acc;
+                const uint32_t dt = tmem_base + half * C::kAcc;
                 const uint32_t idesc = idesc_f16(N);
                 for (int k = 0; k < nst; ++k) {
                     if (!mbar_wait_held<true>(&ready[s], ph, s_abort, status)) {
@@ -486,20 +496,20 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = tmem_base + kI8ABase + s * kI8ACols;
-                    const uint32_t b = smem_u32(smB + s * kI8B);
+                    const uint32_t a = tmem_base + C::kABase + s * C::kACols;
+                    const uint32_t b = smem_u32(smB + s * C::kB);
                     const int steps = min(kI8K, p.H - k * kI8K) / 16;   // 4 or 8
 #pragma unroll
                     for (int kk = 0; kk < kI8K / 16; ++kk)
                         if (kk < steps)
-                            mma_f16_pair_ts(dt, a + kk * 8, sdesc_sw128(b + (kk >> 2) * kI8Sub + (kk & 3) * 32, 16, 1024),
+                            mma_f16_pair_ts(dt, a + kk * 8, sdesc_sw128(b + (kk >> 2) * C::kSub + (kk & 3) * 32, 16, 1024),
                                             idesc, (k | kk) != 0);
                     mma_commit_pair(&free_[s]);
                     if (k == nst - 1) {
                         mma_commit_pair(&tfull[half]);
                         if (big) mma_commit_pair(&tfull[1]);
                     }
-                    if (++s == kI8Slots) {
+                    if (++s == kSlots) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -507,48 +517,87 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                 if (!big) half ^= 1u;
             }
         }
-    } else if (warp < 2 + 4 * kI8Groups) {
+    } else if (warp < 10) {
         const int group = (warp - 2) >> 2, quarter = warp & 3;   // four consecutive warps: each quarter of TMEM's lanes once
         const int n = quarter * 32 + lane;                       // output of this thread, lane of TMEM
-        // rows: 8 lanes take 128 bytes of one, a warp 4 and the group 16 at a time
-        const int rsub = quarter * 4 + (lane >> 3), piece = lane & 7;
+        uint32_t i = group, iph = 0, s = group, sph = 0;         // ring stage and operand slot of this turn
+        int turn = 0;
+        bool live = true;
+        UnitWalk walk(cl0, ncl, MP);
+        for (int unit = cl0; unit < total && live; unit += ncl) {
+            if (walk.take(p, total).expert < 0) continue;
+            for (int k = 0; k < nst; ++k, turn ^= 1) {
+                if (turn != group) continue;
+                if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status)) ||
+                    !__all_sync(0xffffffffu, mbar_wait_held(&wfull[i], iph, s_abort, status))) {
+                    live = false;
+                    break;
+                }
+                const uint8_t* wrow = smW + i * kI8W + n * 128;
+                const uint32_t ta = tmem_base + ((uint32_t)(quarter * 32) << 16) + C::kABase + s * C::kACols;
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t f[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        i8x16_to_f16(*reinterpret_cast<const uint4*>(wrow + (((4 * q + j) ^ (n & 7)) << 4)), f + 8 * j);
+                    tmem_st_32x32b_x32(ta + 32 * q, f);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&wempty[i]);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_rank_shared(&ready[s], 0);
+                i += 2;
+                if (i >= kRing) {
+                    i -= kRing;
+                    iph ^= 1u;
+                }
+                s += 2;
+                if (s >= kSlots) {
+                    s -= kSlots;
+                    sph ^= 1u;
+                }
+            }
+        }
+    } else if (warp < 18) {
+        const int group = (warp - 10) >> 2;
+        // 8 lanes take 128 bytes of a row, a warp 4 rows and the group 16 at a time
+        const int rsub = ((warp - 10) & 3) * 4 + (lane >> 3), piece = lane & 7;
         // a cursor over this group's stages, which are every second one across the units
         UnitWalk walk(cl0, ncl, MP);
         Unit u = walk.take(p, total);
-        int k = group, left = (total - cl0 + ncl - 1) / ncl;   // units from u on, u among them
-        if (total <= cl0) left = 0;
-        auto settle = [&]() {   // to the unit that holds stage k
+        int k = group, left = total > cl0 ? (total - cl0 + ncl - 1) / ncl : 0;   // units from u on, u among them
+        uint4 v[kRows / 32];
+        int half = 0;
+        auto load = [&]() {   // this turn's codes, from the unit that holds stage k
             while (left > 0 && (u.expert < 0 || k >= nst)) {
                 if (u.expert >= 0) k -= nst;
                 u = walk.take(p, total);
                 --left;
             }
-        };
-        uint4 v[8];
-        auto load = [&](int half, int64_t row0, int kk) {   // written while this kernel was starting: no __ldg
-            const bool in = kk * kI8K + piece * 16 < p.H;
+            if (left <= 0) return;
+            half = mma_rows(u.rows) / 2;
+            const int h = k * kI8K + piece * 16;
+            const int64_t row0 = (int64_t)u.row0 + (int)rank * half + rsub;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (16 * j < half) {
+            for (int j = 0; j < kRows / 32; ++j)
+                if (16 * j < half) {   // written while this kernel was starting: no __ldg
                     const int64_t row = min(row0 + 16 * j, p.nrows - 1);
-                    v[j] = in ? *reinterpret_cast<const uint4*>(p.codes + row * p.H + kk * kI8K + piece * 16)
-                              : make_uint4(0, 0, 0, 0);
+                    v[j] = h < p.H ? *reinterpret_cast<const uint4*>(p.codes + row * p.H + h) : make_uint4(0, 0, 0, 0);
                 }
         };
-        settle();
-        int half = 0;
-        if (left > 0) {
-            half = mma_rows(u.rows) / 2;
-            load(half, (int64_t)u.row0 + (int)rank * half + rsub, k);
-        }
-        uint32_t i = group, iph = 0, s = group, sph = 0;   // ring stage and operand slot of this turn
+        load();
+        uint32_t s = group, sph = 0;   // operand slot of this turn
         while (left > 0) {
             if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status))) break;
-            // rows: 16 codes a lane become two 16-byte pieces of a row of 64 fp16 (128-byte swizzle); lanes 4-7 of
+            // 16 codes a lane become two 16-byte pieces of a row of 64 fp16 (128-byte swizzle); lanes 4-7 of
             // eight store their second piece first, so that eight lanes touch all 32 banks
-            uint8_t* sub = smB + s * kI8B + (piece >> 2) * kI8Sub;
+            uint8_t* sub = smB + s * C::kB + (piece >> 2) * C::kSub;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < kRows / 32; ++j)
                 if (16 * j < half) {
                     uint32_t f[8];
                     i8x16_to_f16(v[j], f);
@@ -558,39 +607,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                     *reinterpret_cast<uint4*>(row + (((c + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
                     *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
                 }
-            k += kI8Groups;
-            settle();
-            if (left > 0) {
-                half = mma_rows(u.rows) / 2;
-                load(half, (int64_t)u.row0 + (int)rank * half + rsub, k);
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait_held(&wfull[i], iph, s_abort, status))) break;
-            const uint8_t* wrow = smW + i * kI8W + n * 128;
-            const uint32_t ta = tmem_base + ((uint32_t)(quarter * 32) << 16) + kI8ABase + s * kI8ACols;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t f[32];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    i8x16_to_f16(*reinterpret_cast<const uint4*>(wrow + (((4 * q + j) ^ (n & 7)) << 4)), f + 8 * j);
-                tmem_st_32x32b_x32(ta + 32 * q, f);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&wempty[i]);
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            k += 2;
+            load();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_rank_shared(&ready[s], 0);
-            i += kI8Groups;
-            if (i >= kI8Ring) {
-                i -= kI8Ring;
-                iph ^= 1u;
-            }
-            s += kI8Groups;
-            if (s >= kI8Slots) {
-                s -= kI8Slots;
+            s += 2;
+            if (s >= kSlots) {
+                s -= kSlots;
                 sph ^= 1u;
             }
         }
@@ -598,7 +622,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
         // Four warps, one for each quarter of TMEM's lanes, own every second run of 32 rows. A lane holds one
         // output of 32 rows, and a row's outputs lie together in y, so the run is turned in shared memory and
         // leaves as whole rows of 256 bytes, 16 a lane.
-        const int quarter = warp & 3, second = (warp - 2 - 4 * kI8Groups) >> 2;
+        const int quarter = warp & 3, second = (warp - 18) >> 2;
         uint8_t* stg = smO + second * kI8Out;
         uint32_t half = 0, tph[2] = {0, 0};
         UnitWalk walk(cl0, ncl, MP);
@@ -607,7 +631,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
             const Unit u = next;
             next = walk.take(p, total);
             if (u.expert < 0) continue;
-            const bool big = mma_rows(u.rows) > kI8Acc;
+            const bool big = mma_rows(u.rows) > C::kAcc;
             if (big) half = 0;
             const int n0 = (2 * u.mp + (int)rank) * 128;
             const int n = n0 + quarter * 32 + lane;
@@ -619,7 +643,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
             tph[half] ^= 1u;
             if (big) tph[1] ^= 1u;
             tc_fence_after();
-            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kI8Acc;
+            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * C::kAcc;
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -666,9 +690,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
     if (*s_abort) {
         // A wait gave up: what was started lands before shared memory and TMEM are released, each wait bounded.
         if (warp == 0 && lane == 0) {
-            for (uint32_t i = 0; i < pr_armed && i < (uint32_t)kI8Ring; ++i) {
+            for (uint32_t i = 0; i < pr_armed && i < (uint32_t)kRing; ++i) {
                 if (pr_i == 0) {
-                    pr_i = kI8Ring;
+                    pr_i = kRing;
                     pr_ph ^= 1u;
                 }
                 --pr_i;
@@ -690,15 +714,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
     }
 }
 
-constexpr size_t kI8Smem = 1024 + (size_t)kI8Ring * kI8W + (size_t)kI8Slots * kI8B + kI8EpiWarps / 4 * kI8Out +
-                           (2 * kI8Ring + 2 * kI8Slots + 5) * 8 + 16;
-static_assert(kI8Smem <= 227 * 1024, "shared memory");
-
+template <int kRows>
 cudaLaunchConfig_t i8_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.blockDim = dim3(kI8Threads, 1, 1);
-    cfg.dynamicSmemBytes = kI8Smem;
+    cfg.dynamicSmemBytes = I8Cfg<kRows>::kSmem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -711,6 +732,22 @@ cudaLaunchConfig_t i8_config(int clusters, cudaStream_t st, cudaLaunchAttribute*
     return cfg;
 }
 
+template <int kRows>
+cudaError_t i8_attributes() {
+    return cudaFuncSetAttribute(grouped_gemm_i8_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)I8Cfg<kRows>::kSmem);
+}
+
+template <int kRows>
+cudaError_t run_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const CUtensorMap& tmW, const I8Params& p,
+                        int clusters, cudaStream_t st) {
+    const cudaError_t err = launch_row_tiles<kRows>(d, ws, cu, st);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = i8_config<kRows>(clusters, st, attr);
+    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel<kRows>, tmW, p);
+}
+
 template <int kWarps>
 void run_swiglu_i8(int64_t rows, int F8, const uint4* h, uint2* codes, float* scales, cudaStream_t st) {
     constexpr int kRows = 8 / kWarps;
@@ -719,17 +756,18 @@ void run_swiglu_i8(int64_t rows, int F8, const uint4* h, uint2* codes, float* sc
 
 }  // namespace
 
-// *clusters: pairs of CTAs that can be resident at once: the grid of the product.
+// *clusters: pairs of CTAs that can be resident at once (an SM holds one CTA of any kind): the grid of the product.
 cudaError_t i8_setup(int device, int* clusters) {
-    cudaError_t err =
-        cudaFuncSetAttribute(grouped_gemm_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kI8Smem);
+    cudaError_t err = i8_attributes<64>();
+    if (err == cudaSuccess) err = i8_attributes<128>();
+    if (err == cudaSuccess) err = i8_attributes<256>();
     if (err != cudaSuccess) return err;
     int nsm = 0;
     err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, device);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = i8_config(nsm / 2, nullptr, attr);
-    return cudaOccupancyMaxActiveClusters(clusters, grouped_gemm_i8_kernel, &cfg);
+    cudaLaunchConfig_t cfg = i8_config<256>(nsm / 2, nullptr, attr);
+    return cudaOccupancyMaxActiveClusters(clusters, grouped_gemm_i8_kernel<256>, &cfg);
 }
 
 cudaError_t launch_i8_weight(const Dims& d, const uint16_t* w, int8_t* codes, float* scales, cudaStream_t st) {
@@ -788,11 +826,11 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
     const uint64_t wd[3] = {(uint64_t)d.H, (uint64_t)d.Hp, (uint64_t)d.E};
     CUtensorMap tmW;
     if (!encode_u8(&tmW, w_codes, 3, wd, 128)) return cudaErrorInvalidValue;
-    const cudaError_t err = launch_row_tiles<kI8Rows>(d, ws, cu, st);
-    if (err != cudaSuccess) return err;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = i8_config(clusters, st, attr);
-    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel, tmW, p);
+    // Rows a tile by the mean segment: a tile of fewer rows leaves room for more weight codes under way.
+    const int64_t mean = p.nrows / d.E;
+    if (mean <= 48) return run_gemm_i8<64>(d, ws, cu, tmW, p, clusters, st);
+    if (mean <= 96) return run_gemm_i8<128>(d, ws, cu, tmW, p, clusters, st);
+    return run_gemm_i8<256>(d, ws, cu, tmW, p, clusters, st);
 }
 
 }  // namespace bep
