@@ -18,39 +18,39 @@ namespace {
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------------ format
-// A row's grid: values are multiplied by the power of two `up`, which brings the largest to [1, 4) (and
-// far smaller ones to 0, which their integer is anyway), so that 127 v and the quotient stay inside fp32.
-// 127 v is exact for a bf16 v, and a quotient of two such numbers is a tie or at least 2^-16 of itself
-// away from one, so that one rounding of the division never decides an integer.
+// A row's grid: values are multiplied by the power of two `up`, which brings the largest to [1, 4) (and far
+// smaller ones to 0, which their integer is anyway), then by c = 127 / m: the product is within 2^-22 of 127 v / m.
+// Of two bf16 numbers that quotient is a tie k + 1/2 or at least 2^-17 of itself away from one, so its mantissa is
+// rounded to 19 bits before it becomes an integer: what was a tie is one again, and nothing else becomes one.
 struct Grid {
-    float up, m, scale;
+    float up, c, scale;
 };
 __device__ __forceinline__ Grid grid_of(uint32_t amax_bits) {
     Grid g;
     if (amax_bits >= 0x7f800000u) {   // an infinity or a NaN: every value of the row is NaN
-        g.up = 0.0f;
-        g.m = 1.0f;
+        g.up = g.c = 0.0f;
         g.scale = __uint_as_float(0x7fc00000u);
         return g;
     }
     const float m = __uint_as_float(amax_bits);
-    const int b = (int)(amax_bits >> 23);
-    g.up = __uint_as_float((uint32_t)max(254 - b, 1) << 23);
-    g.m = amax_bits ? m * g.up : 1.0f;
+    g.up = __uint_as_float((uint32_t)max(254 - (int)(amax_bits >> 23), 1) << 23);
+    g.c = amax_bits ? __fdiv_rn(127.0f, m * g.up) : 0.0f;
     g.scale = __fdiv_rn(m, 127.0f);
     return g;
 }
-// 0 for a row with an infinity or a NaN (up is 0: v * up is 0 or NaN, which converts to 0)
-__device__ __forceinline__ int code_of(float v, const Grid& g) {
-    return __float2int_rn(__fdiv_rn(127.0f * (v * g.up), g.m));
+// The integer is in the low byte: adding 1.5 * 2^23 rounds to the nearest one, ties to even. (A row whose values
+// are NaN is cleared by its writer.)
+__device__ __forceinline__ uint32_t code_of(float v, const Grid& g) {
+    const uint32_t q = (__float_as_uint(v * g.up * g.c) + 8u) & 0xfffffff0u;
+    return __float_as_uint(__uint_as_float(q) + 12582912.0f);
 }
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-    return __byte_perm(__byte_perm((uint32_t)a, (uint32_t)b, 0x0040), __byte_perm((uint32_t)c, (uint32_t)d, 0x0040),
-                       0x5410);
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 __device__ __forceinline__ uint2 codes8(const float* f, const Grid& g) {
-    return make_uint2(pack4(code_of(f[0], g), code_of(f[1], g), code_of(f[2], g), code_of(f[3], g)),
-                      pack4(code_of(f[4], g), code_of(f[5], g), code_of(f[6], g), code_of(f[7], g)));
+    const uint2 r = make_uint2(pack4(code_of(f[0], g), code_of(f[1], g), code_of(f[2], g), code_of(f[3], g)),
+                               pack4(code_of(f[4], g), code_of(f[5], g), code_of(f[6], g), code_of(f[7], g)));
+    return g.up == 0.0f ? make_uint2(0, 0) : r;
 }
 // Largest magnitude of eight bf16, as two bf16 bit patterns in a word (NaN above infinity above all).
 __device__ __forceinline__ uint32_t top2(const uint4& v) {
@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads) i8_weight_kernel(const uint4* __rest
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const Grid g = s_grid[8 * v + j];
-                s_codes[8 * v + j][r] = pack4(code_of(f[0][j], g), code_of(f[1][j], g), code_of(f[2][j], g), code_of(f[3][j], g));
+                const uint32_t q = pack4(code_of(f[0][j], g), code_of(f[1][j], g), code_of(f[2][j], g), code_of(f[3][j], g));
+                s_codes[8 * v + j][r] = g.up == 0.0f ? 0 : q;
             }
         }
         __syncthreads();
@@ -135,7 +136,10 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s_warp) {
 
 // codes[dest[tok, k]], scales[dest[tok, k]] = i8(x[tok]). A CTA per token: a thread holds kHold pieces of 16
 // elements between the two passes over them, and what lies beyond (rows of more than 8192 * kHold) it reads again.
-constexpr int kDispatchThreads = 512, kHold = 2;
+#ifndef DHOLD
+#define DHOLD 2
+#endif
+constexpr int kDispatchThreads = 512, kHold = DHOLD;
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_i8_kernel(const uint4* __restrict__ x,
                                                                        const int32_t* __restrict__ dest,
                                                                        uint4* __restrict__ codes,
@@ -151,25 +155,27 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_i8_kernel(const uin
             dl = dest[tok * K + lane];
             ok = dl >= 0 && (int64_t)dl < nrows;
         }
-        const unsigned m = __ballot_sync(0xffffffffu, ok);
-        if (m != 0xffffffffu && threadIdx.x == 0) set_status(status, BEP_DERR_BOUNDS);
         const uint4* src = x + tok * pieces * 2;
         uint4 a[kHold], b[kHold];
-        uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < kHold; ++j) {
             const int p = threadIdx.x + j * blockDim.x;
             a[j] = b[j] = make_uint4(0, 0, 0, 0);
             if (p < pieces) {
-                a[j] = __ldg(src + 2 * p);
-                b[j] = __ldg(src + 2 * p + 1);
+                a[j] = __ldcs(src + 2 * p);
+                b[j] = __ldcs(src + 2 * p + 1);
             }
-            top = __vmaxu2(top, __vmaxu2(top2(a[j]), top2(b[j])));
         }
+        const unsigned m = __ballot_sync(0xffffffffu, ok);
+        if (m != 0xffffffffu && threadIdx.x == 0) set_status(status, BEP_DERR_BOUNDS);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) top = __vmaxu2(top, __vmaxu2(top2(a[j]), top2(b[j])));
         for (int p = threadIdx.x + kHold * blockDim.x; p < pieces; p += blockDim.x)
             top = __vmaxu2(top, __vmaxu2(top2(__ldg(src + 2 * p)), top2(__ldg(src + 2 * p + 1))));
         const Grid g = grid_of(block_max(top_f32(top), s_warp));
-        auto put = [&](const uint4& lo, const uint4& hi, int p) {
+        if (threadIdx.x < K && ok) scales[dl] = g.scale;
+        auto codes16 = [&](const uint4& lo, const uint4& hi) {
             float f[16];
             bf16x8_to_f32(lo, f);
             bf16x8_to_f32(hi, f + 8);
@@ -177,22 +183,19 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_i8_kernel(const uin
             return make_uint4(c0.x, c0.y, c1.x, c1.y);
         };
 #pragma unroll
-        for (int j = 0; j < kHold; ++j) {
-            const int p = threadIdx.x + j * blockDim.x;
-            a[j] = put(a[j], b[j], p);
-        }
+        for (int j = 0; j < kHold; ++j) a[j] = codes16(a[j], b[j]);
         for (int k = 0; k < K; ++k) {
             const int64_t row = __shfl_sync(0xffffffffu, dl, k);
             if (!((m >> k) & 1u)) continue;
+            uint4* out = codes + row * pieces;
 #pragma unroll
             for (int j = 0; j < kHold; ++j) {
                 const int p = threadIdx.x + j * blockDim.x;
-                if (p < pieces) codes[row * pieces + p] = a[j];
+                if (p < pieces) out[p] = a[j];
             }
-            if (threadIdx.x == 0) scales[row] = g.scale;
         }
         for (int p = threadIdx.x + kHold * blockDim.x; p < pieces; p += blockDim.x) {
-            const uint4 c = put(__ldg(src + 2 * p), __ldg(src + 2 * p + 1), p);
+            const uint4 c = codes16(__ldg(src + 2 * p), __ldg(src + 2 * p + 1));
             for (int k = 0; k < K; ++k)
                 if ((m >> k) & 1u) codes[(int64_t)dest[tok * K + k] * pieces + p] = c;
         }
@@ -300,12 +303,13 @@ constexpr int kI8Tmem = 512;
 template <int kRows>
 struct I8Cfg {
     static constexpr int kAcc = kRows < 128 ? kRows : 128;     // TMEM columns of an accumulator, of which there are two
-    static constexpr int kSlots = kRows <= 64 ? 6 : 4;         // stages of fp16 operands
-    static constexpr int kRing = kRows <= 64 ? 8 : kRows <= 128 ? 7 : 5;   // stages of weight codes under way
+    static constexpr int kSlots = kRows <= 64 ? 6 : kRows <= 128 ? 4 : 3;   // stages of fp16 operands
+    static constexpr int kRing = kRows <= 64 ? 8 : kRows <= 128 ? 6 : 3;    // stages of codes under way
+    static constexpr int kStage = kI8W + kRows / 2 * kI8K;     // bytes: outputs' codes, half of the rows' codes
     static constexpr int kB = kRows / 2 * kI8K * 2;            // bytes: half of the rows in fp16
     static constexpr int kSub = kB / 2;                        // 64 reduction steps of them
     static constexpr int kABase = 2 * kAcc, kACols = kI8K / 2;
-    static constexpr size_t kSmem = 1024 + (size_t)kRing * kI8W + (size_t)kSlots * kB + kI8EpiWarps / 4 * kI8Out +
+    static constexpr size_t kSmem = 1024 + (size_t)kRing * kStage + (size_t)kSlots * kB + kI8EpiWarps / 4 * kI8Out +
                                     (2 * kRing + 2 * kSlots + 5) * 8 + 16;
     static_assert(kABase + kSlots * kACols <= kI8Tmem, "TMEM");
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -315,7 +319,6 @@ struct I8Params {
     const MTile* tiles;
     const int32_t* ntiles;
     const int32_t* slot_expert;
-    const int8_t* codes;
     const float* scales;
     const float* w_scales;
     uint16_t* y;
@@ -380,15 +383,17 @@ __device__ __forceinline__ void i8x16_to_f16(const uint4& v, uint32_t* out) {
 }
 
 template <int kRows>
-__global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                                        const I8Params p) {
+__global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX16,
+    const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX64,
+    const __grid_constant__ CUtensorMap tmX128, const I8Params p) {
     using C = I8Cfg<kRows>;
     constexpr int kRing = C::kRing, kSlots = C::kSlots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t* smW = smem;
-    uint8_t* smB = smW + kRing * kI8W;
+    uint8_t* smB = smW + kRing * C::kStage;
     uint8_t* smO = smB + kSlots * C::kB;
     uint64_t* wfull = reinterpret_cast<uint64_t*>(smO + kI8EpiWarps / 4 * kI8Out);
     uint64_t* wempty = wfull + kRing;
@@ -404,11 +409,15 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
     const bool lead = rank == 0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmW)) : "memory");
+    if (threadIdx.x == 32) {
+        const CUtensorMap* maps[] = {&tmW, &tmX16, &tmX32, &tmX64, &tmX128};
+        for (const CUtensorMap* m : maps)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&wfull[i], 1);
-            mbar_init(&wempty[i], 4);
+            mbar_init(&wempty[i], 8);
         }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&ready[s], 16);
@@ -454,14 +463,19 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                     continue;
                 }
                 const int mt = 2 * u.mp + (int)rank;   // past H' for the last odd tile: zeros
+                const int half = mma_rows(u.rows) / 2, row = u.row0 + (int)rank * half;
+                const CUtensorMap* tmX = half <= 16 ? &tmX16 : half <= 32 ? &tmX32 : half <= 64 ? &tmX64 : &tmX128;
+                const int bytes = kI8W + (half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128) * kI8K;
                 for (int k = 0; k < nst; ++k) {
                     if (!mbar_wait_held(&wempty[pr_i], pr_ph ^ 1u, s_abort, status)) {
                         live = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&wfull[pr_i], kI8W);
+                    mbar_arrive_expect_tx(&wfull[pr_i], bytes);
                     ++pr_armed;
-                    tma_load_3d(&tmW, &wfull[pr_i], smW + pr_i * kI8W, k * kI8K, mt * 128, u.expert);
+                    uint8_t* stage = smW + pr_i * C::kStage;
+                    tma_load_3d(&tmW, &wfull[pr_i], stage, k * kI8K, mt * 128, u.expert);
+                    tma_load_2d(tmX, &wfull[pr_i], stage + kI8W, k * kI8K, row);
                     if (++pr_i == kRing) {
                         pr_i = 0;
                         pr_ph ^= 1u;
@@ -533,7 +547,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
                     live = false;
                     break;
                 }
-                const uint8_t* wrow = smW + i * kI8W + n * 128;
+                const uint8_t* wrow = smW + i * C::kStage + n * 128;
                 const uint32_t ta = tmem_base + ((uint32_t)(quarter * 32) << 16) + C::kABase + s * C::kACols;
                 tc_fence_after();
 #pragma unroll
@@ -564,58 +578,60 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(const __
         }
     } else if (warp < 18) {
         const int group = (warp - 10) >> 2;
-        // 8 lanes take 128 bytes of a row, a warp 4 rows and the group 16 at a time
-        const int rsub = ((warp - 10) & 3) * 4 + (lane >> 3), piece = lane & 7;
-        // a cursor over this group's stages, which are every second one across the units
+        // 4 lanes take 64 bytes of a row, a warp 8 rows and the group 32 at a time. Eight lanes in a run take rows r and
+        // r ^ 5, whose swizzled pieces of 16 bytes lie in different banks in the codes and in the fp16 both.
+        const int run = lane >> 2, piece = lane & 3;
+        const int r = ((warp - 10) & 3) * 8 + ((run >> 1) ^ ((run & 1) * 5)), x = r & 7;
+        const int from = kI8W + r * 128, to = r * 128;
+        const int f0 = (piece ^ x) << 4, f1 = f0 ^ 64;                                // pieces of 16 codes
+        const int t0 = ((2 * piece) ^ x) << 4, t1 = t0 ^ 16;                          // pieces of 8 fp16
+        uint32_t i = group, iph = 0, s = group, sph = 0;   // ring stage and operand slot of this turn
+        int turn = 0;
+        bool live = true;
         UnitWalk walk(cl0, ncl, MP);
-        Unit u = walk.take(p, total);
-        int k = group, left = total > cl0 ? (total - cl0 + ncl - 1) / ncl : 0;   // units from u on, u among them
-        uint4 v[kRows / 32];
-        int half = 0;
-        auto load = [&]() {   // this turn's codes, from the unit that holds stage k
-            while (left > 0 && (u.expert < 0 || k >= nst)) {
-                if (u.expert >= 0) k -= nst;
-                u = walk.take(p, total);
-                --left;
-            }
-            if (left <= 0) return;
-            half = mma_rows(u.rows) / 2;
-            const int h = k * kI8K + piece * 16;
-            const int64_t row0 = (int64_t)u.row0 + (int)rank * half + rsub;
-#pragma unroll
-            for (int j = 0; j < kRows / 32; ++j)
-                if (16 * j < half) {   // written while this kernel was starting: no __ldg
-                    const int64_t row = min(row0 + 16 * j, p.nrows - 1);
-                    v[j] = h < p.H ? *reinterpret_cast<const uint4*>(p.codes + row * p.H + h) : make_uint4(0, 0, 0, 0);
+        for (int unit = cl0; unit < total && live; unit += ncl) {
+            const Unit u = walk.take(p, total);
+            if (u.expert < 0) continue;
+            const int half = mma_rows(u.rows) / 2;
+            for (int k = 0; k < nst; ++k, turn ^= 1) {
+                if (turn != group) continue;
+                if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status)) ||
+                    !__all_sync(0xffffffffu, mbar_wait_held(&wfull[i], iph, s_abort, status))) {
+                    live = false;
+                    break;
                 }
-        };
-        load();
-        uint32_t s = group, sph = 0;   // operand slot of this turn
-        while (left > 0) {
-            if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status))) break;
-            // 16 codes a lane become two 16-byte pieces of a row of 64 fp16 (128-byte swizzle); lanes 4-7 of
-            // eight store their second piece first, so that eight lanes touch all 32 banks
-            uint8_t* sub = smB + s * C::kB + (piece >> 2) * C::kSub;
+                // 16 codes become two 16-byte pieces of a row of 64 fp16 (128-byte swizzle)
+                const uint8_t* codes = smW + i * C::kStage + from;
+                uint8_t* slot = smB + s * C::kB + to;
 #pragma unroll
-            for (int j = 0; j < kRows / 32; ++j)
-                if (16 * j < half) {
-                    uint32_t f[8];
-                    i8x16_to_f16(v[j], f);
-                    const int r = 16 * j + rsub, c = 2 * (piece & 3), odd = piece >> 2;
-                    uint8_t* row = sub + r * 128;
-                    const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-                    *reinterpret_cast<uint4*>(row + (((c + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
-                    *reinterpret_cast<uint4*>(row + (((c + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
+                for (int j = 0; j < (kRows / 2 + 31) / 32; ++j)
+                    if (32 * j + r < half) {
+                        const uint4 c0 = *reinterpret_cast<const uint4*>(codes + j * 4096 + f0);
+                        const uint4 c1 = *reinterpret_cast<const uint4*>(codes + j * 4096 + f1);
+                        uint32_t f[8];
+                        i8x16_to_f16(c0, f);
+                        *reinterpret_cast<uint4*>(slot + j * 4096 + t0) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4*>(slot + j * 4096 + t1) = make_uint4(f[4], f[5], f[6], f[7]);
+                        i8x16_to_f16(c1, f);
+                        *reinterpret_cast<uint4*>(slot + C::kSub + j * 4096 + t0) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4*>(slot + C::kSub + j * 4096 + t1) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&wempty[i]);
+                    mbar_arrive_rank_shared(&ready[s], 0);
                 }
-            k += 2;
-            load();
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive_rank_shared(&ready[s], 0);
-            s += 2;
-            if (s >= kSlots) {
-                s -= kSlots;
-                sph ^= 1u;
+                i += 2;
+                if (i >= kRing) {
+                    i -= kRing;
+                    iph ^= 1u;
+                }
+                s += 2;
+                if (s >= kSlots) {
+                    s -= kSlots;
+                    sph ^= 1u;
+                }
             }
         }
     } else {
@@ -739,13 +755,14 @@ cudaError_t i8_attributes() {
 }
 
 template <int kRows>
-cudaError_t run_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const CUtensorMap& tmW, const I8Params& p,
+cudaError_t run_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const CUtensorMap& tmW, const CUtensorMap* tmX,
+                        const I8Params& p,
                         int clusters, cudaStream_t st) {
     const cudaError_t err = launch_row_tiles<kRows>(d, ws, cu, st);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = i8_config<kRows>(clusters, st, attr);
-    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel<kRows>, tmW, p);
+    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel<kRows>, tmW, tmX[0], tmX[1], tmX[2], tmX[3], p);
 }
 
 template <int kWarps>
@@ -780,7 +797,8 @@ cudaError_t launch_dispatch_i8(const Dims& d, const Workspace& ws, const uint16_
                                int8_t* codes, float* scales, int sms, int num_sms, cudaStream_t st) {
     const int64_t ntok = (int64_t)d.R * d.S;
     const int pieces = d.H / 16;
-    const int threads = pieces < kDispatchThreads ? (pieces + 31) / 32 * 32 : kDispatchThreads;
+    const int want = (pieces + kHold - 1) / kHold;
+    const int threads = want < kDispatchThreads ? (want + 31) / 32 * 32 : kDispatchThreads;
     // every token its own CTA, or, under an SM budget, what that many SMs hold
     const int64_t cap = sms < num_sms ? (int64_t)sms * (2048 / threads < 32 ? 2048 / threads : 32) : (int64_t)INT32_MAX;
     dispatch_i8_kernel<<<(unsigned)(ntok < cap ? ntok : cap), threads, 0, st>>>(
@@ -813,7 +831,6 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
     p.tiles = ws.tiles;
     p.ntiles = ws.ntiles;
     p.slot_expert = slot_expert;
-    p.codes = codes;
     p.scales = scales;
     p.w_scales = w_scales;
     p.y = y;
@@ -824,13 +841,17 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
     p.MT = (d.Hp + 127) / 128;
     p.status = ws.status;
     const uint64_t wd[3] = {(uint64_t)d.H, (uint64_t)d.Hp, (uint64_t)d.E};
-    CUtensorMap tmW;
+    const uint64_t xd[2] = {(uint64_t)d.H, (uint64_t)d.R * d.C};
+    const uint32_t boxes[4] = {16, 32, 64, 128};
+    CUtensorMap tmW, tmX[4];
     if (!encode_u8(&tmW, w_codes, 3, wd, 128)) return cudaErrorInvalidValue;
+    for (int i = 0; i < 4; ++i)
+        if (!encode_u8(&tmX[i], codes, 2, xd, boxes[i])) return cudaErrorInvalidValue;
     // Rows a tile by the mean segment: a tile of fewer rows leaves room for more weight codes under way.
     const int64_t mean = p.nrows / d.E;
-    if (mean <= 48) return run_gemm_i8<64>(d, ws, cu, tmW, p, clusters, st);
-    if (mean <= 96) return run_gemm_i8<128>(d, ws, cu, tmW, p, clusters, st);
-    return run_gemm_i8<256>(d, ws, cu, tmW, p, clusters, st);
+    if (mean <= 48) return run_gemm_i8<64>(d, ws, cu, tmW, tmX, p, clusters, st);
+    if (mean <= 96) return run_gemm_i8<128>(d, ws, cu, tmW, tmX, p, clusters, st);
+    return run_gemm_i8<256>(d, ws, cu, tmW, tmX, p, clusters, st);
 }
 
 }  // namespace bep
