@@ -309,7 +309,7 @@ struct I8Cfg {
     static constexpr int kB = kRows / 2 * kI8K * 2;            // bytes: half of the rows in fp16
     static constexpr int kSub = kB / 2;                        // 64 reduction steps of them
     static constexpr int kABase = 2 * kAcc, kACols = kI8K / 2;
-    static constexpr size_t kSmem = 1024 + (size_t)kRing * kStage + (size_t)kSlots * kB + kI8EpiWarps / 4 * kI8Out +
+    static constexpr size_t kSmem = 1024 + (size_t)kRing * kStage + (size_t)kSlots * kB + kI8EpiWarps / 4 * kI8Out + kRows * 4 +
                                     (2 * kRing + 2 * kSlots + 5) * 8 + 16;
     static_assert(kABase + kSlots * kACols <= kI8Tmem, "TMEM");
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -395,7 +395,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
     uint8_t* smW = smem;
     uint8_t* smB = smW + kRing * C::kStage;
     uint8_t* smO = smB + kSlots * C::kB;
-    uint64_t* wfull = reinterpret_cast<uint64_t*>(smO + kI8EpiWarps / 4 * kI8Out);
+    float* smC = reinterpret_cast<float*>(smO + kI8EpiWarps / 4 * kI8Out);   // rows' scales of a unit
+    uint64_t* wfull = reinterpret_cast<uint64_t*>(smC + kRows);
     uint64_t* wempty = wfull + kRing;
     uint64_t* ready = wempty + kRing;
     uint64_t* free_ = ready + kSlots;
@@ -635,11 +636,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
             }
         }
     } else {
-        // Four warps, one for each quarter of TMEM's lanes, own every second run of 32 rows. A lane holds one
-        // output of 32 rows, and a row's outputs lie together in y, so the run is turned in shared memory and
-        // leaves as whole rows of 256 bytes, 16 a lane.
+        // Four warps, one for each quarter of TMEM's lanes, own every second run of 32 rows. A lane holds one output
+        // of 32 rows, and a row's outputs lie together in y, so the run is turned in shared memory, as words of two
+        // rows, and leaves as whole rows of 256 bytes, 16 a lane. The rows' scales come from shared memory, four
+        // to a load: the loads and stores of the warps that convert are what the epilogue competes with.
         const int quarter = warp & 3, second = (warp - 18) >> 2;
         uint8_t* stg = smO + second * kI8Out;
+        float* sc = smC + second * (kRows / 2);
         uint32_t half = 0, tph[2] = {0, 0};
         UnitWalk walk(cl0, ncl, MP);
         Unit next = walk.take(p, total);
@@ -652,6 +655,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
             const int n0 = (2 * u.mp + (int)rank) * 128;
             const int n = n0 + quarter * 32 + lane;
             const float ws = n < p.Hp ? p.w_scales[(int64_t)u.expert * p.Hp + n] : 0.0f;
+            // run `quarter` of this half's: the four warps have read the last unit's (a row behind the segment's
+            // last is never stored)
+            const int64_t srow = (int64_t)u.row0 + 32 * second + 64 * quarter + lane;
+            if (64 * quarter < kRows) sc[32 * quarter + lane] = p.scales[i64min(srow, p.nrows - 1)];
             // one warp waits and the others for it at their barrier; the four give up together
             bool done = quarter != 0 || mbar_wait_held(&tfull[half], tph[half], s_abort, status);
             if (big && quarter == 0 && done) done = mbar_wait_held(&tfull[1], tph[1], s_abort, status);
@@ -670,32 +677,43 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
             };
             bool held = true;
             for (int c0 = 32 * second; c0 < u.rows; c0 += 64) {
-                // (a row behind the segment's last is never stored)
-                const float rs = p.scales[min((int64_t)u.row0 + c0 + lane, p.nrows - 1)];
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tacc + c0, r);
                 if (c0 + 64 >= u.rows) {   // this warp has read all its runs: free them before the stores
                     release();
                     held = false;
                 }
-                quad_sync(1 + second);   // the run before has been read
-                uint16_t* col = reinterpret_cast<uint16_t*>(stg) + quarter * 32 + lane;
+                const float4* s4 = reinterpret_cast<const float4*>(sc + (c0 >> 6) * 32);
+                uint32_t two[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float a = __uint_as_float(r[2 * j]) * ws * __shfl_sync(0xffffffffu, rs, 2 * j);
-                    const float b = __uint_as_float(r[2 * j + 1]) * ws * __shfl_sync(0xffffffffu, rs, 2 * j + 1);
-                    const uint32_t two = pack_bf16x2(a, b);
-                    col[(2 * j) * 128] = (uint16_t)two;
-                    col[(2 * j + 1) * 128] = (uint16_t)(two >> 16);
+                for (int j = 0; j < 8; ++j) {
+                    const float4 f = s4[j];
+                    two[2 * j] = pack_bf16x2(__uint_as_float(r[4 * j]) * ws * f.x, __uint_as_float(r[4 * j + 1]) * ws * f.y);
+                    two[2 * j + 1] =
+                        pack_bf16x2(__uint_as_float(r[4 * j + 2]) * ws * f.z, __uint_as_float(r[4 * j + 3]) * ws * f.w);
                 }
-                quad_sync(1 + second);   // the run is staged
-                const int row = quarter * 8 + (lane >> 4), no = n0 + (lane & 15) * 8;
-                const uint4* pc = reinterpret_cast<const uint4*>(stg) + quarter * 128 + lane;
-                uint16_t* out = p.y + ((int64_t)u.row0 + c0 + row) * p.Hp + no;
-                const int rest = no < p.Hp ? u.rows - c0 - row : 0;
+                quad_sync(1 + second);   // the run before has been read, and this one's scales
+                uint32_t* col = reinterpret_cast<uint32_t*>(stg) + quarter * 32 + lane;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (2 * j < rest) *reinterpret_cast<uint4*>(out + (int64_t)(2 * j) * p.Hp) = pc[32 * j];
+                for (int j = 0; j < 16; ++j) col[j * 128] = two[j];
+                quad_sync(1 + second);   // the run is staged
+                // rows 2 j and 2 j + 1, j = 4 quarter + 2 i + (lane / 16): eight outputs a lane
+                const int j0 = quarter * 4 + (lane >> 4), no = n0 + (lane & 15) * 8;
+                const uint4* pc = reinterpret_cast<const uint4*>(stg) + j0 * 32 + (lane & 15) * 2;
+                uint16_t* out = p.y + ((int64_t)u.row0 + c0 + 2 * j0) * p.Hp + no;
+                const int rest = no < p.Hp ? u.rows - c0 - 2 * j0 : 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 a = pc[64 * i], b = pc[64 * i + 1];
+                    if (4 * i < rest)
+                        *reinterpret_cast<uint4*>(out + (int64_t)(4 * i) * p.Hp) =
+                            make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                       __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+                    if (4 * i + 1 < rest)
+                        *reinterpret_cast<uint4*>(out + (int64_t)(4 * i + 1) * p.Hp) =
+                            make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                       __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+                }
             }
             if (held) release();
             if (!big) half ^= 1u;
