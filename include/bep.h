@@ -443,6 +443,37 @@ int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t*
                         const float* scales, const int8_t* w_codes, const float* w_scales, uint16_t* y,
                         void* stream);
 
+/* Grouped products of any width, beside the plan's own projections: low-rank adapters of the experts, layers
+ * whose widths are not multiples of 64, rows that lie apart (one half of a [g | u] buffer). For rank u and every
+ * non-empty segment, e = rho for rho < E and slot_expert[u][rho - E] for a prefetch slot,
+ *   y[u*S*K + seg, :] = alpha * x[u*S*K + seg, :] @ W(e) + add[u*S*K + seg, :]
+ * W(e) = w[e] [K, N], or w[e]^T with w [E, N, K] where trans is 1 (the input gradient of the product with
+ * the same w). bf16 in, fp32 accumulation, one rounding to bf16 (nearest even). The widths are the call's own and
+ * have nothing to do with the context's H and H'. Rows of y outside every segment are not written; a bad
+ * cu_seqlens is refused as in bep_grouped_gemm. A non-empty slot segment without an expert in [0, E) is skipped and
+ * latches BEP_DERR_BOUNDS. The same call gives the same bits.
+ *   cu_seqlens [R, E+B+1]; slot_expert [R, B]; x [R*S*K, K], rows ldx elements apart; w [E, K, N] or [E, N, K]; add
+ *   [R*S*K, N], rows ldadd apart, or NULL; y [R*S*K, N] out, rows ldy apart. y may be add itself, with the same
+ *   stride, and otherwise overlaps nothing (BEP_ERR_ARG where it is x or w).
+ * BEP_ERR_ARG: K or N not a positive multiple of 8, a stride below its width or not a multiple of 8, an alpha that is
+ * not finite. BEP_ERR_SIZE: K or N above 2^24, a stride above 2^32, 2^27 or more row tiles (64 rows) x 64 columns, or
+ * experts x 128 x 64 columns. */
+int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x,
+                    int64_t ldx, int32_t K, const uint16_t* w, int32_t N, int32_t trans, float alpha,
+                    const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, void* stream);
+
+/* Gradient of w [E, K, N] in that product: with the rows of e in all its segments (home rows, prefetch slots and
+ * overflow rows, on every rank; nothing is left in a reduce buffer),
+ *   g[e] = alpha * sum over rows x[row]^T dy[row]         (accumulate 0; zeros for an expert without rows)
+ *   g[e] += the same                                      (accumulate 1)
+ * bf16 in, fp32 sums. In training and inference contexts alike. A bad cu_seqlens is refused as a whole (nothing is
+ * written), a slot without an expert skipped, as above. The gradient of a w used with trans 1 is this call with x
+ * and dy, K and N exchanged. The same call gives the same bits.
+ *   x [R*S*K, K], rows ldx apart; dy [R*S*K, N], rows lddy apart; g [E, K, N] fp32. Errors as above. */
+int bep_ragged_gemm_dw(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x,
+                       int64_t ldx, int32_t K, const uint16_t* dy, int64_t lddy, int32_t N, float alpha,
+                       int32_t accumulate, float* g, void* stream);
+
 /* SM budget of the token-moving kernels (dispatch, dispatch_mx, dispatch_int, combine, combine_bwd,
  * combine_dgates, dispatch_bwd): their grids are sized for `sms` SMs, so
  * the rest of the GPU stays free for concurrent work, as a communication

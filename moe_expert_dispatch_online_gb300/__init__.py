@@ -49,7 +49,7 @@ SYMBOLS = ("bep_create", "bep_destroy", "bep_plan", "bep_plan_noalloc", "bep_pre
            "bep_weights_destroy", "bep_reduce_grad", "bep_route", "bep_route_bwd", "bep_swiglu",
            "bep_swiglu_bwd", "bep_mx_quantize_weight", "bep_dispatch_mx", "bep_swiglu_mx",
            "bep_grouped_gemm_mx", "bep_int_quantize_weight", "bep_dispatch_int", "bep_swiglu_int",
-           "bep_grouped_gemm_int", "bep_set_comm_sms", "bep_wait_selftest",
+           "bep_grouped_gemm_int", "bep_ragged_gemm", "bep_ragged_gemm_dw", "bep_set_comm_sms", "bep_wait_selftest",
            "bep_status", "bep_clear_status", "bep_strerror")
 
 _lib = None
@@ -83,6 +83,7 @@ def load(path: str = LIB_PATH):
             raise ImportError(f"libbep.so not built ({path}); run __graft_entry__.build()")
         lib = ctypes.CDLL(path)
         vp, i32, p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p
+        i64, f32 = ctypes.c_int64, ctypes.c_float
         sig = {
             "bep_create": (ctypes.c_int, [ctypes.POINTER(_Config), ctypes.POINTER(vp)]),
             "bep_destroy": (None, [vp]),
@@ -119,6 +120,8 @@ def load(path: str = LIB_PATH):
             "bep_dispatch_int": (ctypes.c_int, [vp, p, p, p, p, vp]),
             "bep_swiglu_int": (ctypes.c_int, [vp, p, i32, p, p, vp]),
             "bep_grouped_gemm_int": (ctypes.c_int, [vp, p, p, p, p, p, p, p, vp]),
+            "bep_ragged_gemm": (ctypes.c_int, [vp, p, p, p, i64, i32, p, i32, i32, f32, p, i64, p, i64, vp]),
+            "bep_ragged_gemm_dw": (ctypes.c_int, [vp, p, p, p, i64, i32, p, i64, i32, f32, i32, p, vp]),
             "bep_status": (ctypes.c_int, [vp, ctypes.POINTER(i32), vp]),
             "bep_clear_status": (ctypes.c_int, [vp, vp]),
             "bep_strerror": (ctypes.c_char_p, [i32]),
@@ -742,6 +745,59 @@ def bep_grouped_gemm_int(ctx: Context, cu_seqlens, slot_expert, codes, scales, w
                                       *_i8_weight(c, w_codes, w_scales, "w_"),
                                       _arg(y, _bf16(), ctx._rows * c.Hp, "y"), _stream(stream)),
            "bep_grouped_gemm_int")
+
+
+def _rows_of(t, rows, name):
+    """Device pointer, width and row stride of a [rows, width] bf16 CUDA tensor whose rows are dense but may
+    lie apart (a slice of columns of a wider buffer)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _bf16():
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_bf16()}")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, width)")
+    width = t.shape[1]
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must lie together")
+    # the stride of a single row means nothing
+    return t.data_ptr(), width, t.stride(0) if rows > 1 else max(width, (t.stride(0) + 7) // 8 * 8)
+
+
+def bep_ragged_gemm(ctx: Context, cu_seqlens, slot_expert, x, w, y, trans=False, alpha=1.0, add=None, stream=None):
+    """y[seg] = alpha * x[seg] @ W(expert of seg) (+ add[seg]), W = w[e] with w [E, K, N], or w[e]^T with
+    w [E, N, K] where trans is true. x [rows, K], y and add [rows, N] may be column slices of wider
+    buffers; widths and strides are multiples of 8. add may be y itself."""
+    c = ctx.cfg
+    px, K, ldx = _rows_of(x, ctx._rows, "x")
+    py, N, ldy = _rows_of(y, ctx._rows, "y")
+    pa, lda = None, 0
+    if add is not None:
+        pa, Na, lda = _rows_of(add, ctx._rows, "add")
+        if Na != N:
+            raise ValueError(f"add has {Na} columns, expected {N}")
+    if tuple(w.shape) != ((c.E, N, K) if trans else (c.E, K, N)):
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected {(c.E, N, K) if trans else (c.E, K, N)}")
+    _check(load().bep_ragged_gemm(ctx.handle, _arg(cu_seqlens, _i32(), c.R * (c.E + c.B + 1), "cu_seqlens"),
+                                  _arg(slot_expert, _i32(), c.R * c.B, "slot_expert"), px, ldx, K,
+                                  _arg(w, _bf16(), c.E * K * N, "w"), N, int(bool(trans)), alpha, pa, lda, py, ldy,
+                                  _stream(stream)), "bep_ragged_gemm")
+
+
+def bep_ragged_gemm_dw(ctx: Context, cu_seqlens, slot_expert, x, dy, g, alpha=1.0, accumulate=False, stream=None):
+    """g[e] = (accumulate: +=) alpha * sum over e's rows of x[row]^T dy[row]: the gradient of w [E, K, N] in
+    bep_ragged_gemm, summed over every segment of an expert. x [rows, K], dy [rows, N], g fp32 [E, K, N]."""
+    c = ctx.cfg
+    px, K, ldx = _rows_of(x, ctx._rows, "x")
+    pd, N, ldd = _rows_of(dy, ctx._rows, "dy")
+    if tuple(g.shape) != (c.E, K, N):
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected {(c.E, K, N)}")
+    _check(load().bep_ragged_gemm_dw(ctx.handle, _arg(cu_seqlens, _i32(), c.R * (c.E + c.B + 1), "cu_seqlens"),
+                                     _arg(slot_expert, _i32(), c.R * c.B, "slot_expert"), px, ldx, K, pd, ldd, N,
+                                     alpha, int(bool(accumulate)), _arg(g, _f32(), c.E * K * N, "g"),
+                                     _stream(stream)), "bep_ragged_gemm_dw")
 
 
 def bep_status(ctx: Context, stream=None) -> int:

@@ -28,6 +28,7 @@ struct bep_ctx {
     int num_sms;
     int mx_clusters;   // pairs of CTAs of the 4-bit product that fit the device, 0: it cannot run
     int i8_clusters;   // the same of the 8-bit product, -1 until its first call
+    bool ragged_ready;   // the products of any width have been set up by their first call
     int comm_sms;   // SM budget of the token-moving kernels (0: every SM)
 };
 
@@ -126,6 +127,10 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     add(nslots + 1, 4);             // rg_first
     add(nslots + 1, 4);             // rg_slot
     add(1, 4);                      // rg_count
+    add(E + 1, 4);                  // seg_first
+    add(E, 4);                      // seg_blocks
+    add(bep::kRgTickets, 4);        // tickets
+    add((size_t)sms * bep::kRgPartCols * 128, 4);   // partial
     void* blob = nullptr;
     if (cudaMalloc(&blob, bytes) != cudaSuccess) return BEP_ERR_CUDA;
     if (cudaMemset(blob, 0, bytes) != cudaSuccess) {
@@ -151,6 +156,10 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ws.rg_first = carve<int32_t>(p, nslots + 1);
     ws.rg_slot = carve<int32_t>(p, nslots + 1);
     ws.rg_count = carve<int32_t>(p, 1);
+    ws.seg_first = carve<int32_t>(p, E + 1);
+    ws.seg_blocks = carve<int32_t>(p, E);
+    ws.tickets = carve<int32_t>(p, bep::kRgTickets);
+    ws.partial = carve<float>(p, (size_t)sms * bep::kRgPartCols * 128);
 
     bep_ctx* ctx = static_cast<bep_ctx*>(malloc(sizeof(bep_ctx)));
     if (!ctx) {
@@ -164,6 +173,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ctx->num_sms = sms;
     ctx->mx_clusters = mx_clusters;
     ctx->i8_clusters = -1;
+    ctx->ragged_ready = false;
     ctx->comm_sms = 0;
     *out = ctx;
     return BEP_OK;
@@ -507,6 +517,69 @@ int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t*
     if (ctx->i8_clusters < 1) return BEP_ERR_CUDA;
     return cuda_rc(bep::launch_grouped_gemm_i8(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales, w_codes,
                                                w_scales, y, ctx->i8_clusters, as_stream(stream)));
+}
+
+// Widths and row strides of the products of any width: multiples of 8 elements, so that rows start on 16 bytes.
+static int check_ragged(const bep_ctx* ctx, int32_t K, int32_t N, int64_t ldx, int64_t ldy, float alpha) {
+    if (!ctx || K < 8 || N < 8 || K % 8 != 0 || N % 8 != 0) return BEP_ERR_ARG;
+    if (ldx < K || ldy < N || ldx % 8 != 0 || ldy % 8 != 0) return BEP_ERR_ARG;
+    if (!(alpha - alpha == 0.0f)) return BEP_ERR_ARG;   // infinite or NaN
+    // units (row tiles, or 128 columns of an expert, by 64 columns) and parts of them are counted in 32 bits, a
+    // tensor map's strides in 40
+    const int64_t wide = K > N ? K : N, narrow = K > N ? N : K, most = (int64_t)1 << 27;
+    if (wide > ((int64_t)1 << 24) || ldx > ((int64_t)1 << 32) || ldy > ((int64_t)1 << 32)) return BEP_ERR_SIZE;
+    if (ctx->d.tile_cap * ((wide + 63) / 64) >= most) return BEP_ERR_SIZE;
+    if (ctx->d.E * ((wide + 127) / 128) * ((narrow + 63) / 64) >= most) return BEP_ERR_SIZE;
+    return BEP_OK;
+}
+
+static int ragged_ready(bep_ctx* ctx) {
+    if (ctx->ragged_ready) return BEP_OK;   // nothing here touches a stream: the first call may be a captured one
+    if (bep::ragged_setup() != cudaSuccess) {
+        cudaGetLastError();
+        return BEP_ERR_CUDA;
+    }
+    ctx->ragged_ready = true;
+    return BEP_OK;
+}
+
+int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x, int64_t ldx,
+                    int32_t K, const uint16_t* w, int32_t N, int32_t trans, float alpha, const uint16_t* add,
+                    int64_t ldadd, uint16_t* y, int64_t ldy, void* stream) {
+    BEP_RANGE("bep_ragged_gemm");
+    int rc = check_ragged(ctx, K, N, ldx, ldy, alpha);
+    if (rc) return rc;
+    if (trans != 0 && trans != 1) return BEP_ERR_ARG;
+    if (add && (ldadd < N || ldadd % 8 != 0)) return BEP_ERR_ARG;
+    if (ctx->d.C == 0) return BEP_OK;
+    if (!cu_seqlens || !slot_expert || !x || !w || !y || x == y || w == y) return BEP_ERR_ARG;
+    if (!aligned(cu_seqlens, 4) || !aligned(slot_expert, 4) || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) ||
+        !aligned(add, 16))
+        return BEP_ERR_ALIGN;
+    rc = ragged_ready(ctx);
+    if (rc) return rc;
+    return cuda_rc(bep::launch_ragged(ctx->d, ctx->ws, cu_seqlens, slot_expert, x, ldx, K, w, N, trans, alpha, add, ldadd,
+                                      y, ldy, ctx->num_sms, as_stream(stream)));
+}
+
+int bep_ragged_gemm_dw(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x,
+                       int64_t ldx, int32_t K, const uint16_t* dy, int64_t lddy, int32_t N, float alpha,
+                       int32_t accumulate, float* g, void* stream) {
+    BEP_RANGE("bep_ragged_gemm_dw");
+    int rc = check_ragged(ctx, K, N, ldx, lddy, alpha);
+    if (rc) return rc;
+    if (accumulate != 0 && accumulate != 1) return BEP_ERR_ARG;
+    if (ctx->d.C == 0 && accumulate) return BEP_OK;
+    if (!g) return BEP_ERR_ARG;
+    if (!aligned(g, 16)) return BEP_ERR_ALIGN;
+    if (ctx->d.C == 0)   // no rows: the gradient is zero
+        return cuda_rc(cudaMemsetAsync(g, 0, (size_t)ctx->d.E * K * N * sizeof(float), as_stream(stream)));
+    if (!cu_seqlens || !slot_expert || !x || !dy) return BEP_ERR_ARG;
+    if (!aligned(cu_seqlens, 4) || !aligned(slot_expert, 4) || !aligned(x, 16) || !aligned(dy, 16)) return BEP_ERR_ALIGN;
+    rc = ragged_ready(ctx);
+    if (rc) return rc;
+    return cuda_rc(bep::launch_ragged_dw(ctx->d, ctx->ws, cu_seqlens, slot_expert, x, ldx, K, dy, lddy, N, alpha,
+                                         accumulate, g, ctx->num_sms, as_stream(stream)));
 }
 
 int bep_wait_selftest(bep_ctx* ctx, int32_t timeout_us, void* stream) {

@@ -17,6 +17,9 @@ constexpr int kMaxK = 32;
 constexpr int kBM = 128;
 constexpr int kBK = 64;
 
+constexpr int kRgTickets = 1024;   // units of a reduction that is cut into parts: fewer than SMs
+constexpr int kRgPartCols = 64;    // columns of a part's tile at most
+
 // One GEMM m-tile: receive rows that share a weight row, at most 128, 256 (two m-tiles a unit) or 224 (4-bit
 // product) of them by the kernel that the list is for, fewer at a segment's end; for dW a whole segment.
 struct MTile {
@@ -44,6 +47,10 @@ struct Workspace {
     int32_t* rg_first;   // [R*B+1] first entry of each in rg_slot
     int32_t* rg_slot;    // [R*B] flat slot indices u*B + j, ascending per expert
     int32_t* rg_count;   // [1] number of such experts
+    int32_t* seg_first;  // [E+1] first segment of each expert in tiles (gradients of any width), -1: refused
+    int32_t* seg_blocks; // [E] blocks of 64 rows in them
+    int32_t* tickets;    // [kRgTickets] parts of a unit that have been left in `partial`
+    float* partial;      // [SMs][kRgPartCols][128] fp32 tiles of a reduction cut into parts
 };
 
 struct Dims {
@@ -140,6 +147,15 @@ cudaError_t launch_swiglu_i8(int64_t rows, int F, const uint16_t* h, int8_t* cod
 cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                                    const int8_t* codes, const float* scales, const int8_t* w_codes,
                                    const float* w_scales, uint16_t* y, int clusters, cudaStream_t st);
+
+// grouped products of any width (ragged.cu)
+cudaError_t ragged_setup();
+cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
+                          const uint16_t* x, int64_t ldx, int K, const uint16_t* w, int N, int trans, float alpha,
+                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, cudaStream_t st);
+cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
+                             const uint16_t* x, int64_t ldx, int K, const uint16_t* dy, int64_t lddy, int N, float alpha,
+                             int accumulate, float* g, int num_sms, cudaStream_t st);
 
 __device__ __forceinline__ int64_t i64max(int64_t a, int64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ int64_t i64min(int64_t a, int64_t b) { return a < b ? a : b; }

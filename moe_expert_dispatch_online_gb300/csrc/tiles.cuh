@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(1024) row_tiles_kernel(const int32_t* cu, Dims
     // non-coherent path, which the compiler may move and which wants memory constant from the start
     grid_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x < kRgTickets) ws.tickets[threadIdx.x] = 0;   // for the products that count parts
     const int items = d.R * d.NROW;
     int a[kS], len[kS];
     auto segments = [&](int base) {
