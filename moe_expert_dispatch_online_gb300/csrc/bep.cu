@@ -127,8 +127,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     add(nslots + 1, 4);             // rg_first
     add(nslots + 1, 4);             // rg_slot
     add(1, 4);                      // rg_count
-    add(E + 1, 4);                  // seg_first
-    add(E, 4);                      // seg_blocks
+    add(E + 1, 4);                  // blk_first
     add(bep::kRgTickets, 4);        // tickets
     add((size_t)sms * bep::kRgPartCols * 128, 4);   // partial
     void* blob = nullptr;
@@ -156,8 +155,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ws.rg_first = carve<int32_t>(p, nslots + 1);
     ws.rg_slot = carve<int32_t>(p, nslots + 1);
     ws.rg_count = carve<int32_t>(p, 1);
-    ws.seg_first = carve<int32_t>(p, E + 1);
-    ws.seg_blocks = carve<int32_t>(p, E);
+    ws.blk_first = carve<int32_t>(p, E + 1);
     ws.tickets = carve<int32_t>(p, bep::kRgTickets);
     ws.partial = carve<float>(p, (size_t)sms * bep::kRgPartCols * 128);
 
@@ -608,6 +606,9 @@ int bep_status(bep_ctx* ctx, int32_t* device_err, void* stream) {
 
 int bep_clear_status(bep_ctx* ctx, void* stream) {
     if (!ctx) return BEP_ERR_ARG;
+    // after a wait that ran out, counts of parts may have been left as well
+    const cudaError_t e = cudaMemsetAsync(ctx->ws.tickets, 0, bep::kRgTickets * sizeof(int32_t), as_stream(stream));
+    if (e != cudaSuccess) return BEP_ERR_CUDA;
     return cuda_rc(cudaMemsetAsync(ctx->ws.status, 0, sizeof(int32_t), as_stream(stream)));
 }
 

@@ -47,8 +47,7 @@ struct Workspace {
     int32_t* rg_first;   // [R*B+1] first entry of each in rg_slot
     int32_t* rg_slot;    // [R*B] flat slot indices u*B + j, ascending per expert
     int32_t* rg_count;   // [1] number of such experts
-    int32_t* seg_first;  // [E+1] first segment of each expert in tiles (gradients of any width), -1: refused
-    int32_t* seg_blocks; // [E] blocks of 64 rows in them
+    int32_t* blk_first;  // [E+1] first block of each expert in tiles (gradients of any width), -1: refused
     int32_t* tickets;    // [kRgTickets] parts of a unit that have been left in `partial`
     float* partial;      // [SMs][kRgPartCols][128] fp32 tiles of a reduction cut into parts
 };

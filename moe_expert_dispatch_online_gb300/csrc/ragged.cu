@@ -23,39 +23,50 @@ namespace {
 constexpr int kRgThreads = 32 * 10;
 constexpr int kRgA = 128 * 128;          // bytes: 128 rows (columns) x 64 reduction steps
 constexpr int kRgChunk = 64 * 128;       // bytes: 64 x 64 elements
-constexpr int kRgBox = 32 * 128;         // bytes: an epilogue warp's 32 x 32 fp32
+constexpr int kRgBox = 32 * 128;         // bytes: an epilogue warp's box of 32 rows of 128 bytes
 constexpr int kRgTmem = 512;
 constexpr int kRgMaxStages = 12;
-constexpr int kRgBars = 2 * kRgMaxStages + 5;
-constexpr int kRgRing = 227 * 1024 - 1024 - 8 * kRgBox - kRgBars * 8 - 32;   // bytes of stages
+constexpr int kRgMaxAdds = 4;
 constexpr int kRgMaxParts = 16;
+constexpr int kRgLocal = 256;            // row tiles of a small call, whose list each CTA makes itself
+// Shared memory: up to 1 KB lost to alignment, 1 KB of barriers, then the ring and what the epilogue turns its boxes in.
+constexpr size_t kRgSmem = 227 * 1024;
+constexpr int kRgBytes = 225 * 1024;
+// The tensor core cuts its fp32 sum off at each step of 16 rows, always towards zero; a gradient's chain of steps is
+// therefore ended after this many blocks of 64 rows and added, rounded to nearest, to a sum in registers.
+constexpr int kRgChain = 4;
 
 struct RgParams {
     const MTile* tiles;
     const int32_t* ntiles;
+    const int32_t* cu;        // the table itself, where the CTAs make the list
     const int32_t* slot_expert;
     uint16_t* y;
-    const uint16_t* add;      // or null
+    const uint16_t* add;
     int64_t ldy, ldadd;
     float alpha;
     int E, N, kbn;            // output columns, reduction blocks of 64
     int BN, NT;               // columns of a tile, tiles
-    int stages, a_bytes, b_bytes;
+    FastDiv by_nt;
+    int tile_rows, local;
+    int R, B, NROW;
+    int64_t C;
+    int stages, a_bytes, b_bytes, adds, add_bytes;
     int32_t* tickets;
     float* partial;
     int32_t* status;
 };
 
 struct RgDwParams {
-    const MTile* segs;        // segments by expert, in (rank, row) order
+    const MTile* blocks;      // up to 64 rows of one segment, by expert, in (rank, row) order
     const int32_t* first;     // [E + 1]
-    const int32_t* blocks;    // [E], blocks of 64 rows
     float* g;
     int64_t g_expert;         // elements of an expert's gradient
     int64_t ldm, ldn;         // strides of g along the M side and the N side: one of them is 1
     float alpha;
     int E, Md, Nd;            // widths of the sides
-    int BN, MT, NT, parts;
+    int BN, MI, MT, NT, parts;   // columns of a tile, 128-row tiles of a unit, units along M and N
+    FastDiv by_parts, by_unit, by_nt;
     int stages, b_bytes;
     int accumulate;
     int32_t* tickets;
@@ -111,26 +122,29 @@ __device__ __forceinline__ bool epi_all(bool v) {
 // What both kernels set up and take down alike.
 struct Frame {
     uint8_t* ring;
-    uint8_t* boxes;
-    uint64_t *full, *empty, *tfull, *tempty, *drain;
+    uint64_t *full, *empty, *tfull, *tempty, *afull, *aempty, *drain;
     uint32_t* s_tmem;
     volatile int* s_abort;
     int* s_last;
+    int* s_rows;   // valid rows of each stage
     uint32_t tmem;
 };
 __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages) {
     Frame f;
     const uint32_t raw = smem_u32(smem_raw);
-    f.ring = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    f.boxes = f.ring + kRgRing / 1024 * 1024;
-    f.full = reinterpret_cast<uint64_t*>(f.boxes + 8 * kRgBox);
+    uint8_t* base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    f.ring = base + 1024;
+    f.full = reinterpret_cast<uint64_t*>(base);
     f.empty = f.full + kRgMaxStages;
     f.tfull = f.empty + kRgMaxStages;
     f.tempty = f.tfull + 2;
-    f.drain = f.tempty + 2;
+    f.afull = f.tempty + 2;
+    f.aempty = f.afull + kRgMaxAdds;
+    f.drain = f.aempty + kRgMaxAdds;
     f.s_tmem = reinterpret_cast<uint32_t*>(f.drain + 1);
     f.s_abort = reinterpret_cast<volatile int*>(f.s_tmem + 1);
     f.s_last = reinterpret_cast<int*>(f.s_tmem + 2);
+    f.s_rows = f.s_last + 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&f.full[s], 1);
@@ -139,6 +153,10 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages) {
         for (int a = 0; a < 2; ++a) {
             mbar_init(&f.tfull[a], 1);
             mbar_init(&f.tempty[a], 8);
+        }
+        for (int a = 0; a < kRgMaxAdds; ++a) {
+            mbar_init(&f.afull[a], 1);
+            mbar_init(&f.aempty[a], 8);
         }
         mbar_init(f.drain, 1);
         *f.s_abort = 0;
@@ -156,21 +174,35 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages) {
     f.tmem = *f.s_tmem;
     return f;
 }
-// pr_s, pr_ph, pr_armed: the producer's ring position and the stages that it armed.
-__device__ __forceinline__ void close_frame(const Frame& f, int stages, uint32_t pr_s, uint32_t pr_ph, uint32_t pr_armed) {
+// What the producer started: its place in a ring and how often it armed a barrier there.
+struct Started {
+    uint32_t at = 0, phase = 0, armed = 0;
+    __device__ __forceinline__ void step(uint32_t n) {
+        ++armed;
+        if (++at == n) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void drain(uint64_t* bars, uint32_t n) {
+        for (uint32_t i = 0; i < armed && i < n; ++i) {
+            if (at == 0) {
+                at = n;
+                phase ^= 1u;
+            }
+            --at;
+            mbar_drain(&bars[at], phase);
+        }
+    }
+};
+__device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds, Started ring, Started add) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
     if (*f.s_abort) {
         // A wait gave up: what was started lands before shared memory and TMEM are released, each wait bounded.
         if (warp == 0 && lane == 0) {
-            for (uint32_t i = 0; i < pr_armed && i < (uint32_t)stages; ++i) {
-                if (pr_s == 0) {
-                    pr_s = stages;
-                    pr_ph ^= 1u;
-                }
-                --pr_s;
-                mbar_drain(&f.full[pr_s], pr_ph);
-            }
+            ring.drain(f.full, stages);
+            if (adds) add.drain(f.afull, adds);
         } else if (warp == 1 && lane == 0) {
             mma_commit(f.drain);
             mbar_drain(f.drain, 0);
@@ -189,11 +221,14 @@ __device__ __forceinline__ float* part_tile(float* base, int slot) {
     return base + (int64_t)slot * (kPartRows * kRgPartCols);
 }
 // This thread's row, 32 columns: to a part's tile, and the sum of a unit's parts in their order.
-__device__ __forceinline__ void put_part(float* tile, int c0, int row, const uint32_t* r) {
+template <typename T>
+__device__ __forceinline__ void put_part(float* tile, int c0, int row, const T* r) {
+    static_assert(sizeof(T) == 4, "fp32 or its bits");
 #pragma unroll
-    for (int j = 0; j < 32; ++j) __stcg(tile + (c0 + j) * kPartRows + row, __uint_as_float(r[j]));
+    for (int j = 0; j < 32; ++j) __stcg(tile + (c0 + j) * kPartRows + row, *reinterpret_cast<const float*>(r + j));
 }
-__device__ __forceinline__ void sum_parts(float* base, int slot0, int parts, int c0, int row, uint32_t* r) {
+template <typename T>
+__device__ __forceinline__ void sum_parts(float* base, int slot0, int parts, int c0, int row, T* r) {
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __ldcg(part_tile(base, slot0) + (c0 + j) * kPartRows + row);
@@ -203,7 +238,7 @@ __device__ __forceinline__ void sum_parts(float* base, int slot0, int parts, int
         for (int j = 0; j < 32; ++j) v[j] += __ldcg(t + (c0 + j) * kPartRows + row);
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[j]);
+    for (int j = 0; j < 32; ++j) *reinterpret_cast<float*>(r + j) = v[j];
 }
 // True in the CTA that brings a unit's last part (all 8 epilogue warps call it, their parts written).
 __device__ __forceinline__ bool last_part(int32_t* ticket, int parts, int* s_last) {
@@ -213,6 +248,7 @@ __device__ __forceinline__ bool last_part(int32_t* ticket, int parts, int* s_las
         const int n = atomicAdd(ticket, 1);
         __threadfence();
         *s_last = n == parts - 1;
+        if (n == parts - 1) *ticket = 0;   // for the next call
     }
     epi_sync();
     const bool last = *s_last != 0;
@@ -221,72 +257,155 @@ __device__ __forceinline__ bool last_part(int32_t* ticket, int parts, int* s_las
 }
 
 // ------------------------------------------------------------------------ rows
+// The list of row_tiles_kernel for a table of few row tiles, made in shared memory by every CTA for itself, which
+// saves a launch: up to kRgLocal tiles in (rank, row) order; returns their number (0 for a bad table).
+__device__ __forceinline__ int local_tiles(const RgParams& p, MTile* out, int* s_warp) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int items = p.R * p.NROW, per = (items + kRgThreads - 1) / kRgThreads;
+    const int lo = min(items, t * per), hi = min(items, lo + per);
+    int n = 0, bad = 0;
+    auto segment = [&](int i, int* u, int* rho, int* a, int* b) {
+        *u = i / p.NROW;
+        *rho = i - *u * p.NROW;
+        *a = p.cu[i + *u];   // rank u's table has one more entry than segments
+        *b = p.cu[i + *u + 1];
+    };
+    for (int i = lo; i < hi; ++i) {
+        int u, rho, a, b;
+        segment(i, &u, &rho, &a, &b);
+        bad |= a < 0 || b < a || (int64_t)b > p.C;
+        n += (b - a + p.tile_rows - 1) / p.tile_rows;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) {
+        if (blockIdx.x == 0 && t == 0) set_status(p.status, BEP_DERR_BOUNDS);
+        return 0;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int at = incl - n, total = 0;
+    for (int w = 0; w < kRgThreads / 32; ++w) {
+        if (w < warp) at += s_warp[w];
+        total += s_warp[w];
+    }
+    if (n)
+        for (int i = lo; i < hi; ++i) {
+            int u, rho, a, b;
+            segment(i, &u, &rho, &a, &b);
+            for (; a < b; a += p.tile_rows, ++at)
+                if (at < kRgLocal)
+                    out[at] = MTile{(int32_t)(u * p.C + a), min(p.tile_rows, b - a),
+                                    rho < p.E ? rho : -(1 + u * p.B + (rho - p.E)), 0};
+        }
+    __syncthreads();
+    return min(total, kRgLocal);
+}
+
+// One map for each height of a box of rows.
+struct RowMaps {
+    CUtensorMap m16, m32, m64, m128;
+};
+__device__ __forceinline__ const CUtensorMap* map_for(const RowMaps& m, int rows) {
+    return rows <= 16 ? &m.m16 : rows <= 32 ? &m.m32 : rows <= 64 ? &m.m64 : &m.m128;
+}
+__device__ __forceinline__ int box_for(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
 // A unit: up to 128 rows of a segment x BN columns. A small tile leaves the accumulator's other rows to whatever the
 // stage holds behind its own; they are not stored.
-template <bool kTrans>
-__global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(
-    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX16,
-    const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX64,
-    const __grid_constant__ CUtensorMap tmX128, const RgParams p) {
+// kAdd: what the product is added to arrives by TMA, up to four units ahead, in boxes of 64 columns that the epilogue
+// then turns its outputs in.
+template <bool kTrans, bool kAdd>
+__global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                               const __grid_constant__ RowMaps tmX,
+                                                               const __grid_constant__ RowMaps tmAdd, const RgParams p) {
     extern __shared__ uint8_t smem_raw[];
+    grid_launch_dependents();
     Frame f = open_frame(smem_raw, p.stages);
     uint8_t* smA = f.ring;
     uint8_t* smB = smA + p.stages * p.a_bytes;
+    uint8_t* smT = smB + p.stages * p.b_bytes;   // kAdd: the units' boxes, else a box of each epilogue warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t pr_s = 0, pr_ph = 0, pr_armed = 0;
+    Started pr, ad;
     grid_wait();   // launched early: the work list and the rows are complete from here on
 
-    const int units = *p.ntiles * p.NT;
+    const MTile* tiles = p.tiles;
+    int ntiles;
+    if (p.local) {
+        MTile* list = reinterpret_cast<MTile*>(f.ring + kRgBytes - kRgLocal * sizeof(MTile));
+        ntiles = local_tiles(p, list, f.s_rows);
+        tiles = list;
+    } else {
+        ntiles = *p.ntiles;
+    }
+    const int units = ntiles * p.NT;
     int parts = 1;
     if (p.partial && units > 0) parts = max(1, min(min((int)gridDim.x / units, p.kbn / 4), kRgMaxParts));
     const int total = units * parts;
     struct Item {
         int row0, rows, expert, n0, unit, kb0, kb1;
     };
-    auto item_at = [&](int i) {
+    // A CTA's next tile is read a unit ahead: a unit may last no longer than the load.
+    auto unit_of = [&](int i) { return parts == 1 ? i : i / parts; };
+    auto tile_at = [&](int i) { return i < total ? tiles[fast_div(unit_of(i), p.by_nt)] : MTile{0, 0, 0, 0}; };
+    auto item_of = [&](int i, const MTile& t) {
         Item it;
-        it.unit = i / parts;
-        const int part = i - it.unit * parts, tile = it.unit / p.NT;
-        const MTile t = p.tiles[tile];
+        it.unit = unit_of(i);
         it.row0 = t.row0;
         it.rows = t.rows;
         it.expert = t.wsel >= 0 ? t.wsel : p.slot_expert[-1 - t.wsel];
         if (it.expert >= p.E) it.expert = -1;
-        it.n0 = (it.unit - tile * p.NT) * p.BN;
-        it.kb0 = part * p.kbn / parts;
-        it.kb1 = (part + 1) * p.kbn / parts;
+        it.n0 = (it.unit - (int)fast_div(it.unit, p.by_nt) * p.NT) * p.BN;
+        it.kb0 = 0;
+        it.kb1 = p.kbn;
+        if (parts > 1) {
+            const int part = i - it.unit * parts;
+            it.kb0 = part * p.kbn / parts;
+            it.kb1 = (part + 1) * p.kbn / parts;
+        }
         return it;
     };
+    MTile next = tile_at(blockIdx.x);
 
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
             for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
-                const Item u = item_at(i);
+                const Item u = item_of(i, next);
+                next = tile_at(i + gridDim.x);
                 if (u.expert < 0) {
                     set_status(p.status, BEP_DERR_BOUNDS);
                     continue;
                 }
-                const CUtensorMap* tmX = u.rows <= 16 ? &tmX16 : u.rows <= 32 ? &tmX32 : u.rows <= 64 ? &tmX64 : &tmX128;
-                const int box = u.rows <= 16 ? 16 : u.rows <= 32 ? 32 : u.rows <= 64 ? 64 : 128;
+                const CUtensorMap* mx = map_for(tmX, u.rows);
+                const int box = box_for(u.rows);
                 for (int kb = u.kb0; kb < u.kb1; ++kb) {
-                    if (!mbar_wait_held(&f.empty[pr_s], pr_ph ^ 1u, f.s_abort, p.status)) {
+                    if (!mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
                         live = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&f.full[pr_s], box * 128 + p.b_bytes);
-                    ++pr_armed;
-                    tma_load_2d(tmX, &f.full[pr_s], smA + pr_s * p.a_bytes, kb * 64, u.row0);
-                    uint8_t* b = smB + pr_s * p.b_bytes;
+                    mbar_arrive_expect_tx(&f.full[pr.at], box * 128 + p.b_bytes);
+                    tma_load_2d(mx, &f.full[pr.at], smA + pr.at * p.a_bytes, kb * 64, u.row0);
+                    uint8_t* b = smB + pr.at * p.b_bytes;
                     if (kTrans)
-                        tma_load_3d(&tmW, &f.full[pr_s], b, kb * 64, u.n0, u.expert);
+                        tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, u.n0, u.expert);
                     else
                         for (int c = 0; c * kRgChunk < p.b_bytes; ++c)
-                            tma_load_3d(&tmW, &f.full[pr_s], b + c * kRgChunk, u.n0 + c * 64, kb * 64, u.expert);
-                    if (++pr_s == (uint32_t)p.stages) {
-                        pr_s = 0;
-                        pr_ph ^= 1u;
-                    }
+                            tma_load_3d(&tmW, &f.full[pr.at], b + c * kRgChunk, u.n0 + c * 64, kb * 64, u.expert);
+                    pr.step(p.stages);
+                }
+                if (kAdd && parts == 1 && live) {
+                    if (!mbar_wait_held(&f.aempty[ad.at], ad.phase ^ 1u, f.s_abort, p.status)) break;
+                    const CUtensorMap* ma = map_for(tmAdd, u.rows);
+                    mbar_arrive_expect_tx(&f.afull[ad.at], p.add_bytes / 128 * box);
+                    for (int c = 0; c * kRgA < p.add_bytes; ++c)
+                        tma_load_2d(ma, &f.afull[ad.at], smT + ad.at * p.add_bytes + c * kRgA, u.n0 + c * 64, u.row0);
+                    ad.step(p.adds);
                 }
             }
         }
@@ -297,7 +416,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(
             int it = 0;
             bool live = true;
             for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
-                const Item u = item_at(i);
+                const Item u = item_of(i, next);
+                next = tile_at(i + gridDim.x);
                 if (u.expert < 0) continue;
                 const int acc = it & 1;
                 if (!mbar_wait_held(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status)) break;
@@ -324,29 +444,23 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(
             }
         }
     } else {
+        // Two warps for each quarter of the accumulator's rows, each with half of the boxes of 64 columns. A box is
+        // turned in shared memory, so that 8 lanes write 128 bytes of a row of y.
         const int q = warp & 3, second = (warp - 2) >> 2;
-        uint8_t* stg = f.boxes + (warp - 2) * kRgBox;
-        const int sub = lane >> 2, piece = lane & 3;   // on the way out: 4 lanes take 32 columns of a row
+        const int sub = lane >> 3, piece = lane & 7;
+        const int nbox = (p.BN + 63) / 64, mine = (nbox + 1) / 2, box0 = second * mine, box1 = min(nbox, box0 + mine);
         int it = 0;
+        uint32_t as = 0, aph = 0;
         for (int i = blockIdx.x; i < total; i += gridDim.x) {
-            const Item u = item_at(i);
+            const Item u = item_of(i, next);
+            next = tile_at(i + gridDim.x);
             if (u.expert < 0) continue;
             const int acc = it & 1;
             const int rows = u.rows - 32 * q;          // of this warp's 32
             const int64_t row0 = (int64_t)u.row0 + 32 * q;
-            // what the product is added to is on its way while the product is computed
-            uint4 pre[4][4];
-            if (p.add && parts == 1) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int c = 32 * (2 * b + second) + 8 * piece;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (c < p.BN && u.n0 + c < p.N && 8 * j + sub < rows)
-                            pre[b][j] = *reinterpret_cast<const uint4*>(p.add + (row0 + 8 * j + sub) * p.ldadd + u.n0 + c);
-                }
-            }
-            const bool done = __all_sync(0xffffffffu, mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status));
+            bool done = mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status);
+            if (kAdd && parts == 1) done = done && mbar_wait_held(&f.afull[as], aph, f.s_abort, p.status);
+            done = __all_sync(0xffffffffu, done);
             // (warps that meet at barriers give up together)
             if (parts > 1 ? !epi_all(done) : !done) break;
             ++it;
@@ -360,71 +474,104 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(
                 held = false;
             };
             const int slot0 = u.unit * parts;
+            bool mine_to_store = true;
             if (parts > 1) {
-                for (int c0 = 32 * second; c0 < p.BN; c0 += 64) {
+                for (int c0 = 64 * box0; c0 < min(64 * box1, p.BN); c0 += 32) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tacc + c0, r);
                     put_part(part_tile(p.partial, i), c0, 32 * q + lane, r);
                 }
                 release();
-                if (!last_part(p.tickets + u.unit, parts, f.s_last)) continue;
+                mine_to_store = last_part(p.tickets + u.unit, parts, f.s_last);
             }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int c0 = 32 * (2 * b + second);
-                if (c0 >= p.BN) break;
-                uint32_t r[32];
-                if (parts > 1) sum_parts(p.partial, slot0, parts, c0, 32 * q + lane, r);
-                else tmem_ld_32x32b_x32(tacc + c0, r);
-                if (held && c0 + 64 >= p.BN) release();
-                uint4* line = reinterpret_cast<uint4*>(stg + lane * 128);
+            for (int b = 0; b < 2; ++b) {
+                const int bx = box0 + b;
+                if (bx >= box1 || !mine_to_store) break;
+                uint8_t* stg = kAdd ? smT + as * p.add_bytes + bx * kRgA + q * kRgBox : smT + (warp - 2) * kRgBox;
+                uint4* line = reinterpret_cast<uint4*>(stg + lane * 128);   // this lane's row of the box
+                const int c = 64 * bx + 8 * piece;
+                const bool in = c < p.BN && u.n0 + c < p.N;
                 __syncwarp();   // the box before has been read
+                if (kAdd && parts > 1) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) line[j ^ (lane & 7)] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                __syncwarp();
-                const int c = c0 + 8 * piece;
+                    for (int j = 0; j < 8; ++j)
+                        if (in && 4 * j + sub < rows)
+                            *reinterpret_cast<uint4*>(stg + (4 * j + sub) * 128 + ((piece ^ ((4 * j + sub) & 7)) << 4)) =
+                                *reinterpret_cast<const uint4*>(p.add + (row0 + 4 * j + sub) * p.ldadd + u.n0 + c);
+                    __syncwarp();
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int rr = 8 * j + sub;
-                    const float4 lo = *reinterpret_cast<const float4*>(stg + rr * 128 + (((2 * piece) ^ (rr & 7)) << 4));
-                    const float4 hi = *reinterpret_cast<const float4*>(stg + rr * 128 + (((2 * piece + 1) ^ (rr & 7)) << 4));
-                    if (c >= p.BN || u.n0 + c >= p.N || rr >= rows) continue;
-                    float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                    if (p.add) {
-                        const uint4 t = parts == 1 ? pre[b][j]
-                                                   : *reinterpret_cast<const uint4*>(p.add + (row0 + rr) * p.ldadd + u.n0 + c);
-                        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+                for (int h = 0; h < 2; ++h) {
+                    const int c0 = 64 * bx + 32 * h;
+                    if (c0 >= p.BN) break;
+                    uint32_t r[32];
+                    if (parts > 1) sum_parts(p.partial, slot0, parts, c0, 32 * q + lane, r);
+                    else tmem_ld_32x32b_x32(tacc + c0, r);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4& at = line[(4 * h + j) ^ (lane & 7)];
+                        uint32_t w[4];
+                        if (kAdd) {
+                            const uint4 t = at;
+                            w[0] = t.x;
+                            w[1] = t.y;
+                            w[2] = t.z;
+                            w[3] = t.w;
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            v[2 * e] = fmaf(p.alpha, v[2 * e], __uint_as_float(w[e] << 16));
-                            v[2 * e + 1] = fmaf(p.alpha, v[2 * e + 1], __uint_as_float(w[e] & 0xffff0000u));
+                            float lo = __uint_as_float(r[8 * j + 2 * e]), hi = __uint_as_float(r[8 * j + 2 * e + 1]);
+                            if (kAdd) {
+                                lo = fmaf(p.alpha, lo, __uint_as_float(w[e] << 16));
+                                hi = fmaf(p.alpha, hi, __uint_as_float(w[e] & 0xffff0000u));
+                            } else {
+                                lo *= p.alpha;
+                                hi *= p.alpha;
+                            }
+                            w[e] = pack_bf16x2(lo, hi);
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= p.alpha;
+                        at = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4*>(p.y + (row0 + rr) * p.ldy + u.n0 + c) =
-                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                   pack_bf16x2(v[6], v[7]));
+                }
+                if (held && bx + 1 == box1) release();   // this warp has read all its columns
+                __syncwarp();
+                if (in) {
+                    uint16_t* out = p.y + (row0 + sub) * p.ldy + u.n0 + c;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (4 * j + sub < rows)
+                            *reinterpret_cast<uint4*>(out + (int64_t)(4 * j) * p.ldy) =
+                                *reinterpret_cast<const uint4*>(stg + (4 * j + sub) * 128 + ((piece ^ ((4 * j + sub) & 7)) << 4));
                 }
             }
             if (held) release();   // a warp without columns
+            if (kAdd && parts == 1) {
+                // the boxes were read and written here; the next unit's come by TMA
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&f.aempty[as]);
+                if (++as == (uint32_t)p.adds) {
+                    as = 0;
+                    aph ^= 1u;
+                }
+            }
         }
     }
-    close_frame(f, p.stages, pr_s, pr_ph, pr_armed);
+    close_frame(f, p.stages, kAdd ? p.adds : 0, pr, ad);
 }
 
 // ------------------------------------------------------------------------ matrices
-// The segments of each expert, in (rank, row) order: segs[first[e] .. first[e + 1]). One CTA. A slot whose expert is
-// unknown is reported and left out; a table with any inconsistent segment is refused as a whole.
-__global__ void __launch_bounds__(1024) ragged_segments_kernel(const int32_t* cu, const int32_t* slot_expert, Dims d,
+// Blocks of up to 64 rows of each expert's segments, in (rank, row) order: tiles[first[e] .. first[e + 1]). One CTA. A
+// slot whose expert is unknown is reported and left out; a table with any inconsistent segment is refused as a whole.
+__global__ void __launch_bounds__(1024) ragged_blocks_kernel(const int32_t* cu, const int32_t* slot_expert, Dims d,
                                                                Workspace ws) {
-    __shared__ int s_pos[kMaxE], s_blk[kMaxE];
+    __shared__ int s_pos[kMaxE];
     __shared__ int s_sum[32];
     grid_launch_dependents();
     grid_wait();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    for (int e = t; e < kMaxE; e += 1024) s_pos[e] = s_blk[e] = 0;
+    for (int e = t; e < kMaxE; e += 1024) s_pos[e] = 0;
     if (t < kRgTickets) ws.tickets[t] = 0;
     __syncthreads();
     auto expert_of = [&](int u, int rho) {
@@ -441,14 +588,12 @@ __global__ void __launch_bounds__(1024) ragged_segments_kernel(const int32_t* cu
             if (e < 0) {
                 unknown = 1;
             } else {
-                atomicAdd(&s_pos[e], 1);
-                atomicAdd(&s_blk[e], (b - a + 63) / 64);
+                atomicAdd(&s_pos[e], (b - a + 63) / 64);
             }
         }
     bad = __syncthreads_or(bad);
     if (__syncthreads_or(unknown) && t == 0) set_status(ws.status, BEP_DERR_BOUNDS);
     if (bad && t == 0) set_status(ws.status, BEP_DERR_BOUNDS);
-    for (int e = t; e < d.E; e += 1024) ws.seg_blocks[e] = s_blk[e];
     // exclusive scan of the counts: two experts a thread
     static_assert(kMaxE == 2048, "two experts a thread");
     const int n0 = s_pos[2 * t], n1 = s_pos[2 * t + 1];
@@ -465,20 +610,26 @@ __global__ void __launch_bounds__(1024) ragged_segments_kernel(const int32_t* cu
     const int at = bad ? -1 : before + incl - n0 - n1;
     s_pos[2 * t] = at;
     s_pos[2 * t + 1] = at + n0;
-    if (2 * t <= d.E) ws.seg_first[2 * t] = bad ? -1 : at;
-    if (2 * t + 1 <= d.E) ws.seg_first[2 * t + 1] = bad ? -1 : at + n0;
-    if (t == 1023 && d.E == kMaxE) ws.seg_first[kMaxE] = bad ? -1 : at + n0 + n1;
+    if (2 * t <= d.E) ws.blk_first[2 * t] = bad ? -1 : at;
+    if (2 * t + 1 <= d.E) ws.blk_first[2 * t + 1] = bad ? -1 : at + n0;
+    if (t == 1023 && d.E == kMaxE) ws.blk_first[kMaxE] = bad ? -1 : at + n0 + n1;
     __syncthreads();
     if (bad) return;
+    auto put = [&](int at, int u, int a, int b) {
+        for (; a < b; a += 64) ws.tiles[at++] = MTile{(int32_t)(u * d.C + a), min(64, b - a), 0, 0};
+    };
     for (int u = 0; u < d.R; ++u) {
         const int32_t* row = cu + u * (d.NROW + 1);
         // home rows: every one its own expert
         for (int e = t; e < d.E; e += 1024) {
             const int a = row[e], b = row[e + 1];
-            if (b > a) ws.tiles[s_pos[e]++] = MTile{(int32_t)(u * d.C + a), b - a, e, 0};
+            if (b > a) {
+                put(s_pos[e], u, a, b);
+                s_pos[e] += (b - a + 63) / 64;
+            }
         }
         __syncthreads();
-        // slots: several of a rank may hold one expert, so a slot counts those before it
+        // slots: several of a rank may hold one expert, so a slot counts the blocks of those before it
         for (int j0 = 0; j0 < d.B; j0 += 1024) {
             const int j = j0 + t;
             int e = -1, a = 0, b = 0, ahead = 0;
@@ -489,10 +640,10 @@ __global__ void __launch_bounds__(1024) ragged_segments_kernel(const int32_t* cu
             }
             if (e >= 0)
                 for (int i = j0; i < j; ++i)
-                    ahead += slot_expert[u * d.B + i] == e && row[d.E + i + 1] > row[d.E + i];
-            if (e >= 0) ws.tiles[s_pos[e] + ahead] = MTile{(int32_t)(u * d.C + a), b - a, e, 0};
+                    if (slot_expert[u * d.B + i] == e) ahead += (row[d.E + i + 1] - row[d.E + i] + 63) / 64;
+            if (e >= 0) put(s_pos[e] + ahead, u, a, b);
             __syncthreads();
-            if (e >= 0) atomicAdd(&s_pos[e], 1);
+            if (e >= 0) atomicAdd(&s_pos[e], (b - a + 63) / 64);
             __syncthreads();
         }
     }
@@ -509,29 +660,17 @@ __device__ __forceinline__ void zero_rows(uint8_t* chunk, int chunks, int tail, 
     }
 }
 
-// Calls op(row, rows of the block) for the blocks [b0, b1) until it returns false.
-template <typename F>
-__device__ __forceinline__ bool each_block(const RgDwParams& p, int e, int b0, int b1, F&& op) {
-    int b = 0;
-    for (int s = p.first[e]; s < p.first[e + 1] && b < b1; ++s) {
-        const MTile t = p.segs[s];
-        const int n = (t.rows + 63) / 64;
-        for (int k = max(0, b0 - b); k < n && b + k < b1; ++k)
-            if (!op(t.row0 + 64 * k, min(64, t.rows - 64 * k))) return false;
-        b += n;
-    }
-    return true;
-}
-
-// A unit: 128 x BN of an expert's gradient. The wider side is the M operand; both lie along the rows (MN-major).
+// A unit: MI x 128 x BN of an expert's gradient, MI = 2 where BN leaves both room in an accumulator. The wider side is the
+// M operand; both lie along the rows (MN-major).
 __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
                                                                   const __grid_constant__ CUtensorMap tmN,
                                                                   const RgDwParams p) {
     extern __shared__ uint8_t smem_raw[];
+    grid_launch_dependents();
     Frame f = open_frame(smem_raw, p.stages);
-    const int stage = kRgA + p.b_bytes;
+    const int a_bytes = p.MI * kRgA, stage = a_bytes + p.b_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t pr_s = 0, pr_ph = 0, pr_armed = 0;
+    Started pr;
     grid_wait();   // launched early: the segments and the rows are complete from here on
 
     const int parts = p.parts;
@@ -539,56 +678,82 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
     struct Item {
         int unit, expert, m0, n0, b0, b1;
     };
-    auto item_at = [&](int i) {
+    auto expert_at = [&](int i) { return fast_div(fast_div(i, p.by_parts), p.by_unit); };
+    // An expert's range of blocks is read a unit ahead.
+    auto range_at = [&](int i) {
+        const uint32_t e = i < total ? expert_at(i) : 0;
+        return make_int2(p.first[e], p.first[e + 1]);
+    };
+    auto item_of = [&](int i, const int2& range) {
         Item it;
-        it.unit = i / parts;
-        const int part = i - it.unit * parts, per = p.MT * p.NT;
-        it.expert = it.unit / per;
-        const int rest = it.unit - it.expert * per;
-        it.m0 = rest / p.NT * 128;
-        it.n0 = rest % p.NT * p.BN;
-        const int64_t nb = p.blocks[it.expert];
-        it.b0 = (int)(part * nb / parts);
-        it.b1 = (int)((part + 1) * nb / parts);
+        it.unit = fast_div(i, p.by_parts);
+        const int part = i - it.unit * parts;
+        it.expert = fast_div(it.unit, p.by_unit);
+        const int rest = it.unit - it.expert * p.MT * p.NT, m = fast_div(rest, p.by_nt);
+        it.m0 = m * p.MI * 128;
+        it.n0 = (rest - m * p.NT) * p.BN;
+        const int64_t nb = range.y - range.x;
+        it.b0 = parts == 1 ? range.x : range.x + (int)(part * nb / parts);
+        it.b1 = parts == 1 ? range.y : range.x + (int)((part + 1) * nb / parts);
         return it;
     };
+    int2 next = range_at(blockIdx.x);
 
     if (warp == 0) {
-        if (lane == 0) {
-            bool live = true;
-            for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
-                const Item u = item_at(i);
-                live = each_block(p, u.expert, u.b0, u.b1, [&](int row, int) {
-                    if (!mbar_wait_held(&f.empty[pr_s], pr_ph ^ 1u, f.s_abort, p.status)) return false;
-                    mbar_arrive_expect_tx(&f.full[pr_s], stage);
-                    ++pr_armed;
-                    uint8_t* a = f.ring + pr_s * stage;
-                    for (int c = 0; c < 2; ++c) tma_load_2d(&tmM, &f.full[pr_s], a + c * kRgChunk, u.m0 + 64 * c, row);
+        // 32 blocks at a time, a lane each; a unit's first 32 are read while the unit before runs
+        auto blocks_at = [&](int b, int end) { return b + lane < end ? p.blocks[b + lane] : MTile{0, 0, 0, 0}; };
+        auto first_of = [&](int i) {
+            if (i >= total) return MTile{0, 0, 0, 0};
+            const Item u = item_of(i, next);
+            return blocks_at(u.b0, u.b1);
+        };
+        bool live = true;
+        MTile run = first_of(blockIdx.x);
+        for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+            const Item u = item_of(i, next);
+            next = range_at(i + gridDim.x);
+            MTile cur = run;
+            run = first_of(i + gridDim.x);
+            for (int b = u.b0; b < u.b1; ++b) {
+                const int k = (b - u.b0) & 31;
+                if (k == 0 && b != u.b0) cur = blocks_at(b, u.b1);
+                const int row0 = __shfl_sync(0xffffffffu, cur.row0, k), rows = __shfl_sync(0xffffffffu, cur.rows, k);
+                if (!__all_sync(0xffffffffu, mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status))) {
+                    live = false;
+                    break;
+                }
+                if (elect_one()) {
+                    f.s_rows[pr.at] = rows;   // for the warp that waits on `full`
+                    mbar_arrive_expect_tx(&f.full[pr.at], stage);
+                    uint8_t* at = f.ring + pr.at * stage;
+                    for (int c = 0; c < 2 * p.MI; ++c)
+                        tma_load_2d(&tmM, &f.full[pr.at], at + c * kRgChunk, u.m0 + 64 * c, row0);
                     for (int c = 0; c * kRgChunk < p.b_bytes; ++c)
-                        tma_load_2d(&tmN, &f.full[pr_s], a + kRgA + c * kRgChunk, u.n0 + 64 * c, row);
-                    if (++pr_s == (uint32_t)p.stages) {
-                        pr_s = 0;
-                        pr_ph ^= 1u;
-                    }
-                    return true;
-                });
+                        tma_load_2d(&tmN, &f.full[pr.at], at + a_bytes + c * kRgChunk, u.n0 + 64 * c, row0);
+                }
+                __syncwarp();
+                pr.step(p.stages);
             }
         }
     } else if (warp == 1) {
         const uint32_t idesc = idesc_bf16(p.BN, true, true);
         uint32_t s = 0, ph = 0;
         int it = 0;
-        for (int i = blockIdx.x; i < total; i += gridDim.x) {
-            const Item u = item_at(i);
-            if (u.b0 == u.b1) continue;
-            const int acc = it & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_held(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status))) break;
-            ++it;
-            tc_fence_after();
-            const uint32_t dt = f.tmem + acc * 256;
-            uint32_t add = 0;
-            const bool live = each_block(p, u.expert, u.b0, u.b1, [&](int, int rows) {
-                if (!__all_sync(0xffffffffu, mbar_wait_held(&f.full[s], ph, f.s_abort, p.status))) return false;
+        bool live = true;
+        for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+            const Item u = item_of(i, next);
+            next = range_at(i + gridDim.x);
+            for (int b = u.b0; b < u.b1 && live; ++b) {
+                const int k = (b - u.b0) % kRgChain;
+                const int acc = it & 1;
+                const uint32_t dt = f.tmem + acc * 256;
+                bool ok = k != 0 || mbar_wait_held(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status);
+                ok = ok && mbar_wait_held(&f.full[s], ph, f.s_abort, p.status);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    live = false;
+                    break;
+                }
+                const int rows = f.s_rows[s];
                 uint8_t* at = f.ring + s * stage;
                 if (rows & 15) {   // the rows behind a segment's last are another's, or nobody's
                     zero_rows(at, stage / kRgChunk, rows, lane);
@@ -597,75 +762,92 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
                 }
                 if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t a = smem_u32(at), b = a + kRgA;
+                    const uint32_t a = smem_u32(at), bb = a + a_bytes;
+                    for (int m = 0; m < p.MI; ++m)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (16 * kk < rows) {
-                            mma_bf16(dt, operand<true>(a, kk), operand<true>(b, kk), idesc, add);
-                            add = 1;
-                        }
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (16 * kk < rows)
+                                mma_bf16(dt + m * 128, operand<true>(a + m * kRgA, kk), operand<true>(bb, kk), idesc, k || kk);
                     mma_commit(&f.empty[s]);
+                    if (k == kRgChain - 1 || b == u.b1 - 1) mma_commit(&f.tfull[acc]);
                 }
                 __syncwarp();
+                if (k == kRgChain - 1 || b == u.b1 - 1) ++it;
                 if (++s == (uint32_t)p.stages) {
                     s = 0;
                     ph ^= 1u;
                 }
-                return true;
-            });
-            if (!live) break;
-            if (lane == 0) mma_commit(&f.tfull[acc]);
-            __syncwarp();
+            }
         }
     } else {
         const int q = warp & 3, second = (warp - 2) >> 2;
-        uint8_t* stg = f.boxes + (warp - 2) * kRgBox;
+        uint8_t* stg = f.ring + p.stages * stage + (warp - 2) * kRgBox;
         const int sub = lane >> 3, piece = lane & 7;   // on the way out: 8 lanes take 32 columns of a row
+        // A warp's boxes of 32 columns: every second one of the tile, or, of two tiles, all of one.
+        const int step = p.MI == 2 ? 32 : 64, start = p.MI == 2 ? 0 : 32 * second;
+        const int tile = p.MI == 2 ? second : 0;
         int it = 0;
-        for (int i = blockIdx.x; i < total; i += gridDim.x) {
-            const Item u = item_at(i);
-            const bool none = u.b0 == u.b1;
-            const int acc = it & 1;
-            if (!none) {
-                const bool done = __all_sync(0xffffffffu, mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status));
-                if (parts > 1 ? !epi_all(done) : !done) break;
+        bool live = true;
+        for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+            const Item u = item_of(i, next);
+            next = range_at(i + gridDim.x);
+            if (u.b0 == u.b1 && parts == 1 && p.accumulate) continue;
+            float sum[4][32];   // this thread's row
+            if (u.b0 == u.b1) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[b][j] = 0.0f;
+            }
+            for (int b0 = u.b0; b0 < u.b1; b0 += kRgChain) {
+                const int acc = it & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status))) {
+                    live = false;
+                    break;
+                }
                 ++it;
                 tc_fence_after();
-            }
-            bool held = !none;
-            const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256;
-            auto release = [&]() {
+                const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256 + tile * 128;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int c0 = start + b * step;
+                    if (c0 >= p.BN) break;
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tacc + c0, r);
+                    if (b0 == u.b0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[b][j] = __uint_as_float(r[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[b][j] += __uint_as_float(r[j]);
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&f.tempty[acc]);
-                held = false;
-            };
-            auto read = [&](int c0, uint32_t* r) {
-                if (none) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0u;
-                } else {
-                    tmem_ld_32x32b_x32(tacc + c0, r);
-                }
-            };
-            if (parts > 1) {
-                for (int c0 = 32 * second; c0 < p.BN; c0 += 64) {
-                    uint32_t r[32];
-                    read(c0, r);
-                    put_part(part_tile(p.partial, i), c0, 32 * q + lane, r);
-                }
-                if (held) release();
-                if (!last_part(p.tickets + u.unit, parts, f.s_last)) continue;
-            } else if (none && p.accumulate) {
-                continue;
             }
-            const int m0 = u.m0 + 32 * q;   // this warp's 32 along M
+            if (parts > 1) {
+                // (warps that meet at barriers give up together)
+                if (!epi_all(live)) break;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (start + b * step >= p.BN) break;
+                    put_part(part_tile(p.partial, i), start + b * step, 32 * q + lane, sum[b]);
+                }
+                if (!last_part(p.tickets + u.unit, parts, f.s_last)) continue;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (start + b * step >= p.BN) break;
+                    sum_parts(p.partial, u.unit * parts, parts, start + b * step, 32 * q + lane, sum[b]);
+                }
+            }
+            if (!live) break;
+            const int m0 = u.m0 + tile * 128 + 32 * q;   // this warp's 32 along M
             float* g = p.g + (int64_t)u.expert * p.g_expert;
-            for (int c0 = 32 * second; c0 < p.BN; c0 += 64) {
-                uint32_t r[32];
-                if (parts > 1) sum_parts(p.partial, u.unit * parts, parts, c0, 32 * q + lane, r);
-                else read(c0, r);
-                if (held && c0 + 64 >= p.BN) release();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int c0 = start + b * step;
+                if (c0 >= p.BN || m0 >= p.Md) break;
                 const int n0 = u.n0 + c0;
                 if (p.ldm == 1) {   // the lanes' 32 lie together
                     if (m0 + lane < p.Md) {
@@ -673,47 +855,49 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (c0 + j < p.BN && n0 + j < p.Nd) {
-                                float v = p.alpha * __uint_as_float(r[j]);
-                                if (p.accumulate) v += out[(int64_t)j * p.ldn];
-                                out[(int64_t)j * p.ldn] = v;
+                                float v = p.alpha * sum[b][j];
+                                if (p.accumulate) v += *out;
+                                *out = v;
+                                out += p.ldn;
                             }
                     }
                 } else {
-                    uint4* line = reinterpret_cast<uint4*>(stg + lane * 128);
+                    float4* line = reinterpret_cast<float4*>(stg + lane * 128);
                     __syncwarp();   // the box before has been read
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        line[j ^ (lane & 7)] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        line[j ^ (lane & 7)] = make_float4(sum[b][4 * j], sum[b][4 * j + 1], sum[b][4 * j + 2], sum[b][4 * j + 3]);
                     __syncwarp();
                     const int c = c0 + 4 * piece;
+                    if (c < p.BN && u.n0 + c < p.Nd) {
+                        float4* out = reinterpret_cast<float4*>(g + (int64_t)(m0 + sub) * p.ldm + u.n0 + c);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int rr = 4 * j + sub;
-                        float4 v = *reinterpret_cast<const float4*>(stg + rr * 128 + ((piece ^ (rr & 7)) << 4));
-                        if (c >= p.BN || u.n0 + c >= p.Nd || m0 + rr >= p.Md) continue;
-                        float4* out = reinterpret_cast<float4*>(g + (int64_t)(m0 + rr) * p.ldm + u.n0 + c);
-                        v.x *= p.alpha;
-                        v.y *= p.alpha;
-                        v.z *= p.alpha;
-                        v.w *= p.alpha;
-                        if (p.accumulate) {
-                            const float4 o = *out;
-                            v.x += o.x;
-                            v.y += o.y;
-                            v.z += o.z;
-                            v.w += o.w;
+                        for (int j = 0; j < 8; ++j) {
+                            const int rr = 4 * j + sub;
+                            if (m0 + rr < p.Md) {
+                                float4 v = *reinterpret_cast<const float4*>(stg + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                                v.x *= p.alpha;
+                                v.y *= p.alpha;
+                                v.z *= p.alpha;
+                                v.w *= p.alpha;
+                                if (p.accumulate) {
+                                    const float4 o = *out;
+                                    v.x += o.x;
+                                    v.y += o.y;
+                                    v.z += o.z;
+                                    v.w += o.w;
+                                }
+                                *out = v;
+                            }
+                            out += p.ldm;   // 4 rows of floats
                         }
-                        *out = v;
                     }
                 }
             }
-            if (held) release();   // a warp without columns
         }
     }
-    close_frame(f, p.stages, pr_s, pr_ph, pr_armed);
+    close_frame(f, p.stages, 0, pr, Started());
 }
-
-constexpr size_t kRgSmem = 227 * 1024;
 
 // bf16 tensor of `dims` (innermost first) with row strides in elements, boxes of 64 x box_rows, 128-byte swizzle.
 bool encode_rows(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* ld, uint32_t box_rows) {
@@ -751,13 +935,14 @@ void cut(int width, int most, int* tile, int* tiles) {
 }  // namespace
 
 cudaError_t ragged_setup() {
-    cudaError_t err =
-        cudaFuncSetAttribute(ragged_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
-    if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(ragged_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
-    if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(ragged_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
-    return err;
+    const void* kernels[] = {(const void*)ragged_kernel<false, false>, (const void*)ragged_kernel<false, true>,
+                             (const void*)ragged_kernel<true, false>, (const void*)ragged_kernel<true, true>,
+                             (const void*)ragged_dw_kernel};
+    for (const void* k : kernels) {
+        const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
@@ -767,6 +952,7 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     RgParams p = {};
     p.tiles = ws.tiles;
     p.ntiles = ws.ntiles;
+    p.cu = cu;
     p.slot_expert = slot_expert;
     p.y = y;
     p.add = add;
@@ -774,38 +960,60 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     p.ldadd = ldadd;
     p.alpha = alpha;
     p.E = d.E;
+    p.R = d.R;
+    p.B = d.B;
+    p.NROW = d.NROW;
+    p.C = d.C;
     p.N = N;
     p.kbn = (K + 63) / 64;
     p.status = ws.status;
     p.tickets = ws.tickets;
-    // Tiles of 64 columns, whose reduction may be cut into parts, where even as many row tiles as there can be do not
-    // make a unit for every SM with wider ones.
-    const int64_t segs = (int64_t)d.R * d.NROW < rows ? (int64_t)d.R * d.NROW : rows;
-    const int64_t most = rows / 128 + segs;
-    cut(N, most * ((N + 255) / 256) < num_sms ? 64 : 256, &p.BN, &p.NT);
-    if (p.BN <= kRgPartCols) p.partial = ws.partial;
     // few rows an expert: half the stage bytes for rows, more stages
     const bool few = rows / d.E <= 48;
+    p.tile_rows = few ? 64 : 128;
     p.a_bytes = few ? kRgA / 2 : kRgA;
+    const int64_t segs = (int64_t)d.R * d.NROW < rows ? (int64_t)d.R * d.NROW : rows;
+    const int64_t most = rows / p.tile_rows + segs;   // row tiles at most
+    p.local = most <= kRgLocal && (int64_t)d.R * d.NROW <= 32 * kRgThreads;
+    // Tiles of 64 columns, whose reduction may be cut into parts, where even as many row tiles as there can be do not
+    // make a unit for every SM with wider ones. With a short reduction and something to add, a unit is mostly what
+    // it adds and writes: smaller tiles, more of them under way.
+    const bool thin = add && p.kbn < 16;
+    const int wide = thin ? 128 : 256;
+    cut(N, most * ((N + wide - 1) / wide) < num_sms ? 64 : wide, &p.BN, &p.NT);
+    p.by_nt = make_fast_div((uint32_t)p.NT);
+    if (p.BN <= kRgPartCols) p.partial = ws.partial;
     p.b_bytes = trans ? p.BN * 128 : (p.BN + 63) / 64 * kRgChunk;
-    // (the last stage of small row tiles is read as 128 rows: up to kRgA / 2 behind the rows' stages, inside the ring)
-    const int fit = kRgRing / 1024 * 1024 / (p.a_bytes + p.b_bytes);
+    p.adds = add ? (thin ? kRgMaxAdds : 1) : 0;
+    p.add_bytes = (p.BN + 63) / 64 * kRgA;
+    // (the last stage of small row tiles is read as 128 rows: up to kRgA / 2 behind the rows' stages, inside the rest)
+    const int rest = kRgBytes - (p.local ? kRgLocal * (int)sizeof(MTile) : 0) - (add ? p.adds * p.add_bytes : 8 * kRgBox);
+    const int fit = rest / (p.a_bytes + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;
 
-    CUtensorMap tmW, tmX[4];
+    CUtensorMap tmW;
+    RowMaps tmX, tmAdd = {};
     const uint64_t xd[2] = {(uint64_t)K, (uint64_t)rows}, xs[1] = {(uint64_t)ldx};
-    const uint32_t boxes[4] = {16, 32, 64, 128};
-    for (int i = 0; i < 4; ++i)
-        if (!encode_rows(&tmX[i], x, 2, xd, xs, boxes[i])) return cudaErrorInvalidValue;
+    const uint64_t ad[2] = {(uint64_t)N, (uint64_t)rows}, as[1] = {(uint64_t)ldadd};
+    CUtensorMap* mx[4] = {&tmX.m16, &tmX.m32, &tmX.m64, &tmX.m128};
+    CUtensorMap* ma[4] = {&tmAdd.m16, &tmAdd.m32, &tmAdd.m64, &tmAdd.m128};
+    for (int i = 0; i < 4; ++i) {
+        if (!encode_rows(mx[i], x, 2, xd, xs, 16u << i)) return cudaErrorInvalidValue;
+        if (add && !encode_rows(ma[i], add, 2, ad, as, 16u << i)) return cudaErrorInvalidValue;
+    }
     const uint64_t wd[3] = {(uint64_t)(trans ? K : N), (uint64_t)(trans ? N : K), (uint64_t)d.E};
     const uint64_t wl[2] = {wd[0], wd[0] * wd[1]};
     if (!encode_rows(&tmW, w, 3, wd, wl, trans ? (uint32_t)p.BN : 64)) return cudaErrorInvalidValue;
-    const cudaError_t err = few ? launch_row_tiles<64>(d, ws, cu, st) : launch_row_tiles<128>(d, ws, cu, st);
-    if (err != cudaSuccess) return err;
+    if (!p.local) {
+        const cudaError_t err = few ? launch_row_tiles<64>(d, ws, cu, st) : launch_row_tiles<128>(d, ws, cu, st);
+        if (err != cudaSuccess) return err;
+    }
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = rg_config(num_sms, st, attr);
-    return cudaLaunchKernelEx(&cfg, trans ? ragged_kernel<true> : ragged_kernel<false>, tmW, tmX[0], tmX[1], tmX[2],
-                              tmX[3], p);
+    return cudaLaunchKernelEx(&cfg,
+                              trans ? (add ? ragged_kernel<true, true> : ragged_kernel<true, false>)
+                                    : (add ? ragged_kernel<false, true> : ragged_kernel<false, false>),
+                              tmW, tmX, tmAdd, p);
 }
 
 cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
@@ -813,9 +1021,8 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
                              int accumulate, float* g, int num_sms, cudaStream_t st) {
     const int64_t rows = (int64_t)d.R * d.C;
     RgDwParams p = {};
-    p.segs = ws.tiles;
-    p.first = ws.seg_first;
-    p.blocks = ws.seg_blocks;
+    p.blocks = ws.tiles;
+    p.first = ws.blk_first;
     p.g = g;
     p.g_expert = (int64_t)K * N;
     p.alpha = alpha;
@@ -829,7 +1036,9 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     p.tickets = ws.tickets;
     p.partial = ws.partial;
     p.status = ws.status;
-    p.MT = (p.Md + 127) / 128;
+    // two tiles along M a unit (half the units, each block of the narrow side read half as often) where they fill the SMs
+    p.MI = p.Nd <= 128 && (int64_t)d.E * ((p.Md + 255) / 256) >= 2 * num_sms ? 2 : 1;
+    p.MT = (p.Md + 128 * p.MI - 1) / (128 * p.MI);
     const int64_t units = (int64_t)d.E * p.MT * ((p.Nd + 255) / 256);
     cut(p.Nd, units < num_sms ? 64 : 256, &p.BN, &p.NT);
     p.parts = 1;
@@ -841,8 +1050,11 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
         z = z < kRgMaxParts ? z : kRgMaxParts;
         p.parts = z > 1 ? (int)z : 1;
     }
+    p.by_parts = make_fast_div((uint32_t)p.parts);
+    p.by_unit = make_fast_div((uint32_t)(p.MT * p.NT));
+    p.by_nt = make_fast_div((uint32_t)p.NT);
     p.b_bytes = (p.BN + 63) / 64 * kRgChunk;
-    const int fit = kRgRing / 1024 * 1024 / (kRgA + p.b_bytes);
+    const int fit = (kRgBytes - 8 * kRgBox) / (p.MI * kRgA + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;
 
     CUtensorMap tx, ty;
@@ -853,7 +1065,7 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     cudaLaunchConfig_t cfg = rg_config(1, st, attr);
     cfg.blockDim = dim3(1024, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_segments_kernel, cu, slot_expert, d, ws);
+    cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_blocks_kernel, cu, slot_expert, d, ws);
     if (err != cudaSuccess) return err;
     cfg = rg_config(num_sms, st, attr);
     return cudaLaunchKernelEx(&cfg, ragged_dw_kernel, x_wide ? tx : ty, x_wide ? ty : tx, p);
