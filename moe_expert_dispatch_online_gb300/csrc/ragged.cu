@@ -20,10 +20,12 @@
 namespace bep {
 namespace {
 
-constexpr int kRgThreads = 32 * 10;
+constexpr int kRgThreads = 32 * 10;      // of the rows' kernel: 8 epilogue warps
+constexpr int kRgDwThreads = 32 * 18;    // of the matrices': 16, which hold a unit's sums in registers
 constexpr int kRgA = 128 * 128;          // bytes: 128 rows (columns) x 64 reduction steps
 constexpr int kRgChunk = 64 * 128;       // bytes: 64 x 64 elements
 constexpr int kRgBox = 32 * 128;         // bytes: an epilogue warp's box of 32 rows of 128 bytes
+constexpr int kRgDwBox = 32 * 64;        // bytes: the same of 16 fp32 columns
 constexpr int kRgTmem = 512;
 constexpr int kRgMaxStages = 12;
 constexpr int kRgMaxAdds = 4;
@@ -47,25 +49,26 @@ struct RgParams {
     float alpha;
     int E, N, kbn;            // output columns, reduction blocks of 64
     int BN, NT;               // columns of a tile, tiles
-    FastDiv by_nt;
+    FastDiv by_nt, by_nrow;
     int tile_rows, local;
     int R, B, NROW;
     int64_t C;
-    int stages, a_bytes, b_bytes, adds, add_bytes;
+    int steps;                // of 16 in a block: 4, or fewer where the reduction is shorter than a block
+    int stages, a_bytes, b_bytes, chunk, adds, add_bytes;
     int32_t* tickets;
     float* partial;
     int32_t* status;
 };
 
 struct RgDwParams {
-    const MTile* blocks;      // up to 64 rows of one segment, by expert, in (rank, row) order
+    const MTile* blocks;      // up to 64 rows of one segment, by expert
     const int32_t* first;     // [E + 1]
     float* g;
     int64_t g_expert;         // elements of an expert's gradient
     int64_t ldm, ldn;         // strides of g along the M side and the N side: one of them is 1
     float alpha;
     int E, Md, Nd;            // widths of the sides
-    int BN, MI, MT, NT, parts;   // columns of a tile, 128-row tiles of a unit, units along M and N
+    int BN, MT, NT, parts;    // columns of a tile, units along M and N
     FastDiv by_parts, by_unit, by_nt;
     int stages, b_bytes;
     int accumulate;
@@ -83,10 +86,10 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
 }
 
 // Operand descriptor of 16 reduction steps of a stage: K-major rows of 64 elements (128 bytes), or MN-major
-// chunks of 64 columns x 64 reduction steps, 8 KB each.
+// chunks of 64 columns x 64 reduction steps (or `chunk` bytes of them).
 template <bool kMN>
-__device__ __forceinline__ uint64_t operand(uint32_t base, int kk) {
-    return kMN ? sdesc_sw128(base + kk * 2048, kRgChunk, 1024) : sdesc_sw128(base + kk * 32, 16, 1024);
+__device__ __forceinline__ uint64_t operand(uint32_t base, int kk, uint32_t chunk = kRgChunk) {
+    return kMN ? sdesc_sw128(base + kk * 2048, chunk, 1024) : sdesc_sw128(base + kk * 32, 16, 1024);
 }
 
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, major bits 15/16 (1: MN), M = 128.
@@ -104,17 +107,21 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b
         : "memory");
 }
 
-// The 8 epilogue warps.
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// All epilogue warps of a kernel.
+template <int kWarps>
+__device__ __forceinline__ void epi_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+template <int kWarps>
 __device__ __forceinline__ bool epi_all(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.and.pred p, 1, 256, q;\n\t"
+        "bar.red.and.pred p, 1, %2, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v)
+        : "r"((uint32_t)v), "n"(32 * kWarps)
         : "memory");
     return r != 0;
 }
@@ -129,7 +136,7 @@ struct Frame {
     int* s_rows;   // valid rows of each stage
     uint32_t tmem;
 };
-__device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages) {
+__device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int epi_warps) {
     Frame f;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -152,11 +159,11 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages) {
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&f.tfull[a], 1);
-            mbar_init(&f.tempty[a], 8);
+            mbar_init(&f.tempty[a], epi_warps);
         }
         for (int a = 0; a < kRgMaxAdds; ++a) {
             mbar_init(&f.afull[a], 1);
-            mbar_init(&f.aempty[a], 8);
+            mbar_init(&f.aempty[a], epi_warps);
         }
         mbar_init(f.drain, 1);
         *f.s_abort = 0;
@@ -221,15 +228,18 @@ __device__ __forceinline__ float* part_tile(float* base, int slot) {
     return base + (int64_t)slot * (kPartRows * kRgPartCols);
 }
 // This thread's row, 32 columns: to a part's tile, and the sum of a unit's parts in their order.
-template <typename T>
-__device__ __forceinline__ void put_part(float* tile, int c0, int row, const T* r) {
-    static_assert(sizeof(T) == 4, "fp32 or its bits");
+__device__ __forceinline__ void put_part(float* tile, int c0, int row, const float* v) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) __stcg(tile + (c0 + j) * kPartRows + row, *reinterpret_cast<const float*>(r + j));
+    for (int j = 0; j < 32; ++j) __stcg(tile + (c0 + j) * kPartRows + row, v[j]);
 }
-template <typename T>
-__device__ __forceinline__ void sum_parts(float* base, int slot0, int parts, int c0, int row, T* r) {
-    float v[32];
+// 32 columns of this warp's 32 rows of an accumulator.
+__device__ __forceinline__ void read_tmem(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(taddr, r);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+__device__ __forceinline__ void sum_parts(float* base, int slot0, int parts, int c0, int row, float* v) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __ldcg(part_tile(base, slot0) + (c0 + j) * kPartRows + row);
     for (int z = 1; z < parts; ++z) {
@@ -237,38 +247,40 @@ __device__ __forceinline__ void sum_parts(float* base, int slot0, int parts, int
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] += __ldcg(t + (c0 + j) * kPartRows + row);
     }
-#pragma unroll
-    for (int j = 0; j < 32; ++j) *reinterpret_cast<float*>(r + j) = v[j];
 }
-// True in the CTA that brings a unit's last part (all 8 epilogue warps call it, their parts written).
+// True in the CTA that brings a unit's last part (all epilogue warps call it, their parts written).
+template <int kWarps>
 __device__ __forceinline__ bool last_part(int32_t* ticket, int parts, int* s_last) {
     __threadfence();
-    epi_sync();
+    epi_sync<kWarps>();
     if (threadIdx.x == 64) {
         const int n = atomicAdd(ticket, 1);
         __threadfence();
         *s_last = n == parts - 1;
         if (n == parts - 1) *ticket = 0;   // for the next call
     }
-    epi_sync();
+    epi_sync<kWarps>();
     const bool last = *s_last != 0;
-    epi_sync();   // read before the next unit writes it
+    epi_sync<kWarps>();   // read before the next unit writes it
     return last;
 }
 
 // ------------------------------------------------------------------------ rows
 // The list of row_tiles_kernel for a table of few row tiles, made in shared memory by every CTA for itself, which
 // saves a launch: up to kRgLocal tiles in (rank, row) order; returns their number (0 for a bad table).
-__device__ __forceinline__ int local_tiles(const RgParams& p, MTile* out, int* s_warp) {
+__device__ __forceinline__ int local_tiles(const RgParams& p, int* table, MTile* out, int* s_warp) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int items = p.R * p.NROW, per = (items + kRgThreads - 1) / kRgThreads;
+#pragma unroll 8
+    for (int i = t; i < items + p.R; i += kRgThreads) table[i] = p.cu[i];
+    __syncthreads();
     const int lo = min(items, t * per), hi = min(items, lo + per);
     int n = 0, bad = 0;
     auto segment = [&](int i, int* u, int* rho, int* a, int* b) {
-        *u = i / p.NROW;
+        *u = (int)fast_div(i, p.by_nrow);
         *rho = i - *u * p.NROW;
-        *a = p.cu[i + *u];   // rank u's table has one more entry than segments
-        *b = p.cu[i + *u + 1];
+        *a = table[i + *u];   // rank u's table has one more entry than segments
+        *b = table[i + *u + 1];
     };
     for (int i = lo; i < hi; ++i) {
         int u, rho, a, b;
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                                                                const __grid_constant__ RowMaps tmAdd, const RgParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages);
+    Frame f = open_frame(smem_raw, p.stages, 8);
     uint8_t* smA = f.ring;
     uint8_t* smB = smA + p.stages * p.a_bytes;
     uint8_t* smT = smB + p.stages * p.b_bytes;   // kAdd: the units' boxes, else a box of each epilogue warp
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
     int ntiles;
     if (p.local) {
         MTile* list = reinterpret_cast<MTile*>(f.ring + kRgBytes - kRgLocal * sizeof(MTile));
-        ntiles = local_tiles(p, list, f.s_rows);
+        ntiles = local_tiles(p, reinterpret_cast<int*>(f.ring), list, f.s_rows);   // (the ring is not in use yet)
         tiles = list;
     } else {
         ntiles = *p.ntiles;
@@ -395,8 +407,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     if (kTrans)
                         tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, u.n0, u.expert);
                     else
-                        for (int c = 0; c * kRgChunk < p.b_bytes; ++c)
-                            tma_load_3d(&tmW, &f.full[pr.at], b + c * kRgChunk, u.n0 + c * 64, kb * 64, u.expert);
+                        for (int c = 0; c * p.chunk < p.b_bytes; ++c)
+                            tma_load_3d(&tmW, &f.full[pr.at], b + c * p.chunk, u.n0 + c * 64, kb * 64, u.expert);
                     pr.step(p.stages);
                 }
                 if (kAdd && parts == 1 && live) {
@@ -433,7 +445,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     const uint32_t a = smem_u32(smA + s * p.a_bytes), b = smem_u32(smB + s * p.b_bytes);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16(dt, operand<false>(a, kk), operand<!kTrans>(b, kk), idesc, (kb != u.kb0) || kk);
+                        if (kk < p.steps)
+                            mma_bf16(dt, operand<false>(a, kk), operand<!kTrans>(b, kk, p.chunk), idesc, (kb != u.kb0) || kk);
                     mma_commit(&f.empty[s]);
                     if (++s == (uint32_t)p.stages) {
                         s = 0;
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             if (kAdd && parts == 1) done = done && mbar_wait_held(&f.afull[as], aph, f.s_abort, p.status);
             done = __all_sync(0xffffffffu, done);
             // (warps that meet at barriers give up together)
-            if (parts > 1 ? !epi_all(done) : !done) break;
+            if (parts > 1 ? !epi_all<8>(done) : !done) break;
             ++it;
             tc_fence_after();
             const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256;
@@ -477,12 +490,12 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             bool mine_to_store = true;
             if (parts > 1) {
                 for (int c0 = 64 * box0; c0 < min(64 * box1, p.BN); c0 += 32) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tacc + c0, r);
+                    float r[32];
+                    read_tmem(tacc + c0, r);
                     put_part(part_tile(p.partial, i), c0, 32 * q + lane, r);
                 }
                 release();
-                mine_to_store = last_part(p.tickets + u.unit, parts, f.s_last);
+                mine_to_store = last_part<8>(p.tickets + u.unit, parts, f.s_last);
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -505,9 +518,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                 for (int h = 0; h < 2; ++h) {
                     const int c0 = 64 * bx + 32 * h;
                     if (c0 >= p.BN) break;
-                    uint32_t r[32];
+                    float r[32];
                     if (parts > 1) sum_parts(p.partial, slot0, parts, c0, 32 * q + lane, r);
-                    else tmem_ld_32x32b_x32(tacc + c0, r);
+                    else read_tmem(tacc + c0, r);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint4& at = line[(4 * h + j) ^ (lane & 7)];
@@ -521,7 +534,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float lo = __uint_as_float(r[8 * j + 2 * e]), hi = __uint_as_float(r[8 * j + 2 * e + 1]);
+                            float lo = r[8 * j + 2 * e], hi = r[8 * j + 2 * e + 1];
                             if (kAdd) {
                                 lo = fmaf(p.alpha, lo, __uint_as_float(w[e] << 16));
                                 hi = fmaf(p.alpha, hi, __uint_as_float(w[e] & 0xffff0000u));
@@ -562,40 +575,67 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------------ matrices
-// Blocks of up to 64 rows of each expert's segments, in (rank, row) order: tiles[first[e] .. first[e + 1]). One CTA. A
-// slot whose expert is unknown is reported and left out; a table with any inconsistent segment is refused as a whole.
+// Blocks of up to 64 rows of each expert's segments: first its home rows', then its slots', each in (rank, row) order, at
+// tiles[first[e] .. first[e + 1]). One CTA. A slot whose expert is unknown is reported and left out; a table with any
+// inconsistent segment is refused as a whole.
 __global__ void __launch_bounds__(1024) ragged_blocks_kernel(const int32_t* cu, const int32_t* slot_expert, Dims d,
-                                                               Workspace ws) {
-    __shared__ int s_pos[kMaxE];
+                                                             Workspace ws) {
+    static_assert(kMaxE == 2048, "two experts, and two slots, a thread");   // there are at most as many slots as experts
+    __shared__ int s_home[kMaxE], s_pos[kMaxE];     // blocks of the expert's home rows; of all, then where they begin
+    __shared__ int2 s_slot[kMaxE];                  // expert and blocks of each slot
     __shared__ int s_sum[32];
     grid_launch_dependents();
     grid_wait();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    for (int e = t; e < kMaxE; e += 1024) s_pos[e] = 0;
+    const int nslots = d.R * d.B, pitch = d.NROW + 1;
     if (t < kRgTickets) ws.tickets[t] = 0;
-    __syncthreads();
-    auto expert_of = [&](int u, int rho) {
-        const int e = rho < d.E ? rho : slot_expert[u * d.B + rho - d.E];
-        return e >= 0 && e < d.E ? e : -1;
-    };
+    auto blocks = [](int a, int b) { return (b - a + 63) / 64; };
     int bad = 0, unknown = 0;
-    for (int u = 0; u < d.R; ++u)
-        for (int rho = t; rho < d.NROW; rho += 1024) {
-            const int a = cu[u * (d.NROW + 1) + rho], b = cu[u * (d.NROW + 1) + rho + 1];
-            bad |= a < 0 || b < a || (int64_t)b > d.C;
-            if (b <= a) continue;
-            const int e = expert_of(u, rho);
-            if (e < 0) {
-                unknown = 1;
-            } else {
-                atomicAdd(&s_pos[e], (b - a + 63) / 64);
+    constexpr int kU = 8;   // ranks whose entries are read at once
+    for (int e = t; e < kMaxE; e += 1024) {
+        int n = 0;
+        if (e < d.E)
+            for (int u0 = 0; u0 < d.R; u0 += kU) {
+                int a[kU], b[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    a[u] = b[u] = 0;
+                    if (u0 + u < d.R) {
+                        a[u] = cu[(u0 + u) * pitch + e];
+                        b[u] = cu[(u0 + u) * pitch + e + 1];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    bad |= a[u] < 0 || b[u] < a[u] || (int64_t)b[u] > d.C;
+                    n += blocks(a[u], b[u]);
+                }
             }
+        s_home[e] = s_pos[e] = n;
+    }
+    __syncthreads();
+    int sa[2] = {0, 0}, sb[2] = {0, 0}, se[2] = {-1, -1};   // this thread's slots
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = t + 1024 * k;
+        if (i >= nslots) continue;
+        const int u = i / d.B, j = i - u * d.B;
+        sa[k] = cu[u * pitch + d.E + j];
+        sb[k] = cu[u * pitch + d.E + j + 1];
+        const int e = slot_expert[i];
+        bad |= sa[k] < 0 || sb[k] < sa[k] || (int64_t)sb[k] > d.C;
+        if (sb[k] > sa[k]) {
+            if (e >= 0 && e < d.E) se[k] = e;
+            else unknown = 1;
         }
+        const int n = blocks(sa[k], sb[k]);
+        s_slot[i] = make_int2(se[k], n);
+        if (se[k] >= 0) atomicAdd(&s_pos[se[k]], n);
+    }
     bad = __syncthreads_or(bad);
-    if (__syncthreads_or(unknown) && t == 0) set_status(ws.status, BEP_DERR_BOUNDS);
-    if (bad && t == 0) set_status(ws.status, BEP_DERR_BOUNDS);
-    // exclusive scan of the counts: two experts a thread
-    static_assert(kMaxE == 2048, "two experts a thread");
+    unknown = __syncthreads_or(unknown);
+    if ((bad || unknown) && t == 0) set_status(ws.status, BEP_DERR_BOUNDS);
+    // exclusive scan of the blocks
     const int n0 = s_pos[2 * t], n1 = s_pos[2 * t + 1];
     int incl = n0 + n1;
 #pragma unroll
@@ -607,7 +647,7 @@ __global__ void __launch_bounds__(1024) ragged_blocks_kernel(const int32_t* cu, 
     __syncthreads();
     int before = 0;
     for (int w = 0; w < warp; ++w) before += s_sum[w];
-    const int at = bad ? -1 : before + incl - n0 - n1;
+    const int at = before + incl - n0 - n1;
     s_pos[2 * t] = at;
     s_pos[2 * t + 1] = at + n0;
     if (2 * t <= d.E) ws.blk_first[2 * t] = bad ? -1 : at;
@@ -615,37 +655,39 @@ __global__ void __launch_bounds__(1024) ragged_blocks_kernel(const int32_t* cu, 
     if (t == 1023 && d.E == kMaxE) ws.blk_first[kMaxE] = bad ? -1 : at + n0 + n1;
     __syncthreads();
     if (bad) return;
+    // A warp's lanes hold a segment each; long ones are written by the warp together.
     auto put = [&](int at, int u, int a, int b) {
-        for (; a < b; a += 64) ws.tiles[at++] = MTile{(int32_t)(u * d.C + a), min(64, b - a), 0, 0};
+        const int n = blocks(a, b);
+        const bool many = n > 8;
+        if (!many)
+            for (int k = 0; k < n; ++k)
+                ws.tiles[at + k] = MTile{(int32_t)(u * d.C + a + 64 * k), min(64, b - a - 64 * k), 0, 0};
+        for (unsigned todo = __ballot_sync(0xffffffffu, many); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const int at1 = __shfl_sync(0xffffffffu, at, src), a1 = __shfl_sync(0xffffffffu, a, src);
+            const int b1 = __shfl_sync(0xffffffffu, b, src), u1 = __shfl_sync(0xffffffffu, u, src), n1 = blocks(a1, b1);
+            for (int k = lane; k < n1; k += 32)
+                ws.tiles[at1 + k] = MTile{(int32_t)(u1 * d.C + a1 + 64 * k), min(64, b1 - a1 - 64 * k), 0, 0};
+        }
     };
-    for (int u = 0; u < d.R; ++u) {
-        const int32_t* row = cu + u * (d.NROW + 1);
-        // home rows: every one its own expert
-        for (int e = t; e < d.E; e += 1024) {
-            const int a = row[e], b = row[e + 1];
-            if (b > a) {
-                put(s_pos[e], u, a, b);
-                s_pos[e] += (b - a + 63) / 64;
-            }
+    for (int e = t; e < kMaxE; e += 1024) {
+        int at = s_pos[e];
+        for (int u = 0; u < d.R; ++u) {
+            const int a = e < d.E ? cu[u * pitch + e] : 0, b = e < d.E ? cu[u * pitch + e + 1] : 0;
+            put(at, u, a, b);
+            at += blocks(a, b);
         }
-        __syncthreads();
-        // slots: several of a rank may hold one expert, so a slot counts the blocks of those before it
-        for (int j0 = 0; j0 < d.B; j0 += 1024) {
-            const int j = j0 + t;
-            int e = -1, a = 0, b = 0, ahead = 0;
-            if (j < d.B) {
-                a = row[d.E + j];
-                b = row[d.E + j + 1];
-                if (b > a) e = expert_of(u, d.E + j);
-            }
-            if (e >= 0)
-                for (int i = j0; i < j; ++i)
-                    if (slot_expert[u * d.B + i] == e) ahead += (row[d.E + i + 1] - row[d.E + i] + 63) / 64;
-            if (e >= 0) put(s_pos[e] + ahead, u, a, b);
-            __syncthreads();
-            if (e >= 0) atomicAdd(&s_pos[e], (b - a + 63) / 64);
-            __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // a slot lies behind the expert's earlier slots: several may hold one expert
+        const int i = t + 1024 * k;
+        int at = 0;
+        if (se[k] >= 0) {
+            at = s_pos[se[k]] + s_home[se[k]];
+            for (int j = 0; j < i; ++j)
+                if (s_slot[j].x == se[k]) at += s_slot[j].y;
         }
+        put(at, i < nslots ? i / d.B : 0, se[k] >= 0 ? sa[k] : 0, se[k] >= 0 ? sb[k] : 0);
     }
 }
 
@@ -660,15 +702,17 @@ __device__ __forceinline__ void zero_rows(uint8_t* chunk, int chunks, int tail, 
     }
 }
 
-// A unit: MI x 128 x BN of an expert's gradient, MI = 2 where BN leaves both room in an accumulator. The wider side is the
-// M operand; both lie along the rows (MN-major).
-__global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
+// A unit: MI x 128 x BN of an expert's gradient, MI = 2 where BN leaves both room in an accumulator. Both
+// operands lie along the rows (MN-major).
+template <int MI>
+__global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
                                                                   const __grid_constant__ CUtensorMap tmN,
                                                                   const RgDwParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages);
-    const int a_bytes = p.MI * kRgA, stage = a_bytes + p.b_bytes;
+    Frame f = open_frame(smem_raw, p.stages, 16);
+    constexpr int a_bytes = MI * kRgA;
+    const int stage = a_bytes + p.b_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Started pr;
     grid_wait();   // launched early: the segments and the rows are complete from here on
@@ -690,7 +734,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
         const int part = i - it.unit * parts;
         it.expert = fast_div(it.unit, p.by_unit);
         const int rest = it.unit - it.expert * p.MT * p.NT, m = fast_div(rest, p.by_nt);
-        it.m0 = m * p.MI * 128;
+        it.m0 = m * MI * 128;
         it.n0 = (rest - m * p.NT) * p.BN;
         const int64_t nb = range.y - range.x;
         it.b0 = parts == 1 ? range.x : range.x + (int)(part * nb / parts);
@@ -726,7 +770,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
                     f.s_rows[pr.at] = rows;   // for the warp that waits on `full`
                     mbar_arrive_expect_tx(&f.full[pr.at], stage);
                     uint8_t* at = f.ring + pr.at * stage;
-                    for (int c = 0; c < 2 * p.MI; ++c)
+                    for (int c = 0; c < 2 * MI; ++c)
                         tma_load_2d(&tmM, &f.full[pr.at], at + c * kRgChunk, u.m0 + 64 * c, row0);
                     for (int c = 0; c * kRgChunk < p.b_bytes; ++c)
                         tma_load_2d(&tmN, &f.full[pr.at], at + a_bytes + c * kRgChunk, u.n0 + 64 * c, row0);
@@ -763,7 +807,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
                 if (lane == 0) {
                     tc_fence_after();
                     const uint32_t a = smem_u32(at), bb = a + a_bytes;
-                    for (int m = 0; m < p.MI; ++m)
+#pragma unroll
+                    for (int m = 0; m < MI; ++m)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             if (16 * kk < rows)
@@ -780,25 +825,23 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
             }
         }
     } else {
-        const int q = warp & 3, second = (warp - 2) >> 2;
-        uint8_t* stg = f.ring + p.stages * stage + (warp - 2) * kRgBox;
-        const int sub = lane >> 3, piece = lane & 7;   // on the way out: 8 lanes take 32 columns of a row
-        // A warp's boxes of 32 columns: every second one of the tile, or, of two tiles, all of one.
-        const int step = p.MI == 2 ? 32 : 64, start = p.MI == 2 ? 0 : 32 * second;
-        const int tile = p.MI == 2 ? second : 0;
+        const int q = warp & 3, group = (warp - 2) >> 2;   // four groups of four warps, one a quarter of the rows
+        uint8_t* stg = f.ring + p.stages * stage + (warp - 2) * kRgDwBox;
+        const int sub = lane >> 2, piece = lane & 3;   // on the way out: 4 lanes take 16 columns of a row
+        // A warp's two boxes of 32 columns: every fourth one of the tile, or every second one of one of two tiles.
+        constexpr int step = MI == 2 ? 64 : 128;
+        const int start = MI == 2 ? 32 * (group & 1) : 32 * group, tile = MI == 2 ? group >> 1 : 0;
         int it = 0;
         bool live = true;
         for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
             const Item u = item_of(i, next);
             next = range_at(i + gridDim.x);
             if (u.b0 == u.b1 && parts == 1 && p.accumulate) continue;
-            float sum[4][32];   // this thread's row
-            if (u.b0 == u.b1) {
+            float sum[2][32];   // this thread's row
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) sum[b][j] = 0.0f;
-            }
+                for (int j = 0; j < 32; ++j) sum[b][j] = 0.0f;
             for (int b0 = u.b0; b0 < u.b1; b0 += kRgChain) {
                 const int acc = it & 1;
                 if (!__all_sync(0xffffffffu, mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status))) {
@@ -809,17 +852,15 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
                 tc_fence_after();
                 const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256 + tile * 128;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     const int c0 = start + b * step;
                     if (c0 >= p.BN) break;
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tacc + c0, r);
-                    if (b0 == u.b0) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[b][j] = __uint_as_float(r[j]);
-                    } else {
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(tacc + c0 + 16 * h, r);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[b][j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 16; ++j) sum[b][16 * h + j] += __uint_as_float(r[j]);
                     }
                 }
                 tc_fence_before();
@@ -828,15 +869,15 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
             }
             if (parts > 1) {
                 // (warps that meet at barriers give up together)
-                if (!epi_all(live)) break;
+                if (!epi_all<16>(live)) break;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     if (start + b * step >= p.BN) break;
                     put_part(part_tile(p.partial, i), start + b * step, 32 * q + lane, sum[b]);
                 }
-                if (!last_part(p.tickets + u.unit, parts, f.s_last)) continue;
+                if (!last_part<16>(p.tickets + u.unit, parts, f.s_last)) continue;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     if (start + b * step >= p.BN) break;
                     sum_parts(p.partial, u.unit * parts, parts, start + b * step, 32 * q + lane, sum[b]);
                 }
@@ -845,37 +886,44 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
             const int m0 = u.m0 + tile * 128 + 32 * q;   // this warp's 32 along M
             float* g = p.g + (int64_t)u.expert * p.g_expert;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 const int c0 = start + b * step;
                 if (c0 >= p.BN || m0 >= p.Md) break;
                 const int n0 = u.n0 + c0;
                 if (p.ldm == 1) {   // the lanes' 32 lie together
                     if (m0 + lane < p.Md) {
                         float* out = g + (int64_t)n0 * p.ldn + m0 + lane;
+                        const int cols = min(p.BN - c0, p.Nd - n0);   // a multiple of 8
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c0 + j < p.BN && n0 + j < p.Nd) {
-                                float v = p.alpha * sum[b][j];
-                                if (p.accumulate) v += *out;
-                                *out = v;
-                                out += p.ldn;
+                        for (int j = 0; j < 32; j += 8)
+                            if (j < cols) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    float v = p.alpha * sum[b][j + k];
+                                    if (p.accumulate) v += *out;
+                                    *out = v;
+                                    out += p.ldn;
+                                }
                             }
                     }
                 } else {
-                    float4* line = reinterpret_cast<float4*>(stg + lane * 128);
-                    __syncwarp();   // the box before has been read
+                    float4* line = reinterpret_cast<float4*>(stg + lane * 64);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        line[j ^ (lane & 7)] = make_float4(sum[b][4 * j], sum[b][4 * j + 1], sum[b][4 * j + 2], sum[b][4 * j + 3]);
-                    __syncwarp();
-                    const int c = c0 + 4 * piece;
-                    if (c < p.BN && u.n0 + c < p.Nd) {
+                    for (int h = 0; h < 2; ++h) {
+                        __syncwarp();   // the box before has been read
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            line[j ^ ((lane >> 1) & 3)] = make_float4(sum[b][16 * h + 4 * j], sum[b][16 * h + 4 * j + 1],
+                                                                      sum[b][16 * h + 4 * j + 2], sum[b][16 * h + 4 * j + 3]);
+                        __syncwarp();
+                        const int c = c0 + 16 * h + 4 * piece;
+                        if (c >= p.BN || u.n0 + c >= p.Nd) continue;
                         float4* out = reinterpret_cast<float4*>(g + (int64_t)(m0 + sub) * p.ldm + u.n0 + c);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int rr = 4 * j + sub;
+                        for (int j = 0; j < 4; ++j) {
+                            const int rr = 8 * j + sub;
                             if (m0 + rr < p.Md) {
-                                float4 v = *reinterpret_cast<const float4*>(stg + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                                float4 v = *reinterpret_cast<const float4*>(stg + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4));
                                 v.x *= p.alpha;
                                 v.y *= p.alpha;
                                 v.z *= p.alpha;
@@ -889,7 +937,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_dw_kernel(const __grid_c
                                 }
                                 *out = v;
                             }
-                            out += p.ldm;   // 4 rows of floats
+                            out += 2 * p.ldm;   // 8 rows, in vectors of 4
                         }
                     }
                 }
@@ -937,7 +985,7 @@ void cut(int width, int most, int* tile, int* tiles) {
 cudaError_t ragged_setup() {
     const void* kernels[] = {(const void*)ragged_kernel<false, false>, (const void*)ragged_kernel<false, true>,
                              (const void*)ragged_kernel<true, false>, (const void*)ragged_kernel<true, true>,
-                             (const void*)ragged_dw_kernel};
+                             (const void*)ragged_dw_kernel<1>, (const void*)ragged_dw_kernel<2>};
     for (const void* k : kernels) {
         const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
         if (err != cudaSuccess) return err;
@@ -978,13 +1026,16 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     // Tiles of 64 columns, whose reduction may be cut into parts, where even as many row tiles as there can be do not
     // make a unit for every SM with wider ones. With a short reduction and something to add, a unit is mostly what
     // it adds and writes: smaller tiles, more of them under way.
-    const bool thin = add && p.kbn < 16;
+    const bool thin = add && p.kbn < 16 && !few;
     const int wide = thin ? 128 : 256;
     cut(N, most * ((N + wide - 1) / wide) < num_sms ? 64 : wide, &p.BN, &p.NT);
     p.by_nt = make_fast_div((uint32_t)p.NT);
+    p.by_nrow = make_fast_div((uint32_t)d.NROW);
     if (p.BN <= kRgPartCols) p.partial = ws.partial;
-    p.b_bytes = trans ? p.BN * 128 : (p.BN + 63) / 64 * kRgChunk;
-    p.adds = add ? (thin ? kRgMaxAdds : 1) : 0;
+    p.steps = K >= 64 ? 4 : (K + 15) / 16;
+    p.chunk = p.steps * 16 * 128;   // W [K, N]: boxes of 64 columns no taller than the reduction
+    p.b_bytes = trans ? p.BN * 128 : (p.BN + 63) / 64 * p.chunk;
+    p.adds = add ? (thin ? kRgMaxAdds : few ? 2 : 1) : 0;
     p.add_bytes = (p.BN + 63) / 64 * kRgA;
     // (the last stage of small row tiles is read as 128 rows: up to kRgA / 2 behind the rows' stages, inside the rest)
     const int rest = kRgBytes - (p.local ? kRgLocal * (int)sizeof(MTile) : 0) - (add ? p.adds * p.add_bytes : 8 * kRgBox);
@@ -1003,7 +1054,7 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     }
     const uint64_t wd[3] = {(uint64_t)(trans ? K : N), (uint64_t)(trans ? N : K), (uint64_t)d.E};
     const uint64_t wl[2] = {wd[0], wd[0] * wd[1]};
-    if (!encode_rows(&tmW, w, 3, wd, wl, trans ? (uint32_t)p.BN : 64)) return cudaErrorInvalidValue;
+    if (!encode_rows(&tmW, w, 3, wd, wl, trans ? (uint32_t)p.BN : (uint32_t)p.steps * 16)) return cudaErrorInvalidValue;
     if (!p.local) {
         const cudaError_t err = few ? launch_row_tiles<64>(d, ws, cu, st) : launch_row_tiles<128>(d, ws, cu, st);
         if (err != cudaSuccess) return err;
@@ -1027,7 +1078,11 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     p.g_expert = (int64_t)K * N;
     p.alpha = alpha;
     p.E = d.E;
-    const bool x_wide = K >= N;
+    // The M side is padded to 128 and the other to 16, so it is the wider one; x where that costs little, since then
+    // four columns of g leave at a time.
+    const int64_t pad_x = (int64_t)((K + 127) / 128 * 128) * ((N + 15) / 16 * 16);
+    const int64_t pad_y = (int64_t)((N + 127) / 128 * 128) * ((K + 15) / 16 * 16);
+    const bool x_wide = pad_x <= pad_y + pad_y / 4;
     p.Md = x_wide ? K : N;
     p.Nd = x_wide ? N : K;
     p.ldm = x_wide ? N : 1;
@@ -1037,24 +1092,22 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     p.partial = ws.partial;
     p.status = ws.status;
     // two tiles along M a unit (half the units, each block of the narrow side read half as often) where they fill the SMs
-    p.MI = p.Nd <= 128 && (int64_t)d.E * ((p.Md + 255) / 256) >= 2 * num_sms ? 2 : 1;
-    p.MT = (p.Md + 128 * p.MI - 1) / (128 * p.MI);
+    const int MI = p.Nd <= 128 && (int64_t)d.E * ((p.Md + 255) / 256) >= 2 * num_sms ? 2 : 1;
+    p.MT = (p.Md + 128 * MI - 1) / (128 * MI);
     const int64_t units = (int64_t)d.E * p.MT * ((p.Nd + 255) / 256);
     cut(p.Nd, units < num_sms ? 64 : 256, &p.BN, &p.NT);
     p.parts = 1;
     const int64_t n = (int64_t)d.E * p.MT * p.NT;
     if (p.BN <= kRgPartCols && n < num_sms) {
-        // parts of at least 4 blocks of an expert of mean length
-        const int64_t fit = num_sms / n, len = rows / 64 / d.E / 4;
-        int64_t z = fit < len ? fit : len;
-        z = z < kRgMaxParts ? z : kRgMaxParts;
-        p.parts = z > 1 ? (int)z : 1;
+        // a block takes a third of the time that adding a part does: for an expert of mean length, parts^2 <= blocks / 2
+        const int64_t fit = num_sms / n, len = rows / 64 / d.E / 2;
+        while (p.parts < kRgMaxParts && p.parts < fit && (int64_t)(p.parts + 1) * (p.parts + 1) <= len) ++p.parts;
     }
     p.by_parts = make_fast_div((uint32_t)p.parts);
     p.by_unit = make_fast_div((uint32_t)(p.MT * p.NT));
     p.by_nt = make_fast_div((uint32_t)p.NT);
     p.b_bytes = (p.BN + 63) / 64 * kRgChunk;
-    const int fit = (kRgBytes - 8 * kRgBox) / (p.MI * kRgA + p.b_bytes);
+    const int fit = (kRgBytes - 16 * kRgDwBox) / (MI * kRgA + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;
 
     CUtensorMap tx, ty;
@@ -1068,7 +1121,8 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_blocks_kernel, cu, slot_expert, d, ws);
     if (err != cudaSuccess) return err;
     cfg = rg_config(num_sms, st, attr);
-    return cudaLaunchKernelEx(&cfg, ragged_dw_kernel, x_wide ? tx : ty, x_wide ? ty : tx, p);
+    cfg.blockDim = dim3(kRgDwThreads, 1, 1);
+    return cudaLaunchKernelEx(&cfg, MI == 2 ? ragged_dw_kernel<2> : ragged_dw_kernel<1>, x_wide ? tx : ty, x_wide ? ty : tx, p);
 }
 
 }  // namespace bep
