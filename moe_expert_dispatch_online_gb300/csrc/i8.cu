@@ -136,10 +136,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s_warp) {
 
 // codes[dest[tok, k]], scales[dest[tok, k]] = i8(x[tok]). A CTA per token: a thread holds kHold pieces of 16
 // elements between the two passes over them, and what lies beyond (rows of more than 8192 * kHold) it reads again.
-#ifndef DHOLD
-#define DHOLD 2
-#endif
-constexpr int kDispatchThreads = 512, kHold = DHOLD;
+constexpr int kDispatchThreads = 512, kHold = 2;   // (1 and 4 measured the same)
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_i8_kernel(const uint4* __restrict__ x,
                                                                        const int32_t* __restrict__ dest,
                                                                        uint4* __restrict__ codes,
@@ -298,6 +295,7 @@ constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = 32 * (2 + 8 + 8 + kI8EpiWarps);
 constexpr int kI8Out = 32 * 256;                // bytes: four epilogue warps' 32 rows x 128 outputs
 constexpr int kI8Tmem = 512;
+constexpr int kI8Parts = 8;                     // of a unit's reduction at most, each of at least 7 stages
 
 // kRows: rows of a tile at most. Fewer rows leave room for more stages under way.
 template <int kRows>
@@ -312,6 +310,7 @@ struct I8Cfg {
     static constexpr size_t kSmem = 1024 + (size_t)kRing * kStage + (size_t)kSlots * kB + kI8EpiWarps / 4 * kI8Out + kRows * 4 +
                                     (2 * kRing + 2 * kSlots + 5) * 8 + 16;
     static_assert(kABase + kSlots * kACols <= kI8Tmem, "TMEM");
+    static_assert(kSlots >= 2 && kRing >= 2, "two groups take turns in both");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -324,7 +323,42 @@ struct I8Params {
     uint16_t* y;
     int64_t nrows;
     int E, H, Hp, MT;
+    int32_t* tickets;
+    float* partial;
     int32_t* status;
+};
+
+// Work of a pair of CTAs: whole units, or, in the form for so few units that most pairs would have none, a unit's part
+// z of the reduction's stages. A part leaves its fp32 sums in the workspace, and the CTA of each rank that comes last
+// adds them in order (one token through two experts of 7168 x 512, four units: 26.8 us whole, 13.3 us in eight parts).
+struct I8Geo {
+    int items, z, nst;
+};
+struct I8Item : Unit {
+    int unit, part, k0, k1;   // (parts only) stages of the reduction
+};
+template <bool kSplit>
+struct I8Walk {
+    UnitWalk w;
+    int item;
+    __device__ __forceinline__ I8Walk(int first, int ncl, int MP) : w(first, ncl, MP), item(first) {}
+    __device__ __forceinline__ I8Item take(const I8Params& p, const I8Geo& g) {
+        I8Item u;
+        u.k0 = 0;
+        u.k1 = g.nst;
+        if (!kSplit) {
+            static_cast<Unit&>(u) = w.take(p, g.items);
+        } else {
+            u.unit = item / g.z;
+            u.part = item - u.unit * g.z;
+            UnitWalk one(u.unit, w.ncl, w.MP);
+            static_cast<Unit&>(u) = one.take(p, g.items / g.z);
+            u.k0 = u.part * g.nst / g.z;
+            u.k1 = (u.part + 1) * g.nst / g.z;
+            item += w.ncl;
+        }
+        return u;
+    }
 };
 
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2) {
@@ -365,6 +399,20 @@ __device__ __forceinline__ void mma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem
         : "memory");
 }
 
+// All eight epilogue warps.
+__device__ __forceinline__ bool octet_all(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, 3, 256, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
 // Four int8 to four fp16: the byte with its sign bit turned, behind 0x64, is 1024 + 128 + q in fp16.
 __device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t* out) {
     const uint32_t u = w ^ 0x80808080u;
@@ -382,7 +430,7 @@ __device__ __forceinline__ void i8x16_to_f16(const uint4& v, uint32_t* out) {
     i8x4_to_f16(v.w, out + 6);
 }
 
-template <int kRows>
+template <int kRows, bool kSplit>
 __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX16,
     const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX64,
@@ -405,6 +453,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
     uint64_t* drain = tempty + 2;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    int* s_last = reinterpret_cast<int*>(s_tmem + 2);
     int32_t* status = p.status;
     const uint32_t rank = cluster_rank();
     const bool lead = rank == 0;
@@ -446,19 +495,24 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
     grid_wait();      // launched early: the work list and the rows are complete from here on
 
     const int MP = (p.MT + 1) / 2;             // pairs of 128-output tiles
-    const int total = *p.ntiles * MP;
-    const int nst = (p.H + kI8K - 1) / kI8K;   // stages a unit
     const int cl0 = (int)cluster_id(), ncl = (int)cluster_count();
+    I8Geo geo{*p.ntiles * MP, 1, (p.H + kI8K - 1) / kI8K};
+    if (kSplit && geo.items > 0) {
+        static_assert(!kSplit || kRows <= kRgPartCols, "a part's tile");
+        geo.z = max(1, min(min(ncl / geo.items, geo.nst / 7), kI8Parts));
+        geo.items *= geo.z;
+    }
+    const int total = geo.items;
     uint32_t pr_i = 0, pr_ph = 0, pr_armed = 0;
 
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
-            UnitWalk walk(cl0, ncl, MP);
-            Unit next = walk.take(p, total);   // read a unit ahead
+            I8Walk<kSplit> walk(cl0, ncl, MP);
+            I8Item next = walk.take(p, geo);   // read a unit ahead
             for (int unit = cl0; unit < total && live; unit += ncl) {
-                const Unit u = next;
-                next = walk.take(p, total);
+                const I8Item u = next;
+                next = walk.take(p, geo);
                 if (u.expert < 0) {
                     if (lead) set_status(status, BEP_DERR_BOUNDS);
                     continue;
@@ -467,7 +521,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
                 const int half = mma_rows(u.rows) / 2, row = u.row0 + (int)rank * half;
                 const CUtensorMap* tmX = half <= 16 ? &tmX16 : half <= 32 ? &tmX32 : half <= 64 ? &tmX64 : &tmX128;
                 const int bytes = kI8W + (half <= 16 ? 16 : half <= 32 ? 32 : half <= 64 ? 64 : 128) * kI8K;
-                for (int k = 0; k < nst; ++k) {
+                for (int k = u.k0; k < u.k1; ++k) {
                     if (!mbar_wait_held(&wempty[pr_i], pr_ph ^ 1u, s_abort, status)) {
                         live = false;
                         break;
@@ -490,11 +544,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
             uint32_t half = 0;        // accumulator of the next unit of up to 128 rows
             uint32_t aph[2] = {1, 1};   // the phases that free the accumulators
             bool live = true;
-            UnitWalk walk(cl0, ncl, MP);
-            Unit next = walk.take(p, total);
+            I8Walk<kSplit> walk(cl0, ncl, MP);
+            I8Item next = walk.take(p, geo);
             for (int unit = cl0; unit < total && live; unit += ncl) {
-                const Unit u = next;
-                next = walk.take(p, total);
+                const I8Item u = next;
+                next = walk.take(p, geo);
                 if (u.expert < 0) continue;
                 const int N = mma_rows(u.rows);
                 const bool big = N > C::kAcc;
@@ -505,7 +559,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
                 if (big) aph[1] ^= 1u;
                 const uint32_t dt = tmem_base + half * C::kAcc;
                 const uint32_t idesc = idesc_f16(N);
-                for (int k = 0; k < nst; ++k) {
+                for (int k = u.k0; k < u.k1; ++k) {
                     if (!mbar_wait_held<true>(&ready[s], ph, s_abort, status)) {
                         live = false;
                         break;
@@ -518,9 +572,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
                     for (int kk = 0; kk < kI8K / 16; ++kk)
                         if (kk < steps)
                             mma_f16_pair_ts(dt, a + kk * 8, sdesc_sw128(b + (kk >> 2) * C::kSub + (kk & 3) * 32, 16, 1024),
-                                            idesc, (k | kk) != 0);
+                                            idesc, k != u.k0 || kk != 0);
                     mma_commit_pair(&free_[s]);
-                    if (k == nst - 1) {
+                    if (k == u.k1 - 1) {
                         mma_commit_pair(&tfull[half]);
                         if (big) mma_commit_pair(&tfull[1]);
                     }
@@ -538,10 +592,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
         uint32_t i = group, iph = 0, s = group, sph = 0;         // ring stage and operand slot of this turn
         int turn = 0;
         bool live = true;
-        UnitWalk walk(cl0, ncl, MP);
+        I8Walk<kSplit> walk(cl0, ncl, MP);
         for (int unit = cl0; unit < total && live; unit += ncl) {
-            if (walk.take(p, total).expert < 0) continue;
-            for (int k = 0; k < nst; ++k, turn ^= 1) {
+            const I8Item u = walk.take(p, geo);
+            if (u.expert < 0) continue;
+            for (int k = u.k0; k < u.k1; ++k, turn ^= 1) {
                 if (turn != group) continue;
                 if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status)) ||
                     !__all_sync(0xffffffffu, mbar_wait_held(&wfull[i], iph, s_abort, status))) {
@@ -589,12 +644,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
         uint32_t i = group, iph = 0, s = group, sph = 0;   // ring stage and operand slot of this turn
         int turn = 0;
         bool live = true;
-        UnitWalk walk(cl0, ncl, MP);
+        I8Walk<kSplit> walk(cl0, ncl, MP);
         for (int unit = cl0; unit < total && live; unit += ncl) {
-            const Unit u = walk.take(p, total);
+            const I8Item u = walk.take(p, geo);
             if (u.expert < 0) continue;
             const int half = mma_rows(u.rows) / 2;
-            for (int k = 0; k < nst; ++k, turn ^= 1) {
+            for (int k = u.k0; k < u.k1; ++k, turn ^= 1) {
                 if (turn != group) continue;
                 if (!__all_sync(0xffffffffu, mbar_wait_held(&free_[s], sph ^ 1u, s_abort, status)) ||
                     !__all_sync(0xffffffffu, mbar_wait_held(&wfull[i], iph, s_abort, status))) {
@@ -644,11 +699,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
         uint8_t* stg = smO + second * kI8Out;
         float* sc = smC + second * (kRows / 2);
         uint32_t half = 0, tph[2] = {0, 0};
-        UnitWalk walk(cl0, ncl, MP);
-        Unit next = walk.take(p, total);
+        I8Walk<kSplit> walk(cl0, ncl, MP);
+        I8Item next = walk.take(p, geo);
         for (int unit = cl0; unit < total; unit += ncl) {
-            const Unit u = next;
-            next = walk.take(p, total);
+            const I8Item u = next;
+            next = walk.take(p, geo);
             if (u.expert < 0) continue;
             const bool big = mma_rows(u.rows) > C::kAcc;
             if (big) half = 0;
@@ -662,7 +717,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
             // one warp waits and the others for it at their barrier; the four give up together
             bool done = quarter != 0 || mbar_wait_held(&tfull[half], tph[half], s_abort, status);
             if (big && quarter == 0 && done) done = mbar_wait_held(&tfull[1], tph[1], s_abort, status);
-            if (!quad_all(1 + second, done)) break;
+            // (all eight warps together where they will meet)
+            if (kSplit ? !octet_all(done) : !quad_all(1 + second, done)) break;
             tph[half] ^= 1u;
             if (big) tph[1] ^= 1u;
             tc_fence_after();
@@ -675,11 +731,59 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
                     if (big) mbar_arrive_rank_relaxed(&tempty[1], 0);
                 }
             };
-            bool held = true;
-            for (int c0 = 32 * second; c0 < u.rows; c0 += 64) {
+            bool held = true, last = true;
+            const int lane0 = quarter * 32 + lane;   // output of the tile
+            if (kSplit && geo.z > 1) {
+                float* out = p.partial + (int64_t)(2 * unit + (int)rank) * (kRgPartCols * 128) + lane0;
+                for (int c0 = 32 * second; c0 < u.rows; c0 += 64) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tacc + c0, r);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < u.rows) __stcg(out + (c0 + j) * 128, __uint_as_float(r[j]));
+                }
+                release();
+                held = false;
+                __threadfence();
+                octet_all(true);
+                if (quarter == 0 && second == 0 && lane == 0) {
+                    int32_t* ticket = p.tickets + 2 * u.unit + (int)rank;
+                    const int n = atomicAdd(ticket, 1);
+                    __threadfence();
+                    *s_last = n == geo.z - 1;
+                    if (n == geo.z - 1) *ticket = 0;   // for the next call
+                }
+                octet_all(true);
+                last = *s_last != 0;   // (no pair has two parts: written once a launch)
+            }
+            for (int c0 = 32 * second; last && c0 < u.rows; c0 += 64) {
                 uint32_t r[32];
-                tmem_ld_32x32b_x32(tacc + c0, r);
-                if (c0 + 64 >= u.rows) {   // this warp has read all its runs: free them before the stores
+                if (kSplit && geo.z > 1) {
+                    const float* in = p.partial + (int64_t)(2 * u.unit * geo.z + (int)rank) * (kRgPartCols * 128) + lane0;
+                    // four rows of all parts at a time
+#pragma unroll
+                    for (int j0 = 0; j0 < 32; j0 += 4) {
+                        float v[4][kI8Parts];
+                        if (c0 + j0 >= u.rows) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int z = 0; z < kI8Parts; ++z)
+                                v[j][z] = z < geo.z && c0 + j0 + j < u.rows
+                                              ? __ldcg(in + (int64_t)2 * z * (kRgPartCols * 128) + (c0 + j0 + j) * 128)
+                                              : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float sum = v[j][0];
+#pragma unroll
+                            for (int z = 1; z < kI8Parts; ++z) sum += v[j][z];
+                            r[j0 + j] = __float_as_uint(sum);
+                        }
+                    }
+                } else {
+                    tmem_ld_32x32b_x32(tacc + c0, r);
+                }
+                if (held && c0 + 64 >= u.rows) {   // this warp has read all its runs: free them before the stores
                     release();
                     held = false;
                 }
@@ -766,13 +870,13 @@ cudaLaunchConfig_t i8_config(int clusters, cudaStream_t st, cudaLaunchAttribute*
     return cfg;
 }
 
-template <int kRows>
+template <int kRows, bool kSplit>
 cudaError_t i8_attributes() {
-    return cudaFuncSetAttribute(grouped_gemm_i8_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(grouped_gemm_i8_kernel<kRows, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)I8Cfg<kRows>::kSmem);
 }
 
-template <int kRows>
+template <int kRows, bool kSplit = false>
 cudaError_t run_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const CUtensorMap& tmW, const CUtensorMap* tmX,
                         const I8Params& p,
                         int clusters, cudaStream_t st) {
@@ -780,7 +884,7 @@ cudaError_t run_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, c
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = i8_config<kRows>(clusters, st, attr);
-    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel<kRows>, tmW, tmX[0], tmX[1], tmX[2], tmX[3], p);
+    return cudaLaunchKernelEx(&cfg, grouped_gemm_i8_kernel<kRows, kSplit>, tmW, tmX[0], tmX[1], tmX[2], tmX[3], p);
 }
 
 template <int kWarps>
@@ -793,16 +897,17 @@ void run_swiglu_i8(int64_t rows, int F8, const uint4* h, uint2* codes, float* sc
 
 // *clusters: pairs of CTAs that can be resident at once (an SM holds one CTA of any kind): the grid of the product.
 cudaError_t i8_setup(int device, int* clusters) {
-    cudaError_t err = i8_attributes<64>();
-    if (err == cudaSuccess) err = i8_attributes<128>();
-    if (err == cudaSuccess) err = i8_attributes<256>();
+    cudaError_t err = i8_attributes<64, true>();
+    if (err == cudaSuccess) err = i8_attributes<64, false>();
+    if (err == cudaSuccess) err = i8_attributes<128, false>();
+    if (err == cudaSuccess) err = i8_attributes<256, false>();
     if (err != cudaSuccess) return err;
     int nsm = 0;
     err = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, device);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = i8_config<256>(nsm / 2, nullptr, attr);
-    return cudaOccupancyMaxActiveClusters(clusters, grouped_gemm_i8_kernel<256>, &cfg);
+    return cudaOccupancyMaxActiveClusters(clusters, grouped_gemm_i8_kernel<256, false>, &cfg);
 }
 
 cudaError_t launch_i8_weight(const Dims& d, const uint16_t* w, int8_t* codes, float* scales, cudaStream_t st) {
@@ -857,6 +962,8 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
     p.H = d.H;
     p.Hp = d.Hp;
     p.MT = (d.Hp + 127) / 128;
+    p.tickets = ws.tickets;
+    p.partial = ws.partial;
     p.status = ws.status;
     const uint64_t wd[3] = {(uint64_t)d.H, (uint64_t)d.Hp, (uint64_t)d.E};
     const uint64_t xd[2] = {(uint64_t)d.H, (uint64_t)d.R * d.C};
@@ -867,6 +974,10 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
         if (!encode_u8(&tmX[i], codes, 2, xd, boxes[i])) return cudaErrorInvalidValue;
     // Rows a tile by the mean segment: a tile of fewer rows leaves room for more weight codes under way.
     const int64_t mean = p.nrows / d.E;
+    // Every row a tile of its own, at most: units for less than half of the pairs. (Below 14 stages there is one part, and
+    // the form without parts is 1.4 us quicker.)
+    if (p.nrows <= 64 && p.nrows * ((p.MT + 1) / 2) * 2 <= clusters && d.H >= 14 * kI8K)
+        return run_gemm_i8<64, true>(d, ws, cu, tmW, tmX, p, clusters, st);
     if (mean <= 48) return run_gemm_i8<64>(d, ws, cu, tmW, tmX, p, clusters, st);
     if (mean <= 96) return run_gemm_i8<128>(d, ws, cu, tmW, tmX, p, clusters, st);
     return run_gemm_i8<256>(d, ws, cu, tmW, tmX, p, clusters, st);

@@ -241,6 +241,31 @@ def test_units_of_both_accumulator_kinds_in_one_launch(lib):
     ctx.close()
 
 
+# few units for the pairs of SMs: the reduction is cut into parts, for all units or for those of the last round
+@pytest.mark.parametrize("R,S,E,K,H,Hp", [(1, 1, 8, 3, 7168, 64), (1, 1, 4, 1, 576, 320), (1, 2, 40, 4, 7168, 2048), (8, 1, 64, 4, 3712, 1024),
+                                          (1, 33, 1, 1, 5120, 512), (2, 30, 2, 1, 2048, 10496)])
+def test_few_units(lib, R, S, E, K, H, Hp):
+    bep = lib
+    ctx, t = planned(bep, R, S, E, K, H, Hp, seed=4, skew=0.3)
+    w = weights(bep, ctx)
+    rng = np.random.default_rng([S, H])
+    x = bf16(rng.normal(size=(R, S, H)))
+    rows = bep.IntRows(R * S * K, H)
+    bep.bep_dispatch_int(ctx, x, t["dest"], rows.codes, rows.scales)
+    q, s = rows.codes.cpu().numpy(), rows.scales.cpu().numpy()
+    wq, ws = w.codes.cpu().numpy(), w.scales.cpu().numpy()
+    expert = row_experts(ctx.cfg, t)
+    want = np.zeros((R * S * K, Hp), np.uint16)
+    for e in np.unique(expert):
+        want[expert == e] = ref.product_bits(q[expert == e], s[expert == e], wq[e], ws[e])
+    for _ in range(3):
+        y = torch.full((R * S * K, Hp), 9.0, dtype=torch.bfloat16, device=DEV)
+        bep.bep_grouped_gemm_int(ctx, t["cu"], t["se"], rows.codes, rows.scales, w.codes, w.scales, y)
+        assert np.array_equal(bits(y), want)
+    assert bep.bep_status(ctx) == 0
+    ctx.close()
+
+
 def test_sums_beyond_24_bits(lib):
     """Every code at its limit, 7168 of them: 127 * 127 * 7168 = 1.2e8. A sum over 16 products at a time that is
     truncated to fp32 after each is off by 2^-23 of the magnitudes for each of the H / 16 steps at most."""
