@@ -548,7 +548,8 @@ int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot
     int rc = check_ragged(ctx, K, N, ldx, ldy, alpha);
     if (rc) return rc;
     if (trans != 0 && trans != 1) return BEP_ERR_ARG;
-    if (add && (ldadd < N || ldadd % 8 != 0)) return BEP_ERR_ARG;
+    if (add && (ldadd < N || ldadd % 8 != 0 || (add == y && ldadd != ldy))) return BEP_ERR_ARG;
+    if (add && ldadd > ((int64_t)1 << 32)) return BEP_ERR_SIZE;
     if (ctx->d.C == 0) return BEP_OK;
     if (!cu_seqlens || !slot_expert || !x || !w || !y || x == y || w == y) return BEP_ERR_ARG;
     if (!aligned(cu_seqlens, 4) || !aligned(slot_expert, 4) || !aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) ||

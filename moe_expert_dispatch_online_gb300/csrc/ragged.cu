@@ -85,25 +85,33 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
         : "memory");
 }
 
-// Operand descriptor of 16 reduction steps of a stage: K-major rows of 64 elements (128 bytes), or MN-major
-// chunks of 64 columns x 64 reduction steps (or `chunk` bytes of them).
+// Operand descriptors reach the instruction as a low word (address in 16-byte units, leading offset) beside a constant
+// high word: 8-row groups 1024 bytes apart, version 1, 128-byte swizzle. The issuing thread's time bounds reductions
+// of narrow tiles, so a stage costs it one addition an operand and the 16-step pieces constant ones.
+//   K-major: rows of 64 elements (128 bytes), a piece 32 bytes along them;
+//   MN-major: chunks of 64 columns x 64 reduction steps (or fewer: `chunk` bytes), a piece 16 of their rows.
+#define BEP_RG_OPERAND_HI "0x40004040"
 template <bool kMN>
-__device__ __forceinline__ uint64_t operand(uint32_t base, int kk, uint32_t chunk = kRgChunk) {
-    return kMN ? sdesc_sw128(base + kk * 2048, chunk, 1024) : sdesc_sw128(base + kk * 32, 16, 1024);
+__device__ __forceinline__ uint32_t operand_lo(uint32_t saddr, uint32_t chunk = kRgChunk) {
+    return ((saddr >> 4) & 0x3FFFu) | ((kMN ? chunk >> 4 : 1u) << 16);
 }
+template <bool kMN>
+__host__ __device__ constexpr uint32_t piece_step() { return kMN ? 128 : 2; }
 
-// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, major bits 15/16 (1: MN), M = 128.
-__device__ __forceinline__ uint32_t idesc_bf16(int N, bool a_mn, bool b_mn) {
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, major bits 15/16 (1: MN), M = 128 or 64.
+__device__ __forceinline__ uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(N >> 3) << 17) | (8u << 24);
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, " BEP_RG_OPERAND_HI "};\n\t"
+        "mov.b64 db, {%2, " BEP_RG_OPERAND_HI "};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 
@@ -315,6 +323,8 @@ __device__ __forceinline__ int local_tiles(const RgParams& p, int* table, MTile*
                     out[at] = MTile{(int32_t)(u * p.C + a), min(p.tile_rows, b - a),
                                     rho < p.E ? rho : -(1 + u * p.B + (rho - p.E)), 0};
         }
+    // the table's place is the ring's: what was read and written here comes before the copies that land there
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     return min(total, kRgLocal);
 }
@@ -328,8 +338,8 @@ __device__ __forceinline__ const CUtensorMap* map_for(const RowMaps& m, int rows
 }
 __device__ __forceinline__ int box_for(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
-// A unit: up to 128 rows of a segment x BN columns. A small tile leaves the accumulator's other rows to whatever the
-// stage holds behind its own; they are not stored.
+// A unit: up to 128 rows of a segment x BN columns, or up to 64 where experts have few rows. A small tile leaves the
+// accumulator's other rows to whatever the stage holds behind its own; they are not stored.
 // kAdd: what the product is added to arrives by TMA, up to four units ahead, in boxes of 64 columns that the epilogue
 // then turns its outputs in.
 template <bool kTrans, bool kAdd>
@@ -423,8 +433,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint32_t idesc = idesc_bf16(p.BN, false, !kTrans);
-            uint32_t s = 0, ph = 0;
+            const uint32_t idesc = idesc_bf16(p.tile_rows, p.BN, false, !kTrans);
+            const uint32_t a0 = operand_lo<false>(smem_u32(smA)), b0 = operand_lo<!kTrans>(smem_u32(smB), p.chunk);
+            const uint32_t a_step = p.a_bytes >> 4, b_step = p.b_bytes >> 4;
+            uint32_t s = 0, ph = 0, a = a0, b = b0;
             int it = 0;
             bool live = true;
             for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
@@ -442,15 +454,23 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = smem_u32(smA + s * p.a_bytes), b = smem_u32(smB + s * p.b_bytes);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < p.steps)
-                            mma_bf16(dt, operand<false>(a, kk), operand<!kTrans>(b, kk, p.chunk), idesc, (kb != u.kb0) || kk);
+                    constexpr uint32_t sa = piece_step<false>(), sb = piece_step<!kTrans>();
+                    mma_bf16(dt, a, b, idesc, kb != u.kb0);
+                    if (p.steps == 4) {
+                        mma_bf16(dt, a + sa, b + sb, idesc, 1);
+                        mma_bf16(dt, a + 2 * sa, b + 2 * sb, idesc, 1);
+                        mma_bf16(dt, a + 3 * sa, b + 3 * sb, idesc, 1);
+                    } else {
+                        for (int kk = 1; kk < p.steps; ++kk) mma_bf16(dt, a + kk * sa, b + kk * sb, idesc, 1);
+                    }
                     mma_commit(&f.empty[s]);
+                    a += a_step;
+                    b += b_step;
                     if (++s == (uint32_t)p.stages) {
                         s = 0;
                         ph ^= 1u;
+                        a = a0;
+                        b = b0;
                     }
                 }
                 if (live) mma_commit(&f.tfull[acc]);
@@ -459,7 +479,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
     } else {
         // Two warps for each quarter of the accumulator's rows, each with half of the boxes of 64 columns. A box is
         // turned in shared memory, so that 8 lanes write 128 bytes of a row of y.
-        const int q = warp & 3, second = (warp - 2) >> 2;
+        // (a tile of 64 rows has 16 of them in each quarter's first lanes)
+        const int q = warp & 3, second = (warp - 2) >> 2, span = p.tile_rows / 4;
         const int sub = lane >> 3, piece = lane & 7;
         const int nbox = (p.BN + 63) / 64, mine = (nbox + 1) / 2, box0 = second * mine, box1 = min(nbox, box0 + mine);
         int it = 0;
@@ -469,8 +490,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             next = tile_at(i + gridDim.x);
             if (u.expert < 0) continue;
             const int acc = it & 1;
-            const int rows = u.rows - 32 * q;          // of this warp's 32
-            const int64_t row0 = (int64_t)u.row0 + 32 * q;
+            const int rows = min(u.rows - span * q, span);   // this warp's
+            const int64_t row0 = (int64_t)u.row0 + span * q;
             bool done = mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status);
             if (kAdd && parts == 1) done = done && mbar_wait_held(&f.afull[as], aph, f.s_abort, p.status);
             done = __all_sync(0xffffffffu, done);
@@ -501,7 +522,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             for (int b = 0; b < 2; ++b) {
                 const int bx = box0 + b;
                 if (bx >= box1 || !mine_to_store) break;
-                uint8_t* stg = kAdd ? smT + as * p.add_bytes + bx * kRgA + q * kRgBox : smT + (warp - 2) * kRgBox;
+                uint8_t* stg = kAdd ? smT + as * p.add_bytes + bx * kRgA + q * span * 128 : smT + (warp - 2) * kRgBox;
                 uint4* line = reinterpret_cast<uint4*>(stg + lane * 128);   // this lane's row of the box
                 const int c = 64 * bx + 8 * piece;
                 const bool in = c < p.BN && u.n0 + c < p.N;
@@ -526,7 +547,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                         uint4& at = line[(4 * h + j) ^ (lane & 7)];
                         uint32_t w[4];
                         if (kAdd) {
-                            const uint4 t = at;
+                            const uint4 t = lane < span ? at : make_uint4(0, 0, 0, 0);
                             w[0] = t.x;
                             w[1] = t.y;
                             w[2] = t.z;
@@ -544,7 +565,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                             }
                             w[e] = pack_bf16x2(lo, hi);
                         }
-                        at = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (lane < span) at = make_uint4(w[0], w[1], w[2], w[3]);   // (the others' place is another warp's)
                     }
                 }
                 if (held && bx + 1 == box1) release();   // this warp has read all its columns
@@ -780,7 +801,7 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
             }
         }
     } else if (warp == 1) {
-        const uint32_t idesc = idesc_bf16(p.BN, true, true);
+        const uint32_t idesc = idesc_bf16(128, p.BN, true, true);
         uint32_t s = 0, ph = 0;
         int it = 0;
         bool live = true;
@@ -806,13 +827,14 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                 }
                 if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t a = smem_u32(at), bb = a + a_bytes;
+                    const uint32_t a = operand_lo<true>(smem_u32(at)), bb = a + (a_bytes >> 4);
+                    constexpr uint32_t st = piece_step<true>();
 #pragma unroll
                     for (int m = 0; m < MI; ++m)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             if (16 * kk < rows)
-                                mma_bf16(dt + m * 128, operand<true>(a + m * kRgA, kk), operand<true>(bb, kk), idesc, k || kk);
+                                mma_bf16(dt + m * 128, a + m * (kRgA >> 4) + kk * st, bb + kk * st, idesc, k || kk);
                     mma_commit(&f.empty[s]);
                     if (k == kRgChain - 1 || b == u.b1 - 1) mma_commit(&f.tfull[acc]);
                 }
@@ -1037,7 +1059,6 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     p.b_bytes = trans ? p.BN * 128 : (p.BN + 63) / 64 * p.chunk;
     p.adds = add ? (thin ? kRgMaxAdds : few ? 2 : 1) : 0;
     p.add_bytes = (p.BN + 63) / 64 * kRgA;
-    // (the last stage of small row tiles is read as 128 rows: up to kRgA / 2 behind the rows' stages, inside the rest)
     const int rest = kRgBytes - (p.local ? kRgLocal * (int)sizeof(MTile) : 0) - (add ? p.adds * p.add_bytes : 8 * kRgBox);
     const int fit = rest / (p.a_bytes + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;

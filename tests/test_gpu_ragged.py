@@ -430,6 +430,8 @@ def test_refusals(lib):
     refused(arg, gemm, x, w, y, alpha=float("nan"))
     refused(arg, gemm, x, w, y, alpha=float("inf"))
     refused(arg, gemm, x, ints((1, 16, 16), 2), x)                                       # onto its own input
+    both = ints((8, 48), 4)
+    refused(arg, gemm, x, w, both[:, :24], add=both.view(-1)[:192].view(8, 24))          # in place, other strides
     refused(arg, dw, ints((8, 12), 1), y, torch.empty(1, 12, 24, device=DEV))
     for bad, kind in ((dict(x=x.float()), TypeError), (dict(x=x[:7]), ValueError), (dict(w=w[0]), ValueError),
                       (dict(w=w.transpose(1, 2)), ValueError), (dict(y=y.t().contiguous().t()), ValueError),
