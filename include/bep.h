@@ -32,9 +32,10 @@
  *     not balance, a timed-out wait) are OR-ed into the context's status
  *     word; kernels that would read invalid indices skip the bad element.
  *     bep_status() reads and reports the word.
- *   - The context owns only its planning/scheduling workspace, allocated
- *     once in bep_create (static shapes: no allocation afterwards). Calls
- *     sharing one context must be ordered on one stream.
+ *   - The context owns only its planning/scheduling workspace (about 5 MB of
+ *     it for reductions that are cut into parts), allocated once in
+ *     bep_create (static shapes: no allocation afterwards). Calls sharing
+ *     one context must be ordered on one stream.
  */
 #ifndef BEP_H_
 #define BEP_H_

@@ -7,11 +7,16 @@
 //
 // Both kernels are persistent, one CTA an SM:
 //   warp 0      TMA (128-byte swizzle) into a ring of stages of 64 reduction steps
-//   warp 1      tcgen05.mma.kind::f16, M = 128, N <= 256, into one of two accumulators
-//   warps 2-9   epilogue: TMEM, turned in shared memory, to whole pieces of rows
+//   warp 1      tcgen05.mma.kind::f16, M = 128 (rows: 64 where experts have few), N <= 256, into one of two accumulators
+//   the rest    epilogue (rows: 8 warps, gradients: 16): TMEM, turned in shared memory, to whole pieces of rows
 // What lies outside a matrix arrives as zeros (the tensor maps end at the widths). Where there are fewer units
 // than SMs, the reduction is cut into parts; each part leaves its fp32 tile in the context's workspace and the CTA that
 // comes last adds them in the order of the parts, so that the result does not depend on who that was.
+//
+// Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
+// of it writes), their gradient 351 us (5.9 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
+// with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
+// 197 us (1.16 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 285 us.
 
 #include <cudaTypedefs.h>
 
