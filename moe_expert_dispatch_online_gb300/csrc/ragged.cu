@@ -16,7 +16,7 @@
 // Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
 // of it writes), their gradient 351 us (5.9 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
 // with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
-// 197 us (1.16 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 285 us.
+// 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 230 us.
 
 #include <cudaTypedefs.h>
 
@@ -345,9 +345,13 @@ __device__ __forceinline__ int box_for(int rows) { return rows <= 16 ? 16 : rows
 
 // A unit: up to 128 rows of a segment x BN columns, or up to 64 where experts have few rows. A small tile leaves the
 // accumulator's other rows to whatever the stage holds behind its own; they are not stored.
+// kDual: a unit has two such tiles of 128 rows, in both accumulators, on each stage of W, which therefore comes half as
+// often. The epilogue frees the first accumulator before it reads the second, and the next unit's first tile runs over
+// the stages in the ring meanwhile; then its second tile on the same stages. (65,536 rows by 1096 x 1544: 285 us with
+// one tile a unit, 230 us with two; back 274 and 220 us.)
 // kAdd: what the product is added to arrives by TMA, up to four units ahead, in boxes of 64 columns that the epilogue
 // then turns its outputs in.
-template <bool kTrans, bool kAdd>
+template <bool kTrans, bool kAdd, bool kDual>
 __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                const __grid_constant__ RowMaps tmX,
                                                                const __grid_constant__ RowMaps tmAdd, const RgParams p) {
@@ -409,15 +413,17 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     set_status(p.status, BEP_DERR_BOUNDS);
                     continue;
                 }
-                const CUtensorMap* mx = map_for(tmX, u.rows);
-                const int box = box_for(u.rows);
+                const int rows1 = kDual ? min(u.rows, 128) : u.rows, rows2 = u.rows - rows1;
+                const CUtensorMap *mx = map_for(tmX, rows1), *mx2 = map_for(tmX, rows2);
+                const int box = box_for(rows1), box2 = kDual && rows2 > 0 ? box_for(rows2) : 0;
                 for (int kb = u.kb0; kb < u.kb1; ++kb) {
                     if (!mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
                         live = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&f.full[pr.at], box * 128 + p.b_bytes);
+                    mbar_arrive_expect_tx(&f.full[pr.at], (box + box2) * 128 + p.b_bytes);
                     tma_load_2d(mx, &f.full[pr.at], smA + pr.at * p.a_bytes, kb * 64, u.row0);
+                    if (kDual && box2) tma_load_2d(mx2, &f.full[pr.at], smA + pr.at * p.a_bytes + kRgA, kb * 64, u.row0 + 128);
                     uint8_t* b = smB + pr.at * p.b_bytes;
                     if (kTrans)
                         tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, u.n0, u.expert);
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         }
     } else if (warp == 1) {
         if (elect_one()) {
-            const uint32_t idesc = idesc_bf16(p.tile_rows, p.BN, false, !kTrans);
+            const uint32_t idesc = idesc_bf16(kDual ? 128 : p.tile_rows, p.BN, false, !kTrans);
             const uint32_t a0 = operand_lo<false>(smem_u32(smA)), b0 = operand_lo<!kTrans>(smem_u32(smB), p.chunk);
             const uint32_t a_step = p.a_bytes >> 4, b_step = p.b_bytes >> 4;
             uint32_t s = 0, ph = 0, a = a0, b = b0;
@@ -448,6 +454,64 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                 const Item u = item_of(i, next);
                 next = tile_at(i + gridDim.x);
                 if (u.expert < 0) continue;
+                constexpr uint32_t sa = piece_step<false>(), sb = piece_step<!kTrans>();
+                if (kDual) {
+                    auto tile = [&](uint32_t dt, uint32_t aa, uint32_t bb, bool add) {
+                        mma_bf16(dt, aa, bb, idesc, add);
+                        mma_bf16(dt, aa + sa, bb + sb, idesc, 1);
+                        mma_bf16(dt, aa + 2 * sa, bb + 2 * sb, idesc, 1);
+                        mma_bf16(dt, aa + 3 * sa, bb + 3 * sb, idesc, 1);
+                    };
+                    const uint32_t aph = (it & 1) ^ 1u;
+                    const bool two = u.rows > 128;
+                    ++it;
+                    const int pre = min(p.stages, p.kbn);
+                    if (!mbar_wait_held(&f.tempty[0], aph, f.s_abort, p.status)) break;
+                    tc_fence_after();
+                    uint32_t s1 = s, ph1 = ph, a1 = a, b1 = b;
+                    for (int kb = 0; kb < pre; ++kb) {   // the first tile over the stages of the ring
+                        if (!mbar_wait_held(&f.full[s1], ph1, f.s_abort, p.status)) {
+                            live = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        tile(f.tmem, a1, b1, kb != 0);
+                        a1 += a_step;
+                        b1 += b_step;
+                        if (++s1 == (uint32_t)p.stages) {
+                            s1 = 0;
+                            ph1 ^= 1u;
+                            a1 = a0;
+                            b1 = b0;
+                        }
+                    }
+                    if (!live || !mbar_wait_held(&f.tempty[1], aph, f.s_abort, p.status)) break;
+                    tc_fence_after();
+                    for (int kb = 0; kb < p.kbn; ++kb) {
+                        if (kb >= pre) {
+                            if (!mbar_wait_held(&f.full[s], ph, f.s_abort, p.status)) {
+                                live = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            tile(f.tmem, a, b, true);
+                        }
+                        if (two) tile(f.tmem + 256, a + (kRgA >> 4), b, kb != 0);
+                        mma_commit(&f.empty[s]);
+                        a += a_step;
+                        b += b_step;
+                        if (++s == (uint32_t)p.stages) {
+                            s = 0;
+                            ph ^= 1u;
+                            a = a0;
+                            b = b0;
+                        }
+                    }
+                    if (!live) break;
+                    mma_commit(&f.tfull[0]);
+                    mma_commit(&f.tfull[1]);
+                    continue;
+                }
                 const int acc = it & 1;
                 if (!mbar_wait_held(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status)) break;
                 ++it;
@@ -459,7 +523,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                         break;
                     }
                     tc_fence_after();
-                    constexpr uint32_t sa = piece_step<false>(), sb = piece_step<!kTrans>();
                     mma_bf16(dt, a, b, idesc, kb != u.kb0);
                     if (p.steps == 4) {
                         mma_bf16(dt, a + sa, b + sb, idesc, 1);
@@ -485,7 +548,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         // Two warps for each quarter of the accumulator's rows, each with half of the boxes of 64 columns. A box is
         // turned in shared memory, so that 8 lanes write 128 bytes of a row of y.
         // (a tile of 64 rows has 16 of them in each quarter's first lanes)
-        const int q = warp & 3, second = (warp - 2) >> 2, span = p.tile_rows / 4;
+        const int q = warp & 3, second = (warp - 2) >> 2, span = kDual ? 32 : p.tile_rows / 4;
         const int sub = lane >> 3, piece = lane & 7;
         const int nbox = (p.BN + 63) / 64, mine = (nbox + 1) / 2, box0 = second * mine, box1 = min(nbox, box0 + mine);
         int it = 0;
@@ -494,15 +557,21 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             const Item u = item_of(i, next);
             next = tile_at(i + gridDim.x);
             if (u.expert < 0) continue;
-            const int acc = it & 1;
-            const int rows = min(u.rows - span * q, span);   // this warp's
-            const int64_t row0 = (int64_t)u.row0 + span * q;
-            bool done = mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status);
+            bool live = true;
+#pragma unroll 1
+            for (int tile = 0; tile < (kDual ? 2 : 1); ++tile) {
+            const int acc = kDual ? tile : it & 1;
+            const int rows = min(u.rows - 128 * tile - span * q, span);   // this warp's
+            const int64_t row0 = (int64_t)u.row0 + 128 * tile + span * q;
+            bool done = mbar_wait_held(&f.tfull[acc], kDual ? it & 1 : (it >> 1) & 1, f.s_abort, p.status);
             if (kAdd && parts == 1) done = done && mbar_wait_held(&f.afull[as], aph, f.s_abort, p.status);
             done = __all_sync(0xffffffffu, done);
             // (warps that meet at barriers give up together)
-            if (parts > 1 ? !epi_all<8>(done) : !done) break;
-            ++it;
+            if (parts > 1 ? !epi_all<8>(done) : !done) {
+                live = false;
+                break;
+            }
+            if (!kDual || tile) ++it;
             tc_fence_after();
             const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256;
             bool held = true;
@@ -526,7 +595,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int bx = box0 + b;
-                if (bx >= box1 || !mine_to_store) break;
+                if (bx >= box1 || !mine_to_store || (kDual && rows <= 0)) break;
                 uint8_t* stg = kAdd ? smT + as * p.add_bytes + bx * kRgA + q * span * 128 : smT + (warp - 2) * kRgBox;
                 uint4* line = reinterpret_cast<uint4*>(stg + lane * 128);   // this lane's row of the box
                 const int c = 64 * bx + 8 * piece;
@@ -584,7 +653,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                                 *reinterpret_cast<const uint4*>(stg + (4 * j + sub) * 128 + ((piece ^ ((4 * j + sub) & 7)) << 4));
                 }
             }
-            if (held) release();   // a warp without columns
+            if (held) release();   // a warp without columns or rows
             if (kAdd && parts == 1) {
                 // the boxes were read and written here; the next unit's come by TMA
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -595,6 +664,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     aph ^= 1u;
                 }
             }
+            }
+            if (!live) break;
         }
     }
     close_frame(f, p.stages, kAdd ? p.adds : 0, pr, ad);
@@ -1010,8 +1081,9 @@ void cut(int width, int most, int* tile, int* tiles) {
 }  // namespace
 
 cudaError_t ragged_setup() {
-    const void* kernels[] = {(const void*)ragged_kernel<false, false>, (const void*)ragged_kernel<false, true>,
-                             (const void*)ragged_kernel<true, false>, (const void*)ragged_kernel<true, true>,
+    const void* kernels[] = {(const void*)ragged_kernel<false, false, false>, (const void*)ragged_kernel<false, true, false>,
+                             (const void*)ragged_kernel<true, false, false>, (const void*)ragged_kernel<true, true, false>,
+                             (const void*)ragged_kernel<false, false, true>, (const void*)ragged_kernel<true, false, true>,
                              (const void*)ragged_dw_kernel<1>, (const void*)ragged_dw_kernel<2>};
     for (const void* k : kernels) {
         const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
@@ -1056,6 +1128,13 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     const bool thin = add && p.kbn < 16 && !few;
     const int wide = thin ? 128 : 256;
     cut(N, most * ((N + wide - 1) / wide) < num_sms ? 64 : wide, &p.BN, &p.NT);
+    // Two row tiles a unit where experts have several and the reduction is worth it: one tile's MMAs do not hide the way of
+    // their operands into shared memory.
+    const bool dual = !add && !p.local && p.BN > 128 && p.kbn >= 8 && rows / d.E >= 512;
+    if (dual) {
+        p.tile_rows = 256;
+        p.a_bytes = 2 * kRgA;
+    }
     p.by_nt = make_fast_div((uint32_t)p.NT);
     p.by_nrow = make_fast_div((uint32_t)d.NROW);
     if (p.BN <= kRgPartCols) p.partial = ws.partial;
@@ -1082,14 +1161,19 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     const uint64_t wl[2] = {wd[0], wd[0] * wd[1]};
     if (!encode_rows(&tmW, w, 3, wd, wl, trans ? (uint32_t)p.BN : (uint32_t)p.steps * 16)) return cudaErrorInvalidValue;
     if (!p.local) {
-        const cudaError_t err = few ? launch_row_tiles<64>(d, ws, cu, st) : launch_row_tiles<128>(d, ws, cu, st);
+        const cudaError_t err = dual  ? launch_row_tiles<256>(d, ws, cu, st)
+                                : few ? launch_row_tiles<64>(d, ws, cu, st)
+                                      : launch_row_tiles<128>(d, ws, cu, st);
         if (err != cudaSuccess) return err;
     }
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = rg_config(num_sms, st, attr);
+    if (dual)
+        return cudaLaunchKernelEx(&cfg, trans ? ragged_kernel<true, false, true> : ragged_kernel<false, false, true>, tmW,
+                                  tmX, tmAdd, p);
     return cudaLaunchKernelEx(&cfg,
-                              trans ? (add ? ragged_kernel<true, true> : ragged_kernel<true, false>)
-                                    : (add ? ragged_kernel<false, true> : ragged_kernel<false, false>),
+                              trans ? (add ? ragged_kernel<true, true, false> : ragged_kernel<true, false, false>)
+                                    : (add ? ragged_kernel<false, true, false> : ragged_kernel<false, false, false>),
                               tmW, tmX, tmAdd, p);
 }
 

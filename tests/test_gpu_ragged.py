@@ -68,6 +68,9 @@ SHAPES = [
     (2, 700, 4, 2, 1096, 24, None, 0.6),
     (1, 129, 1, 1, 64, 2048, None, 0.0),
     (2, 900, 2, 1, 64, 8, None, 0.0),
+    (1, 1300, 2, 1, 520, 264, None, 0.3),
+    (2, 1500, 4, 2, 1096, 200, None, 1.5),
+    (3, 2000, 6, 2, 488, 776, 1, 2.0),
 ]
 
 
