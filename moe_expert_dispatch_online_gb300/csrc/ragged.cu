@@ -14,7 +14,7 @@
 // comes last adds them in the order of the parts, so that the result does not depend on who that was.
 //
 // Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
-// of it writes), their gradient 351 us (5.9 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
+// of it writes), their gradient 327 us (6.3 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
 // with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
 // 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 230 us.
 
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     const uint32_t a = operand_lo<true>(smem_u32(at)), bb = a + (a_bytes >> 4);
                     constexpr uint32_t st = piece_step<true>();
