@@ -28,7 +28,7 @@ struct bep_ctx {
     int num_sms;
     int mx_clusters;   // pairs of CTAs of the 4-bit product that fit the device, 0: it cannot run
     int i8_clusters;   // the same of the 8-bit product, -1 until its first call
-    bool ragged_ready;   // the products of any width have been set up by their first call
+    int ragged_pairs;  // the same of the gradients of any width, -1 until the first call of the products of any width
     int comm_sms;   // SM budget of the token-moving kernels (0: every SM)
 };
 
@@ -171,7 +171,7 @@ int bep_create(const bep_config* cfg, bep_ctx** out) {
     ctx->num_sms = sms;
     ctx->mx_clusters = mx_clusters;
     ctx->i8_clusters = -1;
-    ctx->ragged_ready = false;
+    ctx->ragged_pairs = -1;
     ctx->comm_sms = 0;
     *out = ctx;
     return BEP_OK;
@@ -532,12 +532,13 @@ static int check_ragged(const bep_ctx* ctx, int32_t K, int32_t N, int64_t ldx, i
 }
 
 static int ragged_ready(bep_ctx* ctx) {
-    if (ctx->ragged_ready) return BEP_OK;   // nothing here touches a stream: the first call may be a captured one
-    if (bep::ragged_setup() != cudaSuccess) {
+    if (ctx->ragged_pairs >= 0) return BEP_OK;   // nothing here touches a stream: the first call may be a captured one
+    int pairs = 0;
+    if (bep::ragged_setup(ctx->num_sms, &pairs) != cudaSuccess) {
         cudaGetLastError();
         return BEP_ERR_CUDA;
     }
-    ctx->ragged_ready = true;
+    ctx->ragged_pairs = pairs;
     return BEP_OK;
 }
 
@@ -578,7 +579,7 @@ int bep_ragged_gemm_dw(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* s
     rc = ragged_ready(ctx);
     if (rc) return rc;
     return cuda_rc(bep::launch_ragged_dw(ctx->d, ctx->ws, cu_seqlens, slot_expert, x, ldx, K, dy, lddy, N, alpha,
-                                         accumulate, g, ctx->num_sms, as_stream(stream)));
+                                         accumulate, g, ctx->num_sms, ctx->ragged_pairs, as_stream(stream)));
 }
 
 int bep_wait_selftest(bep_ctx* ctx, int32_t timeout_us, void* stream) {

@@ -14,7 +14,7 @@
 // comes last adds them in the order of the parts, so that the result does not depend on who that was.
 //
 // Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
-// of it writes), their gradient 327 us (6.3 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
+// of it writes), their gradient 323 us (6.4 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
 // with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
 // 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 230 us.
 
@@ -30,7 +30,7 @@ constexpr int kRgDwThreads = 32 * 18;    // of the matrices': 16, which hold a u
 constexpr int kRgA = 128 * 128;          // bytes: 128 rows (columns) x 64 reduction steps
 constexpr int kRgChunk = 64 * 128;       // bytes: 64 x 64 elements
 constexpr int kRgBox = 32 * 128;         // bytes: an epilogue warp's box of 32 rows of 128 bytes
-constexpr int kRgDwBox = 32 * 64;        // bytes: the same of 16 fp32 columns
+constexpr int kRgDwBox = 16 * 128;       // bytes: the same of 16 rows of 32 fp32, written by TMA
 constexpr int kRgTmem = 512;
 constexpr int kRgMaxStages = 12;
 constexpr int kRgMaxAdds = 4;
@@ -68,9 +68,7 @@ struct RgParams {
 struct RgDwParams {
     const MTile* blocks;      // up to 64 rows of one segment, by expert
     const int32_t* first;     // [E + 1]
-    float* g;
-    int64_t g_expert;         // elements of an expert's gradient
-    int64_t ldm, ldn;         // strides of g along the M side and the N side: one of them is 1
+    int m_inner;              // the M side lies along g's rows, else the N side
     float alpha;
     int E, Md, Nd;            // widths of the sides
     int BN, MT, NT, parts;    // columns of a tile, units along M and N
@@ -87,6 +85,34 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// A box of g written, or added (one fp32 rounding an element).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+// The same box for both CTAs of a pair, at the same place in each, counted on the barrier of each.
+__device__ __forceinline__ void tma_load_2d_both(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "h"((uint16_t)3)
+        : "memory");
+}
+// This CTA's MMAs up to here, on the barrier of each CTA of the pair.
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
         : "memory");
 }
 
@@ -149,7 +175,7 @@ struct Frame {
     int* s_rows;   // valid rows of each stage
     uint32_t tmem;
 };
-__device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int epi_warps) {
+__device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int epi_warps, int readers = 1) {
     Frame f;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -168,7 +194,7 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&f.full[s], 1);
-            mbar_init(&f.empty[s], 1);
+            mbar_init(&f.empty[s], readers);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&f.tfull[a], 1);
@@ -215,6 +241,7 @@ struct Started {
         }
     }
 };
+template <bool kPair = false>
 __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds, Started ring, Started add) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
@@ -227,8 +254,11 @@ __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds
             mma_commit(f.drain);
             mbar_drain(f.drain, 0);
         }
+        if (kPair && threadIdx.x == 0)   // what it started for the other CTA
+            for (int i = 0; i < 20; ++i) __nanosleep(10000);
         __syncthreads();
     }
+    if (kPair) cluster_sync();   // neither CTA leaves while the other may still write to it or signal it
     if (warp == 0) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
@@ -801,13 +831,19 @@ __device__ __forceinline__ void zero_rows(uint8_t* chunk, int chunks, int tail, 
 
 // A unit: MI x 128 x BN of an expert's gradient, MI = 2 where BN leaves both room in an accumulator. Both
 // operands lie along the rows (MN-major).
-template <int MI>
+// kPair: two CTAs of a cluster take neighbouring tiles along M and the same blocks in step; each loads its own M side
+// and 32 of a block's 64 rows of the N side for both. A stage is free when both have read it.
+template <int MI, bool kPair>
 __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
                                                                   const __grid_constant__ CUtensorMap tmN,
+                                                                  const __grid_constant__ CUtensorMap tmG,
                                                                   const RgDwParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages, 16);
+    Frame f = open_frame(smem_raw, p.stages, 16, kPair ? 2 : 1);
+    if (kPair) cluster_sync();   // both CTAs' barriers exist
+    const int rank = kPair ? (int)cluster_rank() : 0;
+    const int first = kPair ? (int)cluster_id() : (int)blockIdx.x, stride = kPair ? (int)cluster_count() : (int)gridDim.x;
     constexpr int a_bytes = MI * kRgA;
     const int stage = a_bytes + p.b_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -831,14 +867,14 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
         const int part = i - it.unit * parts;
         it.expert = fast_div(it.unit, p.by_unit);
         const int rest = it.unit - it.expert * p.MT * p.NT, m = fast_div(rest, p.by_nt);
-        it.m0 = m * MI * 128;
+        it.m0 = (kPair ? 2 * m + rank : m) * MI * 128;
         it.n0 = (rest - m * p.NT) * p.BN;
         const int64_t nb = range.y - range.x;
         it.b0 = parts == 1 ? range.x : range.x + (int)(part * nb / parts);
         it.b1 = parts == 1 ? range.y : range.x + (int)((part + 1) * nb / parts);
         return it;
     };
-    int2 next = range_at(blockIdx.x);
+    int2 next = range_at(first);
 
     if (warp == 0) {
         // 32 blocks at a time, a lane each; a unit's first 32 are read while the unit before runs
@@ -849,17 +885,17 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
             return blocks_at(u.b0, u.b1);
         };
         bool live = true;
-        MTile run = first_of(blockIdx.x);
-        for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+        MTile run = first_of(first);
+        for (int i = first; i < total && live; i += stride) {
             const Item u = item_of(i, next);
-            next = range_at(i + gridDim.x);
+            next = range_at(i + stride);
             MTile cur = run;
-            run = first_of(i + gridDim.x);
+            run = first_of(i + stride);
             for (int b = u.b0; b < u.b1; ++b) {
                 const int k = (b - u.b0) & 31;
                 if (k == 0 && b != u.b0) cur = blocks_at(b, u.b1);
                 const int row0 = __shfl_sync(0xffffffffu, cur.row0, k), rows = __shfl_sync(0xffffffffu, cur.rows, k);
-                if (!__all_sync(0xffffffffu, mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status))) {
+                if (!__all_sync(0xffffffffu, mbar_wait_held<kPair>(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status))) {
                     live = false;
                     break;
                 }
@@ -869,21 +905,30 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                     uint8_t* at = f.ring + pr.at * stage;
                     for (int c = 0; c < 2 * MI; ++c)
                         tma_load_2d(&tmM, &f.full[pr.at], at + c * kRgChunk, u.m0 + 64 * c, row0);
-                    for (int c = 0; c * kRgChunk < p.b_bytes; ++c)
-                        tma_load_2d(&tmN, &f.full[pr.at], at + a_bytes + c * kRgChunk, u.n0 + 64 * c, row0);
+                    for (int c = 0; c * kRgChunk < p.b_bytes; ++c) {
+                        uint8_t* b = at + a_bytes + c * kRgChunk;
+                        if (kPair)
+                            tma_load_2d_both(&tmN, &f.full[pr.at], b + rank * (kRgChunk / 2), u.n0 + 64 * c, row0 + 32 * rank);
+                        else
+                            tma_load_2d(&tmN, &f.full[pr.at], b, u.n0 + 64 * c, row0);
+                    }
                 }
                 __syncwarp();
                 pr.step(p.stages);
             }
+        }
+        if (kPair && live && lane == 0) {   // the other CTA has read what came from here, and said so
+            Started e = pr;
+            e.drain(f.empty, p.stages);
         }
     } else if (warp == 1) {
         const uint32_t idesc = idesc_bf16(128, p.BN, true, true);
         uint32_t s = 0, ph = 0;
         int it = 0;
         bool live = true;
-        for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+        for (int i = first; i < total && live; i += stride) {
             const Item u = item_of(i, next);
-            next = range_at(i + gridDim.x);
+            next = range_at(i + stride);
             for (int b = u.b0; b < u.b1 && live; ++b) {
                 const int k = (b - u.b0) % kRgChain;
                 const int acc = it & 1;
@@ -911,7 +956,8 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                         for (int kk = 0; kk < 4; ++kk)
                             if (16 * kk < rows)
                                 mma_bf16(dt + m * 128, a + m * (kRgA >> 4) + kk * st, bb + kk * st, idesc, k || kk);
-                    mma_commit(&f.empty[s]);
+                    if (kPair) mma_commit_both(&f.empty[s]);
+                    else mma_commit(&f.empty[s]);
                     if (k == kRgChain - 1 || b == u.b1 - 1) mma_commit(&f.tfull[acc]);
                 }
                 __syncwarp();
@@ -925,15 +971,14 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
     } else {
         const int q = warp & 3, group = (warp - 2) >> 2;   // four groups of four warps, one a quarter of the rows
         uint8_t* stg = f.ring + p.stages * stage + (warp - 2) * kRgDwBox;
-        const int sub = lane >> 2, piece = lane & 3;   // on the way out: 4 lanes take 16 columns of a row
         // A warp's two boxes of 32 columns: every fourth one of the tile, or every second one of one of two tiles.
         constexpr int step = MI == 2 ? 64 : 128;
         const int start = MI == 2 ? 32 * (group & 1) : 32 * group, tile = MI == 2 ? group >> 1 : 0;
         int it = 0;
         bool live = true;
-        for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+        for (int i = first; i < total && live; i += stride) {
             const Item u = item_of(i, next);
-            next = range_at(i + gridDim.x);
+            next = range_at(i + stride);
             if (u.b0 == u.b1 && parts == 1 && p.accumulate) continue;
             float sum[2][32];   // this thread's row
 #pragma unroll
@@ -981,68 +1026,46 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                 }
             }
             if (!live) break;
+            // Boxes of 16 rows of g, 32 values of each, leave by TMA, which ends them at g's edges: the M side's 32 of
+            // 16 columns, or 16 of the M side by 32 columns. (128-byte swizzle: 16-byte pieces, turned by the row.)
             const int m0 = u.m0 + tile * 128 + 32 * q;   // this warp's 32 along M
-            float* g = p.g + (int64_t)u.expert * p.g_expert;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int c0 = start + b * step;
-                if (c0 >= p.BN || m0 >= p.Md) break;
-                const int n0 = u.n0 + c0;
-                if (p.ldm == 1) {   // the lanes' 32 lie together
-                    if (m0 + lane < p.Md) {
-                        float* out = g + (int64_t)n0 * p.ldn + m0 + lane;
-                        const int cols = min(p.BN - c0, p.Nd - n0);   // a multiple of 8
+                const int c0 = start + b * step, n0 = u.n0 + c0;
+                if (c0 >= p.BN || n0 >= p.Nd || m0 >= p.Md) break;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            if (j < cols) {
+                for (int h = 0; h < 2; ++h) {
+                    const int m = p.m_inner ? m0 : m0 + 16 * h, n = p.m_inner ? n0 + 16 * h : n0;
+                    if (m >= p.Md || n >= p.Nd || (p.m_inner && c0 + 16 * h >= p.BN)) break;
+                    if (lane == 0) bulk_wait_read_all();   // the box before has been read
+                    __syncwarp();
+                    if (p.m_inner) {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    float v = p.alpha * sum[b][j + k];
-                                    if (p.accumulate) v += *out;
-                                    *out = v;
-                                    out += p.ldn;
-                                }
-                            }
+                        for (int j = 0; j < 16; ++j)
+                            *reinterpret_cast<float*>(stg + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) + (lane & 3) * 4) =
+                                p.alpha * sum[b][16 * h + j];
+                    } else if ((lane >> 4) == h) {
+                        uint8_t* line = stg + (lane & 15) * 128;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4*>(line + ((j ^ (lane & 7)) << 4)) =
+                                make_float4(p.alpha * sum[b][4 * j], p.alpha * sum[b][4 * j + 1],
+                                            p.alpha * sum[b][4 * j + 2], p.alpha * sum[b][4 * j + 3]);
                     }
-                } else {
-                    float4* line = reinterpret_cast<float4*>(stg + lane * 64);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        __syncwarp();   // the box before has been read
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            line[j ^ ((lane >> 1) & 3)] = make_float4(sum[b][16 * h + 4 * j], sum[b][16 * h + 4 * j + 1],
-                                                                      sum[b][16 * h + 4 * j + 2], sum[b][16 * h + 4 * j + 3]);
-                        __syncwarp();
-                        const int c = c0 + 16 * h + 4 * piece;
-                        if (c >= p.BN || u.n0 + c >= p.Nd) continue;
-                        float4* out = reinterpret_cast<float4*>(g + (int64_t)(m0 + sub) * p.ldm + u.n0 + c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int rr = 8 * j + sub;
-                            if (m0 + rr < p.Md) {
-                                float4 v = *reinterpret_cast<const float4*>(stg + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4));
-                                v.x *= p.alpha;
-                                v.y *= p.alpha;
-                                v.z *= p.alpha;
-                                v.w *= p.alpha;
-                                if (p.accumulate) {
-                                    const float4 o = *out;
-                                    v.x += o.x;
-                                    v.y += o.y;
-                                    v.z += o.z;
-                                    v.w += o.w;
-                                }
-                                *out = v;
-                            }
-                            out += 2 * p.ldm;   // 8 rows, in vectors of 4
-                        }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int x = p.m_inner ? m : n, y = p.m_inner ? n : m;
+                        if (p.accumulate) tma_reduce_add_3d(&tmG, stg, x, y, u.expert);
+                        else tma_store_3d(&tmG, stg, x, y, u.expert);
+                        bulk_commit();
                     }
                 }
             }
         }
+        if (lane == 0) bulk_wait_all();
     }
-    close_frame(f, p.stages, 0, pr, Started());
+    close_frame<kPair>(f, p.stages, 0, pr, Started());
 }
 
 // bf16 tensor of `dims` (innermost first) with row strides in elements, boxes of 64 x box_rows, 128-byte swizzle.
@@ -1059,6 +1082,19 @@ bool encode_rows(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// g fp32 [E, K, N], boxes of 16 rows of 32, 128-byte swizzle.
+bool encode_g(CUtensorMap* m, float* g, int E, int K, int N) {
+    void* fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)K, (cuuint64_t)E};
+    const cuuint64_t strides[2] = {(cuuint64_t)N * 4, (cuuint64_t)N * K * 4};
+    const cuuint32_t box[3] = {32, 16, 1}, estr[3] = {1, 1, 1};
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
+               m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, g, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 cudaLaunchConfig_t rg_config(int grid, cudaStream_t st, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
@@ -1072,24 +1108,40 @@ cudaLaunchConfig_t rg_config(int grid, cudaStream_t st, cudaLaunchAttribute* att
     return cfg;
 }
 
-// `width` in tiles of at most `most` columns, all of one size (a multiple of 16).
-void cut(int width, int most, int* tile, int* tiles) {
+// Pairs of CTAs.
+cudaLaunchConfig_t rg_pair_config(int pairs, cudaStream_t st, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = rg_config(2 * pairs, st, attr);
+    cfg.blockDim = dim3(kRgDwThreads, 1, 1);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// `width` in tiles of at most `most` columns, all of one size (a multiple of 16, or of `unit` where there are several).
+void cut(int width, int most, int* tile, int* tiles, int unit = 16) {
     *tiles = (width + most - 1) / most;
-    *tile = ((width + *tiles - 1) / *tiles + 15) / 16 * 16;
+    if (*tiles == 1) unit = 16;
+    *tile = ((width + *tiles - 1) / *tiles + unit - 1) / unit * unit;
 }
 
 }  // namespace
 
-cudaError_t ragged_setup() {
+cudaError_t ragged_setup(int num_sms, int* pairs) {
     const void* kernels[] = {(const void*)ragged_kernel<false, false, false>, (const void*)ragged_kernel<false, true, false>,
                              (const void*)ragged_kernel<true, false, false>, (const void*)ragged_kernel<true, true, false>,
                              (const void*)ragged_kernel<false, false, true>, (const void*)ragged_kernel<true, false, true>,
-                             (const void*)ragged_dw_kernel<1>, (const void*)ragged_dw_kernel<2>};
+                             (const void*)ragged_dw_kernel<1, false>, (const void*)ragged_dw_kernel<2, false>,
+                             (const void*)ragged_dw_kernel<1, true>};
     for (const void* k : kernels) {
         const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
         if (err != cudaSuccess) return err;
     }
-    return cudaSuccess;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = rg_pair_config(num_sms / 2, nullptr, attr);
+    return cudaOccupancyMaxActiveClusters(pairs, ragged_dw_kernel<1, true>, &cfg);
 }
 
 cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
@@ -1179,24 +1231,21 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
 
 cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                              const uint16_t* x, int64_t ldx, int K, const uint16_t* dy, int64_t lddy, int N, float alpha,
-                             int accumulate, float* g, int num_sms, cudaStream_t st) {
+                             int accumulate, float* g, int num_sms, int pairs, cudaStream_t st) {
     const int64_t rows = (int64_t)d.R * d.C;
     RgDwParams p = {};
     p.blocks = ws.tiles;
     p.first = ws.blk_first;
-    p.g = g;
-    p.g_expert = (int64_t)K * N;
     p.alpha = alpha;
     p.E = d.E;
     // The M side is padded to 128 and the other to 16, so it is the wider one; x where that costs little, since then
-    // four columns of g leave at a time.
+    // a row of g leaves in 16-byte pieces.
     const int64_t pad_x = (int64_t)((K + 127) / 128 * 128) * ((N + 15) / 16 * 16);
     const int64_t pad_y = (int64_t)((N + 127) / 128 * 128) * ((K + 15) / 16 * 16);
     const bool x_wide = pad_x <= pad_y + pad_y / 4;
     p.Md = x_wide ? K : N;
     p.Nd = x_wide ? N : K;
-    p.ldm = x_wide ? N : 1;
-    p.ldn = x_wide ? 1 : N;
+    p.m_inner = !x_wide;
     p.accumulate = accumulate;
     p.tickets = ws.tickets;
     p.partial = ws.partial;
@@ -1205,7 +1254,7 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     const int MI = p.Nd <= 128 && (int64_t)d.E * ((p.Md + 255) / 256) >= 2 * num_sms ? 2 : 1;
     p.MT = (p.Md + 128 * MI - 1) / (128 * MI);
     const int64_t units = (int64_t)d.E * p.MT * ((p.Nd + 255) / 256);
-    cut(p.Nd, units < num_sms ? 64 : 256, &p.BN, &p.NT);
+    cut(p.Nd, units < num_sms ? 64 : 256, &p.BN, &p.NT, 32);   // (a box of 32 columns is one tile's)
     p.parts = 1;
     const int64_t n = (int64_t)d.E * p.MT * p.NT;
     if (p.BN <= kRgPartCols && n < num_sms) {
@@ -1213,6 +1262,14 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
         const int64_t fit = num_sms / n, len = rows / 64 / d.E / 2;
         while (p.parts < kRgMaxParts && p.parts < fit && (int64_t)(p.parts + 1) * (p.parts + 1) <= len) ++p.parts;
     }
+    // Neighbouring tiles along M on pairs of CTAs, which share the other operand, where experts are long or have
+    // many tiles, and there are pairs of tiles enough for two rounds. An odd tile's partner has nothing to load or store. (64 experts of 4,096
+    // rows: 1016 x 1544 1000 -> 780 us, 600 x 1000, five tiles, 450 -> 385 us, 360 x 1000, three, 307 -> 267 us;
+    // 1024 x 1024, whose rows start on 128-byte lines, 535 -> 525 us. Of 128
+    // rows: 1096 x 1544 125 -> 119 us, 360 x 1000 38.5 -> 40.6.)
+    const bool pair = MI == 1 && p.BN > 128 && p.MT > 1 && (rows / d.E >= 512 || p.MT > 4) && pairs > 0 &&
+                      (int64_t)d.E * ((p.MT + 1) / 2) * p.NT >= 2 * pairs;
+    if (pair) p.MT = (p.MT + 1) / 2;
     p.by_parts = make_fast_div((uint32_t)p.parts);
     p.by_unit = make_fast_div((uint32_t)(p.MT * p.NT));
     p.by_nt = make_fast_div((uint32_t)p.NT);
@@ -1220,19 +1277,27 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     const int fit = (kRgBytes - 16 * kRgDwBox) / (MI * kRgA + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;
 
-    CUtensorMap tx, ty;
+    CUtensorMap tx, ty, tg;
+    if (!encode_g(&tg, g, d.E, K, N)) return cudaErrorInvalidValue;
     const uint64_t xd[2] = {(uint64_t)K, (uint64_t)rows}, xs[1] = {(uint64_t)ldx};
     const uint64_t yd[2] = {(uint64_t)N, (uint64_t)rows}, ys[1] = {(uint64_t)lddy};
-    if (!encode_rows(&tx, x, 2, xd, xs, 64) || !encode_rows(&ty, dy, 2, yd, ys, 64)) return cudaErrorInvalidValue;
-    cudaLaunchAttribute attr[1];
+    const uint32_t n_box = pair ? 32 : 64;   // rows of a box of the N side
+    if (!encode_rows(&tx, x, 2, xd, xs, x_wide ? 64 : n_box) || !encode_rows(&ty, dy, 2, yd, ys, x_wide ? n_box : 64))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = rg_config(1, st, attr);
     cfg.blockDim = dim3(1024, 1, 1);
     cfg.dynamicSmemBytes = 0;
     cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_blocks_kernel, cu, slot_expert, d, ws);
     if (err != cudaSuccess) return err;
+    if (pair) {
+        cfg = rg_pair_config(pairs, st, attr);
+        return cudaLaunchKernelEx(&cfg, ragged_dw_kernel<1, true>, x_wide ? tx : ty, x_wide ? ty : tx, tg, p);
+    }
     cfg = rg_config(num_sms, st, attr);
     cfg.blockDim = dim3(kRgDwThreads, 1, 1);
-    return cudaLaunchKernelEx(&cfg, MI == 2 ? ragged_dw_kernel<2> : ragged_dw_kernel<1>, x_wide ? tx : ty, x_wide ? ty : tx, p);
+    return cudaLaunchKernelEx(&cfg, MI == 2 ? ragged_dw_kernel<2, false> : ragged_dw_kernel<1, false>, x_wide ? tx : ty, x_wide ? ty : tx,
+                              tg, p);
 }
 
 }  // namespace bep

@@ -113,6 +113,30 @@ def test_gradient(lib, R, S, E, top, K, N, B, skew, accumulate):
     ctx.close()
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("R,S,E,top,K,N,skew", [
+    (2, 2100, 8, 1, 1024, 1040, 0.5),    # an even number of tiles on either side
+    (3, 1600, 9, 1, 840, 1096, 2.5),     # an odd one, experts of very different lengths
+    (2, 2650, 20, 2, 360, 1000, 0.7),    # three tiles
+    (2, 2650, 20, 2, 136, 2048, 0.0),    # dy on the side that is cut into pairs of tiles
+])
+def test_gradient_of_long_experts(lib, R, S, E, top, K, N, skew, accumulate):
+    """Lengths and widths at which two blocks share an operand. The rows behind each segment are another's."""
+    bep = lib
+    ctx, t = planned(bep, R, S, E, top, 64, 64, seed=4, skew=skew)
+    expert = row_experts(ctx.cfg, t)
+    rows = R * S * top
+    x, _ = wide(ints((rows, K), 1), 8, 16)
+    dy, _ = wide(ints((rows, N), 2), 24, 8)
+    want = want_g(x, dy, expert, E, 0.5) + (3.0 if accumulate else 0.0)
+    for _ in range(2):
+        g = torch.full((E, K, N), 3.0, device=DEV)
+        bep.bep_ragged_gemm_dw(ctx, t["cu"], t["se"], x, dy, g, alpha=0.5, accumulate=accumulate)
+        assert bep.bep_status(ctx) == 0
+        assert np.array_equal(g.cpu().numpy(), want)
+    ctx.close()
+
+
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 33, 48, 63, 64, 65, 100, 127, 128, 129, 191, 200, 257, 300])
 @pytest.mark.parametrize("K,N", [(104, 72), (72, 104)])
 def test_every_segment_height(lib, rows, K, N):
