@@ -28,7 +28,7 @@ struct bep_ctx {
     int num_sms;
     int mx_clusters;   // pairs of CTAs of the 4-bit product that fit the device, 0: it cannot run
     int i8_clusters;   // the same of the 8-bit product, -1 until its first call
-    int ragged_pairs;  // the same of the gradients of any width, -1 until the first call of the products of any width
+    int ragged_pairs;  // the same of the products of any width
     int comm_sms;   // SM budget of the token-moving kernels (0: every SM)
 };
 
@@ -559,7 +559,7 @@ int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot
     rc = ragged_ready(ctx);
     if (rc) return rc;
     return cuda_rc(bep::launch_ragged(ctx->d, ctx->ws, cu_seqlens, slot_expert, x, ldx, K, w, N, trans, alpha, add, ldadd,
-                                      y, ldy, ctx->num_sms, as_stream(stream)));
+                                      y, ldy, ctx->num_sms, ctx->ragged_pairs, as_stream(stream)));
 }
 
 int bep_ragged_gemm_dw(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x,

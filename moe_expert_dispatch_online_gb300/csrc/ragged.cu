@@ -16,7 +16,7 @@
 // Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
 // of it writes), their gradient 323 us (6.4 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
 // with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
-// 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 230 us.
+// 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 213 us.
 
 #include <cudaTypedefs.h>
 
@@ -378,16 +378,21 @@ __device__ __forceinline__ int box_for(int rows) { return rows <= 16 ? 16 : rows
 // kDual: a unit has two such tiles of 128 rows, in both accumulators, on each stage of W, which therefore comes half as
 // often. The epilogue frees the first accumulator before it reads the second, and the next unit's first tile runs over
 // the stages in the ring meanwhile; then its second tile on the same stages. (65,536 rows by 1096 x 1544: 285 us with
-// one tile a unit, 230 us with two; back 274 and 220 us.)
+// one tile a unit, 230 us with two, 213 us on pairs; back 274, 220 and 198 us.)
 // kAdd: what the product is added to arrives by TMA, up to four units ahead, in boxes of 64 columns that the epilogue
 // then turns its outputs in.
-template <bool kTrans, bool kAdd, bool kDual>
+// kPair: two CTAs of a cluster take neighbouring columns of the same rows in step; each loads its own tile of W and one
+// of the two row tiles for both. A stage is free when both have read it.
+template <bool kTrans, bool kAdd, bool kDual, bool kPair>
 __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                const __grid_constant__ RowMaps tmX,
                                                                const __grid_constant__ RowMaps tmAdd, const RgParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages, 8);
+    Frame f = open_frame(smem_raw, p.stages, 8, kPair ? 2 : 1);
+    if (kPair) cluster_sync();   // both CTAs' barriers exist
+    const int rank = kPair ? (int)cluster_rank() : 0;
+    const int first = kPair ? (int)cluster_id() : (int)blockIdx.x, stride = kPair ? (int)cluster_count() : (int)gridDim.x;
     uint8_t* smA = f.ring;
     uint8_t* smB = smA + p.stages * p.a_bytes;
     uint8_t* smT = smB + p.stages * p.b_bytes;   // kAdd: the units' boxes, else a box of each epilogue warp
@@ -421,7 +426,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         it.rows = t.rows;
         it.expert = t.wsel >= 0 ? t.wsel : p.slot_expert[-1 - t.wsel];
         if (it.expert >= p.E) it.expert = -1;
-        it.n0 = (it.unit - (int)fast_div(it.unit, p.by_nt) * p.NT) * p.BN;
+        it.n0 = it.unit - (int)fast_div(it.unit, p.by_nt) * p.NT;
+        it.n0 = (kPair ? 2 * it.n0 + rank : it.n0) * p.BN;
         it.kb0 = 0;
         it.kb1 = p.kbn;
         if (parts > 1) {
@@ -431,14 +437,14 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         }
         return it;
     };
-    MTile next = tile_at(blockIdx.x);
+    MTile next = tile_at(first);
 
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
-            for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+            for (int i = first; i < total && live; i += stride) {
                 const Item u = item_of(i, next);
-                next = tile_at(i + gridDim.x);
+                next = tile_at(i + stride);
                 if (u.expert < 0) {
                     set_status(p.status, BEP_DERR_BOUNDS);
                     continue;
@@ -447,13 +453,19 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                 const CUtensorMap *mx = map_for(tmX, rows1), *mx2 = map_for(tmX, rows2);
                 const int box = box_for(rows1), box2 = kDual && rows2 > 0 ? box_for(rows2) : 0;
                 for (int kb = u.kb0; kb < u.kb1; ++kb) {
-                    if (!mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
+                    if (!mbar_wait_held<kPair>(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
                         live = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&f.full[pr.at], (box + box2) * 128 + p.b_bytes);
-                    tma_load_2d(mx, &f.full[pr.at], smA + pr.at * p.a_bytes, kb * 64, u.row0);
-                    if (kDual && box2) tma_load_2d(mx2, &f.full[pr.at], smA + pr.at * p.a_bytes + kRgA, kb * 64, u.row0 + 128);
+                    uint8_t* a = smA + pr.at * p.a_bytes;
+                    if (kPair) {
+                        if (rank == 0) tma_load_2d_both(mx, &f.full[pr.at], a, kb * 64, u.row0);
+                        else if (box2) tma_load_2d_both(mx2, &f.full[pr.at], a + kRgA, kb * 64, u.row0 + 128);
+                    } else {
+                        tma_load_2d(mx, &f.full[pr.at], a, kb * 64, u.row0);
+                        if (kDual && box2) tma_load_2d(mx2, &f.full[pr.at], a + kRgA, kb * 64, u.row0 + 128);
+                    }
                     uint8_t* b = smB + pr.at * p.b_bytes;
                     if (kTrans)
                         tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, u.n0, u.expert);
@@ -471,6 +483,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     ad.step(p.adds);
                 }
             }
+            if (kPair && live) {   // the other CTA has read what came from here, and said so
+                Started e = pr;
+                e.drain(f.empty, p.stages);
+            }
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -480,9 +496,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             uint32_t s = 0, ph = 0, a = a0, b = b0;
             int it = 0;
             bool live = true;
-            for (int i = blockIdx.x; i < total && live; i += gridDim.x) {
+            for (int i = first; i < total && live; i += stride) {
                 const Item u = item_of(i, next);
-                next = tile_at(i + gridDim.x);
+                next = tile_at(i + stride);
                 if (u.expert < 0) continue;
                 constexpr uint32_t sa = piece_step<false>(), sb = piece_step<!kTrans>();
                 if (kDual) {
@@ -527,7 +543,8 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                             tile(f.tmem, a, b, true);
                         }
                         if (two) tile(f.tmem + 256, a + (kRgA >> 4), b, kb != 0);
-                        mma_commit(&f.empty[s]);
+                        if (kPair) mma_commit_both(&f.empty[s]);
+                        else mma_commit(&f.empty[s]);
                         a += a_step;
                         b += b_step;
                         if (++s == (uint32_t)p.stages) {
@@ -583,9 +600,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         const int nbox = (p.BN + 63) / 64, mine = (nbox + 1) / 2, box0 = second * mine, box1 = min(nbox, box0 + mine);
         int it = 0;
         uint32_t as = 0, aph = 0;
-        for (int i = blockIdx.x; i < total; i += gridDim.x) {
+        for (int i = first; i < total; i += stride) {
             const Item u = item_of(i, next);
-            next = tile_at(i + gridDim.x);
+            next = tile_at(i + stride);
             if (u.expert < 0) continue;
             bool live = true;
 #pragma unroll 1
@@ -698,7 +715,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             if (!live) break;
         }
     }
-    close_frame(f, p.stages, kAdd ? p.adds : 0, pr, ad);
+    close_frame<kPair>(f, p.stages, kAdd ? p.adds : 0, pr, ad);
 }
 
 // ------------------------------------------------------------------------ matrices
@@ -1111,7 +1128,6 @@ cudaLaunchConfig_t rg_config(int grid, cudaStream_t st, cudaLaunchAttribute* att
 // Pairs of CTAs.
 cudaLaunchConfig_t rg_pair_config(int pairs, cudaStream_t st, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = rg_config(2 * pairs, st, attr);
-    cfg.blockDim = dim3(kRgDwThreads, 1, 1);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
@@ -1130,9 +1146,14 @@ void cut(int width, int most, int* tile, int* tiles, int unit = 16) {
 }  // namespace
 
 cudaError_t ragged_setup(int num_sms, int* pairs) {
-    const void* kernels[] = {(const void*)ragged_kernel<false, false, false>, (const void*)ragged_kernel<false, true, false>,
-                             (const void*)ragged_kernel<true, false, false>, (const void*)ragged_kernel<true, true, false>,
-                             (const void*)ragged_kernel<false, false, true>, (const void*)ragged_kernel<true, false, true>,
+    const void* kernels[] = {(const void*)ragged_kernel<false, false, false, false>,
+                             (const void*)ragged_kernel<false, true, false, false>,
+                             (const void*)ragged_kernel<true, false, false, false>,
+                             (const void*)ragged_kernel<true, true, false, false>,
+                             (const void*)ragged_kernel<false, false, true, false>,
+                             (const void*)ragged_kernel<true, false, true, false>,
+                             (const void*)ragged_kernel<false, false, true, true>,
+                             (const void*)ragged_kernel<true, false, true, true>,
                              (const void*)ragged_dw_kernel<1, false>, (const void*)ragged_dw_kernel<2, false>,
                              (const void*)ragged_dw_kernel<1, true>};
     for (const void* k : kernels) {
@@ -1141,12 +1162,14 @@ cudaError_t ragged_setup(int num_sms, int* pairs) {
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = rg_pair_config(num_sms / 2, nullptr, attr);
+    cfg.blockDim = dim3(kRgDwThreads, 1, 1);   // (an SM holds one CTA of either kernel)
     return cudaOccupancyMaxActiveClusters(pairs, ragged_dw_kernel<1, true>, &cfg);
 }
 
 cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                           const uint16_t* x, int64_t ldx, int K, const uint16_t* w, int N, int trans, float alpha,
-                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, cudaStream_t st) {
+                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, int pairs,
+                          cudaStream_t st) {
     const int64_t rows = (int64_t)d.R * d.C;
     RgParams p = {};
     p.tiles = ws.tiles;
@@ -1187,6 +1210,14 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
         p.tile_rows = 256;
         p.a_bytes = 2 * kRgA;
     }
+    // An even number of tiles of columns on pairs of CTAs. One tile more costs less than it saves where rows of x start
+    // inside 128-byte lines and take two requests each (1096 x 1544, 7 tiles: 230 -> 213 us, back, 5 tiles: 220 -> 198 us;
+    // 262,144 rows by 600 x 1000, 4 tiles: 315 -> 275 us), and more where they do not (1088 x 1600: 182 -> 195 us).
+    const bool pair = dual && p.NT > 1 && pairs > 0 && (p.NT % 2 == 0 || ldx % 64 != 0);
+    if (pair) {
+        p.NT = (p.NT + 1) / 2;
+        p.BN = ((N + 2 * p.NT - 1) / (2 * p.NT) + 15) / 16 * 16;
+    }
     p.by_nt = make_fast_div((uint32_t)p.NT);
     p.by_nrow = make_fast_div((uint32_t)d.NROW);
     if (p.BN <= kRgPartCols) p.partial = ws.partial;
@@ -1218,15 +1249,19 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
                                       : launch_row_tiles<128>(d, ws, cu, st);
         if (err != cudaSuccess) return err;
     }
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = rg_config(num_sms, st, attr);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pair ? rg_pair_config(pairs, st, attr) : rg_config(num_sms, st, attr);
+    if (pair)
+        return cudaLaunchKernelEx(
+            &cfg, trans ? ragged_kernel<true, false, true, true> : ragged_kernel<false, false, true, true>, tmW, tmX, tmAdd, p);
     if (dual)
-        return cudaLaunchKernelEx(&cfg, trans ? ragged_kernel<true, false, true> : ragged_kernel<false, false, true>, tmW,
-                                  tmX, tmAdd, p);
-    return cudaLaunchKernelEx(&cfg,
-                              trans ? (add ? ragged_kernel<true, true, false> : ragged_kernel<true, false, false>)
-                                    : (add ? ragged_kernel<false, true, false> : ragged_kernel<false, false, false>),
-                              tmW, tmX, tmAdd, p);
+        return cudaLaunchKernelEx(
+            &cfg, trans ? ragged_kernel<true, false, true, false> : ragged_kernel<false, false, true, false>, tmW, tmX, tmAdd, p);
+    return cudaLaunchKernelEx(
+        &cfg,
+        trans ? (add ? ragged_kernel<true, true, false, false> : ragged_kernel<true, false, false, false>)
+              : (add ? ragged_kernel<false, true, false, false> : ragged_kernel<false, false, false, false>),
+        tmW, tmX, tmAdd, p);
 }
 
 cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
@@ -1292,6 +1327,7 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     if (err != cudaSuccess) return err;
     if (pair) {
         cfg = rg_pair_config(pairs, st, attr);
+        cfg.blockDim = dim3(kRgDwThreads, 1, 1);
         return cudaLaunchKernelEx(&cfg, ragged_dw_kernel<1, true>, x_wide ? tx : ty, x_wide ? ty : tx, tg, p);
     }
     cfg = rg_config(num_sms, st, attr);

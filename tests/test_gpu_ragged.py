@@ -137,6 +137,31 @@ def test_gradient_of_long_experts(lib, R, S, E, top, K, N, skew, accumulate):
     ctx.close()
 
 
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("R,S,E,top,K,N,skew", [
+    (2, 1100, 4, 1, 520, 1096, 0.5),     # an odd number of tiles of columns
+    (1, 1664, 3, 1, 1544, 264, 2.0),     # two; experts of very different lengths
+    (3, 1400, 9, 2, 512, 2048, 0.0),     # nothing ragged but the rows
+])
+def test_products_of_long_experts(lib, R, S, E, top, K, N, skew, trans):
+    """Lengths and widths at which two blocks share the rows."""
+    bep = lib
+    ctx, t = planned(bep, R, S, E, top, 64, 64, seed=6, skew=skew)
+    expert = row_experts(ctx.cfg, t)
+    rows = R * S * top
+    x, _ = wide(ints((rows, K), 1), 8, 16)
+    w = ints((E, N, K) if trans else (E, K, N), 2)
+    y, yb = wide(torch.zeros(rows, N, dtype=torch.bfloat16, device=DEV), 24, 16, 9.0)
+    want = ref.bf16_bits(want_y(x, w, expert, 0.25, None, trans).astype(np.float32))
+    for _ in range(2):
+        y.zero_()
+        bep.bep_ragged_gemm(ctx, t["cu"], t["se"], x, w, y, trans=trans, alpha=0.25)
+        assert bep.bep_status(ctx) == 0
+        assert np.array_equal(bits(y.contiguous()), want)
+        assert (yb[:, :24] == 9).all() and (yb[:, 24 + N:] == 9).all()
+    ctx.close()
+
+
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 33, 48, 63, 64, 65, 100, 127, 128, 129, 191, 200, 257, 300])
 @pytest.mark.parametrize("K,N", [(104, 72), (72, 104)])
 def test_every_segment_height(lib, rows, K, N):
