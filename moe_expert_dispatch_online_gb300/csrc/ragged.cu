@@ -7,7 +7,8 @@
 //
 // Both kernels are persistent, one CTA an SM:
 //   warp 0      TMA (128-byte swizzle) into a ring of stages of 64 reduction steps
-//   warp 1      tcgen05.mma.kind::f16, M = 128 (rows: 64 where experts have few), N <= 256, into one of two accumulators
+//   warp 1      tcgen05.mma.kind::f16, M = 128 (rows: 64 where experts have few; gradients: 256 on a pair of CTAs),
+//               N <= 256, into one of two accumulators
 //   the rest    epilogue (rows: 8 warps, gradients: 16): TMEM, turned in shared memory, to whole pieces of rows
 // What lies outside a matrix arrives as zeros (the tensor maps end at the widths). Where there are fewer units
 // than SMs, the reduction is cut into parts; each part leaves its fp32 tile in the context's workspace and the CTA that
@@ -129,7 +130,7 @@ __device__ __forceinline__ uint32_t operand_lo(uint32_t saddr, uint32_t chunk = 
 template <bool kMN>
 __host__ __device__ constexpr uint32_t piece_step() { return kMN ? 128 : 2; }
 
-// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, major bits 15/16 (1: MN), M = 128 or 64.
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, major bits 15/16 (1: MN), M = 256 (a pair), 128 or 64.
 __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -142,6 +143,18 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint32_t a, uint32_t b
         "mov.b64 db, {%2, " BEP_RG_OPERAND_HI "};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// The same on a pair of SMs: M = 256, of which each CTA holds 128 rows of A and of D, and half of B's columns.
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, " BEP_RG_OPERAND_HI "};\n\t"
+        "mov.b64 db, {%2, " BEP_RG_OPERAND_HI "};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a), "r"(b), "r"(idesc), "r"(add)
         : "memory");
 }
@@ -168,13 +181,15 @@ __device__ __forceinline__ bool epi_all(bool v) {
 // What both kernels set up and take down alike.
 struct Frame {
     uint8_t* ring;
-    uint64_t *full, *empty, *tfull, *tempty, *afull, *aempty, *drain;
+    uint64_t *full, *empty, *ready, *tfull, *tempty, *afull, *aempty, *drain;
     uint32_t* s_tmem;
     volatile int* s_abort;
     int* s_last;
     int* s_rows;   // valid rows of each stage
     uint32_t tmem;
 };
+// kPairMma: MMAs are a pair's (cta_group::2). `readers` free a stage.
+template <bool kPairMma = false>
 __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int epi_warps, int readers = 1) {
     Frame f;
     const uint32_t raw = smem_u32(smem_raw);
@@ -182,7 +197,8 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
     f.ring = base + 1024;
     f.full = reinterpret_cast<uint64_t*>(base);
     f.empty = f.full + kRgMaxStages;
-    f.tfull = f.empty + kRgMaxStages;
+    f.ready = f.empty + kRgMaxStages;
+    f.tfull = f.ready + kRgMaxStages;
     f.tempty = f.tfull + 2;
     f.afull = f.tempty + 2;
     f.aempty = f.afull + kRgMaxAdds;
@@ -195,10 +211,11 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
         for (int s = 0; s < stages; ++s) {
             mbar_init(&f.full[s], 1);
             mbar_init(&f.empty[s], readers);
+            mbar_init(&f.ready[s], 2);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&f.tfull[a], 1);
-            mbar_init(&f.tempty[a], epi_warps);
+            mbar_init(&f.tempty[a], (kPairMma ? 2 : 1) * epi_warps);
         }
         for (int a = 0; a < kRgMaxAdds; ++a) {
             mbar_init(&f.afull[a], 1);
@@ -209,10 +226,17 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (threadIdx.x < 32) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(f.s_tmem)),
-                     "r"(kRgTmem)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (kPairMma) {   // a warp of each CTA together
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(f.s_tmem)),
+                         "r"(kRgTmem)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(f.s_tmem)),
+                         "r"(kRgTmem)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -241,7 +265,7 @@ struct Started {
         }
     }
 };
-template <bool kPair = false>
+template <bool kPair = false, bool kPairMma = false>
 __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds, Started ring, Started add) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
@@ -250,8 +274,9 @@ __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds
         if (warp == 0 && lane == 0) {
             ring.drain(f.full, stages);
             if (adds) add.drain(f.afull, adds);
-        } else if (warp == 1 && lane == 0) {
-            mma_commit(f.drain);
+        } else if (warp == 1 && lane == 0 && !(kPairMma && cluster_rank() != 0)) {
+            if (kPairMma) mma_commit_pair_lead(f.drain);
+            else mma_commit(f.drain);
             mbar_drain(f.drain, 0);
         }
         if (kPair && threadIdx.x == 0)   // what it started for the other CTA
@@ -261,7 +286,10 @@ __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds
     if (kPair) cluster_sync();   // neither CTA leaves while the other may still write to it or signal it
     if (warp == 0) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
+        if (kPairMma)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
     }
 }
 
@@ -848,16 +876,26 @@ __device__ __forceinline__ void zero_rows(uint8_t* chunk, int chunks, int tail, 
 
 // A unit: MI x 128 x BN of an expert's gradient, MI = 2 where BN leaves both room in an accumulator. Both
 // operands lie along the rows (MN-major).
-// kPair: two CTAs of a cluster take neighbouring tiles along M and the same blocks in step; each loads its own M side
-// and 32 of a block's 64 rows of the N side for both. A stage is free when both have read it.
+// kPair: 256 x BN on two CTAs of a cluster (cta_group::2): CTA r holds 128 of the M side's columns and half of the N
+// side's, 32 KB a stage where a CTA alone loads 48 for half of the tile (65,536 rows by 1096 x 1544: 325 us on CTAs of
+// their own, 302 us where each loaded half of the N side for both, 272 us with MMAs of the pair). In each CTA one more
+// warp waits for the stage, clears the rows behind the segment's last and tells CTA 0, whose warp 1 issues the MMAs of
+// both. (That signal releases shared memory alone: one that waits for all of the thread's stores took 2,000 cycles a
+// stage, twice the time.)
+//   barrier    owner   arrivals
+//   full[s]    each    the producer's expect_tx + TMA bytes
+//   ready[s]   CTA 0   the clearing warp of each CTA
+//   empty[s]   each    the MMA thread's multicast commit
+//   tfull[a]   each    the MMA thread's multicast commit at the end of a chain
+//   tempty[a]  CTA 0   the 16 epilogue warps of each CTA
 template <int MI, bool kPair>
-__global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
+__global__ void __launch_bounds__(kRgDwThreads + (kPair ? 32 : 0), 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
                                                                   const __grid_constant__ CUtensorMap tmN,
                                                                   const __grid_constant__ CUtensorMap tmG,
                                                                   const RgDwParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages, 16, kPair ? 2 : 1);
+    Frame f = open_frame<kPair>(smem_raw, p.stages, 16);
     if (kPair) cluster_sync();   // both CTAs' barriers exist
     const int rank = kPair ? (int)cluster_rank() : 0;
     const int first = kPair ? (int)cluster_id() : (int)blockIdx.x, stride = kPair ? (int)cluster_count() : (int)gridDim.x;
@@ -912,7 +950,7 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                 const int k = (b - u.b0) & 31;
                 if (k == 0 && b != u.b0) cur = blocks_at(b, u.b1);
                 const int row0 = __shfl_sync(0xffffffffu, cur.row0, k), rows = __shfl_sync(0xffffffffu, cur.rows, k);
-                if (!__all_sync(0xffffffffu, mbar_wait_held<kPair>(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status))) {
+                if (!__all_sync(0xffffffffu, mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status))) {
                     live = false;
                     break;
                 }
@@ -922,27 +960,23 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                     uint8_t* at = f.ring + pr.at * stage;
                     for (int c = 0; c < 2 * MI; ++c)
                         tma_load_2d(&tmM, &f.full[pr.at], at + c * kRgChunk, u.m0 + 64 * c, row0);
-                    for (int c = 0; c * kRgChunk < p.b_bytes; ++c) {
-                        uint8_t* b = at + a_bytes + c * kRgChunk;
-                        if (kPair)
-                            tma_load_2d_both(&tmN, &f.full[pr.at], b + rank * (kRgChunk / 2), u.n0 + 64 * c, row0 + 32 * rank);
-                        else
-                            tma_load_2d(&tmN, &f.full[pr.at], b, u.n0 + 64 * c, row0);
-                    }
+                    const int n0 = u.n0 + rank * (p.BN / 2);
+                    for (int c = 0; c * kRgChunk < p.b_bytes; ++c)
+                        tma_load_2d(&tmN, &f.full[pr.at], at + a_bytes + c * kRgChunk, n0 + 64 * c, row0);
                 }
                 __syncwarp();
                 pr.step(p.stages);
             }
         }
-        if (kPair && live && lane == 0) {   // the other CTA has read what came from here, and said so
+        if (kPair && live && lane == 0) {   // CTA 0's commits have arrived
             Started e = pr;
             e.drain(f.empty, p.stages);
         }
     } else if (warp == 1) {
-        const uint32_t idesc = idesc_bf16(128, p.BN, true, true);
+        const uint32_t idesc = idesc_bf16(kPair ? 256 : 128, p.BN, true, true);
         uint32_t s = 0, ph = 0;
         int it = 0;
-        bool live = true;
+        bool live = !kPair || rank == 0;
         for (int i = first; i < total && live; i += stride) {
             const Item u = item_of(i, next);
             next = range_at(i + stride);
@@ -950,15 +984,15 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                 const int k = (b - u.b0) % kRgChain;
                 const int acc = it & 1;
                 const uint32_t dt = f.tmem + acc * 256;
-                bool ok = k != 0 || mbar_wait_held(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status);
-                ok = ok && mbar_wait_held(&f.full[s], ph, f.s_abort, p.status);
+                bool ok = k != 0 || mbar_wait_held<kPair>(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status);
+                ok = ok && mbar_wait_held<kPair>(kPair ? &f.ready[s] : &f.full[s], ph, f.s_abort, p.status);
                 if (!__all_sync(0xffffffffu, ok)) {
                     live = false;
                     break;
                 }
                 const int rows = f.s_rows[s];
                 uint8_t* at = f.ring + s * stage;
-                if (rows & 15) {   // the rows behind a segment's last are another's, or nobody's
+                if (!kPair && (rows & 15)) {   // the rows behind a segment's last are another's, or nobody's
                     zero_rows(at, stage / kRgChunk, rows, lane);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -971,14 +1005,45 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                     for (int m = 0; m < MI; ++m)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            if (16 * kk < rows)
-                                mma_bf16(dt + m * 128, a + m * (kRgA >> 4) + kk * st, bb + kk * st, idesc, k || kk);
-                    if (kPair) mma_commit_both(&f.empty[s]);
-                    else mma_commit(&f.empty[s]);
-                    if (k == kRgChain - 1 || b == u.b1 - 1) mma_commit(&f.tfull[acc]);
+                            if (16 * kk < rows) {
+                                if (kPair) mma_bf16_pair(dt, a + kk * st, bb + kk * st, idesc, k || kk);
+                                else mma_bf16(dt + m * 128, a + m * (kRgA >> 4) + kk * st, bb + kk * st, idesc, k || kk);
+                            }
+                    const bool end = k == kRgChain - 1 || b == u.b1 - 1;
+                    if (kPair) {
+                        mma_commit_pair(&f.empty[s]);
+                        if (end) mma_commit_pair(&f.tfull[acc]);
+                    } else {
+                        mma_commit(&f.empty[s]);
+                        if (end) mma_commit(&f.tfull[acc]);
+                    }
                 }
                 __syncwarp();
                 if (k == kRgChain - 1 || b == u.b1 - 1) ++it;
+                if (++s == (uint32_t)p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else if (kPair && warp == kRgDwThreads / 32) {
+        uint32_t s = 0, ph = 0;
+        bool live = true;
+        for (int i = first; i < total && live; i += stride) {
+            const Item u = item_of(i, next);
+            next = range_at(i + stride);
+            for (int b = u.b0; b < u.b1; ++b) {
+                if (!__all_sync(0xffffffffu, mbar_wait_held(&f.full[s], ph, f.s_abort, p.status))) {
+                    live = false;
+                    break;
+                }
+                const int rows = f.s_rows[s];
+                if (rows & 15) {
+                    zero_rows(f.ring + s * stage, stage / kRgChunk, rows, lane);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_rank_shared(&f.ready[s], 0);
                 if (++s == (uint32_t)p.stages) {
                     s = 0;
                     ph ^= 1u;
@@ -1025,7 +1090,10 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&f.tempty[acc]);
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_rank_relaxed(&f.tempty[acc], 0);
+                    else mbar_arrive(&f.tempty[acc]);
+                }
             }
             if (parts > 1) {
                 // (warps that meet at barriers give up together)
@@ -1082,7 +1150,7 @@ __global__ void __launch_bounds__(kRgDwThreads, 1) ragged_dw_kernel(const __grid
         }
         if (lane == 0) bulk_wait_all();
     }
-    close_frame<kPair>(f, p.stages, 0, pr, Started());
+    close_frame<kPair, kPair>(f, p.stages, 0, pr, Started());
 }
 
 // bf16 tensor of `dims` (innermost first) with row strides in elements, boxes of 64 x box_rows, 128-byte swizzle.
@@ -1162,7 +1230,7 @@ cudaError_t ragged_setup(int num_sms, int* pairs) {
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = rg_pair_config(num_sms / 2, nullptr, attr);
-    cfg.blockDim = dim3(kRgDwThreads, 1, 1);   // (an SM holds one CTA of either kernel)
+    cfg.blockDim = dim3(kRgDwThreads + 32, 1, 1);   // (an SM holds one CTA of either kernel)
     return cudaOccupancyMaxActiveClusters(pairs, ragged_dw_kernel<1, true>, &cfg);
 }
 
@@ -1297,18 +1365,19 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
         const int64_t fit = num_sms / n, len = rows / 64 / d.E / 2;
         while (p.parts < kRgMaxParts && p.parts < fit && (int64_t)(p.parts + 1) * (p.parts + 1) <= len) ++p.parts;
     }
-    // Neighbouring tiles along M on pairs of CTAs, which share the other operand, where experts are long or have
-    // many tiles, and there are pairs of tiles enough for two rounds. An odd tile's partner has nothing to load or store. (64 experts of 4,096
-    // rows: 1016 x 1544 1000 -> 780 us, 600 x 1000, five tiles, 450 -> 385 us, 360 x 1000, three, 307 -> 267 us;
-    // 1024 x 1024, whose rows start on 128-byte lines, 535 -> 525 us. Of 128
-    // rows: 1096 x 1544 125 -> 119 us, 360 x 1000 38.5 -> 40.6.)
-    const bool pair = MI == 1 && p.BN > 128 && p.MT > 1 && (rows / d.E >= 512 || p.MT > 4) && pairs > 0 &&
+    // Tiles of 256 along M on pairs of CTAs, where there are enough of them for two rounds; an odd tile's partner only
+    // brings its half of the N side. (262,144 rows of 64 experts by 1024 x 1024: 535 -> 425 us, by 600 x 1000, five tiles,
+    // 450 -> 366 us, by 360 x 1000, three, 307 -> 264 us; 8,192 rows by 1096 x 1544: 114 -> 97 us, by 360 x 1000 the same.)
+    const bool pair = MI == 1 && p.BN > 128 && p.MT > 1 && pairs > 0 &&
                       (int64_t)d.E * ((p.MT + 1) / 2) * p.NT >= 2 * pairs;
-    if (pair) p.MT = (p.MT + 1) / 2;
+    if (pair) {
+        p.MT = (p.MT + 1) / 2;
+        p.BN = (p.BN + 31) / 32 * 32;   // halves of 16
+    }
     p.by_parts = make_fast_div((uint32_t)p.parts);
     p.by_unit = make_fast_div((uint32_t)(p.MT * p.NT));
     p.by_nt = make_fast_div((uint32_t)p.NT);
-    p.b_bytes = (p.BN + 63) / 64 * kRgChunk;
+    p.b_bytes = ((pair ? p.BN / 2 : p.BN) + 63) / 64 * kRgChunk;
     const int fit = (kRgBytes - 16 * kRgDwBox) / (MI * kRgA + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;
 
@@ -1316,9 +1385,7 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     if (!encode_g(&tg, g, d.E, K, N)) return cudaErrorInvalidValue;
     const uint64_t xd[2] = {(uint64_t)K, (uint64_t)rows}, xs[1] = {(uint64_t)ldx};
     const uint64_t yd[2] = {(uint64_t)N, (uint64_t)rows}, ys[1] = {(uint64_t)lddy};
-    const uint32_t n_box = pair ? 32 : 64;   // rows of a box of the N side
-    if (!encode_rows(&tx, x, 2, xd, xs, x_wide ? 64 : n_box) || !encode_rows(&ty, dy, 2, yd, ys, x_wide ? n_box : 64))
-        return cudaErrorInvalidValue;
+    if (!encode_rows(&tx, x, 2, xd, xs, 64) || !encode_rows(&ty, dy, 2, yd, ys, 64)) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = rg_config(1, st, attr);
     cfg.blockDim = dim3(1024, 1, 1);
@@ -1327,7 +1394,7 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     if (err != cudaSuccess) return err;
     if (pair) {
         cfg = rg_pair_config(pairs, st, attr);
-        cfg.blockDim = dim3(kRgDwThreads, 1, 1);
+        cfg.blockDim = dim3(kRgDwThreads + 32, 1, 1);
         return cudaLaunchKernelEx(&cfg, ragged_dw_kernel<1, true>, x_wide ? tx : ty, x_wide ? ty : tx, tg, p);
     }
     cfg = rg_config(num_sms, st, attr);
