@@ -53,6 +53,37 @@ __device__ __forceinline__ uint2 codes8(const float* f, const Grid& g) {
                                pack4(code_of(f[4], g), code_of(f[5], g), code_of(f[6], g), code_of(f[7], g)));
     return g.up == 0.0f ? make_uint2(0, 0) : r;
 }
+// The same of eight fp32 values, whose quotients may lie arbitrarily close to a tie without being one: the fused product
+// is within 127 * 2^-23 < kNear of 127 v / m. `off` is the largest distance of a product from its integer so far; from
+// 1/2 - kNear on, the writer calls codes8_near_tie instead.
+constexpr float kNear = 0x1p-15f, kMagic = 12582912.0f;   // 1.5 * 2^23
+__device__ __forceinline__ float off_code(float v, const Grid& g, uint32_t* q) {
+    const float s = v * g.up, r = fmaf(s, g.c, kMagic);
+    *q = __float_as_uint(r);
+    return fmaf(s, g.c, kMagic - r);
+}
+__device__ __forceinline__ uint2 codes8_f32(const float* f, const Grid& g, float* off) {
+    uint32_t q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) *off = fmaxf(*off, fabsf(off_code(f[k], g, &q[k])));
+    const uint2 r = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+    return g.up == 0.0f ? make_uint2(0, 0) : r;
+}
+// Between j and j + 1, by 254 v against (2 j + 1) m, both exact in fp64 (m: the row's largest magnitude).
+__device__ __noinline__ uint2 codes8_near_tie(float4 lo, float4 hi, Grid g, float m) {
+    const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float d = off_code(f[k], g, &q[k]);
+        if (fabsf(d) > 0.5f - kNear) {
+            const int j = (int)(__uint_as_float(q[k]) - kMagic) - (d > 0.0f ? 0 : 1);
+            const double x = 254.0 * (double)f[k], t = (double)(2 * j + 1) * (double)m;
+            q[k] = (uint32_t)(x > t || (x == t && (j & 1)) ? j + 1 : j);
+        }
+    }
+    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+}
 // Largest magnitude of eight bf16, as two bf16 bit patterns in a word (NaN above infinity above all).
 __device__ __forceinline__ uint32_t top2(const uint4& v) {
     const uint32_t m = 0x7fff7fffu;
@@ -204,11 +235,11 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_i8_kernel(const uin
 // ------------------------------------------------------------------------ activation
 // codes, scales = i8(g * sigmoid(g) * u) for h = [g | u]: kWarps warps a row. The activation stays in fp32
 // until its integers; a thread holds 8 * kActHold of its values between the two passes and makes the others
-// (rows longer than 8192) again. 524,288 rows of 1024 + 1024, 2.7 GB: 451 us (5.9 TB/s), the rest of the copy rate
-// goes to the row's maximum between its loads and its stores.
+// (rows longer than 8192) again. 524,288 rows of 1024 + 1024, 2.7 GB: 453 us (5.9 TB/s; 497 us with three CTAs an SM
+// instead of four), the rest of the copy rate goes to the row's maximum between its loads and its stores.
 constexpr int kActHold = 4;
 template <int kWarps>
-__global__ void __launch_bounds__(kThreads) swiglu_i8_kernel(const uint4* __restrict__ h, uint2* __restrict__ codes,
+__global__ void __launch_bounds__(kThreads, 4) swiglu_i8_kernel(const uint4* __restrict__ h, uint2* __restrict__ codes,
                                                              float* __restrict__ scales, int64_t rows, int F8) {
     __shared__ uint32_t s_warp[kThreads / 32];
     constexpr int kRowThreads = 32 * kWarps, kRows = kThreads / kRowThreads;
@@ -257,15 +288,27 @@ __global__ void __launch_bounds__(kThreads) swiglu_i8_kernel(const uint4* __rest
     const Grid g = grid_of(top);
     if (in && t == 0) scales[row] = g.scale;
     uint2* out = codes + row * F8;
+    float off = 0.0f;
+    auto exact = [&](const float* v) {
+        return codes8_near_tie(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]), g, __uint_as_float(top));
+    };
 #pragma unroll
     for (int j = 0; j < kActHold; ++j) {
         const int c = t + j * kRowThreads;
-        if (c < n) out[c] = codes8(a[j], g);
+        if (c < n) out[c] = codes8_f32(a[j], g, &off);
     }
+    if (off > 0.5f - kNear)   // one thread in 500
+#pragma unroll
+        for (int j = 0; j < kActHold; ++j) {
+            const int c = t + j * kRowThreads;
+            if (c < n) out[c] = exact(a[j]);
+        }
     for (int c = t + kActHold * kRowThreads; c < n; c += kRowThreads) {
         float b[8];
         act(__ldg(src + c), __ldg(src + F8 + c), b);
-        out[c] = codes8(b, g);
+        off = 0.0f;
+        out[c] = codes8_f32(b, g, &off);
+        if (off > 0.5f - kNear) out[c] = exact(b);
     }
 }
 
