@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(ModeCfg<MODE>::kThreads, 1) grouped_gemm_kerne
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(s_tmem)),
                      "r"(p.tmem_cols)
@@ -800,6 +801,7 @@ __global__ void __launch_bounds__(ModeCfg<MODE>::kThreads, 1) grouped_gemm_kerne
     }
     if (warp == 0) {
         tc_fence_after();
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(p.tmem_cols)
                      : "memory");
@@ -887,6 +889,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) grouped_gemm_dw_pair_kernel(
     }
     if (warp == 0) {
         // one warp of each CTA performs the pair's allocation together
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(s_tmem)),
                      "r"(p.tmem_cols)
@@ -1130,6 +1133,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) grouped_gemm_dw_pair_kernel(
     cluster_sync();   // neither CTA leaves while the other may still signal it or read its tiles
     if (warp == 0) {
         tc_fence_after();
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(p.tmem_cols)
                      : "memory");

@@ -423,6 +423,7 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
 
 // 32 columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+    __syncwarp();
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
@@ -454,6 +455,7 @@ __device__ __forceinline__ void mma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem
 // All eight epilogue warps.
 __device__ __forceinline__ bool octet_all(bool v) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
@@ -534,6 +536,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
                      "r"(kI8Tmem)
                      : "memory");
@@ -668,6 +671,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&wempty[i]);
+                __syncwarp();
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
@@ -899,6 +903,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) grouped_gemm_i8_kernel(
     cluster_sync();   // neither CTA leaves while the other may still signal it or read its tiles
     if (warp == 1) {
         tc_fence_after();
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kI8Tmem)
                      : "memory");
     }

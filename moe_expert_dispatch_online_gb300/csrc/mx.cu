@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     }
     if (warp == 1) {
         // one warp of each CTA performs the pair's allocation together (all of both TMEMs)
+        __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(s_tmem)),
                      "r"(kMxTmemCols)
@@ -600,6 +601,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) grouped_gemm_mx_kernel(
     cluster_sync();   // neither CTA leaves while the other may still signal it or read its tiles
     if (warp == 1) {
         tc_fence_after();
+        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                      "r"(kMxTmemCols)
                      : "memory");

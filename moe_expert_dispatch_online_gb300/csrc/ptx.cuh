@@ -36,10 +36,14 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
                  : "memory");
 }
 
+// Instructions that all threads of a warp execute together (.aligned, named barriers, elect) come behind a __syncwarp:
+// lanes that left a branch or a polling loop at different times need not have met again by themselves.
+
 // One lane of a converged warp, known to the compiler as such: code in its branch keeps
 // warp-uniform operands in uniform registers, where tcgen05 instructions take them from.
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "elect.sync _|p, 0xffffffff;\n\t"
@@ -224,6 +228,7 @@ __device__ __forceinline__ uint32_t cluster_count() {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
@@ -319,6 +324,7 @@ __device__ __forceinline__ void mma_commit_pair_lead(uint64_t* bar) {
 // Load 32 columns of this warp's 32 TMEM lanes; the wait sits in the same asm
 // statement so no use of r[] can be scheduled before the data has arrived.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t* r) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -336,6 +342,7 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t* r) 
 
 // The same of 16 columns.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"

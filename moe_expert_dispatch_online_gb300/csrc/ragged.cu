@@ -162,11 +162,13 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint32_t a, uint3
 // All epilogue warps of a kernel.
 template <int kWarps>
 __device__ __forceinline__ void epi_sync() {
+    __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
 template <int kWarps>
 __device__ __forceinline__ bool epi_all(bool v) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %1, 0;\n\t"
@@ -226,6 +228,7 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (threadIdx.x < 32) {
+        __syncwarp();
         if (kPairMma) {   // a warp of each CTA together
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(f.s_tmem)),
                          "r"(kRgTmem)
@@ -286,6 +289,7 @@ __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds
     if (kPair) cluster_sync();   // neither CTA leaves while the other may still write to it or signal it
     if (warp == 0) {
         tc_fence_after();
+        __syncwarp();
         if (kPairMma)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
         else
@@ -359,6 +363,7 @@ __device__ __forceinline__ int local_tiles(const RgParams& p, int* table, MTile*
         bad |= a < 0 || b < a || (int64_t)b > p.C;
         n += (b - a + p.tile_rows - 1) / p.tile_rows;
     }
+    __syncwarp();   // lanes leave the loops of this list at different times
     bad = __syncthreads_or(bad);
     if (bad) {
         if (blockIdx.x == 0 && t == 0) set_status(p.status, BEP_DERR_BOUNDS);
@@ -386,6 +391,7 @@ __device__ __forceinline__ int local_tiles(const RgParams& p, int* table, MTile*
                     out[at] = MTile{(int32_t)(u * p.C + a), min(p.tile_rows, b - a),
                                     rho < p.E ? rho : -(1 + u * p.B + (rho - p.E)), 0};
         }
+    __syncwarp();
     // the table's place is the ring's: what was read and written here comes before the copies that land there
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();

@@ -55,10 +55,12 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* map, uint32_
 
 // Named barriers of four epilogue warps.
 __device__ __forceinline__ void quad_sync(int id) {
+    __syncwarp();
     asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
 __device__ __forceinline__ bool quad_all(int id, bool v) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %2, 0;\n\t"

@@ -1,0 +1,29 @@
+"""Properties of the kernels' sources that no run shows (CPU)."""
+import glob
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SOURCES = sorted(glob.glob(os.path.join(ROOT, "moe_expert_dispatch_online_gb300", "csrc", "*.cu*")))
+
+
+def code(path):
+    with open(path) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_warps_converge_before_warp_wide_instructions(path):
+    """An instruction that all threads of a warp execute together comes right behind a __syncwarp (or another such
+    instruction): the end of a branch or of a loop that lanes left at different times does not bring them together."""
+    lines = code(path).split("\n")
+    start = 0                                  # of the statement
+    for i, line in enumerate(lines):
+        if re.search(r"asm volatile\(", line):
+            start = i
+        if re.search(r"\.aligned|\bbar\.(sync|red)|\belect\.sync", line):
+            before = [x for x in lines[max(0, start - 8):start] if x.strip()]
+            assert any("__syncwarp();" in x or ".aligned" in x for x in before[-4:]), (os.path.basename(path), i + 1, line)
