@@ -17,7 +17,7 @@
 // Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
 // of it writes), their gradient 323 us (6.4 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
 // with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
-// 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 213 us.
+// 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 230 us.
 
 #include <cudaTypedefs.h>
 
@@ -100,23 +100,6 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap* map, const 
                  ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-// The same box for both CTAs of a pair, at the same place in each, counted on the barrier of each.
-__device__ __forceinline__ void tma_load_2d_both(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "h"((uint16_t)3)
-        : "memory");
-}
-// This CTA's MMAs up to here, on the barrier of each CTA of the pair.
-__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
 // Operand descriptors reach the instruction as a low word (address in 16-byte units, leading offset) beside a constant
 // high word: 8-row groups 1024 bytes apart, version 1, 128-byte swizzle. The issuing thread's time bounds reductions
 // of narrow tiles, so a stage costs it one addition an operand and the 16-step pieces constant ones.
@@ -190,9 +173,9 @@ struct Frame {
     int* s_rows;   // valid rows of each stage
     uint32_t tmem;
 };
-// kPairMma: MMAs are a pair's (cta_group::2). `readers` free a stage.
-template <bool kPairMma = false>
-__device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int epi_warps, int readers = 1) {
+// kPair: MMAs are a pair's (cta_group::2).
+template <bool kPair = false>
+__device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int epi_warps) {
     Frame f;
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -212,12 +195,12 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(&f.full[s], 1);
-            mbar_init(&f.empty[s], readers);
+            mbar_init(&f.empty[s], 1);
             mbar_init(&f.ready[s], 2);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&f.tfull[a], 1);
-            mbar_init(&f.tempty[a], (kPairMma ? 2 : 1) * epi_warps);
+            mbar_init(&f.tempty[a], (kPair ? 2 : 1) * epi_warps);
         }
         for (int a = 0; a < kRgMaxAdds; ++a) {
             mbar_init(&f.afull[a], 1);
@@ -229,7 +212,7 @@ __device__ __forceinline__ Frame open_frame(uint8_t* smem_raw, int stages, int e
     }
     if (threadIdx.x < 32) {
         __syncwarp();
-        if (kPairMma) {   // a warp of each CTA together
+        if (kPair) {   // a warp of each CTA together
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(f.s_tmem)),
                          "r"(kRgTmem)
                          : "memory");
@@ -268,7 +251,7 @@ struct Started {
         }
     }
 };
-template <bool kPair = false, bool kPairMma = false>
+template <bool kPair = false>
 __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds, Started ring, Started add) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
@@ -277,8 +260,8 @@ __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds
         if (warp == 0 && lane == 0) {
             ring.drain(f.full, stages);
             if (adds) add.drain(f.afull, adds);
-        } else if (warp == 1 && lane == 0 && !(kPairMma && cluster_rank() != 0)) {
-            if (kPairMma) mma_commit_pair_lead(f.drain);
+        } else if (warp == 1 && lane == 0 && !(kPair && cluster_rank() != 0)) {
+            if (kPair) mma_commit_pair_lead(f.drain);
             else mma_commit(f.drain);
             mbar_drain(f.drain, 0);
         }
@@ -290,7 +273,7 @@ __device__ __forceinline__ void close_frame(const Frame& f, int stages, int adds
     if (warp == 0) {
         tc_fence_after();
         __syncwarp();
-        if (kPairMma)
+        if (kPair)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
         else
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(f.tmem), "r"(kRgTmem) : "memory");
@@ -412,21 +395,17 @@ __device__ __forceinline__ int box_for(int rows) { return rows <= 16 ? 16 : rows
 // kDual: a unit has two such tiles of 128 rows, in both accumulators, on each stage of W, which therefore comes half as
 // often. The epilogue frees the first accumulator before it reads the second, and the next unit's first tile runs over
 // the stages in the ring meanwhile; then its second tile on the same stages. (65,536 rows by 1096 x 1544: 285 us with
-// one tile a unit, 230 us with two, 213 us on pairs; back 274, 220 and 198 us.)
+// one tile a unit, 230 us with two; back 274 and 220 us.)
 // kAdd: what the product is added to arrives by TMA, up to four units ahead, in boxes of 64 columns that the epilogue
 // then turns its outputs in.
-// kPair: two CTAs of a cluster take neighbouring columns of the same rows in step; each loads its own tile of W and one
-// of the two row tiles for both. A stage is free when both have read it.
-template <bool kTrans, bool kAdd, bool kDual, bool kPair>
+template <bool kTrans, bool kAdd, bool kDual>
 __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                const __grid_constant__ RowMaps tmX,
                                                                const __grid_constant__ RowMaps tmAdd, const RgParams p) {
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages, 8, kPair ? 2 : 1);
-    if (kPair) cluster_sync();   // both CTAs' barriers exist
-    const int rank = kPair ? (int)cluster_rank() : 0;
-    const int first = kPair ? (int)cluster_id() : (int)blockIdx.x, stride = kPair ? (int)cluster_count() : (int)gridDim.x;
+    Frame f = open_frame(smem_raw, p.stages, 8);
+    const int first = (int)blockIdx.x, stride = (int)gridDim.x;
     uint8_t* smA = f.ring;
     uint8_t* smB = smA + p.stages * p.a_bytes;
     uint8_t* smT = smB + p.stages * p.b_bytes;   // kAdd: the units' boxes, else a box of each epilogue warp
@@ -460,8 +439,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
         it.rows = t.rows;
         it.expert = t.wsel >= 0 ? t.wsel : p.slot_expert[-1 - t.wsel];
         if (it.expert >= p.E) it.expert = -1;
-        it.n0 = it.unit - (int)fast_div(it.unit, p.by_nt) * p.NT;
-        it.n0 = (kPair ? 2 * it.n0 + rank : it.n0) * p.BN;
+        it.n0 = (it.unit - (int)fast_div(it.unit, p.by_nt) * p.NT) * p.BN;
         it.kb0 = 0;
         it.kb1 = p.kbn;
         if (parts > 1) {
@@ -487,19 +465,14 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                 const CUtensorMap *mx = map_for(tmX, rows1), *mx2 = map_for(tmX, rows2);
                 const int box = box_for(rows1), box2 = kDual && rows2 > 0 ? box_for(rows2) : 0;
                 for (int kb = u.kb0; kb < u.kb1; ++kb) {
-                    if (!mbar_wait_held<kPair>(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
+                    if (!mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
                         live = false;
                         break;
                     }
                     mbar_arrive_expect_tx(&f.full[pr.at], (box + box2) * 128 + p.b_bytes);
                     uint8_t* a = smA + pr.at * p.a_bytes;
-                    if (kPair) {
-                        if (rank == 0) tma_load_2d_both(mx, &f.full[pr.at], a, kb * 64, u.row0);
-                        else if (box2) tma_load_2d_both(mx2, &f.full[pr.at], a + kRgA, kb * 64, u.row0 + 128);
-                    } else {
-                        tma_load_2d(mx, &f.full[pr.at], a, kb * 64, u.row0);
-                        if (kDual && box2) tma_load_2d(mx2, &f.full[pr.at], a + kRgA, kb * 64, u.row0 + 128);
-                    }
+                    tma_load_2d(mx, &f.full[pr.at], a, kb * 64, u.row0);
+                    if (kDual && box2) tma_load_2d(mx2, &f.full[pr.at], a + kRgA, kb * 64, u.row0 + 128);
                     uint8_t* b = smB + pr.at * p.b_bytes;
                     if (kTrans)
                         tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, u.n0, u.expert);
@@ -516,10 +489,6 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                         tma_load_2d(ma, &f.afull[ad.at], smT + ad.at * p.add_bytes + c * kRgA, u.n0 + c * 64, u.row0);
                     ad.step(p.adds);
                 }
-            }
-            if (kPair && live) {   // the other CTA has read what came from here, and said so
-                Started e = pr;
-                e.drain(f.empty, p.stages);
             }
         }
     } else if (warp == 1) {
@@ -577,8 +546,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                             tile(f.tmem, a, b, true);
                         }
                         if (two) tile(f.tmem + 256, a + (kRgA >> 4), b, kb != 0);
-                        if (kPair) mma_commit_both(&f.empty[s]);
-                        else mma_commit(&f.empty[s]);
+                        mma_commit(&f.empty[s]);
                         a += a_step;
                         b += b_step;
                         if (++s == (uint32_t)p.stages) {
@@ -749,7 +717,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
             if (!live) break;
         }
     }
-    close_frame<kPair>(f, p.stages, kAdd ? p.adds : 0, pr, ad);
+    close_frame(f, p.stages, kAdd ? p.adds : 0, pr, ad);
 }
 
 // ------------------------------------------------------------------------ matrices
@@ -1156,7 +1124,7 @@ __global__ void __launch_bounds__(kRgDwThreads + (kPair ? 32 : 0), 1) ragged_dw_
         }
         if (lane == 0) bulk_wait_all();
     }
-    close_frame<kPair, kPair>(f, p.stages, 0, pr, Started());
+    close_frame<kPair>(f, p.stages, 0, pr, Started());
 }
 
 // bf16 tensor of `dims` (innermost first) with row strides in elements, boxes of 64 x box_rows, 128-byte swizzle.
@@ -1220,14 +1188,9 @@ void cut(int width, int most, int* tile, int* tiles, int unit = 16) {
 }  // namespace
 
 cudaError_t ragged_setup(int num_sms, int* pairs) {
-    const void* kernels[] = {(const void*)ragged_kernel<false, false, false, false>,
-                             (const void*)ragged_kernel<false, true, false, false>,
-                             (const void*)ragged_kernel<true, false, false, false>,
-                             (const void*)ragged_kernel<true, true, false, false>,
-                             (const void*)ragged_kernel<false, false, true, false>,
-                             (const void*)ragged_kernel<true, false, true, false>,
-                             (const void*)ragged_kernel<false, false, true, true>,
-                             (const void*)ragged_kernel<true, false, true, true>,
+    const void* kernels[] = {(const void*)ragged_kernel<false, false, false>, (const void*)ragged_kernel<false, true, false>,
+                             (const void*)ragged_kernel<true, false, false>, (const void*)ragged_kernel<true, true, false>,
+                             (const void*)ragged_kernel<false, false, true>, (const void*)ragged_kernel<true, false, true>,
                              (const void*)ragged_dw_kernel<1, false>, (const void*)ragged_dw_kernel<2, false>,
                              (const void*)ragged_dw_kernel<1, true>};
     for (const void* k : kernels) {
@@ -1242,8 +1205,7 @@ cudaError_t ragged_setup(int num_sms, int* pairs) {
 
 cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                           const uint16_t* x, int64_t ldx, int K, const uint16_t* w, int N, int trans, float alpha,
-                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, int pairs,
-                          cudaStream_t st) {
+                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, cudaStream_t st) {
     const int64_t rows = (int64_t)d.R * d.C;
     RgParams p = {};
     p.tiles = ws.tiles;
@@ -1284,14 +1246,6 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
         p.tile_rows = 256;
         p.a_bytes = 2 * kRgA;
     }
-    // An even number of tiles of columns on pairs of CTAs. One tile more costs less than it saves where rows of x start
-    // inside 128-byte lines and take two requests each (1096 x 1544, 7 tiles: 230 -> 213 us, back, 5 tiles: 220 -> 198 us;
-    // 262,144 rows by 600 x 1000, 4 tiles: 315 -> 275 us), and more where they do not (1088 x 1600: 182 -> 195 us).
-    const bool pair = dual && p.NT > 1 && pairs > 0 && (p.NT % 2 == 0 || ldx % 64 != 0);
-    if (pair) {
-        p.NT = (p.NT + 1) / 2;
-        p.BN = ((N + 2 * p.NT - 1) / (2 * p.NT) + 15) / 16 * 16;
-    }
     p.by_nt = make_fast_div((uint32_t)p.NT);
     p.by_nrow = make_fast_div((uint32_t)d.NROW);
     if (p.BN <= kRgPartCols) p.partial = ws.partial;
@@ -1323,19 +1277,14 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
                                       : launch_row_tiles<128>(d, ws, cu, st);
         if (err != cudaSuccess) return err;
     }
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair ? rg_pair_config(pairs, st, attr) : rg_config(num_sms, st, attr);
-    if (pair)
-        return cudaLaunchKernelEx(
-            &cfg, trans ? ragged_kernel<true, false, true, true> : ragged_kernel<false, false, true, true>, tmW, tmX, tmAdd, p);
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = rg_config(num_sms, st, &attr);
     if (dual)
-        return cudaLaunchKernelEx(
-            &cfg, trans ? ragged_kernel<true, false, true, false> : ragged_kernel<false, false, true, false>, tmW, tmX, tmAdd, p);
-    return cudaLaunchKernelEx(
-        &cfg,
-        trans ? (add ? ragged_kernel<true, true, false, false> : ragged_kernel<true, false, false, false>)
-              : (add ? ragged_kernel<false, true, false, false> : ragged_kernel<false, false, false, false>),
-        tmW, tmX, tmAdd, p);
+        return cudaLaunchKernelEx(&cfg, trans ? ragged_kernel<true, false, true> : ragged_kernel<false, false, true>, tmW, tmX, tmAdd, p);
+    return cudaLaunchKernelEx(&cfg,
+                              trans ? (add ? ragged_kernel<true, true, false> : ragged_kernel<true, false, false>)
+                                    : (add ? ragged_kernel<false, true, false> : ragged_kernel<false, false, false>),
+                              tmW, tmX, tmAdd, p);
 }
 
 cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,

@@ -27,3 +27,11 @@ def test_warps_converge_before_warp_wide_instructions(path):
         if re.search(r"\.aligned|\bbar\.(sync|red)|\belect\.sync", line):
             before = [x for x in lines[max(0, start - 8):start] if x.strip()]
             assert any("__syncwarp();" in x or ".aligned" in x for x in before[-4:]), (os.path.basename(path), i + 1, line)
+
+
+@pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
+def test_no_load_is_multicast(path):
+    """A tensor copy with cluster multicast may only read this GPU's own memory, and the calls take whatever device
+    pointers they are given. (A multicast commit is a signal between the two CTAs and reads nothing.)"""
+    text = re.sub(r'"\s*"', "", code(path))
+    assert not re.findall(r"cp\.async\.bulk[^;\"]*multicast", text)
