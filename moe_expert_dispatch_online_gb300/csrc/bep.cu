@@ -559,7 +559,7 @@ int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot
     rc = ragged_ready(ctx);
     if (rc) return rc;
     return cuda_rc(bep::launch_ragged(ctx->d, ctx->ws, cu_seqlens, slot_expert, x, ldx, K, w, N, trans, alpha, add, ldadd,
-                                      y, ldy, ctx->num_sms, as_stream(stream)));
+                                      y, ldy, ctx->num_sms, ctx->ragged_pairs, as_stream(stream)));
 }
 
 int bep_ragged_gemm_dw(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x,

@@ -151,7 +151,7 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
 cudaError_t ragged_setup(int num_sms, int* pairs);
 cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                           const uint16_t* x, int64_t ldx, int K, const uint16_t* w, int N, int trans, float alpha,
-                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, cudaStream_t st);
+                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, int pairs, cudaStream_t st);
 cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                              const uint16_t* x, int64_t ldx, int K, const uint16_t* dy, int64_t lddy, int N, float alpha,
                              int accumulate, float* g, int num_sms, int pairs, cudaStream_t st);

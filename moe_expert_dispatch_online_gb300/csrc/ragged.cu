@@ -7,9 +7,9 @@
 //
 // Both kernels are persistent, one CTA an SM:
 //   warp 0      TMA (128-byte swizzle) into a ring of stages of 64 reduction steps
-//   warp 1      tcgen05.mma.kind::f16, M = 128 (rows: 64 where experts have few; gradients: 256 on a pair of CTAs),
-//               N <= 256, into one of two accumulators
-//   the rest    epilogue (rows: 8 warps, gradients: 16): TMEM, turned in shared memory, to whole pieces of rows
+//   warp 1      tcgen05.mma.kind::f16, M = 128 (64 where experts have few rows, 256 on a pair of CTAs), N <= 256, into
+//               one of two accumulators
+//   the rest    epilogue (8 or 16 warps): TMEM, summed over chains of steps, turned in shared memory, to whole pieces of rows
 // What lies outside a matrix arrives as zeros (the tensor maps end at the widths). Where there are fewer units
 // than SMs, the reduction is cut into parts; each part leaves its fp32 tile in the context's workspace and the CTA that
 // comes last adds them in the order of the parts, so that the result does not depend on who that was.
@@ -26,8 +26,8 @@
 namespace bep {
 namespace {
 
-constexpr int kRgThreads = 32 * 10;      // of the rows' kernel: 8 epilogue warps
-constexpr int kRgDwThreads = 32 * 18;    // of the matrices': 16, which hold a unit's sums in registers
+constexpr int kRgThreads = 32 * 10;      // 8 epilogue warps
+constexpr int kRgSumThreads = 32 * 18;   // 16, where the sums of more than 128 columns are held in registers
 constexpr int kRgA = 128 * 128;          // bytes: 128 rows (columns) x 64 reduction steps
 constexpr int kRgChunk = 64 * 128;       // bytes: 64 x 64 elements
 constexpr int kRgBox = 32 * 128;         // bytes: an epilogue warp's box of 32 rows of 128 bytes
@@ -40,9 +40,12 @@ constexpr int kRgLocal = 256;            // row tiles of a small call, whose lis
 // Shared memory: up to 1 KB lost to alignment, 1 KB of barriers, then the ring and what the epilogue turns its boxes in.
 constexpr size_t kRgSmem = 227 * 1024;
 constexpr int kRgBytes = 225 * 1024;
-// The tensor core cuts its fp32 sum off at each step of 16 rows, always towards zero; a gradient's chain of steps is
-// therefore ended after this many blocks of 64 rows and added, rounded to nearest, to a sum in registers.
+// The tensor core cuts its fp32 sum off at each step of 16, always towards zero (7.7e-5 of a sum of 16,384 positive
+// products in one chain of steps); a chain is therefore ended after this many blocks of 64 and added, rounded to nearest,
+// to a sum in registers. Outputs of 16 bits have longer chains than gradients of 32 (65,536 rows by 1088 x 1600: 201 us
+// with 8 blocks, 208 us with 4).
 constexpr int kRgChain = 4;
+constexpr int kRgRowChain = 8;
 
 struct RgParams {
     const MTile* tiles;
@@ -326,11 +329,12 @@ __device__ __forceinline__ bool last_part(int32_t* ticket, int parts, int* s_las
 // ------------------------------------------------------------------------ rows
 // The list of row_tiles_kernel for a table of few row tiles, made in shared memory by every CTA for itself, which
 // saves a launch: up to kRgLocal tiles in (rank, row) order; returns their number (0 for a bad table).
+template <int kThreads>
 __device__ __forceinline__ int local_tiles(const RgParams& p, int* table, MTile* out, int* s_warp) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int items = p.R * p.NROW, per = (items + kRgThreads - 1) / kRgThreads;
+    const int items = p.R * p.NROW, per = (items + kThreads - 1) / kThreads;
 #pragma unroll 8
-    for (int i = t; i < items + p.R; i += kRgThreads) table[i] = p.cu[i];
+    for (int i = t; i < items + p.R; i += kThreads) table[i] = p.cu[i];
     __syncthreads();
     const int lo = min(items, t * per), hi = min(items, lo + per);
     int n = 0, bad = 0;
@@ -361,7 +365,7 @@ __device__ __forceinline__ int local_tiles(const RgParams& p, int* table, MTile*
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
     int at = incl - n, total = 0;
-    for (int w = 0; w < kRgThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) at += s_warp[w];
         total += s_warp[w];
     }
@@ -392,23 +396,35 @@ __device__ __forceinline__ int box_for(int rows) { return rows <= 16 ? 16 : rows
 
 // A unit: up to 128 rows of a segment x BN columns, or up to 64 where experts have few rows. A small tile leaves the
 // accumulator's other rows to whatever the stage holds behind its own; they are not stored.
-// kDual: a unit has two such tiles of 128 rows, in both accumulators, on each stage of W, which therefore comes half as
-// often. The epilogue frees the first accumulator before it reads the second, and the next unit's first tile runs over
-// the stages in the ring meanwhile; then its second tile on the same stages. (65,536 rows by 1096 x 1544: 285 us with
-// one tile a unit, 230 us with two; back 274 and 220 us.)
 // kAdd: what the product is added to arrives by TMA, up to four units ahead, in boxes of 64 columns that the epilogue
 // then turns its outputs in.
-template <bool kTrans, bool kAdd, bool kDual>
-__global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_constant__ CUtensorMap tmW,
-                                                               const __grid_constant__ RowMaps tmX,
-                                                               const __grid_constant__ RowMaps tmAdd, const RgParams p) {
+// kSum: a reduction of more than kRgRowChain blocks, whose chains take the two accumulators in turn and are summed in
+// registers by so many epilogue warps, 64 columns each (0: one chain, read out of the accumulator by 8).
+// kPair: up to 256 rows x BN on two CTAs of a cluster (cta_group::2): CTA r holds rows 128 r.. of A and of the output and
+// half of W's columns, 32 KB a stage for 256 columns where a CTA alone loads 48 for the same rows. CTA 0's producer arms a
+// stage for both and its warp 1 issues the MMAs of both.
+//   barrier    owner   arrivals
+//   full[s]    CTA 0   its producer's expect_tx + the TMA bytes of both
+//   empty[s]   each    the MMA thread's multicast commit
+//   tfull[a]   each    the MMA thread's multicast commit at the end of a chain
+//   tempty[a]  CTA 0   the 16 epilogue warps of each CTA
+template <bool kTrans, bool kAdd, int kSum, bool kPair>
+__global__ void __launch_bounds__(kSum == 16 ? kRgSumThreads : kRgThreads, 1)
+    ragged_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ RowMaps tmX,
+                  const __grid_constant__ RowMaps tmAdd, const RgParams p) {
+    static_assert(!kPair || (kSum && !kAdd), "a pair's reduction is long, and it adds nothing");
+    constexpr bool kChain = kSum != 0;
+    constexpr int kThreads = kSum == 16 ? kRgSumThreads : kRgThreads, kEpi = kThreads / 32 - 2;
     extern __shared__ uint8_t smem_raw[];
     grid_launch_dependents();
-    Frame f = open_frame(smem_raw, p.stages, 8);
-    const int first = (int)blockIdx.x, stride = (int)gridDim.x;
+    const int nbox = (p.BN + 63) / 64;   // boxes of 64 columns
+    Frame f = open_frame<kPair>(smem_raw, p.stages, kChain ? 4 * nbox : kEpi);
+    if (kPair) cluster_sync();   // both CTAs' barriers exist
+    const int rank = kPair ? (int)cluster_rank() : 0;
+    const int first = kPair ? (int)cluster_id() : (int)blockIdx.x, stride = kPair ? (int)cluster_count() : (int)gridDim.x;
     uint8_t* smA = f.ring;
     uint8_t* smB = smA + p.stages * p.a_bytes;
-    uint8_t* smT = smB + p.stages * p.b_bytes;   // kAdd: the units' boxes, else a box of each epilogue warp
+    uint8_t* smT = smB + p.stages * p.b_bytes;   // kAdd: the units' boxes, else a box of each epilogue warp with columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Started pr, ad;
     grid_wait();   // launched early: the work list and the rows are complete from here on
@@ -417,7 +433,7 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
     int ntiles;
     if (p.local) {
         MTile* list = reinterpret_cast<MTile*>(f.ring + kRgBytes - kRgLocal * sizeof(MTile));
-        ntiles = local_tiles(p, reinterpret_cast<int*>(f.ring), list, f.s_rows);   // (the ring is not in use yet)
+        ntiles = local_tiles<kThreads>(p, reinterpret_cast<int*>(f.ring), list, f.s_rows);   // (the ring is not in use yet)
         tiles = list;
     } else {
         ntiles = *p.ntiles;
@@ -454,31 +470,45 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
     if (warp == 0) {
         if (lane == 0) {
             bool live = true;
+            uint32_t bar0 = kPair ? cluster_addr(f.full, 0) : 0;
             for (int i = first; i < total && live; i += stride) {
                 const Item u = item_of(i, next);
                 next = tile_at(i + stride);
                 if (u.expert < 0) {
-                    set_status(p.status, BEP_DERR_BOUNDS);
+                    if (rank == 0) set_status(p.status, BEP_DERR_BOUNDS);
                     continue;
                 }
-                const int rows1 = kDual ? min(u.rows, 128) : u.rows, rows2 = u.rows - rows1;
-                const CUtensorMap *mx = map_for(tmX, rows1), *mx2 = map_for(tmX, rows2);
-                const int box = box_for(rows1), box2 = kDual && rows2 > 0 ? box_for(rows2) : 0;
+                // rows of the unit's first 128 and of the others; this CTA's
+                const int rows0 = kPair ? min(u.rows, 128) : u.rows, rows1 = u.rows - rows0;
+                const int box0 = box_for(rows0), box1 = rows1 > 0 ? box_for(rows1) : 0;
+                const int box = rank ? box1 : box0, row0 = u.row0 + 128 * rank;
+                const CUtensorMap* mx = map_for(tmX, rank ? rows1 : rows0);
+                const int bytes = kPair ? (box0 + box1) * 128 + 2 * p.b_bytes : box * 128 + p.b_bytes;
+                const int n0 = kPair ? u.n0 + rank * (p.BN / 2) : u.n0;
                 for (int kb = u.kb0; kb < u.kb1; ++kb) {
                     if (!mbar_wait_held(&f.empty[pr.at], pr.phase ^ 1u, f.s_abort, p.status)) {
                         live = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&f.full[pr.at], (box + box2) * 128 + p.b_bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&f.full[pr.at], bytes);
                     uint8_t* a = smA + pr.at * p.a_bytes;
-                    tma_load_2d(mx, &f.full[pr.at], a, kb * 64, u.row0);
-                    if (kDual && box2) tma_load_2d(mx2, &f.full[pr.at], a + kRgA, kb * 64, u.row0 + 128);
                     uint8_t* b = smB + pr.at * p.b_bytes;
-                    if (kTrans)
-                        tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, u.n0, u.expert);
-                    else
-                        for (int c = 0; c * p.chunk < p.b_bytes; ++c)
-                            tma_load_3d(&tmW, &f.full[pr.at], b + c * p.chunk, u.n0 + c * 64, kb * 64, u.expert);
+                    if (kPair) {
+                        const uint32_t bar = bar0 + pr.at * 8;
+                        if (box) tma_load_2d_pair(mx, bar, a, kb * 64, row0);
+                        if (kTrans)
+                            tma_load_3d_pair(&tmW, bar, b, kb * 64, n0, u.expert);
+                        else
+                            for (int c = 0; c * p.chunk < p.b_bytes; ++c)
+                                tma_load_3d_pair(&tmW, bar, b + c * p.chunk, n0 + c * 64, kb * 64, u.expert);
+                    } else {
+                        tma_load_2d(mx, &f.full[pr.at], a, kb * 64, row0);
+                        if (kTrans)
+                            tma_load_3d(&tmW, &f.full[pr.at], b, kb * 64, n0, u.expert);
+                        else
+                            for (int c = 0; c * p.chunk < p.b_bytes; ++c)
+                                tma_load_3d(&tmW, &f.full[pr.at], b + c * p.chunk, n0 + c * 64, kb * 64, u.expert);
+                    }
                     pr.step(p.stages);
                 }
                 if (kAdd && parts == 1 && live) {
@@ -490,12 +520,25 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     ad.step(p.adds);
                 }
             }
+            if (kPair && live) {   // CTA 0's commits have arrived
+                Started e = pr;
+                e.drain(f.empty, p.stages);
+            }
         }
     } else if (warp == 1) {
-        if (elect_one()) {
-            const uint32_t idesc = idesc_bf16(kDual ? 128 : p.tile_rows, p.BN, false, !kTrans);
+        if (rank == 0 && elect_one()) {
+            const uint32_t idesc = idesc_bf16(kPair ? 256 : p.tile_rows, p.BN, false, !kTrans);
             const uint32_t a0 = operand_lo<false>(smem_u32(smA)), b0 = operand_lo<!kTrans>(smem_u32(smB), p.chunk);
             const uint32_t a_step = p.a_bytes >> 4, b_step = p.b_bytes >> 4;
+            constexpr uint32_t sa = piece_step<false>(), sb = piece_step<!kTrans>();
+            auto mma = [&](uint32_t dt, uint32_t aa, uint32_t bb, uint32_t add) {
+                if (kPair) mma_bf16_pair(dt, aa, bb, idesc, add);
+                else mma_bf16(dt, aa, bb, idesc, add);
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (kPair) mma_commit_pair(bar);
+                else mma_commit(bar);
+            };
             uint32_t s = 0, ph = 0, a = a0, b = b0;
             int it = 0;
             bool live = true;
@@ -503,50 +546,32 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                 const Item u = item_of(i, next);
                 next = tile_at(i + stride);
                 if (u.expert < 0) continue;
-                constexpr uint32_t sa = piece_step<false>(), sb = piece_step<!kTrans>();
-                if (kDual) {
-                    auto tile = [&](uint32_t dt, uint32_t aa, uint32_t bb, bool add) {
-                        mma_bf16(dt, aa, bb, idesc, add);
-                        mma_bf16(dt, aa + sa, bb + sb, idesc, 1);
-                        mma_bf16(dt, aa + 2 * sa, bb + 2 * sb, idesc, 1);
-                        mma_bf16(dt, aa + 3 * sa, bb + 3 * sb, idesc, 1);
-                    };
-                    const uint32_t aph = (it & 1) ^ 1u;
-                    const bool two = u.rows > 128;
-                    ++it;
-                    const int pre = min(p.stages, p.kbn);
-                    if (!mbar_wait_held(&f.tempty[0], aph, f.s_abort, p.status)) break;
+                int left = u.kb1 - u.kb0;   // blocks
+                // chains of about the same length: each hides the way of the one before into registers
+                for (int nc = kChain ? (left + kRgRowChain - 1) / kRgRowChain : 1; nc > 0 && live; --nc, ++it) {
+                    const int acc = it & 1, len = kChain ? (left + nc - 1) / nc : left;
+                    left -= len;
+                    if (!mbar_wait_held<kPair>(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status)) {
+                        live = false;
+                        break;
+                    }
                     tc_fence_after();
-                    uint32_t s1 = s, ph1 = ph, a1 = a, b1 = b;
-                    for (int kb = 0; kb < pre; ++kb) {   // the first tile over the stages of the ring
-                        if (!mbar_wait_held(&f.full[s1], ph1, f.s_abort, p.status)) {
+                    const uint32_t dt = f.tmem + acc * 256;
+                    for (int k = 0; k < len; ++k) {
+                        if (!mbar_wait_held(&f.full[s], ph, f.s_abort, p.status)) {
                             live = false;
                             break;
                         }
                         tc_fence_after();
-                        tile(f.tmem, a1, b1, kb != 0);
-                        a1 += a_step;
-                        b1 += b_step;
-                        if (++s1 == (uint32_t)p.stages) {
-                            s1 = 0;
-                            ph1 ^= 1u;
-                            a1 = a0;
-                            b1 = b0;
+                        mma(dt, a, b, k != 0);
+                        if (kChain || p.steps == 4) {
+                            mma(dt, a + sa, b + sb, 1);
+                            mma(dt, a + 2 * sa, b + 2 * sb, 1);
+                            mma(dt, a + 3 * sa, b + 3 * sb, 1);
+                        } else {
+                            for (int kk = 1; kk < p.steps; ++kk) mma(dt, a + kk * sa, b + kk * sb, 1);
                         }
-                    }
-                    if (!live || !mbar_wait_held(&f.tempty[1], aph, f.s_abort, p.status)) break;
-                    tc_fence_after();
-                    for (int kb = 0; kb < p.kbn; ++kb) {
-                        if (kb >= pre) {
-                            if (!mbar_wait_held(&f.full[s], ph, f.s_abort, p.status)) {
-                                live = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            tile(f.tmem, a, b, true);
-                        }
-                        if (two) tile(f.tmem + 256, a + (kRgA >> 4), b, kb != 0);
-                        mma_commit(&f.empty[s]);
+                        commit(&f.empty[s]);
                         a += a_step;
                         b += b_step;
                         if (++s == (uint32_t)p.stages) {
@@ -556,96 +581,100 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                             b = b0;
                         }
                     }
-                    if (!live) break;
-                    mma_commit(&f.tfull[0]);
-                    mma_commit(&f.tfull[1]);
-                    continue;
+                    if (live) commit(&f.tfull[acc]);
                 }
-                const int acc = it & 1;
-                if (!mbar_wait_held(&f.tempty[acc], ((it >> 1) & 1) ^ 1u, f.s_abort, p.status)) break;
-                ++it;
-                tc_fence_after();
-                const uint32_t dt = f.tmem + acc * 256;
-                for (int kb = u.kb0; kb < u.kb1; ++kb) {
-                    if (!mbar_wait_held(&f.full[s], ph, f.s_abort, p.status)) {
-                        live = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    mma_bf16(dt, a, b, idesc, kb != u.kb0);
-                    if (p.steps == 4) {
-                        mma_bf16(dt, a + sa, b + sb, idesc, 1);
-                        mma_bf16(dt, a + 2 * sa, b + 2 * sb, idesc, 1);
-                        mma_bf16(dt, a + 3 * sa, b + 3 * sb, idesc, 1);
-                    } else {
-                        for (int kk = 1; kk < p.steps; ++kk) mma_bf16(dt, a + kk * sa, b + kk * sb, idesc, 1);
-                    }
-                    mma_commit(&f.empty[s]);
-                    a += a_step;
-                    b += b_step;
-                    if (++s == (uint32_t)p.stages) {
-                        s = 0;
-                        ph ^= 1u;
-                        a = a0;
-                        b = b0;
-                    }
-                }
-                if (live) mma_commit(&f.tfull[acc]);
             }
         }
     } else {
-        // Two warps for each quarter of the accumulator's rows, each with half of the boxes of 64 columns. A box is
-        // turned in shared memory, so that 8 lanes write 128 bytes of a row of y.
+        // The warps of each quarter of the accumulator's rows share its boxes of 64 columns. A box is turned in shared
+        // memory, so that 8 lanes write 128 bytes of a row of y.
         // (a tile of 64 rows has 16 of them in each quarter's first lanes)
-        const int q = warp & 3, second = (warp - 2) >> 2, span = kDual ? 32 : p.tile_rows / 4;
+        const int q = warp & 3, group = (warp - 2) >> 2, span = kPair ? 32 : p.tile_rows / 4;
         const int sub = lane >> 3, piece = lane & 7;
-        const int nbox = (p.BN + 63) / 64, mine = (nbox + 1) / 2, box0 = second * mine, box1 = min(nbox, box0 + mine);
+        const int mine = kChain ? 1 : (nbox + 1) / 2;
+        const int box0 = group * mine, box1 = min(nbox, box0 + mine);
+        const bool idle = kChain && box0 >= box1;   // such warps only meet the others at barriers
+        constexpr int kBoxes = kChain ? 1 : 2;       // a warp's at most
+        constexpr bool kHalf = kChain && !kAdd;      // turned 16 rows at a time, which leaves room for more stages
         int it = 0;
         uint32_t as = 0, aph = 0;
         for (int i = first; i < total; i += stride) {
             const Item u = item_of(i, next);
             next = tile_at(i + stride);
             if (u.expert < 0) continue;
-            bool live = true;
-#pragma unroll 1
-            for (int tile = 0; tile < (kDual ? 2 : 1); ++tile) {
-            const int acc = kDual ? tile : it & 1;
-            const int rows = min(u.rows - 128 * tile - span * q, span);   // this warp's
-            const int64_t row0 = (int64_t)u.row0 + 128 * tile + span * q;
-            bool done = mbar_wait_held(&f.tfull[acc], kDual ? it & 1 : (it >> 1) & 1, f.s_abort, p.status);
-            if (kAdd && parts == 1) done = done && mbar_wait_held(&f.afull[as], aph, f.s_abort, p.status);
-            done = __all_sync(0xffffffffu, done);
-            // (warps that meet at barriers give up together)
-            if (parts > 1 ? !epi_all<8>(done) : !done) {
-                live = false;
-                break;
-            }
-            if (!kDual || tile) ++it;
-            tc_fence_after();
-            const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256;
-            bool held = true;
-            auto release = [&]() {
+            const int rows = min(u.rows - 128 * rank - span * q, span);   // this warp's
+            const int64_t row0 = (int64_t)u.row0 + 128 * rank + span * q;
+            float sum[kChain ? 2 : 1][32];   // this thread's row of the warp's box, else of 32 columns at a time
+            bool done = true, held = true;
+            auto release = [&](int acc) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&f.tempty[acc]);
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_rank_relaxed(&f.tempty[acc], 0);
+                    else mbar_arrive(&f.tempty[acc]);
+                }
                 held = false;
             };
+            if (kChain) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[kChain ? h : 0][j] = 0.0f;
+                for (int c0 = u.kb0; c0 < u.kb1 && !idle; c0 += kRgRowChain) {
+                    const int acc = it & 1;
+                    done = __all_sync(0xffffffffu, mbar_wait_held(&f.tfull[acc], (it >> 1) & 1, f.s_abort, p.status));
+                    if (!done) break;
+                    ++it;
+                    tc_fence_after();
+                    const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256 + 64 * box0;
+                    if (rows > 0)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            if (64 * box0 + 16 * h >= p.BN) break;
+                            uint32_t r[16];
+                            tmem_ld_32x32b_x16(tacc + 16 * h, r);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[kChain ? h >> 1 : 0][16 * (h & 1) + j] += __uint_as_float(r[j]);
+                        }
+                    release(acc);
+                }
+            } else {
+                done = __all_sync(0xffffffffu, mbar_wait_held(&f.tfull[it & 1], (it >> 1) & 1, f.s_abort, p.status));
+            }
+            if (kAdd && parts == 1 && !idle)
+                done = done && __all_sync(0xffffffffu, mbar_wait_held(&f.afull[as], aph, f.s_abort, p.status));
+            // (warps that meet at barriers give up together)
+            if (parts > 1 ? !epi_all<kEpi>(done) : !done) break;
+            const int acc = it & 1;   // (!kChain)
+            const uint32_t tacc = f.tmem + ((uint32_t)(q * 32) << 16) + acc * 256;
+            if (!kChain) {
+                ++it;
+                tc_fence_after();
+            }
             const int slot0 = u.unit * parts;
             bool mine_to_store = true;
             if (parts > 1) {
-                for (int c0 = 64 * box0; c0 < min(64 * box1, p.BN); c0 += 32) {
-                    float r[32];
-                    read_tmem(tacc + c0, r);
-                    put_part(part_tile(p.partial, i), c0, 32 * q + lane, r);
+                if (kChain) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (!idle && 64 * box0 + 32 * h < p.BN)
+                            put_part(part_tile(p.partial, i), 64 * box0 + 32 * h, 32 * q + lane, sum[kChain ? h : 0]);
+                } else {
+                    for (int c0 = 64 * box0; c0 < min(64 * box1, p.BN); c0 += 32) {
+                        float r[32];
+                        read_tmem(tacc + c0, r);
+                        put_part(part_tile(p.partial, i), c0, 32 * q + lane, r);
+                    }
+                    release(acc);
                 }
-                release();
-                mine_to_store = last_part<8>(p.tickets + u.unit, parts, f.s_last);
+                mine_to_store = last_part<kEpi>(p.tickets + u.unit, parts, f.s_last);
             }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kBoxes; ++b) {
                 const int bx = box0 + b;
-                if (bx >= box1 || !mine_to_store || (kDual && rows <= 0)) break;
-                uint8_t* stg = kAdd ? smT + as * p.add_bytes + bx * kRgA + q * span * 128 : smT + (warp - 2) * kRgBox;
+                if (bx >= box1 || !mine_to_store || (kChain && rows <= 0)) break;
+                uint8_t* stg = kAdd ? smT + as * p.add_bytes + bx * kRgA + q * span * 128
+                                    : smT + (warp - 2) * (kHalf ? kRgBox / 2 : kRgBox);
                 uint4* line = reinterpret_cast<uint4*>(stg + lane * 128);   // this lane's row of the box
                 const int c = 64 * bx + 8 * piece;
                 const bool in = c < p.BN && u.n0 + c < p.N;
@@ -662,9 +691,9 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                 for (int h = 0; h < 2; ++h) {
                     const int c0 = 64 * bx + 32 * h;
                     if (c0 >= p.BN) break;
-                    float r[32];
+                    float* r = sum[kChain ? h : 0];
                     if (parts > 1) sum_parts(p.partial, slot0, parts, c0, 32 * q + lane, r);
-                    else read_tmem(tacc + c0, r);
+                    else if (!kChain) read_tmem(tacc + c0, r);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint4& at = line[(4 * h + j) ^ (lane & 7)];
@@ -688,22 +717,41 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                             }
                             w[e] = pack_bf16x2(lo, hi);
                         }
-                        if (lane < span) at = make_uint4(w[0], w[1], w[2], w[3]);   // (the others' place is another warp's)
+                        if (kHalf) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) r[4 * j + e] = __uint_as_float(w[e]);
+                        } else if (lane < span) {   // (the others' place is another warp's)
+                            at = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
                 }
-                if (held && bx + 1 == box1) release();   // this warp has read all its columns
-                __syncwarp();
-                if (in) {
-                    uint16_t* out = p.y + (row0 + sub) * p.ldy + u.n0 + c;
+                if (!kChain && held && bx + 1 == box1) release(acc);   // this warp has read all its columns
+                uint16_t* out = p.y + (row0 + sub) * p.ldy + u.n0 + c;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (4 * j + sub < rows)
-                            *reinterpret_cast<uint4*>(out + (int64_t)(4 * j) * p.ldy) =
-                                *reinterpret_cast<const uint4*>(stg + (4 * j + sub) * 128 + ((piece ^ ((4 * j + sub) & 7)) << 4));
+                for (int half = 0; half < (kHalf ? 2 : 1); ++half) {
+                    if (kHalf) {
+                        if (half) __syncwarp();   // the first 16 rows have been read
+                        if ((lane >> 4) == half)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                reinterpret_cast<float4*>(stg + (lane & 15) * 128)[j ^ (lane & 7)] = make_float4(
+                                    sum[kChain ? j >> 2 : 0][4 * (j & 3)], sum[kChain ? j >> 2 : 0][4 * (j & 3) + 1],
+                                    sum[kChain ? j >> 2 : 0][4 * (j & 3) + 2], sum[kChain ? j >> 2 : 0][4 * (j & 3) + 3]);
+                    }
+                    __syncwarp();
+                    if (in) {
+#pragma unroll
+                        for (int j = 0; j < (kHalf ? 4 : 8); ++j) {
+                            const int row = 4 * j + sub, at = 16 * half + 4 * j;   // in the box, and of the warp's rows
+                            if (at + sub < rows)
+                                *reinterpret_cast<uint4*>(out + (int64_t)at * p.ldy) =
+                                    *reinterpret_cast<const uint4*>(stg + row * 128 + ((piece ^ (row & 7)) << 4));
+                        }
+                    }
                 }
             }
-            if (held) release();   // a warp without columns or rows
-            if (kAdd && parts == 1) {
+            if (!kChain && held) release(acc);   // a warp without columns
+            if (kAdd && parts == 1 && !idle) {
                 // the boxes were read and written here; the next unit's come by TMA
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -713,11 +761,10 @@ __global__ void __launch_bounds__(kRgThreads, 1) ragged_kernel(const __grid_cons
                     aph ^= 1u;
                 }
             }
-            }
-            if (!live) break;
         }
     }
-    close_frame(f, p.stages, kAdd ? p.adds : 0, pr, ad);
+    // (what CTA 1 loads counts on CTA 0's barriers)
+    close_frame<kPair>(f, p.stages, kAdd ? p.adds : 0, rank ? Started() : pr, ad);
 }
 
 // ------------------------------------------------------------------------ matrices
@@ -863,7 +910,7 @@ __device__ __forceinline__ void zero_rows(uint8_t* chunk, int chunks, int tail, 
 //   tfull[a]   each    the MMA thread's multicast commit at the end of a chain
 //   tempty[a]  CTA 0   the 16 epilogue warps of each CTA
 template <int MI, bool kPair>
-__global__ void __launch_bounds__(kRgDwThreads + (kPair ? 32 : 0), 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
+__global__ void __launch_bounds__(kRgSumThreads + (kPair ? 32 : 0), 1) ragged_dw_kernel(const __grid_constant__ CUtensorMap tmM,
                                                                   const __grid_constant__ CUtensorMap tmN,
                                                                   const __grid_constant__ CUtensorMap tmG,
                                                                   const RgDwParams p) {
@@ -1000,7 +1047,7 @@ __global__ void __launch_bounds__(kRgDwThreads + (kPair ? 32 : 0), 1) ragged_dw_
                 }
             }
         }
-    } else if (kPair && warp == kRgDwThreads / 32) {
+    } else if (kPair && warp == kRgSumThreads / 32) {
         uint32_t s = 0, ph = 0;
         bool live = true;
         for (int i = first; i < total && live; i += stride) {
@@ -1154,10 +1201,10 @@ bool encode_g(CUtensorMap* m, float* g, int E, int K, int N) {
            CUDA_SUCCESS;
 }
 
-cudaLaunchConfig_t rg_config(int grid, cudaStream_t st, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t rg_config(int grid, int threads, cudaStream_t st, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kRgThreads, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = kRgSmem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1168,14 +1215,21 @@ cudaLaunchConfig_t rg_config(int grid, cudaStream_t st, cudaLaunchAttribute* att
 }
 
 // Pairs of CTAs.
-cudaLaunchConfig_t rg_pair_config(int pairs, cudaStream_t st, cudaLaunchAttribute* attr) {
-    cudaLaunchConfig_t cfg = rg_config(2 * pairs, st, attr);
+cudaLaunchConfig_t rg_pair_config(int pairs, int threads, cudaStream_t st, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = rg_config(2 * pairs, threads, st, attr);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     return cfg;
+}
+
+using RowKernel = void (*)(CUtensorMap, RowMaps, RowMaps, RgParams);
+template <int kSum, bool kPair>
+RowKernel row_kernel(bool trans, bool add) {
+    if (kPair || !add) return trans ? ragged_kernel<true, false, kSum, kPair> : ragged_kernel<false, false, kSum, kPair>;
+    return trans ? ragged_kernel<true, !kPair, kSum, kPair> : ragged_kernel<false, !kPair, kSum, kPair>;
 }
 
 // `width` in tiles of at most `most` columns, all of one size (a multiple of 16, or of `unit` where there are several).
@@ -1188,24 +1242,29 @@ void cut(int width, int most, int* tile, int* tiles, int unit = 16) {
 }  // namespace
 
 cudaError_t ragged_setup(int num_sms, int* pairs) {
-    const void* kernels[] = {(const void*)ragged_kernel<false, false, false>, (const void*)ragged_kernel<false, true, false>,
-                             (const void*)ragged_kernel<true, false, false>, (const void*)ragged_kernel<true, true, false>,
-                             (const void*)ragged_kernel<false, false, true>, (const void*)ragged_kernel<true, false, true>,
-                             (const void*)ragged_dw_kernel<1, false>, (const void*)ragged_dw_kernel<2, false>,
-                             (const void*)ragged_dw_kernel<1, true>};
+    const void* kernels[] = {
+        (const void*)ragged_kernel<false, false, 0, false>, (const void*)ragged_kernel<true, false, 0, false>,
+        (const void*)ragged_kernel<false, true, 0, false>, (const void*)ragged_kernel<true, true, 0, false>,
+        (const void*)ragged_kernel<false, false, 8, false>, (const void*)ragged_kernel<true, false, 8, false>,
+        (const void*)ragged_kernel<false, true, 8, false>, (const void*)ragged_kernel<true, true, 8, false>,
+        (const void*)ragged_kernel<false, false, 16, false>, (const void*)ragged_kernel<true, false, 16, false>,
+        (const void*)ragged_kernel<false, true, 16, false>, (const void*)ragged_kernel<true, true, 16, false>,
+        (const void*)ragged_kernel<false, false, 16, true>, (const void*)ragged_kernel<true, false, 16, true>,
+        (const void*)ragged_dw_kernel<1, false>, (const void*)ragged_dw_kernel<2, false>,
+        (const void*)ragged_dw_kernel<1, true>};
     for (const void* k : kernels) {
         const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRgSmem);
         if (err != cudaSuccess) return err;
     }
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = rg_pair_config(num_sms / 2, nullptr, attr);
-    cfg.blockDim = dim3(kRgDwThreads + 32, 1, 1);   // (an SM holds one CTA of either kernel)
+    cudaLaunchConfig_t cfg = rg_pair_config(num_sms / 2, kRgSumThreads + 32, nullptr, attr);   // (an SM holds one CTA of either kernel)
     return cudaOccupancyMaxActiveClusters(pairs, ragged_dw_kernel<1, true>, &cfg);
 }
 
 cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                           const uint16_t* x, int64_t ldx, int K, const uint16_t* w, int N, int trans, float alpha,
-                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, cudaStream_t st) {
+                          const uint16_t* add, int64_t ldadd, uint16_t* y, int64_t ldy, int num_sms, int pairs,
+                          cudaStream_t st) {
     const int64_t rows = (int64_t)d.R * d.C;
     RgParams p = {};
     p.tiles = ws.tiles;
@@ -1239,22 +1298,24 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     const bool thin = add && p.kbn < 16 && !few;
     const int wide = thin ? 128 : 256;
     cut(N, most * ((N + wide - 1) / wide) < num_sms ? 64 : wide, &p.BN, &p.NT);
-    // Two row tiles a unit where experts have several and the reduction is worth it: one tile's MMAs do not hide the way of
-    // their operands into shared memory.
-    const bool dual = !add && !p.local && p.BN > 128 && p.kbn >= 8 && rows / d.E >= 512;
-    if (dual) {
+    // Tiles of 256 rows on pairs of SMs where experts have several and the reduction is worth it: one SM's MMAs do not hide
+    // the way of their operands into shared memory.
+    const bool pair = !add && !p.local && p.BN > 128 && p.kbn >= 8 && rows / d.E >= 512 && pairs > 0;
+    const int sum = !pair && p.kbn <= kRgRowChain ? 0 : p.BN <= 128 ? 8 : 16;
+    if (pair) {
         p.tile_rows = 256;
-        p.a_bytes = 2 * kRgA;
+        p.BN = (p.BN + 31) / 32 * 32;   // halves of 16
     }
     p.by_nt = make_fast_div((uint32_t)p.NT);
     p.by_nrow = make_fast_div((uint32_t)d.NROW);
     if (p.BN <= kRgPartCols) p.partial = ws.partial;
     p.steps = K >= 64 ? 4 : (K + 15) / 16;
     p.chunk = p.steps * 16 * 128;   // W [K, N]: boxes of 64 columns no taller than the reduction
-    p.b_bytes = trans ? p.BN * 128 : (p.BN + 63) / 64 * p.chunk;
-    p.adds = add ? (thin ? kRgMaxAdds : few ? 2 : 1) : 0;
+    const int bn = pair ? p.BN / 2 : p.BN;   // W's columns in a CTA
+    p.b_bytes = trans ? bn * 128 : (bn + 63) / 64 * p.chunk;
+    p.adds = add ? (thin ? kRgMaxAdds : few || p.BN <= 64 ? 2 : 1) : 0;
     p.add_bytes = (p.BN + 63) / 64 * kRgA;
-    const int rest = kRgBytes - (p.local ? kRgLocal * (int)sizeof(MTile) : 0) - (add ? p.adds * p.add_bytes : 8 * kRgBox);
+    const int rest = kRgBytes - (p.local ? kRgLocal * (int)sizeof(MTile) : 0) - (add ? p.adds * p.add_bytes : sum ? 2 * ((p.BN + 63) / 64) * kRgBox : 8 * kRgBox);
     const int fit = rest / (p.a_bytes + p.b_bytes);
     p.stages = fit < kRgMaxStages ? fit : kRgMaxStages;
 
@@ -1270,21 +1331,21 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     }
     const uint64_t wd[3] = {(uint64_t)(trans ? K : N), (uint64_t)(trans ? N : K), (uint64_t)d.E};
     const uint64_t wl[2] = {wd[0], wd[0] * wd[1]};
-    if (!encode_rows(&tmW, w, 3, wd, wl, trans ? (uint32_t)p.BN : (uint32_t)p.steps * 16)) return cudaErrorInvalidValue;
+    if (!encode_rows(&tmW, w, 3, wd, wl, trans ? (uint32_t)bn : (uint32_t)p.steps * 16)) return cudaErrorInvalidValue;
     if (!p.local) {
-        const cudaError_t err = dual  ? launch_row_tiles<256>(d, ws, cu, st)
+        const cudaError_t err = pair  ? launch_row_tiles<256>(d, ws, cu, st)
                                 : few ? launch_row_tiles<64>(d, ws, cu, st)
                                       : launch_row_tiles<128>(d, ws, cu, st);
         if (err != cudaSuccess) return err;
     }
-    cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = rg_config(num_sms, st, &attr);
-    if (dual)
-        return cudaLaunchKernelEx(&cfg, trans ? ragged_kernel<true, false, true> : ragged_kernel<false, false, true>, tmW, tmX, tmAdd, p);
-    return cudaLaunchKernelEx(&cfg,
-                              trans ? (add ? ragged_kernel<true, true, false> : ragged_kernel<true, false, false>)
-                                    : (add ? ragged_kernel<false, true, false> : ragged_kernel<false, false, false>),
-                              tmW, tmX, tmAdd, p);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg =
+        pair ? rg_pair_config(pairs, kRgSumThreads, st, attr) : rg_config(num_sms, sum == 16 ? kRgSumThreads : kRgThreads, st, attr);
+    auto* kernel = pair        ? row_kernel<16, true>(trans, false)
+                   : sum == 16 ? row_kernel<16, false>(trans, add)
+                   : sum == 8  ? row_kernel<8, false>(trans, add)
+                               : row_kernel<0, false>(trans, add);
+    return cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, tmAdd, p);
 }
 
 cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
@@ -1342,18 +1403,15 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     const uint64_t yd[2] = {(uint64_t)N, (uint64_t)rows}, ys[1] = {(uint64_t)lddy};
     if (!encode_rows(&tx, x, 2, xd, xs, 64) || !encode_rows(&ty, dy, 2, yd, ys, 64)) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = rg_config(1, st, attr);
-    cfg.blockDim = dim3(1024, 1, 1);
+    cudaLaunchConfig_t cfg = rg_config(1, 1024, st, attr);
     cfg.dynamicSmemBytes = 0;
     cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_blocks_kernel, cu, slot_expert, d, ws);
     if (err != cudaSuccess) return err;
     if (pair) {
-        cfg = rg_pair_config(pairs, st, attr);
-        cfg.blockDim = dim3(kRgDwThreads + 32, 1, 1);
+        cfg = rg_pair_config(pairs, kRgSumThreads + 32, st, attr);
         return cudaLaunchKernelEx(&cfg, ragged_dw_kernel<1, true>, x_wide ? tx : ty, x_wide ? ty : tx, tg, p);
     }
-    cfg = rg_config(num_sms, st, attr);
-    cfg.blockDim = dim3(kRgDwThreads, 1, 1);
+    cfg = rg_config(num_sms, kRgSumThreads, st, attr);
     return cudaLaunchKernelEx(&cfg, MI == 2 ? ragged_dw_kernel<2, false> : ragged_dw_kernel<1, false>, x_wide ? tx : ty, x_wide ? ty : tx,
                               tg, p);
 }
