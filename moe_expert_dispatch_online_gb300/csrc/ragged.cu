@@ -1182,9 +1182,14 @@ bool encode_rows(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
     cuuint32_t box[3] = {64, box_rows, 1}, estr[3] = {1, 1, 1};
     for (int i = 0; i < rank; ++i) d[i] = dims[i];
     for (int i = 0; i + 1 < rank; ++i) strides[i] = ld[i] * 2;
+    // L2 fetches lines in pairs where no row starts inside a pair: 262,144 rows of 600 and 1000, whose rows do, take 319 us
+    // instead of 334 (product) and 353 instead of 412 (gradient) with single lines, 131,072 of 7168, which do not, 332 instead of 326.
+    bool whole = reinterpret_cast<uintptr_t>(base) % 256 == 0;
+    for (int i = 0; i + 1 < rank; ++i) whole = whole && strides[i] % 256 == 0;
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
                m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               whole ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
