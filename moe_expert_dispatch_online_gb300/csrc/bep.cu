@@ -3,6 +3,8 @@
 
 #include <stdlib.h>
 
+#include <atomic>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "bep_internal.cuh"
@@ -34,6 +36,30 @@ struct bep_ctx {
 
 namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// What a kernel's set-up (function attributes, occupancy) found on each device, once for all contexts: pairs of CTAs that
+// fit + 1, or 0 before the first call there. A set-up that failed is tried again by the next call.
+constexpr int kDevices = 64;
+using Found = std::atomic<int>[kDevices];
+Found g_i8_clusters, g_ragged_pairs;
+
+// Fills `mine`, a field of the context, before the context's first call of the kernel. Nothing here touches a stream:
+// that call may be a captured one.
+template <typename Setup>
+int first_use(const bep_ctx* ctx, Found& found, int* mine, Setup setup) {
+    if (*mine >= 0) return BEP_OK;
+    std::atomic<int>* known = ctx->device < kDevices ? &found[ctx->device] : nullptr;
+    int n = known ? known->load(std::memory_order_acquire) - 1 : -1;
+    if (n < 0) {
+        if (setup(&n) != cudaSuccess) {
+            cudaGetLastError();
+            return BEP_ERR_CUDA;
+        }
+        if (known) known->store(n + 1, std::memory_order_release);
+    }
+    *mine = n;
+    return BEP_OK;
+}
 }  // namespace
 
 int bep::make_dims(const bep_config* c, bep::Dims* d) {
@@ -504,14 +530,8 @@ int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t*
         return BEP_ERR_ALIGN;
     // work units (row tiles x 128-column output tiles) are counted in 32 bits
     if (ctx->d.tile_cap * (int64_t)((ctx->d.Hp + 127) / 128) >= ((int64_t)1 << 31)) return BEP_ERR_SIZE;
-    if (ctx->i8_clusters < 0) {   // nothing here touches the stream, so the first call may be a captured one
-        int clusters = 0;
-        if (bep::i8_setup(ctx->device, &clusters) != cudaSuccess) {
-            cudaGetLastError();
-            return BEP_ERR_CUDA;
-        }
-        ctx->i8_clusters = clusters;
-    }
+    const int rc = first_use(ctx, g_i8_clusters, &ctx->i8_clusters, [&](int* n) { return bep::i8_setup(ctx->device, n); });
+    if (rc) return rc;
     if (ctx->i8_clusters < 1) return BEP_ERR_CUDA;
     return cuda_rc(bep::launch_grouped_gemm_i8(ctx->d, ctx->ws, cu_seqlens, slot_expert, codes, scales, w_codes,
                                                w_scales, y, ctx->i8_clusters, as_stream(stream)));
@@ -532,14 +552,7 @@ static int check_ragged(const bep_ctx* ctx, int32_t K, int32_t N, int64_t ldx, i
 }
 
 static int ragged_ready(bep_ctx* ctx) {
-    if (ctx->ragged_pairs >= 0) return BEP_OK;   // nothing here touches a stream: the first call may be a captured one
-    int pairs = 0;
-    if (bep::ragged_setup(ctx->num_sms, &pairs) != cudaSuccess) {
-        cudaGetLastError();
-        return BEP_ERR_CUDA;
-    }
-    ctx->ragged_pairs = pairs;
-    return BEP_OK;
+    return first_use(ctx, g_ragged_pairs, &ctx->ragged_pairs, [&](int* n) { return bep::ragged_setup(ctx->num_sms, n); });
 }
 
 int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const uint16_t* x, int64_t ldx,
