@@ -515,7 +515,8 @@ int bep_swiglu_int(bep_ctx* ctx, const uint16_t* h, int32_t F, int8_t* codes, fl
     if (ctx->d.C == 0) return BEP_OK;
     if (!h || !codes || !scales) return BEP_ERR_ARG;
     if (!aligned(h, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return BEP_ERR_ALIGN;
-    return cuda_rc(bep::launch_swiglu_i8((int64_t)ctx->d.R * ctx->d.C, F, h, codes, scales, as_stream(stream)));
+    return cuda_rc(bep::launch_swiglu_i8((int64_t)ctx->d.R * ctx->d.C, F, h, codes, scales, ctx->num_sms,
+                                         as_stream(stream)));
 }
 
 int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot_expert, const int8_t* codes,

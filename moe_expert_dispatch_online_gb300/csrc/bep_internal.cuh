@@ -142,7 +142,8 @@ cudaError_t i8_setup(int device, int* clusters);
 cudaError_t launch_i8_weight(const Dims& d, const uint16_t* w, int8_t* codes, float* scales, cudaStream_t st);
 cudaError_t launch_dispatch_i8(const Dims& d, const Workspace& ws, const uint16_t* x, const int32_t* dest,
                                int8_t* codes, float* scales, int sms, int num_sms, cudaStream_t st);
-cudaError_t launch_swiglu_i8(int64_t rows, int F, const uint16_t* h, int8_t* codes, float* scales, cudaStream_t st);
+cudaError_t launch_swiglu_i8(int64_t rows, int F, const uint16_t* h, int8_t* codes, float* scales, int num_sms,
+                             cudaStream_t st);
 cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int32_t* cu, const int32_t* slot_expert,
                                    const int8_t* codes, const float* scales, const int8_t* w_codes,
                                    const float* w_scales, uint16_t* y, int clusters, cudaStream_t st);

@@ -413,14 +413,6 @@ struct I8Walk {
     }
 };
 
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
 // 32 columns of this warp's 32 TMEM lanes.
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
     __syncwarp();
@@ -987,14 +979,15 @@ cudaError_t launch_dispatch_i8(const Dims& d, const Workspace& ws, const uint16_
     return cudaGetLastError();
 }
 
-cudaError_t launch_swiglu_i8(int64_t rows, int F, const uint16_t* h, int8_t* codes, float* scales, cudaStream_t st) {
+cudaError_t launch_swiglu_i8(int64_t rows, int F, const uint16_t* h, int8_t* codes, float* scales, int num_sms,
+                             cudaStream_t st) {
     const int F8 = F / 8;
     const uint4* hp = reinterpret_cast<const uint4*>(h);
     uint2* cp = reinterpret_cast<uint2*>(codes);
     // as few warps a row as hold it (kActHold * 256 elements each), so that small rows share a CTA; more where
     // the rows alone would leave SMs idle
     int warps = 1;
-    while (warps < 8 && (F8 > warps * 32 * kActHold || (rows * warps < 152 * 16 && F8 > warps * 32))) warps *= 2;
+    while (warps < 8 && (F8 > warps * 32 * kActHold || (rows * warps < num_sms * 16 && F8 > warps * 32))) warps *= 2;
     switch (warps) {
         case 1: run_swiglu_i8<1>(rows, F8, hp, cp, scales, st); break;
         case 2: run_swiglu_i8<2>(rows, F8, hp, cp, scales, st); break;
@@ -1029,13 +1022,15 @@ cudaError_t launch_grouped_gemm_i8(const Dims& d, const Workspace& ws, const int
     if (!encode_u8(&tmW, w_codes, 3, wd, 128)) return cudaErrorInvalidValue;
     for (int i = 0; i < 4; ++i)
         if (!encode_u8(&tmX[i], codes, 2, xd, boxes[i])) return cudaErrorInvalidValue;
-    // Rows a tile by the mean segment: a tile of fewer rows leaves room for more weight codes under way.
+    // Rows a tile by the mean segment: a tile of fewer rows leaves room for more weight codes under way, but a second tile of
+    // a segment reads the weights again. (96 experts of 7168 x 2048, segments of half to one and a half of the mean: 40 rows
+    // 254 us with tiles of 64, 256 with 128; 48 279 and 260; 96 298 with 128, 330 with 256; 112 345 and 323.)
     const int64_t mean = p.nrows / d.E;
     // Every row a tile of its own, at most: units for less than half of the pairs. (Below 14 stages there is one part, and
     // the form without parts is 1.4 us quicker.)
     if (p.nrows <= 64 && p.nrows * ((p.MT + 1) / 2) * 2 <= clusters && d.H >= 14 * kI8K)
         return run_gemm_i8<64, true>(d, ws, cu, tmW, tmX, p, clusters, st);
-    if (mean <= 48) return run_gemm_i8<64>(d, ws, cu, tmW, tmX, p, clusters, st);
+    if (mean <= 40) return run_gemm_i8<64>(d, ws, cu, tmW, tmX, p, clusters, st);
     if (mean <= 96) return run_gemm_i8<128>(d, ws, cu, tmW, tmX, p, clusters, st);
     return run_gemm_i8<256>(d, ws, cu, tmW, tmX, p, clusters, st);
 }

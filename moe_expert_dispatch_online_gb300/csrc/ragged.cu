@@ -84,14 +84,6 @@ struct RgDwParams {
     int32_t* status;
 };
 
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int c0, int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
 // A box of g written, or added (one fp32 rounding an element).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
@@ -1290,7 +1282,8 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     p.kbn = (K + 63) / 64;
     p.status = ws.status;
     p.tickets = ws.tickets;
-    // few rows an expert: half the stage bytes for rows, more stages
+    // Few rows an expert: half the stage bytes for rows, more stages. (384 experts, 16 onto 2048: 40 rows an expert 54 us,
+    // 68 with tiles of 128 rows; 48 60 and 69; 56 67 and 69. 7168 into 16: 73.8 and 74.0, 73.7 and 75.3, 94.9 and 77.4.)
     const bool few = rows / d.E <= 48;
     p.tile_rows = few ? 64 : 128;
     p.a_bytes = few ? kRgA / 2 : kRgA;
@@ -1303,10 +1296,11 @@ cudaError_t launch_ragged(const Dims& d, const Workspace& ws, const int32_t* cu,
     const bool thin = add && p.kbn < 16 && !few;
     const int wide = thin ? 128 : 256;
     cut(N, most * ((N + wide - 1) / wide) < num_sms ? 64 : wide, &p.BN, &p.NT);
-    // Tiles of 256 rows on pairs of SMs where experts have several and the reduction is worth it: one SM's MMAs do not hide
-    // the way of their operands into shared memory.
-    const bool pair = !add && !p.local && p.BN > 128 && p.kbn >= 8 && rows / d.E >= 512 && pairs > 0;
-    const int sum = !pair && p.kbn <= kRgRowChain ? 0 : p.BN <= 128 ? 8 : 16;
+    // Tiles of 256 rows on pairs of SMs where experts have several and the reduction is in chains anyway: one SM's MMAs do
+    // not hide the way of their operands into shared memory. (64 experts to 1024 columns. Rows of 1024: 320 an expert 63 us
+    // on pairs and 64 without, 448 67 and 70, 1024 120 and 133, 2048 205 and 237; 512 rows of 640 55 and 59, of 512 50 and 44.)
+    const bool pair = !add && !p.local && p.BN > 128 && p.kbn > kRgRowChain && rows / d.E >= 384 && pairs > 0;
+    const int sum = p.kbn <= kRgRowChain ? 0 : p.BN <= 128 ? 8 : 16;
     if (pair) {
         p.tile_rows = 256;
         p.BN = (p.BN + 31) / 32 * 32;   // halves of 16

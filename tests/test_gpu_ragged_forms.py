@@ -31,9 +31,9 @@ def exact_rows(x, w, lens, alpha, trans, out):
 
 @pytest.mark.parametrize("trans", [False, True])
 @pytest.mark.parametrize("K,N,pad", [
-    (512, 136, 64),     # one chain of 8 blocks, one tile of columns, rows that start on whole lines
-    (456, 264, 24),     # a last block of 8, two tiles
-    (520, 520, 24),     # two chains, three tiles
+    (576, 136, 64),     # nine blocks in two chains, one tile of columns, rows that start on whole lines
+    (520, 264, 24),     # a last block of 8, two tiles
+    (1032, 520, 24),    # three chains, three tiles
     (1096, 1096, 8),    # more blocks than the ring has stages, five tiles
     (1600, 256, 0),     # one full tile
     (1024, 2048, 64),   # eight full tiles
