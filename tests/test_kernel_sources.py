@@ -20,13 +20,22 @@ def test_warps_converge_before_warp_wide_instructions(path):
     """An instruction that all threads of a warp execute together comes right behind a __syncwarp (or another such
     instruction): the end of a branch or of a loop that lanes left at different times does not bring them together."""
     lines = code(path).split("\n")
-    start = 0                                  # of the statement
+    start, inside = 0, ""                      # of the statement; the function it is in
     for i, line in enumerate(lines):
+        name = re.match(r"(?:template|__device__|__global__)[^(]* (\w+)\(", line)
+        if name:
+            inside = name.group(1)
         if re.search(r"asm volatile\(", line):
             start = i
-        if re.search(r"\.aligned|\bbar\.(sync|red)|\belect\.sync", line):
+        if re.search(r"\.aligned|\bbar\.(sync|red)|\belect\.sync", line) and not inside.endswith("_converged"):
             before = [x for x in lines[max(0, start - 8):start] if x.strip()]
             assert any("__syncwarp();" in x or ".aligned" in x for x in before[-4:]), (os.path.basename(path), i + 1, line)
+        # a helper that relies on its caller: no lane has branched off since the warp was last together
+        if re.search(r"_converged\(", line) and not name:
+            for j in range(i - 1, -1, -1):
+                if re.search(r"__syncwarp\(\)|__all_sync\(", lines[j]):
+                    break
+                assert not re.search(r"\bif \((lane|threadIdx)|\bwhile\b", lines[j]), (os.path.basename(path), i + 1, line)
 
 
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
