@@ -432,8 +432,9 @@ int bep_swiglu_int(bep_ctx* ctx, const uint16_t* h, int32_t F, int8_t* codes, fl
  *   y[u*S*K + seg, n] = (sum_h code[row, h] * w_code[expert, n, h]) * w_scale[expert, n] * scale[row],
  * expert = rho for rho < E and slot_expert[u][rho - E] for a prefetch slot: the slots' replicas are read from
  * the home rows, which all R ranks of this GPU share, so nothing is prefetched.
- * The sum is exact as long as its parts stay below 2^24 (with H <= 1040 always), rounded to fp32 as it grows
- * beyond; y is bf16 (round to nearest even). Rows outside every segment are not written; a bad cu_seqlens is
+ * The sum is exact as long as its parts stay below 2^24 (with H <= 1040 always); beyond, the tensor core truncates it to
+ * fp32 at each 16 products. The two scales follow in fp32, from left to right (a sum that the channel's scale takes beyond
+ * fp32 is infinite, whatever the row's scale); y is bf16 (round to nearest even). Rows outside every segment are not written; a bad cu_seqlens is
  * refused as in bep_grouped_gemm. A non-empty slot segment without an expert in [0, E) is skipped and latches
  * BEP_DERR_BOUNDS.
  *   cu_seqlens [R, E+B+1]; slot_expert [R, B]; codes, scales as bep_dispatch_int or bep_swiglu_int (F = H) wrote
@@ -449,7 +450,8 @@ int bep_grouped_gemm_int(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t*
  * non-empty segment, e = rho for rho < E and slot_expert[u][rho - E] for a prefetch slot,
  *   y[u*S*K + seg, :] = alpha * x[u*S*K + seg, :] @ W(e) + add[u*S*K + seg, :]
  * W(e) = w[e] [K, N], or w[e]^T with w [E, N, K] where trans is 1 (the input gradient of the product with
- * the same w). bf16 in, fp32 accumulation, one rounding to bf16 (nearest even). The widths are the call's own and
+ * the same w). bf16 in, fp32 accumulation, one rounding to bf16 (nearest even): within a chain of up to 512 products the
+ * tensor core truncates the sum at each 16, chains are added rounding to nearest. The widths are the call's own and
  * have nothing to do with the context's H and H'. Rows of y outside every segment are not written; a bad
  * cu_seqlens is refused as in bep_grouped_gemm. A non-empty slot segment without an expert in [0, E) is skipped and
  * latches BEP_DERR_BOUNDS. The same call gives the same bits.
@@ -467,7 +469,7 @@ int bep_ragged_gemm(bep_ctx* ctx, const int32_t* cu_seqlens, const int32_t* slot
  * overflow rows, on every rank; nothing is left in a reduce buffer),
  *   g[e] = alpha * sum over rows x[row]^T dy[row]         (accumulate 0; zeros for an expert without rows)
  *   g[e] += the same                                      (accumulate 1)
- * bf16 in, fp32 sums. In training and inference contexts alike. A bad cu_seqlens is refused as a whole (nothing is
+ * bf16 in, fp32 sums (chains of up to 256 rows, as above). In training and inference contexts alike. A bad cu_seqlens is refused as a whole (nothing is
  * written), a slot without an expert skipped, as above. The gradient of a w used with trans 1 is this call with x
  * and dy, K and N exchanged. The same call gives the same bits.
  *   x [R*S*K, K], rows ldx apart; dy [R*S*K, N], rows lddy apart; g [E, K, N] fp32. Errors as above. */

@@ -93,7 +93,9 @@ __device__ __forceinline__ uint32_t top_f32(uint32_t two) { return max(two & 0xf
 
 // ------------------------------------------------------------------------ weights
 // One CTA: 32 columns n of one expert over the whole reduction, twice: the columns' largest magnitudes, then
-// (from L2) their integers, which meet in shared memory, 256 rows h at a time, and leave as runs along h.
+// their integers, which meet in shared memory, 256 rows h at a time, and leave as runs along h. The CTAs under way hold more
+// than L2 where the reduction is long, so w comes from HBM twice: 384 experts of 7168 x 2048, 11.3 GB, 4.18 ms (6.7 TB/s
+// with both reads), of 1024 x 7168 1.59 ms.
 constexpr int kWCols = 32, kWRows = 256;
 __global__ void __launch_bounds__(kThreads) i8_weight_kernel(const uint4* __restrict__ w, int8_t* __restrict__ codes,
                                                              float* __restrict__ scales, int H, int Hp) {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_i8_kernel(const uint4* __r
 // This GPU's tensor cores multiply integers at a small fraction of their bf16 rate, so the integers become
 // fp16 on the way, which holds them exactly: 1 byte an element in HBM and L2, kind::f16 in the tensor core. Their
 // products and the sums below 2^24 are exact in the fp32 accumulator (any sum of 1,040 products; of rows
-// as they occur, all of them), larger sums are rounded to fp32 as they grow.
+// as they occur, all of them), larger sums are truncated to fp32 at each step of 16.
 // The weights are the M operand, written to TMEM by the warps that convert them, so that shared memory carries
 // them once (1 byte) and not three times; the rows of one segment are the N operand (32..256), in shared memory.
 // A cluster of two CTAs shares a tile of 256 outputs x N rows (cta_group::2): CTA r holds outputs 128 r.. and
@@ -335,9 +337,9 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_i8_kernel(const uint4* __r
 //   free[s]    both    the MMA thread's multicast commit
 //   tfull[a]   both    the MMA thread's multicast commit at the end of a unit
 //   tempty[a]  CTA 0   the 8 epilogue warps of each CTA
-// Few rows: the weights' stream bounds it (64 rows by 384 experts of 7168 x 2048: 155 us, 5.5 TB/s with its start and
-// end). Many: the tensor pipe (80% active) and the hand-over of three stages (524,288 rows by 7168 x 2048: 8.8 ms,
-// 1.75 PFLOP/s; 22 ms with two groups of warps that turned weights and rows both, 12 ms with the rows' codes loaded by
+// Few rows: the weights' stream bounds it (64 rows by 384 experts of 7168 x 2048: 158 us, 5.5 TB/s with its start and
+// end). Many: the tensor pipe (80% active), the hand-over of three stages and, in a long run, power (524,288 rows by 7168 x
+// 2048: 9.2-9.6 ms, 1.6-1.7 PFLOP/s, of 1.68 that a plain product sustains; 22 ms with two groups of warps that turned weights and rows both, 12 ms with the rows' codes loaded by
 // the warps themselves a turn ahead). The conversion (five instructions for four codes) keeps the integer pipe at
 // half of its rate; it and the narrow MMAs are what a short reduction with few rows feels (768 rows by 384 experts of
 // 1024 x 7168: 439 us, 5.6 TB/s; 402 us without either).
@@ -461,7 +463,8 @@ __device__ __forceinline__ bool octet_all(bool v) {
     return r != 0;
 }
 
-// Four int8 to four fp16: the byte with its sign bit turned, behind 0x64, is 1024 + 128 + q in fp16.
+// Four int8 to four fp16, as weight-only quantisation is known to do it: the byte with its sign bit turned, behind 0x64, is
+// 1024 + 128 + q in fp16.
 __device__ __forceinline__ void i8x4_to_f16(uint32_t w, uint32_t* out) {
     const uint32_t u = w ^ 0x80808080u;
     const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));   // 1152

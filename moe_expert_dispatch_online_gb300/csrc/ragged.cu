@@ -14,10 +14,11 @@
 // than SMs, the reduction is cut into parts; each part leaves its fp32 tile in the context's workspace and the CTA that
 // comes last adds them in the order of the parts, so that the result does not depend on who that was.
 //
-// Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 310 us (6.4 TB/s), back from 16: 378 us (5.2 TB/s, all
-// of it writes), their gradient 323 us (6.4 TB/s); 64 onto 2048 with another output to add to: 207 us (5.7 TB/s; 316 us
-// with the epilogue loading that itself). Wide ones by the operands' way into shared memory: 65,536 rows by 1088 x 1600
-// 182 us (1.26 PFLOP/s), by 1096 x 1544, whose rows start inside 128-byte lines and take two requests a piece, 230 us.
+// Narrow products are bound by HBM: 131,072 rows of 7168 into 16: 307 us (6.4 TB/s), back from 16: 376 us (5.2 TB/s, all
+// of it writes), their gradient 327 us (6.4 TB/s; 347 us added to what was there); 64 onto 2048 with another output to add
+// to: 212 us (5.6 TB/s; 316 us with the epilogue loading that itself). Wide ones by the operands' way into shared memory:
+// 65,536 rows by 1088 x 1600 201 us (1.13 PFLOP/s), back 180 us, by 1096 x 1544, whose rows start inside 128-byte lines and
+// take two requests a piece, 236 us, back 215 us.
 
 #include <cudaTypedefs.h>
 
@@ -1382,7 +1383,7 @@ cudaError_t launch_ragged_dw(const Dims& d, const Workspace& ws, const int32_t* 
     }
     // Tiles of 256 along M on pairs of CTAs, where there are enough of them for two rounds; an odd tile's partner only
     // brings its half of the N side. (262,144 rows of 64 experts by 1024 x 1024: 535 -> 425 us, by 600 x 1000, five tiles,
-    // 450 -> 366 us, by 360 x 1000, three, 307 -> 264 us; 8,192 rows by 1096 x 1544: 114 -> 97 us, by 360 x 1000 the same.)
+    // 450 -> 366 us (353 with single L2 lines), by 360 x 1000, three, 307 -> 264 us; 8,192 rows by 1096 x 1544: 114 -> 97 us, by 360 x 1000 the same.)
     const bool pair = MI == 1 && p.BN > 128 && p.MT > 1 && pairs > 0 &&
                       (int64_t)d.E * ((p.MT + 1) / 2) * p.NT >= 2 * pairs;
     if (pair) {
