@@ -147,3 +147,37 @@ def test_two_streams_of_pairs(lib):
         assert bep.bep_status(ctx) == 0
         assert (bits(y[0]) == bits(y[1])).all()
         ctx.close()
+
+
+def test_captured_pairs_with_a_changing_table(lib):
+    """A graph of a product on pairs of SMs and its matrices' gradient, whose table changes between replays: other lengths,
+    no rows at all, a table that is refused."""
+    bep = lib
+    cu, se, n = table(PAIR_LENS, slots=[(1, 300)])
+    E, K, N = len(PAIR_LENS), 584, 264
+    ctx = context(bep, E, 1, n)
+    x, w, dy = ints((n, K), 1), ints((E, K, N), 2), ints((n, N), 3)
+    y = torch.empty(n, N, dtype=torch.bfloat16, device=DEV)
+    g = torch.empty(E, K, N, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        bep.bep_ragged_gemm(ctx, cu, se, x, w, y)
+        bep.bep_ragged_gemm_dw(ctx, cu, se, x, dy, g)
+    for lens in (PAIR_LENS, PAIR_LENS[::-1], [0] * E, [n] + [0] * (E - 1), [1] * E):
+        at = torch.tensor([0, *lens, 0]).cumsum(0)
+        cu[0] = at.to(torch.int32)
+        y.fill_(9.0)
+        graph.replay()
+        assert bep.bep_status(ctx) == 0
+        want = exact_rows(x, w, lens, 1.0, False, torch.full_like(y, 9.0))
+        assert torch.equal(y, want)
+        for e, rows in spans(lens):
+            assert torch.equal(g[e].double(), x[rows].double().t() @ dy[rows].double())
+    cu[0, 3] = n + 1
+    y.fill_(9.0)
+    g.fill_(9.0)
+    graph.replay()
+    assert bep.bep_status(ctx) == bep.BEP_DERR_BOUNDS
+    assert (y == 9).all() and (g == 9).all()
+    ctx.close()
